@@ -11,12 +11,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdt.so")
 
 DT_OK, DT_ERR_ARG, DT_ERR_CUDA, DT_ERR_DEVICE, DT_ERR_DEVICE_TIMEOUT = 0, -1, -2, -3, -4
-DT_BF16, DT_F32 = 0, 1
+DT_BF16, DT_F32, DT_F16 = 0, 1, 2
 DT_GREEDY, DT_SAMPLE = 0, 1
 DT_VERIFY_PACKED = 2
 DT_POLICY_CAST_WIDTH_DEPTH, DT_POLICY_CAST_VERIFY, DT_POLICY_GRAFT_CHECKPOINT, DT_POLICY_NONE = 0, 1, 2, 3
 DT_DEV_BAD_LOGITS, DT_DEV_BAD_TOKEN, DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_INTERNAL = 1, 2, 4, 8, 16
-DT_DEV_KV_FULL = 32
+DT_DEV_KV_FULL, DT_DEV_BAD_PAGE = 32, 64
+DT_SEEN_PROMPT = 0x40000000
 DT_FLAG_TEST_TIMEOUT = 1
 DT_ANCHOR_ROOT, DT_ANCHOR_TAIL = 0, 1
 
@@ -25,7 +26,9 @@ EXPORTS = ["dt_last_error_string", "dt_create", "dt_destroy", "dt_get_tree", "dt
            "dt_rerank", "dt_graft_retrieve", "dt_build_tree_meta", "dt_verify", "dt_adj_update",
            "dt_row_topk_static", "dt_cast_prune_select",
            "dt_cast_verify_rerank", "dt_expand_prune_select", "dt_verify_rows", "dt_verify_accept",
-           "dt_commit_kv", "dt_block_expand", "dt_expand_layer_sampled", "dt_verify_sampled"]
+           "dt_commit_kv", "dt_block_expand", "dt_expand_layer_sampled", "dt_verify_sampled",
+           "dt_kv_reserve", "dt_kv_release", "dt_commit_kv_paged", "dt_tree_attention",
+           "dt_tree_attention_workspace", "dt_count_tokens", "dt_logits_process"]
 
 c_i32p = ctypes.c_void_p
 vp = ctypes.c_void_p
@@ -69,6 +72,41 @@ class DtTreeMeta(ctypes.Structure):
                 ("retrieve", vp), ("n_leaves", vp), ("n_pos", vp), ("row_off", vp)]
 
 
+class DtBlockPool(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("block_table", vp), ("n_owned", vp), ("free_list", vp), ("free_count", vp)]
+
+
+class DtKvRows(ctypes.Structure):
+    _fields_ = [("tmp", vp), ("tmp_plane", ctypes.c_int64), ("tmp_row", ctypes.c_int64),
+                ("tmp_head", ctypes.c_int64), ("rows", ctypes.c_int64), ("cache", vp),
+                ("cache_plane", ctypes.c_int64), ("cache_block", ctypes.c_int64), ("cache_tok", ctypes.c_int64),
+                ("cache_head", ctypes.c_int64), ("planes", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_bytes", ctypes.c_int64), ("page", ctypes.c_int32), ("n_blocks", ctypes.c_int32)]
+
+
+class DtAttnArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("P", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("shared_len", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("q", vp), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("out", vp), ("o_row", ctypes.c_int64), ("o_head", ctypes.c_int64),
+                ("k_new", vp), ("v_new", vp), ("kn_row", ctypes.c_int64), ("kn_head", ctypes.c_int64),
+                ("vn_row", ctypes.c_int64), ("vn_head", ctypes.c_int64),
+                ("k_pages", vp), ("v_pages", vp), ("k_block", ctypes.c_int64), ("k_tok", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_block", ctypes.c_int64), ("v_tok", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("n_blocks", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("block_table", vp), ("max_blocks", ctypes.c_int32), ("seq_len", vp), ("n_pos", vp), ("mask", vp),
+                ("row_off", vp), ("workspace", vp), ("workspace_bytes", ctypes.c_int64)]
+
+
+class DtLogitsParams(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int32), ("n_pos", vp), ("row_off", vp), ("rows", ctypes.c_int64), ("tokens", vp),
+                ("mask", vp), ("counts", vp), ("repetition", vp), ("frequency", vp), ("presence", vp),
+                ("bias_ids", vp), ("bias_vals", vp), ("n_bias", ctypes.c_int32), ("allow", vp),
+                ("allow_ld", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libdt.so not found at {LIB_PATH}: build it with __graft_entry__.build() "
@@ -109,6 +147,17 @@ def _load():
         "dt_commit_kv": ([vp, vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int64,
                           ctypes.c_int32, ctypes.c_int64, vp, vp, vp, ctypes.c_int32, vp, vp], I),
         "dt_cast_verify_rerank": ([vp, ctypes.POINTER(DtPruneParams), ctypes.POINTER(DtPruneOut), vp, vp], I),
+        "dt_kv_reserve": ([vp, ctypes.c_int32, ctypes.POINTER(DtBlockPool), vp, vp, ctypes.c_int32, vp,
+                           ctypes.c_int64, ctypes.c_int32, vp, vp], I),
+        "dt_kv_release": ([vp, ctypes.c_int32, ctypes.POINTER(DtBlockPool), vp, vp], I),
+        "dt_commit_kv_paged": ([vp, ctypes.c_int32, ctypes.POINTER(DtKvRows), ctypes.c_int32, vp, vp, ctypes.c_int32,
+                                vp, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, vp, vp], I),
+        "dt_tree_attention": ([vp, ctypes.POINTER(DtAttnArgs), vp], I),
+        "dt_tree_attention_workspace": ([vp] + [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int64)], I),
+        "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
+                             ctypes.c_int32, vp], I),
+        "dt_logits_process": ([vp, ctypes.c_int32, vp, ctypes.c_int64, vp, ctypes.c_int64,
+                               ctypes.POINTER(DtLogitsParams), vp], I),
         "dt_row_topk_static": ([vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                 vp, vp, vp, vp], I),
     }

@@ -553,6 +553,173 @@ int dt_commit_kv(dt_handle* h, const void* tmp_kv, int64_t tmp_pos_stride, int64
   return DT_OK;
 }
 
+static int check_batch(const dt_handle* h, const char* who, int32_t B) {
+  if (!h) return fail(DT_ERR_ARG, "%s: null handle", who);
+  if (B < 1 || B > h->cfg.B_max) return fail(DT_ERR_ARG, "%s: B must be in [1, B_max]", who);
+  return DT_OK;
+}
+
+static bool good_page(int32_t page) { return page >= 8 && page <= 256 && (page & (page - 1)) == 0; }
+
+static int check_pool(const char* who, const dt_block_pool* p) {
+  if (!p || !p->block_table || !p->n_owned || !p->free_list || !p->free_count)
+    return fail(DT_ERR_ARG, "%s: null pool argument", who);
+  if (!good_page(p->page)) return fail(DT_ERR_ARG, "%s: page must be a power of two in [8, 256]", who);
+  if (p->n_blocks < 1 || p->max_blocks < 1) return fail(DT_ERR_ARG, "%s: n_blocks and max_blocks must be >= 1", who);
+  if (!aligned(p->block_table, 4) || !aligned(p->n_owned, 4) || !aligned(p->free_list, 4) || !aligned(p->free_count, 4))
+    return fail(DT_ERR_ARG, "%s: int32 arrays must be 4-byte aligned", who);
+  return DT_OK;
+}
+
+int dt_kv_reserve(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* seq_len, const int32_t* n_new,
+                  int32_t n_extra, int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
+                  cudaStream_t s) {
+  int rc = check_batch(h, "dt_kv_reserve", B);
+  if (rc == DT_OK) rc = check_pool("dt_kv_reserve", pool);
+  if (rc != DT_OK) return rc;
+  if (!seq_len || !n_new || !slots) return fail(DT_ERR_ARG, "dt_kv_reserve: null argument");
+  if (S < 1 || n_extra < 0) return fail(DT_ERR_ARG, "dt_kv_reserve: S >= 1 and n_extra >= 0");
+  if (n_slots < 0 || (!slot_off && n_slots < (int64_t)B * S))
+    return fail(DT_ERR_ARG, "dt_kv_reserve: slots holds fewer than B * S entries");
+  if (!aligned(slots, 8) || !aligned(seq_len, 4) || !aligned(n_new, 4) || !aligned(slot_off, 4))
+    return fail(DT_ERR_ARG, "dt_kv_reserve: misaligned array");
+  cudaError_t e = dt::launch_kv_reserve(h, B, pool, seq_len, n_new, n_extra, slots, n_slots, S, slot_off, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_kv_reserve");
+  return DT_OK;
+}
+
+int dt_kv_release(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* keep_len, cudaStream_t s) {
+  int rc = check_batch(h, "dt_kv_release", B);
+  if (rc == DT_OK) rc = check_pool("dt_kv_release", pool);
+  if (rc != DT_OK) return rc;
+  if (!keep_len) return fail(DT_ERR_ARG, "dt_kv_release: null argument");
+  if (!aligned(keep_len, 4)) return fail(DT_ERR_ARG, "dt_kv_release: misaligned array");
+  cudaError_t e = dt::launch_kv_release(h, B, pool, keep_len, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_kv_release");
+  return DT_OK;
+}
+
+int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P, const int32_t* row_off,
+                       const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra,
+                       const int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
+                       const int32_t* seq_len, int32_t* len_out, cudaStream_t s) {
+  const int rc = check_batch(h, "dt_commit_kv_paged", B);
+  if (rc != DT_OK) return rc;
+  if (!kv || !kv->tmp || !kv->cache || !n_new || !slots || !seq_len || !len_out)
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: null argument");
+  if (P < 1 || S < 1 || n_extra < 0 || (path && D_path < 1) || kv->rows < 1)
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: P, S, rows, D_path >= 1 and n_extra >= 0");
+  if (kv->planes < 1 || kv->planes > 65535) return fail(DT_ERR_ARG, "dt_commit_kv_paged: planes must be in [1, 65535]");
+  if (!good_page(kv->page) || kv->n_blocks < 1)
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: page must be a power of two in [8, 256] and n_blocks >= 1");
+  if (kv->heads < 1 || kv->head_bytes < 16 || kv->heads > (int64_t)(1 << 20) / kv->head_bytes)
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: heads >= 1, head_bytes >= 16, a plane's row at most 1 MB");
+  if (!aligned(kv->tmp, 16) || !aligned(kv->cache, 16) || kv->tmp_plane % 16 || kv->tmp_row % 16 || kv->tmp_head % 16 ||
+      kv->cache_plane % 16 || kv->cache_block % 16 || kv->cache_tok % 16 || kv->cache_head % 16 || kv->head_bytes % 16)
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: pointers, strides and head_bytes must be multiples of 16 bytes");
+  if (n_slots < 0 || (!slot_off && n_slots < (int64_t)B * S))
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: slots holds fewer than B * S entries");
+  if (!aligned(slots, 8) || !aligned(seq_len, 4) || !aligned(len_out, 4) || !aligned(n_new, 4) || !aligned(path, 4) ||
+      !aligned(row_off, 4) || !aligned(slot_off, 4))
+    return fail(DT_ERR_ARG, "dt_commit_kv_paged: misaligned array");
+  cudaError_t e = dt::launch_commit_kv_paged(h, B, kv, P, row_off, path, D_path, n_new, n_extra, slots, n_slots, S,
+                                             slot_off, seq_len, len_out, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_commit_kv_paged");
+  return DT_OK;
+}
+
+static int check_attn_sizes(const dt_handle* h, const char* who, int32_t B, int32_t P, int32_t H_q, int32_t H_kv,
+                            int32_t D) {
+  const int rc = check_batch(h, who, B);
+  if (rc != DT_OK) return rc;
+  if (P < 1 || P > h->cfg.P_max) return fail(DT_ERR_ARG, "%s: P must be in [1, P_max]", who);
+  if (H_kv < 1 || H_q < H_kv || H_q % H_kv || H_q / H_kv > 128 || H_q > 4096)
+    return fail(DT_ERR_ARG, "%s: H_q must be a multiple of H_kv, H_q / H_kv <= 128, H_q <= 4096", who);
+  if (D < 8 || D > 128 || D % 8) return fail(DT_ERR_ARG, "%s: D must be a multiple of 8 in [8, 128]", who);
+  return DT_OK;
+}
+
+int dt_tree_attention_workspace(dt_handle* h, int32_t B, int32_t P, int32_t H_q, int32_t H_kv, int32_t D,
+                                int32_t shared, int64_t* bytes) {
+  const int rc = check_attn_sizes(h, "dt_tree_attention_workspace", B, P, H_q, H_kv, D);
+  if (rc != DT_OK) return rc;
+  if (!bytes) return fail(DT_ERR_ARG, "dt_tree_attention_workspace: null argument");
+  *bytes = dt::attn_workspace_bytes(h, B, P, H_q, H_kv, D, shared ? 1 : 0);
+  return DT_OK;
+}
+
+int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
+  if (!h || !a) return fail(DT_ERR_ARG, "dt_tree_attention: null argument");
+  const int rc = check_attn_sizes(h, "dt_tree_attention", a->B, a->P, a->H_q, a->H_kv, a->D);
+  if (rc != DT_OK) return rc;
+  if (!a->q || !a->out || !a->k_new || !a->v_new || !a->k_pages || !a->v_pages || !a->block_table || !a->seq_len ||
+      !a->n_pos || !a->workspace)
+    return fail(DT_ERR_ARG, "dt_tree_attention: null argument");
+  if (a->dtype != DT_BF16 && a->dtype != DT_F16) return fail(DT_ERR_ARG, "dt_tree_attention: dtype must be DT_BF16 or DT_F16");
+  if (!good_page(a->page) || a->n_blocks < 1 || a->max_blocks < 1)
+    return fail(DT_ERR_ARG, "dt_tree_attention: page must be a power of two in [8, 256], n_blocks and max_blocks >= 1");
+  if (a->shared_len < 0 || a->shared_len % a->page || a->shared_len / a->page > a->max_blocks)
+    return fail(DT_ERR_ARG, "dt_tree_attention: shared_len must be a multiple of page within max_blocks");
+  if (!(a->scale > 0.0f) || a->scale > 1e30f) return fail(DT_ERR_ARG, "dt_tree_attention: scale must be positive and finite");
+  if (a->rows < 1 || a->rows > 0x7FFFFFFFll || (!a->row_off && a->rows < (int64_t)a->B * a->P))
+    return fail(DT_ERR_ARG, "dt_tree_attention: rows must hold B * P rows and fit 31 bits");
+  const void* p16[] = {a->q, a->out, a->k_new, a->v_new, a->k_pages, a->v_pages};
+  for (const void* p : p16)
+    if (!aligned(p, 16)) return fail(DT_ERR_ARG, "dt_tree_attention: tensors must be 16-byte aligned");
+  const int64_t st[] = {a->q_row,  a->q_head,  a->o_row, a->o_head, a->kn_row,  a->kn_head, a->vn_row,
+                        a->vn_head, a->k_block, a->k_tok, a->k_head, a->v_block, a->v_tok,   a->v_head};
+  for (int64_t x : st)
+    if (x < a->D || x % 8 || x > (int64_t)1 << 38)
+      return fail(DT_ERR_ARG, "dt_tree_attention: strides must be multiples of 8 elements, at least D");
+  if (!aligned(a->block_table, 4) || !aligned(a->seq_len, 4) || !aligned(a->n_pos, 4) || !aligned(a->row_off, 4))
+    return fail(DT_ERR_ARG, "dt_tree_attention: int32 arrays must be 4-byte aligned");
+  if (!aligned(a->workspace, 256) ||
+      a->workspace_bytes < dt::attn_workspace_bytes(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0))
+    return fail(DT_ERR_ARG, "dt_tree_attention: workspace too small (dt_tree_attention_workspace) or not 256-byte aligned");
+  cudaError_t e = dt::launch_attention(h, a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_tree_attention");
+  return DT_OK;
+}
+
+int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int32_t P, const int32_t* row_off,
+                    const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra, int32_t prompt,
+                    cudaStream_t s) {
+  const int rc = check_batch(h, "dt_count_tokens", B);
+  if (rc != DT_OK) return rc;
+  if (!counts || !tokens || !n_new) return fail(DT_ERR_ARG, "dt_count_tokens: null argument");
+  if (P < 1 || n_extra < 0 || (path && D_path < 1)) return fail(DT_ERR_ARG, "dt_count_tokens: P, D_path >= 1 and n_extra >= 0");
+  if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(n_new, 4) || !aligned(path, 4) || !aligned(row_off, 4))
+    return fail(DT_ERR_ARG, "dt_count_tokens: int32 arrays must be 4-byte aligned");
+  cudaError_t e = dt::launch_count_tokens(h, B, counts, tokens, P, row_off, path, D_path, n_new, n_extra,
+                                          prompt ? 1 : 0, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_count_tokens");
+  return DT_OK;
+}
+
+int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, void* out, int64_t ld_out,
+                      const dt_logits_params* p, cudaStream_t s) {
+  const int rc = check_batch(h, "dt_logits_process", B);
+  if (rc != DT_OK) return rc;
+  if (!logits || !out || !p || !p->n_pos) return fail(DT_ERR_ARG, "dt_logits_process: null argument");
+  if (p->P < 1 || p->P > h->cfg.P_max) return fail(DT_ERR_ARG, "dt_logits_process: P must be in [1, P_max]");
+  if (ld < h->cfg.V || ld_out < h->cfg.V) return fail(DT_ERR_ARG, "dt_logits_process: ld < V");
+  if (p->rows < 1 || (!p->row_off && p->rows < (int64_t)B * p->P))
+    return fail(DT_ERR_ARG, "dt_logits_process: rows must hold B * P rows");
+  if (p->n_bias < 0 || p->n_bias > 4096 || (p->n_bias > 0 && p->bias_ids && !p->bias_vals))
+    return fail(DT_ERR_ARG, "dt_logits_process: n_bias must be in [0, 4096], with ids and values");
+  if (p->allow && p->allow_ld < (h->cfg.V + 31) / 32) return fail(DT_ERR_ARG, "dt_logits_process: allow_ld < ceil(V / 32)");
+  const size_t esz = h->cfg.dtype == DT_BF16 ? 2 : 4;
+  if (!aligned(logits, esz) || !aligned(out, esz)) return fail(DT_ERR_ARG, "dt_logits_process: rows not aligned to their element size");
+  if (logits == out && ld != ld_out) return fail(DT_ERR_ARG, "dt_logits_process: in place needs the same ld");
+  if (!aligned(p->n_pos, 4) || !aligned(p->row_off, 4) || !aligned(p->tokens, 4) || !aligned(p->counts, 4) ||
+      !aligned(p->repetition, 4) || !aligned(p->frequency, 4) || !aligned(p->presence, 4) || !aligned(p->bias_ids, 4) ||
+      !aligned(p->bias_vals, 4) || !aligned(p->allow, 4))
+    return fail(DT_ERR_ARG, "dt_logits_process: arrays must be 4-byte aligned");
+  cudaError_t e = dt::launch_logits(h, B, logits, ld, out, ld_out, p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_logits_process");
+  return DT_OK;
+}
+
 int dt_row_topk_static(const void* logits, int64_t ld, int32_t rows, int32_t V, int32_t K, int32_t dtype,
                        float* logp, int32_t* ids, int32_t* status, cudaStream_t s) {
   if (!logits || !logp || !ids) return fail(DT_ERR_ARG, "dt_row_topk_static: null argument");

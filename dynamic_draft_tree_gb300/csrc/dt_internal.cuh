@@ -179,6 +179,21 @@ cudaError_t launch_commit_kv(dt_handle* h, const void* tmp_kv, int64_t tmp_pos_s
                              int64_t row_bytes, int32_t* cache_len, const int32_t* accept_len,
                              const int32_t* accept_path, int D_path, const int32_t* tmp_row_off,
                              cudaStream_t s);
+cudaError_t launch_kv_reserve(dt_handle* h, int B, const dt_block_pool* pool, const int32_t* seq_len,
+                              const int32_t* n_new, int n_extra, int64_t* slots, int64_t n_slots, int S,
+                              const int32_t* slot_off, cudaStream_t s);
+cudaError_t launch_kv_release(dt_handle* h, int B, const dt_block_pool* pool, const int32_t* keep_len, cudaStream_t s);
+cudaError_t launch_commit_kv_paged(dt_handle* h, int B, const dt_kv_rows* kv, int P, const int32_t* row_off,
+                                   const int32_t* path, int D_path, const int32_t* n_new, int n_extra,
+                                   const int64_t* slots, int64_t n_slots, int S, const int32_t* slot_off,
+                                   const int32_t* seq_len, int32_t* len_out, cudaStream_t s);
+cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
+int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared);
+cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
+                          const dt_logits_params* p, cudaStream_t s);
+cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int P,
+                                const int32_t* row_off, const int32_t* path, int D_path, const int32_t* n_new,
+                                int n_extra, int prompt, cudaStream_t s);
 cudaError_t launch_row_topk_static(const void* logits, int64_t ld, int rows, int V, int K, int dtype, float* logp,
                                    int32_t* ids, int32_t* status, cudaStream_t s);
 

@@ -50,7 +50,7 @@ extern "C" {
 #endif
 
 enum { DT_OK = 0, DT_ERR_ARG = -1, DT_ERR_CUDA = -2, DT_ERR_DEVICE = -3, DT_ERR_DEVICE_TIMEOUT = -4 };
-enum { DT_BF16 = 0, DT_F32 = 1 };
+enum { DT_BF16 = 0, DT_F32 = 1, DT_F16 = 2 }; /* DT_F16: dt_tree_attention only */
 enum { DT_GREEDY = 0, DT_SAMPLE = 1 };
 /* OR-ed into the verify mode: padding-free target rows. Request b's used rows are packed after those
  * of requests 0..b-1: row (b, i) is row row_off[b] + i of the logits buffer, with
@@ -70,7 +70,9 @@ enum {
   DT_DEV_BAD_TREE = 4,     /* selection not parent-closed, or a tree deeper than D_path - 1    */
   DT_DEV_TIMEOUT = 8,      /* a bounded wait on an asynchronous copy ran out                   */
   DT_DEV_INTERNAL = 16,    /* an internal iteration bound was hit                              */
-  DT_DEV_KV_FULL = 32      /* dt_commit_kv: a request's rows would pass the cache's capacity   */
+  DT_DEV_KV_FULL = 32,     /* dt_commit_kv: a request's rows would pass the cache's capacity;
+                              dt_kv_reserve, dt_commit_kv_paged: no pages for a request's tokens */
+  DT_DEV_BAD_PAGE = 64     /* a block id, slot, length or row offset outside its pool or buffer  */
 };
 /* dt_config.flags */
 enum { DT_FLAG_TEST_TIMEOUT = 1 }; /* test only: the expansion row scans (dt_expand_layer and the
@@ -395,6 +397,154 @@ int dt_commit_kv(dt_handle* h, const void* tmp_kv, int64_t tmp_pos_stride, int64
                  void* cache, int64_t cache_pos_stride, int64_t cache_req_stride, int32_t L_max, int64_t row_bytes,
                  int32_t* cache_len, const int32_t* accept_len, const int32_t* accept_path, int32_t D_path,
                  const int32_t* tmp_row_off, cudaStream_t s);
+
+/* ---- Paged KV cache and the target's verify forward -------------------------------------------
+ * The calls below serve the target model's forward between dt_build_tree_meta and dt_verify, and the
+ * commit after it. They take the batch size themselves (1 <= B <= B_max) and need no tree in the
+ * handle; the handle gives the status word, B_max, V and the logits type. The pages continue the
+ * temporary-KV convention of dt_commit_kv: the tree's keys and values live in a temporary buffer, one
+ * row a position (padded [B][P] or packed by row_off), and accepted rows move into the cache. */
+
+/* Pages of `page` tokens (8..256, a power of two) and who owns them. All arrays device, caller-owned.
+ * The block of request b's tokens [e*page, (e+1)*page) is block_table[b][e]; entries at and past
+ * n_owned[b] are -1. free_list holds free_count[0] free block ids, taken from and given back to its end. */
+typedef struct {
+  int32_t page, n_blocks, max_blocks;
+  int32_t* block_table; /* [B][max_blocks]                   */
+  int32_t* n_owned;     /* [B]                               */
+  int32_t* free_list;   /* [n_blocks]                        */
+  int32_t* free_count;  /* [1]                               */
+} dt_block_pool;
+
+/* Pages and slots for the n = n_new[b] + n_extra tokens that follow request b's seq_len[b] ones (n_new =
+ * accept_len, n_extra = 1: a round's commit; n_new = prompt lengths: a prefill). A request that owns fewer
+ * than ceil((seq_len + n) / page) blocks takes the missing ones from the end of the free list, requests in
+ * ascending order; one whose blocks, together with those that the requests before it lack, are more than
+ * the list holds gets none, and neither does one that needs more than max_blocks or whose n exceeds its
+ * room for slots: it keeps its table, its slots are -1 and DT_DEV_KV_FULL is set (DT_DEV_BAD_PAGE for a
+ * negative length or a corrupt table). Calling it twice without a commit reserves nothing more.
+ * slots: device int64, slot of token seq_len[b] + j = block * page + offset in the block, -1 past n:
+ *   slot_off NULL: [B][S]; else (device [B+1]) packed: request b's at slot_off[b] .. slot_off[b+1] - 1,
+ *   at most S of them; entries past slot_off[B] are left as they were.
+ * n_slots: entries of the slots buffer (offsets beyond it set DT_DEV_BAD_PAGE, the request gets none).
+ * Two launches, or one for a few slots. seq_len is read only (dt_commit_kv_paged advances it). */
+int dt_kv_reserve(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* seq_len, const int32_t* n_new,
+                  int32_t n_extra, int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
+                  cudaStream_t s);
+
+/* Gives back the blocks past the first ceil(keep_len[b] / page) of every request (keep_len = seq_len rolls an
+ * unused reservation back, 0 ends a request): the entries become -1. Blocks go back so that the
+ * reservation that took them last is undone exactly: the last block of the last request lowest. */
+int dt_kv_release(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* keep_len, cudaStream_t s);
+
+/* KV rows and pages as strided bytes (every stride, pointer and head_bytes a multiple of 16). A plane is one
+ * layer's keys or values; a row is `heads` runs of head_bytes. Row r of plane p, head x is at
+ * tmp + p*tmp_plane + r*tmp_row + x*tmp_head; slot t at cache + p*cache_plane + (t / page)*cache_block +
+ * (t % page)*cache_tok + x*cache_head (so pages may be [page][heads] or [heads][page]). */
+typedef struct {
+  const void* tmp;
+  int64_t tmp_plane, tmp_row, tmp_head;
+  int64_t rows;           /* rows of tmp: a row outside sets DT_DEV_BAD_TREE and is not copied */
+  void* cache;
+  int64_t cache_plane, cache_block, cache_tok, cache_head;
+  int32_t planes, heads;
+  int64_t head_bytes;
+  int32_t page, n_blocks;
+} dt_kv_rows;
+
+/* dt_commit_kv into pages: the KV row of token j < n = n_new[b] + n_extra of request b, at row
+ * (row_off ? row_off[b] : b*P) + (path ? path[b*D_path + j] : j) of tmp, goes to slot j of request b
+ * (slots, n_slots, S, slot_off as in dt_kv_reserve). path, n_new with n_extra = 1: accept_path and accept_len of
+ * dt_verify; path NULL: a prefill. len_out[b] = seq_len[b] + n (may be seq_len itself). A request whose first or
+ * last slot is -1, or whose n exceeds its slots or D_path, commits nothing, keeps its length and sets
+ * DT_DEV_KV_FULL; a slot outside the pages sets DT_DEV_BAD_PAGE and is not written. One launch. */
+int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P, const int32_t* row_off,
+                       const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra,
+                       const int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
+                       const int32_t* seq_len, int32_t* len_out, cudaStream_t s);
+
+/* Attention of the verify tree (EAGLE-2 page, the reranking step's ancestor-only mask): query position i of
+ * request b attends to the request's seq_len[b] cached tokens (pages, through block_table) and to the tree
+ * positions j < n_pos[b] with mask[b][i][j] != 0 (mask NULL: j <= i, a chain, so that P = 1 is a plain
+ * decode step). out = softmax(scale * q k^T) v for query head x with key head x / (H_q / H_kv). A position
+ * that attends to nothing gets zeros. Rows of tmp buffers (q, k_new, v_new, out) as in DT_VERIFY_PACKED:
+ * b*P + i, or row_off[b] + i; rows of no position are left as they were. K and V of tokens past seq_len, of
+ * positions past n_pos and of masked positions may hold anything (NaN and infinities too).
+ * shared_len: the first shared_len tokens (a multiple of page) of every request are the same blocks, those of
+ * block_table[0]: their attention is computed once for the rows of all requests and read once; a request with
+ * seq_len < shared_len sets DT_DEV_BAD_PAGE and its rows are computed as if seq_len = shared_len.
+ * Types: DT_BF16 or DT_F16 for all of q, k, v, out; scores, softmax statistics and sums in fp32, the softmax
+ * weights rounded to the input type for the second product. D: a multiple of 8, up to 128. H_q / H_kv <= 128.
+ * Strides in elements, multiples of 8; pointers 16-byte aligned. */
+typedef struct {
+  int32_t B, P, H_q, H_kv, D, dtype;
+  float scale;
+  int32_t shared_len;
+  int64_t rows;                 /* rows of q, out, k_new, v_new                     */
+  const void* q;
+  int64_t q_row, q_head;
+  void* out;
+  int64_t o_row, o_head;
+  const void *k_new, *v_new;
+  int64_t kn_row, kn_head, vn_row, vn_head;
+  const void *k_pages, *v_pages;
+  int64_t k_block, k_tok, k_head, v_block, v_tok, v_head;
+  int32_t n_blocks, page;
+  const int32_t* block_table;   /* [B][max_blocks]; entries of tokens past seq_len are not read */
+  int32_t max_blocks;
+  const int32_t* seq_len;       /* [B] */
+  const int32_t* n_pos;         /* [B] */
+  const uint8_t* mask;          /* [B][P][P] or NULL */
+  const int32_t* row_off;       /* [B+1] or NULL     */
+  void* workspace;              /* dt_tree_attention_workspace bytes, 256-byte aligned; used by this call
+                                   until it has run: calls that may overlap need one each */
+  int64_t workspace_bytes;
+} dt_attn_args;
+int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
+int dt_tree_attention_workspace(dt_handle* h, int32_t B, int32_t P, int32_t H_q, int32_t H_kv, int32_t D,
+                                int32_t shared, int64_t* bytes);
+
+/* Per-request token history for dt_logits_process: counts[b][v] = generated occurrences of v, plus
+ * DT_SEEN_PROMPT when v is in the prompt. A new request's row is cleared by the caller. */
+enum { DT_SEEN_PROMPT = 0x40000000 };
+/* Adds request b's tokens tokens[(row_off ? row_off[b] : b*P) + (path ? path[b*D_path + j] : j)],
+ * j < n_new[b] + n_extra, to counts [B][V] (prompt != 0: marks them instead): after a verify, tokens =
+ * dt_tree_meta.tokens, path = accept_path, n_new = accept_len, n_extra = 1 add the root and the accepted
+ * tokens, the ones whose KV dt_commit_kv commits. A token outside [0, V) sets DT_DEV_BAD_TOKEN and is
+ * skipped; n past D_path (with a path) or P (without row_off) sets DT_DEV_BAD_TREE and adds nothing. */
+int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int32_t P, const int32_t* row_off,
+                    const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra, int32_t prompt,
+                    cudaStream_t s);
+
+/* Target rows prepared for dt_verify: penalties for repeated tokens, biases and grammar masks, in one pass.
+ * For every used row (b, i) (padded b*P + i, or row_off[b] + i) and token v, in fp32, rounded once:
+ *   c = (counts[b][v] without DT_SEEN_PROMPT) + occurrences of v among the tokens on i's path (the tree
+ *       positions j with mask[b][i][j] != 0; mask NULL: j <= i), seen = c > 0 or DT_SEEN_PROMPT;
+ *   y = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x;
+ *   y = y - frequency[b] * c - (c > 0 ? presence[b] : 0);
+ *   y = y + the sum of bias_vals[b][k] over bias_ids[b][k] == v in list order (-1: unused entry);
+ *   out = allow bit v of the row's words (bit v & 31 of word v >> 5) ? y : -inf.
+ * Any of counts, tokens, repetition, frequency, presence, bias_ids and allow may be NULL: that part is left
+ * out (identity). A token or bias id outside [0, V) is ignored (-1) or sets DT_DEV_BAD_TOKEN (other). out may
+ * be logits itself (same ld), not overlap it otherwise. A row whose words allow nothing becomes all -inf, which
+ * dt_verify reports as DT_DEV_BAD_LOGITS. Rows of no position are left as they were. */
+typedef struct {
+  int32_t P;
+  const int32_t* n_pos;      /* [B]                                            */
+  const int32_t* row_off;    /* [B+1] or NULL                                  */
+  int64_t rows;              /* rows of logits, out and allow                  */
+  const int32_t* tokens;     /* [B][P] or NULL                                 */
+  const uint8_t* mask;       /* [B][P][P] or NULL                              */
+  const int32_t* counts;     /* [B][V] or NULL                                 */
+  const float *repetition, *frequency, *presence; /* [B] or NULL               */
+  const int32_t* bias_ids;   /* [B][n_bias] or NULL                            */
+  const float* bias_vals;    /* [B][n_bias]                                    */
+  int32_t n_bias;            /* 0..4096                                        */
+  const uint32_t* allow;     /* [rows][allow_ld] or NULL                       */
+  int64_t allow_ld;          /* words between rows, >= ceil(V / 32)            */
+} dt_logits_params;
+int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, void* out, int64_t ld_out,
+                      const dt_logits_params* p, cudaStream_t s);
 
 /* Standalone row log-softmax top-K that allocates nothing. This entry point has no counterpart in
  * the method's pages: it is the expansion's row pass (EAGLE-2 §扩展阶段: the children of a node
