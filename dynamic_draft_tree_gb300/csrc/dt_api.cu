@@ -79,6 +79,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   if (e == cudaSuccess) e = dt::init_select_attributes();
   if (e == cudaSuccess) e = dt::init_meta_attributes();
   if (e == cudaSuccess) e = dt::init_block_attributes();
+  if (e == cudaSuccess) e = dt::init_attn_attributes();
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail(e, "cudaFuncSetAttribute");
@@ -660,7 +661,7 @@ int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
     return fail(DT_ERR_ARG, "dt_tree_attention: page must be a power of two in [8, 256], n_blocks and max_blocks >= 1");
   if (a->shared_len < 0 || a->shared_len % a->page || a->shared_len / a->page > a->max_blocks)
     return fail(DT_ERR_ARG, "dt_tree_attention: shared_len must be a multiple of page within max_blocks");
-  if (!(a->scale > 0.0f) || a->scale > 1e30f) return fail(DT_ERR_ARG, "dt_tree_attention: scale must be positive and finite");
+  if (!(a->scale >= 1e-30f) || a->scale > 1e30f) return fail(DT_ERR_ARG, "dt_tree_attention: scale must be in [1e-30, 1e30]");
   if (a->rows < 1 || a->rows > 0x7FFFFFFFll || (!a->row_off && a->rows < (int64_t)a->B * a->P))
     return fail(DT_ERR_ARG, "dt_tree_attention: rows must hold B * P rows and fit 31 bits");
   const void* p16[] = {a->q, a->out, a->k_new, a->v_new, a->k_pages, a->v_pages};

@@ -204,6 +204,7 @@ cudaError_t init_verify_attributes();
 cudaError_t init_select_attributes();
 cudaError_t init_meta_attributes();
 cudaError_t init_block_attributes();
+cudaError_t init_attn_attributes();
 
 
 }  // namespace dt

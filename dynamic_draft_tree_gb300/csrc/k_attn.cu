@@ -1,100 +1,1037 @@
-// Attention of the verify tree over a paged cache: one CTA a query row and head.
+// Attention of the verify tree over a paged cache.
+//
+// For query row f = (position, head of the group) of request b and key head h, with c = scale * log2 e:
+//   out_f = sum_j 2^(c s_fj - m_f) v_j / sum_j 2^(c s_fj - m_f),  s_fj = q_f k_j,
+// j over the cached tokens and the tree positions that f's mask row allows. The n_pos * G rows of a request and
+// key head attend to the same cached tokens, so they are the 128-row operand of the matrix instructions and
+// every key and value is read once for up to 256 of them; a prefix that all requests share is read once for
+// 256 rows of any requests.
+//
+// Work. An item is up to 256 rows of one key head over a list of 128-token tiles: the shared prefix's, or one
+// request's own cached tokens and then its tree positions. All tiles in item order form one line that the CTAs
+// (one a SM) cut into equal runs, whatever the lengths; a CTA's run of one item is a segment. A segment that is a
+// whole item of an unshared call writes the result; others leave sum, maximum and unnormalised result in
+// fp32, and attn_merge_kernel joins them in a fixed order. Every CTA derives the cuts from the lengths on the
+// device, so a captured call follows them.
+//
+// A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads K tiles, warp 11 V tiles (TMA, one
+// box a page and 64 elements), warp 9 issues the matrix instructions, warp 10 clears value rows past the end.
+// The line of work is a sequence of units u = 0, 1, ... for groups u & 1: with more than 128 rows a tile gives two
+// units, one for each half of the rows; with fewer, tiles alternate between the groups, whose results are
+// joined at the end. S = Q K^T of unit u + 2 is issued right behind O += P V of unit u, so the tensor cores
+// work for one group while the other takes its softmax. S (fp32) and P (16-bit, over S) and O live in tensor
+// memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "dt_internal.cuh"
+#include "tc.cuh"
 
 namespace dt {
 namespace {
 
-__device__ __forceinline__ float tof(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float tof(__half x) { return __half2float(x); }
-__device__ __forceinline__ void put(__nv_bfloat16& o, float x) { o = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void put(__half& o, float x) { o = __float2half_rn(x); }
+constexpr int kTile = 128;      // tokens of a tile, rows of a group
+constexpr int kItemRows = 256;  // rows of an item
+constexpr int kAttnThreads = 384;
+constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes it by 2^kLazy
+constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
+                                // small ones stay normal in fp16 for longer; it cancels in the quotient
 
-// Grid (position, head, request); warp w takes every fourth key, lane l the elements l, l + 32, ...
-template <typename T>
-__global__ void __launch_bounds__(128) attn_rows_kernel(dt_attn_args a, int32_t* status) {
-  __shared__ float m_s[4], l_s[4], o_s[4][128];
-  pdl_begin();
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = min(max(a.n_pos[b], 0), a.P);
-  if (i >= n) return;
-  const int64_t base = a.row_off ? (int64_t)a.row_off[b] : (int64_t)b * a.P;
-  if (base < 0 || base + n > a.rows) {
-    set_status(status, DT_DEV_BAD_PAGE);
-    return;
+struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
+  int64_t per;     // tiles of a CTA
+  int64_t w_shared;
+  int32_t ts, mp_s, rows_s, pad;
+};
+
+struct AttnParams {
+  dt_attn_args a;
+  int32_t G, page_shift, tree_box;
+  float c;            // scale * log2 e
+  int32_t ns;         // tiles of the shared prefix
+  int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
+  AttnHead* head;
+  int64_t* t_pre;     // [B] tile offset of a request among the own tiles
+  int32_t* k_pre;     // [B] item offset
+  float2* ml_own;     // [slot][own_rows] (m, l)
+  float* o_own;       // [slot][own_rows][D]
+  float2* ml_sh;      // [slot][kItemRows]
+  float* o_sh;
+  int32_t* status;
+};
+
+struct Request {
+  int len, n;      // cached tokens, positions
+  int64_t base;    // row of position 0
+  bool bad;
+};
+
+__device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_shift, int b) {
+  Request r;
+  const int len = a.seq_len[b], n = a.n_pos[b];
+  r.base = a.row_off ? (int64_t)a.row_off[b] : (int64_t)b * a.P;
+  const int64_t most = min((int64_t)a.max_blocks << page_shift, (int64_t)0x7FFFFF00);
+  r.len = (int)min((int64_t)max(len, a.shared_len), most);
+  r.n = min(max(n, 0), a.P);
+  r.bad = len < a.shared_len || len > most || n < 0 || n > a.P;
+  if (r.base < 0 || r.base + r.n > a.rows) {
+    r.bad = true;
+    r.n = 0;
   }
-  int len = a.seq_len[b];
-  if (len < a.shared_len || len > (int64_t)a.max_blocks * a.page) {
-    set_status(status, DT_DEV_BAD_PAGE);
-    len = (int)min((int64_t)max(len, a.shared_len), (int64_t)a.max_blocks * a.page);
+  return r;
+}
+
+// Items of a request for all key heads, tiles of one item.
+struct Extent {
+  int mp, tp, tt;  // row blocks a head; prefix tiles, all tiles
+};
+__device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
+  Extent e;
+  e.mp = (r.n * p.G + kItemRows - 1) / kItemRows;
+  e.tp = (r.len - p.a.shared_len + kTile - 1) / kTile;
+  e.tt = r.n > 0 ? e.tp + (r.n + kTile - 1) / kTile : 0;
+  return e;
+}
+
+// A CTA's share and where it starts.
+struct Plan {
+  int64_t x0, x1;       // tiles [x0, x1) of the line
+  int64_t w_shared;
+  int64_t t_b;          // own tile offset of request b
+  int32_t b, k_b;       // first own request, its item offset
+  int32_t ts, mp_s, rows_s;
+};
+
+struct Segment {
+  bool shared, whole;
+  int b, h, mp;
+  int t0, t1;           // tiles
+  int tp, len;          // own: prefix tiles, cached tokens; shared: ts, shared_len
+  int n;                // own: positions
+  int64_t base;         // row of the first position
+  int rows;             // rows of the item
+  int64_t slot;
+};
+
+struct Walk {
+  int64_t x;
+  int64_t t_b;
+  int b, k_b;
+  int loaded;           // request whose extent is held
+  Request r;
+  Extent e;
+
+  __device__ void start(const Plan& pl) {
+    x = pl.x0;
+    t_b = pl.t_b;
+    b = pl.b;
+    k_b = pl.k_b;
+    loaded = -1;
   }
-  const int kvh = h / (a.H_q / a.H_kv);
-  const T* q = (const T*)a.q + (base + i) * a.q_row + h * a.q_head;
-  float qf[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
+  __device__ bool next(const AttnParams& p, const Plan& pl, Segment& s) {
+    if (x >= pl.x1) return false;
+    if (x < pl.w_shared) {
+      const int item = (int)(x / pl.ts);
+      s.shared = true;
+      s.whole = false;
+      s.b = 0;
+      s.h = item / pl.mp_s;
+      s.mp = item - s.h * pl.mp_s;
+      s.t0 = (int)(x - (int64_t)item * pl.ts);
+      s.t1 = (int)min((int64_t)pl.ts, s.t0 + pl.x1 - x);
+      s.tp = pl.ts;
+      s.len = p.a.shared_len;
+      s.n = 0;
+      s.base = 0;
+      s.rows = min(kItemRows, pl.rows_s - s.mp * kItemRows);
+      s.slot = item + blockIdx.x;
+      x += s.t1 - s.t0;
+      return true;
+    }
+    const int64_t y = x - pl.w_shared;
+    while (true) {
+      if (b >= p.a.B) return false;
+      if (loaded != b) {
+        r = request_of(p.a, p.page_shift, b);
+        e = extent_of(p, r);
+        loaded = b;
+      }
+      const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
+      if (y < t_b + w) break;
+      t_b += w;
+      k_b += p.a.H_kv * e.mp;
+      ++b;
+    }
+    const int item = (int)((y - t_b) / e.tt);
+    s.shared = false;
+    s.b = b;
+    s.h = item / e.mp;
+    s.mp = item - s.h * e.mp;
+    s.t0 = (int)(y - t_b - (int64_t)item * e.tt);
+    s.t1 = (int)min((int64_t)e.tt, s.t0 + pl.x1 - x);
+    s.tp = e.tp;
+    s.len = r.len;
+    s.n = r.n;
+    s.base = r.base;
+    s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
+    s.whole = s.t0 == 0 && s.t1 == e.tt && p.a.shared_len == 0;
+    s.slot = (int64_t)k_b + item + blockIdx.x;
+    x += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// Tokens or positions of tile t that exist, and whether the tile holds tree positions.
+__device__ __forceinline__ int tile_valid(const AttnParams& p, const Segment& s, int t, bool& tree) {
+  tree = !s.shared && t >= s.tp;
+  if (tree) return min(kTile, s.n - (t - s.tp) * kTile);
+  const int tok = (s.shared ? 0 : p.a.shared_len) + t * kTile;
+  return min(kTile, s.len - tok);
+}
+
+template <int DP>
+struct Smem {
+  static constexpr int kHalf = kTile * 128;              // bytes of 64 elements of 128 rows
+  static constexpr int kBlock = (DP / 64) * kHalf;       // a tile of Q, K or V
+  static constexpr int kStages = DP == 128 ? 2 : 4;      // tiles of K and of V in flight
+  static constexpr int kBytes = (2 + 2 * kStages) * kBlock + 1024;
+};
+
+struct Shared {
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vfix[4];
+  uint64_t sfull[2], pready[2], odone[2], qready[2], mlready;
+  float2 ml[kTile];
+  Plan plan;
+  int64_t sums[2][12];
+  uint32_t tmem;
+  int stop, odd_values;
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t d;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ float unpack16(uint16_t x) {
+  return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+
+// Every CTA: the line's length and where its own run starts.
+__device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = (p.a.B + kAttnThreads - 1) / kAttnThreads, b0 = tid * chunk, b1 = min(p.a.B, b0 + chunk);
+  int64_t tiles = 0, items = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request_of(p.a, p.page_shift, b);
+    const Extent e = extent_of(p, r);
+    tiles += (int64_t)p.a.H_kv * e.mp * e.tt;
+    items += p.a.H_kv * e.mp;
+    if (blockIdx.x == 0 && r.bad) set_status(p.status, DT_DEV_BAD_PAGE);
+  }
+  int64_t st = tiles, si = items;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) qf[u] = lane + 32 * u < a.D ? tof(q[lane + 32 * u]) * a.scale : 0.0f;
-  for (int t = warp; t < len + n; t += 4) {
-    const T *k, *v;
-    if (t < len) {
-      const int e = t / a.page;
-      const int id = a.block_table[(t < a.shared_len ? 0 : (int64_t)b * a.max_blocks) + e];
-      if (id < 0 || id >= a.n_blocks) {
-        set_status(status, DT_DEV_BAD_PAGE);
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t a = (int64_t)shfl_u64((uint64_t)st, max(lane - d, 0)), c = (int64_t)shfl_u64((uint64_t)si, max(lane - d, 0));
+    if (lane >= d) {
+      st += a;
+      si += c;
+    }
+  }
+  if (lane == 31) {
+    sh.sums[0][warp] = st;
+    sh.sums[1][warp] = si;
+  }
+  int64_t rows_used = (int64_t)p.a.B * p.a.P;
+  if (p.a.row_off) {
+    const int64_t last = p.a.row_off[p.a.B];
+    if (blockIdx.x == 0 && tid == 0 && (last < 0 || last > min(rows_used, p.a.rows))) set_status(p.status, DT_DEV_BAD_PAGE);
+    rows_used = min(max(last, (int64_t)0), min(rows_used, p.a.rows));
+  }
+  __syncthreads();
+  int64_t total = 0, t_b = st - tiles, k_b = si - items;
+  for (int w = 0; w < kAttnThreads / 32; ++w) {
+    if (w < warp) {
+      t_b += sh.sums[0][w];
+      k_b += sh.sums[1][w];
+    }
+    total += sh.sums[0][w];
+  }
+  const int64_t rows_s = p.ns ? rows_used * p.G : 0;
+  const int mp_s = (int)((rows_s + kItemRows - 1) / kItemRows);
+  const int64_t w_shared = (int64_t)p.a.H_kv * mp_s * p.ns;
+  total += w_shared;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t x0 = min(total, per * blockIdx.x), x1 = min(total, x0 + per);
+  if (tid == 0) {
+    Plan& pl = sh.plan;
+    pl.x0 = x0;
+    pl.x1 = x1;
+    pl.w_shared = w_shared;
+    pl.ts = p.ns;
+    pl.mp_s = mp_s;
+    pl.rows_s = (int)min(rows_s, (int64_t)0x7FFFFFFF);
+    if (x0 <= w_shared) {  // the own requests from the first
+      pl.b = 0;
+      pl.t_b = 0;
+      pl.k_b = 0;
+    }
+    if (blockIdx.x == 0) *p.head = AttnHead{per, w_shared, p.ns, mp_s, pl.rows_s, 0};
+  }
+  const int64_t y0 = x0 - w_shared;
+  for (int b = b0; b < b1; ++b) {
+    const Extent e = extent_of(p, request_of(p.a, p.page_shift, b));
+    const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
+    if (y0 > 0 && t_b <= y0 && y0 < t_b + w) {
+      sh.plan.b = b;
+      sh.plan.t_b = t_b;
+      sh.plan.k_b = (int32_t)k_b;
+    }
+    if (blockIdx.x == 0) {
+      p.t_pre[b] = t_b;
+      p.k_pre[b] = (int32_t)k_b;
+    }
+    t_b += w;
+    k_b += p.a.H_kv * e.mp;
+  }
+}
+
+// Ring position of the n-th tile: stage and the parity of its use.
+template <int N>
+__device__ __forceinline__ void ring(uint32_t n, int& stage, uint32_t& parity) {
+  stage = (int)(n % N);
+  parity = (n / N) & 1;
+}
+
+// One warp loads the K (or V) tiles of the CTA's line in order.
+template <int DP, bool IS_K>
+__device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* pages, const CUtensorMap* tree_map,
+                           uint32_t smem, int lane) {
+  using S = Smem<DP>;
+  uint64_t* full = IS_K ? sh.kfull : sh.vfull;
+  uint64_t* empty = IS_K ? sh.kempty : sh.vempty;
+  constexpr int kHalves = DP / 64;
+  const int shift = p.page_shift, page = p.a.page;
+  const int box = min(page, kTile);  // tokens of a page box
+  const int box_shift = min(shift, 7);
+  Walk w;
+  w.start(sh.plan);
+  Segment s;
+  uint32_t n = 0;
+  bool ok = true;
+  const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
+  while (ok && w.next(p, sh.plan, s)) {
+    const int32_t* table = p.a.block_table + (s.shared ? 0 : (int64_t)s.b * p.a.max_blocks);
+    const int tok0 = s.shared ? 0 : p.a.shared_len;
+    // block id of this lane's box in tile t (-1: none)
+    auto block_at = [&](int t) {
+      const int tok = tok0 + t * kTile + (part << box_shift);
+      if (t >= s.tp || (part << box_shift) >= kTile || tok >= s.len) return -1;
+      int id = table[tok >> shift];
+      if (id < 0 || id >= p.a.n_blocks) {
+        set_status(p.status, DT_DEV_BAD_PAGE);
+        id = p.a.n_blocks;  // outside the tensor: zeros
+      }
+      return id;
+    };
+    int id = block_at(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++n) {
+      int stage;
+      uint32_t parity;
+      ring<S::kStages>(n, stage, parity);
+      const int next_id = t + 1 < s.t1 ? block_at(t + 1) : -1;
+      ok = tc::bar_wait_warp(&empty[stage], parity ^ 1, &sh.stop);
+      if (!ok) break;
+      const uint32_t at = smem + stage * S::kBlock;
+      bool tree;
+      const int valid = tile_valid(p, s, t, tree);
+      if (tree) {
+        // one box of tree_box rows and 64 elements for every tree_box positions that exist
+        const int boxes = (valid + p.tree_box - 1) / p.tree_box;
+        if (lane == 0) tc::bar_expect(&full[stage], boxes * kHalves * p.tree_box * 128);
+        __syncwarp();
+        for (int k = lane; k < boxes * kHalves; k += 32) {
+          const int hf = k & (kHalves - 1), i = k / kHalves * p.tree_box;
+          tc::tma_load_3d(at + hf * S::kHalf + i * 128, tree_map, hf * 64, s.h, (int)s.base + (t - s.tp) * kTile + i,
+                          &full[stage]);
+        }
+      } else {
+        const int boxes = (valid + box - 1) >> box_shift;
+        if (lane == 0) tc::bar_expect(&full[stage], boxes * kHalves * box * 128);
+        __syncwarp();
+        if (part < boxes) {
+          const int tok = tok0 + t * kTile + (part << box_shift);
+          tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id,
+                          &full[stage]);
+        }
+      }
+      id = next_id;
+    }
+  }
+  // after a give-up: no load may land once the CTA is gone
+  if (!ok)
+    for (uint32_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k) {
+      int stage;
+      uint32_t parity;
+      ring<S::kStages>(k, stage, parity);
+      const long long t0 = clock64();
+      while (!tc::bar_try(&full[stage], parity) && clock64() - t0 < tc::kWaitClocks) {
+      }
+    }
+}
+
+// One thread issues the matrix instructions of the CTA's line.
+template <int DP, bool BF16>
+__device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+  using S = Smem<DP>;
+  constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false);
+  constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
+  const int steps = (p.a.D + 15) / 16;  // the padding elements of a row are zero
+  const uint32_t tm = sh.tmem;
+  Walk w;
+  w.start(sh.plan);
+  Segment s;
+  uint32_t seen = 0;          // tiles of the segments before this one
+  uint32_t np[2] = {0, 0};    // units of each group so far (phase of pready)
+  uint32_t nq[2] = {0, 0};    // uses of each Q buffer
+  uint32_t fix = 0;           // parity of every stage's vfix
+  bool ok = true;
+  while (ok && w.next(p, sh.plan, s)) {
+    const bool dual = s.rows > kTile;
+    const int tiles = s.t1 - s.t0, units = dual ? 2 * tiles : tiles;
+    ok = tc::bar_wait(&sh.qready[0], nq[0]++ & 1, &sh.stop);
+    if (ok && dual) ok = tc::bar_wait(&sh.qready[1], nq[1]++ & 1, &sh.stop);
+    auto issue_s = [&](int u) {
+      const int k = dual ? u >> 1 : u, g = u & 1;
+      int stage;
+      uint32_t parity;
+      ring<S::kStages>(seen + k, stage, parity);
+      if (!dual || g == 0) {
+        if (!tc::bar_wait(&sh.kfull[stage], parity, &sh.stop)) return false;
+      }
+      tc::fence_after();
+      const uint32_t qa = q_smem + (dual ? g : 0) * S::kBlock, ka = k_smem + stage * S::kBlock;
+      for (int x = 0; x < steps; ++x) {
+        const uint32_t off = (x >> 2) * S::kHalf + (x & 3) * 32;
+        tc::mma_ss(tm + g * kTile, tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(ka + off, 16, 1024), kDescS, x > 0);
+      }
+      tc::mma_commit(&sh.sfull[g]);
+      if (!dual || g == 1) tc::mma_commit(&sh.kempty[stage]);
+      return true;
+    };
+    for (int u = 0; ok && u < min(2, units); ++u) ok = issue_s(u);
+    for (int u = 0; ok && u < units; ++u) {
+      const int k = dual ? u >> 1 : u, g = u & 1, t = s.t0 + k;
+      int stage;
+      uint32_t parity;
+      ring<S::kStages>(seen + k, stage, parity);
+      bool tree;
+      const int valid = tile_valid(p, s, t, tree);
+      if (!dual || g == 0) {
+        ok = tc::bar_wait(&sh.vfull[stage], parity, &sh.stop);
+        if (ok && (tree || valid < kTile)) {
+          ok = tc::bar_wait(&sh.vfix[stage], fix >> stage & 1, &sh.stop);
+          fix ^= 1u << stage;
+        }
+        if (!ok) break;
+      }
+      ok = tc::bar_wait(&sh.pready[g], np[g]++ & 1, &sh.stop);
+      if (!ok) break;
+      tc::fence_after();
+      const bool first = u < 2;  // the group's first unit starts its accumulator
+      const uint32_t va = v_smem + stage * S::kBlock;
+      for (int x = 0; x < (valid + 15) / 16; ++x)
+        tc::mma_ts(tm + 2 * kTile + g * DP, tm + g * kTile + x * 8, tc::smem_desc(va + x * 2048, S::kHalf, 1024), kDescO,
+                   !(first && x == 0));
+      tc::mma_commit(&sh.odone[g]);
+      if (!dual || g == 1) tc::mma_commit(&sh.vempty[stage]);
+      if (u + 2 < units) ok = issue_s(u + 2);
+    }
+    seen += tiles;
+  }
+}
+
+// One warp: value rows past the end of a tile become zero (a weight of zero times what lies there need not be
+// zero), and so do NaN and infinities at tree positions, which only some rows attend to: the rows that do add
+// them in finish_row.
+template <int DP, bool BF16>
+__device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int lane) {
+  using S = Smem<DP>;
+  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+  Walk w;
+  w.start(sh.plan);
+  Segment s;
+  uint32_t n = 0;
+  while (w.next(p, sh.plan, s)) {
+    for (int t = s.t0; t < s.t1; ++t, ++n) {
+      bool tree;
+      const int valid = tile_valid(p, s, t, tree);
+      int stage;
+      uint32_t parity;
+      ring<S::kStages>(n, stage, parity);
+      // every tile is waited for and let go here too, so that the ring never runs ahead of this warp
+      if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
+      if (!tree && valid == kTile) {
+        if (lane == 0) tc::bar_arrive(&sh.vempty[stage]);
         continue;
       }
-      k = (const T*)a.k_pages + id * a.k_block + (t - e * a.page) * a.k_tok + kvh * a.k_head;
-      v = (const T*)a.v_pages + id * a.v_block + (t - e * a.page) * a.v_tok + kvh * a.v_head;
-    } else {
-      const int j = t - len;
-      if (a.mask ? !a.mask[((int64_t)b * a.P + i) * a.P + j] : j > i) continue;
-      k = (const T*)a.k_new + (base + j) * a.kn_row + kvh * a.kn_head;
-      v = (const T*)a.v_new + (base + j) * a.vn_row + kvh * a.vn_head;
+      uint8_t* at = v_smem + stage * S::kBlock;
+      const int upto = (valid + 15) / 16 * 16;
+      for (int hf = 0; hf < DP / 64; ++hf) {
+        for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(at + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+        if (tree) {
+          bool odd = false;
+          for (int c = lane; c < valid * 8; c += 32) {
+            uint4 q = *(uint4*)(at + hf * S::kHalf + c * 16);
+            uint32_t* e = &q.x;
+            bool mine = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((e[k] & kExp) == kExp) {
+                e[k] &= 0xFFFF0000u;
+                mine = true;
+              }
+              if ((e[k] >> 16 & kExp) == kExp) {
+                e[k] &= 0xFFFFu;
+                mine = true;
+              }
+            }
+            if (mine) *(uint4*)(at + hf * S::kHalf + c * 16) = q;
+            odd |= mine;
+          }
+          if (odd) *(volatile int*)&sh.odd_values = 1;
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::bar_arrive(&sh.vfix[stage]);
+        tc::bar_arrive(&sh.vempty[stage]);
+      }
     }
-    float s = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (lane + 32 * u < a.D) s += qf[u] * tof(k[lane + 32 * u]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    const float mn = fmaxf(m, s), c = m == -INFINITY ? 0.0f : __expf(m - mn), p = mn == -INFINITY ? 0.0f : __expf(s - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (lane + 32 * u < a.D) o[u] = o[u] * c + p * tof(v[lane + 32 * u]);
-    m = mn;
   }
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
-  }
+}
+
+// What a softmax thread keeps of its row.
+struct Row {
+  float m, l;  // reference maximum (log2 units), sum of weights
+};
+
+// The 128 tree columns that row `f` of the item attends to in tree tile jt, as bits; all lanes of the warp.
+__device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s, int jt, int f, bool live, uint32_t* bits) {
+  const int lane = threadIdx.x & 31, j0 = jt * kTile, i = live ? f / p.G : -1;
+  bits[0] = bits[1] = bits[2] = bits[3] = 0;
+  if (!p.a.mask) {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) o_s[warp][lane + 32 * u] = o[u];
+    for (int w = 0; w < 4; ++w) {
+      const int k = i - (j0 + 32 * w);
+      bits[w] = i < 0 || k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
+    }
+    return;
+  }
+  // rows of a warp are neighbours: positions first..last, one coalesced read and ballot for 32 columns of each
+  const int first = __shfl_sync(0xFFFFFFFFu, i, 0);
+  const int last = __reduce_max_sync(0xFFFFFFFFu, i);
+  if (last < 0) return;
+  const uint8_t* m = p.a.mask + (int64_t)s.b * p.a.P * p.a.P;
+  for (int x = first; x <= last; ++x) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int j = j0 + 32 * w + lane;
+      const uint32_t word = __ballot_sync(0xFFFFFFFFu, j < s.n && m[(int64_t)x * p.a.P + j] != 0);
+      if (x == i) bits[w] = word;
+    }
+  }
+}
+
+// Values that are no numbers at tree positions this row attends to: weight times value, from global memory.
+template <int DP, bool BF16>
+__device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& s, int f, float m, int d0, float* o) {
+  const int i = f / p.G, g = f - i * p.G;
+  const uint16_t* q = (const uint16_t*)p.a.q + (s.base + i) * p.a.q_row + ((int64_t)s.h * p.G + g) * p.a.q_head;
+  for (int j = (max(s.t0, s.tp) - s.tp) * kTile; j < min(s.n, (s.t1 - s.tp) * kTile); ++j) {
+    if (p.a.mask ? p.a.mask[((int64_t)s.b * p.a.P + i) * p.a.P + j] == 0 : j > i) continue;
+    const uint16_t* v = (const uint16_t*)p.a.v_new + (s.base + j) * p.a.vn_row + s.h * p.a.vn_head;
+    const uint16_t* k = (const uint16_t*)p.a.k_new + (s.base + j) * p.a.kn_row + s.h * p.a.kn_head;
+    bool odd = false;
+    for (int d = d0; d < min(d0 + 32, p.a.D); ++d) odd |= !isfinite(unpack16<BF16>(v[d]));
+    if (!odd) continue;
+    float dot = 0.0f;
+    for (int d = 0; d < p.a.D; ++d) dot += unpack16<BF16>(q[d]) * unpack16<BF16>(k[d]);
+    const float wgt = exp2f(dot * p.c - m + kShift);
+    for (int d = 0; d < min(32, p.a.D - d0); ++d) {
+      const float x = unpack16<BF16>(v[d0 + d]);
+      if (!isfinite(x)) o[d] += wgt * x;
+    }
+  }
+}
+
+// The segment's rows of a softmax group leave tensor memory. `other`: the second group's accumulator is joined.
+template <int DP, bool BF16>
+__device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool other, uint32_t tm) {
+  const int wl = threadIdx.x & 127;         // row of the group
+  const int r = (s.rows > kTile ? group * kTile : 0) + wl;
+  const bool live = r < s.rows;
+  float f0 = 1.0f, f1 = 0.0f, m = row.m, l = row.l;
+  if (other) {
+    const float2 o = sh.ml[wl];
+    m = fmaxf(row.m, o.x);
+    f0 = row.m == -INFINITY ? 0.0f : exp2f(row.m - m);
+    f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - m);
+    l = row.l * f0 + o.y * f1;
+  }
+  const int f = s.mp * kItemRows + r;
+  const bool odd = *(volatile int*)&sh.odd_values && !s.shared && s.t1 > s.tp;
+  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // nothing attended to: zeros; NaN stays
+  uint16_t* out = nullptr;
+  float* part = nullptr;
+  if (live) {
+    const int i = f / p.G, g = f - i * p.G;
+    if (s.whole) {
+      out = (uint16_t*)p.a.out + (s.base + i) * p.a.o_row + ((int64_t)s.h * p.G + g) * p.a.o_head;
+    } else if (s.shared) {
+      const int64_t at = s.slot * kItemRows + r;
+      part = p.o_sh + at * p.a.D;
+      p.ml_sh[at] = make_float2(m, l);
+    } else {
+      const int64_t at = s.slot * p.own_rows + r;
+      part = p.o_own + at * p.a.D;
+      p.ml_own[at] = make_float2(m, l);
+    }
+  }
+  const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
+  const bool any = __any_sync(0xFFFFFFFFu, live);
+  if (!any) return;
+#pragma unroll 1
+  for (int d0 = 0; d0 < p.a.D; d0 += 32) {
+    uint32_t raw[32];
+    float o[32];
+    tc::tmem_ld32(tm + lanes + 2 * kTile + group * DP + d0, raw);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(raw[k]) * f0;
+    if (other) {
+      tc::tmem_ld32(tm + lanes + 2 * kTile + (group ^ 1) * DP + d0, raw);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(raw[k]), f1, o[k]);
+    }
+    if (odd && live) {
+      float x[32];  // its own array: one whose address is taken does not stay in registers
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = o[k];
+      add_odd_values<DP, BF16>(p, s, f, m == -INFINITY ? 0.0f : m, d0, x);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = x[k];
+    }
+    if (out) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        if (d0 + k < p.a.D)
+          *(uint4*)(out + d0 + k) = make_uint4(pack16<BF16>(o[k] * inv, o[k + 1] * inv), pack16<BF16>(o[k + 2] * inv, o[k + 3] * inv),
+                                               pack16<BF16>(o[k + 4] * inv, o[k + 5] * inv), pack16<BF16>(o[k + 6] * inv, o[k + 7] * inv));
+    } else if (part) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        if (d0 + k < p.a.D) *(float4*)(part + d0 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    }
+    __syncwarp();
+  }
+}
+
+// A group of 128 threads: loads its Q rows, then turns every S of its units into weights.
+template <int DP, bool BF16>
+__device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, int group) {
+  using S = Smem<DP>;
+  const int wl = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
+  const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
+  Walk w;
+  w.start(sh.plan);
+  Segment s;
+  uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
+  while (w.next(p, sh.plan, s)) {
+    const bool dual = s.rows > kTile;
+    const int tiles = s.t1 - s.t0;
+    const int mine = dual ? tiles : (tiles + 1 - group) / 2;
+    const int r0 = dual ? group * kTile : 0;  // the group's first row of the item
+    const int r = r0 + wl, f = s.mp * kItemRows + r;
+    const bool live = r < s.rows;
+    if (dual || group == 0) {
+      // Q rows into the swizzled layout, zeros past the end and past D
+      uint8_t* at = q_smem + group * S::kBlock;
+      const int i = f / p.G, g = f - i * p.G;
+      const uint4* q = (const uint4*)((const uint16_t*)p.a.q + (live ? (s.base + i) * p.a.q_row + ((int64_t)s.h * p.G + g) * p.a.q_head : 0));
+#pragma unroll
+      for (int c = 0; c < DP / 8; ++c) {
+        const uint4 x = live && c * 8 < p.a.D ? q[c] : make_uint4(0, 0, 0, 0);
+        *(uint4*)(at + (c >> 3) * S::kHalf + wl * 128 + (((c & 7) ^ (wl & 7)) << 4)) = x;
+      }
+      tc::fence_async_smem();
+      tc::fence_before();  // also: the last segment's accumulators have been read
+      tc::bar_arrive(&sh.qready[group]);
+    }
+    Row row{-INFINITY, 0.0f};
+    const bool work = __any_sync(0xFFFFFFFFu, live);
+    for (int k = 0; k < mine; ++k) {
+      const int t = s.t0 + (dual ? k : 2 * k + group);
+      bool tree;
+      const int valid = tile_valid(p, s, t, tree);
+      uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+      const bool masked = tree || valid < kTile;
+      if (tree && work) tree_bits(p, s, t - s.tp, f, live, bits);
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int left = valid - 32 * x;
+          bits[x] &= left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+        }
+      }
+      if (!tc::bar_wait_warp(&sh.sfull[group], ns++ & 1, &sh.stop)) return;
+      // the unit before this one has been added up (S of this one was issued behind it)
+      if (k > 0 && !tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
+      tc::fence_after();
+      if (work) {
+        uint32_t raw[64];
+        float top = -INFINITY;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          tc::tmem_ld64(s_at + hf * 64, raw);
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (bits[2 * hf + (x >> 5)] >> (x & 31) & 1) top = fmaxf(top, __uint_as_float(raw[x]));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 64; ++x) top = fmaxf(top, __uint_as_float(raw[x]));
+          }
+        }
+        top *= p.c;
+        if (k == 0) {
+          row.m = top;
+        } else {
+          const bool up = top > row.m + kLazy;
+          if (__any_sync(0xFFFFFFFFu, up)) {
+            // the accumulator of the rows so far moves to the new reference
+            const float fac = up ? (row.m == -INFINITY ? 0.0f : exp2f(row.m - top)) : 1.0f;
+            if (up) {
+              row.m = top;
+              row.l *= fac;
+            }
+#pragma unroll 1
+            for (int d0 = 0; d0 < DP; d0 += 32) {
+              tc::tmem_ld32(o_at + d0, raw);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) raw[x] = __float_as_uint(__uint_as_float(raw[x]) * fac);
+              tc::tmem_st32(o_at + d0, raw);
+            }
+            tc::wait_st();
+          }
+        }
+        const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
+        float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          tc::tmem_ld64(s_at + hf * 64, raw);
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            float a = ex2(fmaf(__uint_as_float(raw[x]), p.c, off)), b = ex2(fmaf(__uint_as_float(raw[x + 1]), p.c, off));
+            if (masked) {
+              if (!(bits[2 * hf + (x >> 5)] >> (x & 31) & 1)) a = 0.0f;
+              if (!(bits[2 * hf + (x >> 5)] >> ((x + 1) & 31) & 1)) b = 0.0f;
+            }
+            l0 += a;
+            l1 += b;
+            pk[x >> 1] = pack16<BF16>(a, b);
+          }
+          // both halves of S are read before P overwrites the first: P's 64 columns lie over S's first half
+          if (hf == 0) {
+            tc::tmem_st32(s_at, pk);
+          } else {
+            tc::tmem_st32(s_at + 32, pk);
+          }
+        }
+        row.l += l0 + l1;
+        tc::wait_st();
+      }
+      tc::fence_before();
+      tc::bar_arrive(&sh.pready[group]);
+    }
+    // the group's last product
+    if (mine > 0) {
+      if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
+      tc::fence_after();
+    }
+    if (dual) {
+      finish_rows<DP, BF16>(p, sh, s, group, row, false, tm);
+    } else if (group == 1) {
+      if (mine > 0) {
+        sh.ml[wl] = make_float2(row.m, row.l);
+        tc::fence_before();
+        tc::bar_arrive(&sh.mlready);
+      }
+    } else {
+      const bool other = tiles > 1;
+      if (other) {
+        if (!tc::bar_wait_warp(&sh.mlready, nml++ & 1, &sh.stop)) return;
+        tc::fence_after();
+      }
+      finish_rows<DP, BF16>(p, sh, s, 0, row, other, tm);
+    }
+  }
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map) {
+  using S = Smem<DP>;
+  extern __shared__ uint8_t dyn[];
+  __shared__ Shared sh;
+  uint8_t* smem = dyn + ((1024 - (tc::smem_addr(dyn) & 1023)) & 1023);
+  uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kBlock, *v_smem = k_smem + S::kStages * S::kBlock;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 9) tc::tmem_alloc<512>(&sh.tmem);
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      tc::bar_init(&sh.kfull[i], 1);
+      tc::bar_init(&sh.kempty[i], 1);
+      tc::bar_init(&sh.vfull[i], 1);
+      tc::bar_init(&sh.vempty[i], 2);  // the products' end and the fixing warp
+      tc::bar_init(&sh.vfix[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      tc::bar_init(&sh.sfull[g], 1);
+      tc::bar_init(&sh.pready[g], kTile);
+      tc::bar_init(&sh.odone[g], 1);
+      tc::bar_init(&sh.qready[g], kTile);
+    }
+    tc::bar_init(&sh.mlready, kTile);
+    tc::bar_init_fence();
+    sh.stop = 0;
+    sh.odd_values = 0;
+    tc::tma_prefetch_map(&k_map);
+    tc::tma_prefetch_map(&v_map);
+    tc::tma_prefetch_map(&kn_map);
+    tc::tma_prefetch_map(&vn_map);
+  }
+  pdl_begin();
+  make_plan(p, sh);
+  tc::fence_before();
   __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= a.D) return;
-  const float mm = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
-  float ll = 0, oo = 0;
-  for (int w = 0; w < 4; ++w) {
-    const float c = m_s[w] == -INFINITY ? 0.0f : __expf(m_s[w] - mm);
-    ll += l_s[w] * c;
-    oo += o_s[w][d] * c;
+  tc::fence_after();
+  if (warp < 8) {
+    softmax_group<DP, BF16>(p, sh, q_smem, warp >> 2);
+  } else if (warp == 8) {
+    load_tiles<DP, true>(p, sh, &k_map, &kn_map, tc::smem_addr(k_smem), lane);
+  } else if (warp == 9) {
+    if (lane == 0) issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem));
+    __syncwarp();
+  } else if (warp == 10) {
+    fix_values<DP, BF16>(p, sh, v_smem, lane);
+  } else {
+    load_tiles<DP, false>(p, sh, &v_map, &vn_map, tc::smem_addr(v_smem), lane);
   }
-  put(((T*)a.out)[(base + i) * a.o_row + h * a.o_head + d], ll > 0 ? oo / ll : 0.0f);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) {
+    if (sh.stop) {  // products in flight end before their memory goes
+      if (lane == 0) {
+        set_status(p.status, DT_DEV_TIMEOUT);
+        tc::bar_init(&sh.mlready, 1);
+        tc::bar_init_fence();
+        tc::mma_commit(&sh.mlready);
+        const long long t0 = clock64();
+        while (!tc::bar_try(&sh.mlready, 0) && clock64() - t0 < tc::kWaitClocks) {
+        }
+      }
+      __syncwarp();
+    }
+    tc::tmem_free<512>(sh.tmem);
+  }
+}
+
+// ------------------------------------------------------------------------------- merge ----------
+// A CTA joins the partial results of one position, a warp a head at a time. Partials in the order of the line:
+// the shared prefix's first, then the request's own.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
+  pdl_begin();
+  const int i = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Request rq = request_of(p.a, p.page_shift, b);
+  if (i >= rq.n) return;
+  const AttnHead hd = *p.head;
+  const Extent e = extent_of(p, rq);
+  const int64_t t_b = p.t_pre[b];
+  const int k_b = p.k_pre[b];
+  const int d = lane * 4;
+  for (int x = warp; x < p.a.H_q; x += 8) {
+    const int h = x / p.G, g = x - h * p.G;
+    const int f = i * p.G + g, item = h * e.mp + f / kItemRows;
+    const int64_t t0 = hd.w_shared + t_b + (int64_t)item * e.tt;
+    const int64_t c0 = t0 / hd.per, c1 = (t0 + e.tt - 1) / hd.per;
+    if (!p.ns && c0 == c1) continue;  // written by the segment itself
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    auto join = [&](float2 ml, const float* src) {
+      if (ml.x == -INFINITY && !(ml.y != ml.y)) return;
+      const float4 v = d < p.a.D ? *(const float4*)(src + d) : make_float4(0, 0, 0, 0);
+      const float mm = fmaxf(m, ml.x), a = m == -INFINITY ? 0.0f : exp2f(m - mm), c = exp2f(ml.x - mm);
+      o.x = o.x * a + v.x * c;
+      o.y = o.y * a + v.y * c;
+      o.z = o.z * a + v.z * c;
+      o.w = o.w * a + v.w * c;
+      l = l * a + ml.y * c;
+      m = mm;
+    };
+    if (p.ns) {
+      const int64_t fs = (rq.base + i) * p.G + g, ms = fs / kItemRows;
+      const int64_t is = (int64_t)h * hd.mp_s + ms, s0 = is * hd.ts;
+      for (int64_t c = s0 / hd.per; c <= (s0 + hd.ts - 1) / hd.per; ++c) {
+        const int64_t at = (is + c) * kItemRows + fs - ms * kItemRows;
+        join(p.ml_sh[at], p.o_sh + at * p.a.D);
+      }
+    }
+    for (int64_t c = c0; c <= c1; ++c) {
+      const int64_t at = (k_b + item + c) * p.own_rows + f % kItemRows;
+      join(p.ml_own[at], p.o_own + at * p.a.D);
+    }
+    if (d < p.a.D) {
+      const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+      uint16_t* out = (uint16_t*)p.a.out + (rq.base + i) * p.a.o_row + (int64_t)x * p.a.o_head + d;
+      *(uint2*)out = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- host -----------
+struct Layout {
+  int64_t own_slots, own_rows, sh_slots;
+  int64_t t_pre, k_pre, ml_own, o_own, ml_sh, o_sh, total;
+};
+
+Layout layout_of(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, bool shared) {
+  Layout L{};
+  const int64_t G = H_q / H_kv, rows = (int64_t)P * G;
+  // a segment's slot is item + CTA: the pair grows along the line, so slots are distinct
+  L.own_slots = (int64_t)B * H_kv * ((rows + kItemRows - 1) / kItemRows) + h->num_sms;
+  L.own_rows = std::min<int64_t>(kItemRows, rows);
+  L.sh_slots = shared ? (int64_t)H_kv * ((B * rows + kItemRows - 1) / kItemRows) + h->num_sms : 0;
+  int64_t at = 256;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  L.t_pre = take(8ll * B);
+  L.k_pre = take(4ll * B);
+  L.ml_own = take(8 * L.own_slots * L.own_rows);
+  L.o_own = take(4 * L.own_slots * L.own_rows * D);
+  L.ml_sh = take(8 * L.sh_slots * kItemRows);
+  L.o_sh = take(4 * L.sh_slots * kItemRows * D);
+  L.total = at;
+  return L;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder (a host function that touches no device state).
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeFn)f;
+  }();
+  return fn;
+}
+
+// 64 elements of `box` rows a copy, 128-byte rows swizzled; strides in elements, the innermost one is 1.
+bool encode(CUtensorMap* m, int dtype, const void* at, int rank, const int64_t* dims, const int64_t* strides,
+            const int* box) {
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i) st[i - 1] = (cuuint64_t)strides[i] * 2;
+  }
+  const EncodeFn fn = encoder();
+  return fn && fn(m, dtype == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                  const_cast<void*>(at), d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, bool BF16>
+cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
+  launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3]);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  launch_k(attn_merge_kernel<BF16>, dim3(p.a.P, p.a.B), dim3(256), 0, s, p);
+  return cudaGetLastError();
+}
+
+template <int DP, bool BF16>
+cudaError_t init_t() {
+  return cudaFuncSetAttribute(attn_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::kBytes);
 }
 
 }  // namespace
 
-int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared) { return 256; }
+cudaError_t init_attn_attributes() {
+  cudaError_t e = init_t<64, true>();
+  if (e == cudaSuccess) e = init_t<64, false>();
+  if (e == cudaSuccess) e = init_t<128, true>();
+  if (e == cudaSuccess) e = init_t<128, false>();
+  return e;
+}
+
+int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared) {
+  return layout_of(h, B, P, H_q, H_kv, D, shared != 0).total;
+}
 
 cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
-  const dim3 grid(a->P, a->H_q, a->B);
-  if (a->dtype == DT_BF16)
-    launch_k(attn_rows_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, *a, h->ws.status);
-  else
-    launch_k(attn_rows_kernel<__half>, grid, dim3(128), 0, s, *a, h->ws.status);
-  return cudaGetLastError();
+  AttnParams p{};
+  p.a = *a;
+  p.G = a->H_q / a->H_kv;
+  while ((1 << p.page_shift) < a->page) ++p.page_shift;
+  p.tree_box = 8;  // positions of a tree box: a power of two that covers P, up to a tile
+  while (p.tree_box < a->P && p.tree_box < kTile) p.tree_box *= 2;
+  p.c = a->scale * kLog2e;
+  p.ns = (a->shared_len + kTile - 1) / kTile;
+  const Layout L = layout_of(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0);
+  char* ws = (char*)a->workspace;
+  p.own_slots = L.own_slots;
+  p.own_rows = L.own_rows;
+  p.head = (AttnHead*)ws;
+  p.t_pre = (int64_t*)(ws + L.t_pre);
+  p.k_pre = (int32_t*)(ws + L.k_pre);
+  p.ml_own = (float2*)(ws + L.ml_own);
+  p.o_own = (float*)(ws + L.o_own);
+  p.ml_sh = (float2*)(ws + L.ml_sh);
+  p.o_sh = (float*)(ws + L.o_sh);
+  p.status = h->ws.status;
+  CUtensorMap m[4];
+  const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
+  const int64_t ks[4] = {1, a->k_head, a->k_tok, a->k_block}, vs[4] = {1, a->v_head, a->v_tok, a->v_block};
+  const int pb[4] = {64, 1, std::min<int>(a->page, kTile), 1};
+  const int64_t td[3] = {a->D, a->H_kv, a->rows};
+  const int64_t kn[3] = {1, a->kn_head, a->kn_row}, vn[3] = {1, a->vn_head, a->vn_row};
+  const int tb[3] = {64, 1, p.tree_box};
+  if (!encode(&m[0], a->dtype, a->k_pages, 4, pd, ks, pb) || !encode(&m[1], a->dtype, a->v_pages, 4, pd, vs, pb) ||
+      !encode(&m[2], a->dtype, a->k_new, 3, td, kn, tb) || !encode(&m[3], a->dtype, a->v_new, 3, td, vn, tb))
+    return cudaErrorInvalidValue;
+  if (a->D <= 64) return a->dtype == DT_BF16 ? launch_t<64, true>(h, p, m, s) : launch_t<64, false>(h, p, m, s);
+  return a->dtype == DT_BF16 ? launch_t<128, true>(h, p, m, s) : launch_t<128, false>(h, p, m, s);
 }
 
 }  // namespace dt
