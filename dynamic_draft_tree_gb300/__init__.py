@@ -6,6 +6,7 @@ stream); all work runs in libdt's sm_103a kernels. See include/dt.h for the
 semantics, layouts and error behaviour of each call.
 """
 import ctypes
+import struct
 
 import torch
 
@@ -261,29 +262,50 @@ def dt_row_topk_static(logits, K, logp, ids, V=None, status=None, stream=None):
                                  _stream(stream)))
 
 
-def _dev(t, dtype, name, *lead):
-    """Pointer of a contiguous CUDA tensor on the current device with this dtype and leading sizes; None stays."""
-    if t is None:
-        return None
+# The calls below run beside kernels of a few microseconds, so their marshalling is kept short: one look at
+# the current device and stream a call, one condition a tensor, the argument struct packed in one go.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+
+def _packer(struct_type):
+    """Packs the fields of a ctypes structure (integers, floats, pointers) with the same layout."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    s = struct.Struct("@" + "".join(codes[f[1]] for f in struct_type._fields_) + "0P")
+    assert s.size == ctypes.sizeof(struct_type)
+    return s.pack
+
+
+_pack_kv_rows, _pack_attn, _pack_logits = _packer(DtKvRows), _packer(DtAttnArgs), _packer(DtLogitsParams)
+
+
+def _refuse(t, dtype, dev, name, n):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    for i, n in enumerate(lead):
-        if t.shape[i] < n:
-            raise ValueError(f"{name} has {t.shape[i]} entries in dimension {i}, {n} are needed")
+    if t.dim() < 1 or t.shape[0] < n:
+        raise ValueError(f"{name} has fewer than {n} entries")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dev(t, dtype, dev, name, n=1):
+    """Pointer of a contiguous tensor on device `dev` with this dtype and at least n (leading) entries; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (t.numel() if n == 1 else len(t)) < n:
+        _refuse(t, dtype, dev, name, n)
     return t.data_ptr()
 
 
-def _strided(t, dtype, name):
-    """Pointer of a CUDA tensor on the current device whose last dimension is contiguous."""
+def _strided(t, dtype, dev, st, name):
+    """Pointer of a tensor on device `dev` with this dtype and a contiguous last dimension (st: its strides)."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if t.stride(-1) != 1:
+    if st[-1] != 1:
         raise ValueError(f"{name} needs a contiguous last dimension")
     return t.data_ptr()
 
@@ -294,50 +316,58 @@ class BlockPool:
     block_table [B][max_blocks], n_owned [B], free_list [n_blocks], free_count [1], all int32."""
 
     def __init__(self, block_table, n_owned, free_list, free_count, page):
-        i32 = torch.int32
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B][max_blocks]")
         self.B, self.max_blocks = block_table.shape
         self.page, self.n_blocks = page, free_list.numel()
         self.block_table, self.n_owned, self.free_list, self.free_count = block_table, n_owned, free_list, free_count
-        self.c = DtBlockPool(page, self.n_blocks, self.max_blocks, _dev(block_table, i32, "block_table"),
-                             _dev(n_owned, i32, "n_owned", self.B), _dev(free_list, i32, "free_list"),
-                             _dev(free_count, i32, "free_count", 1))
+        self.device = _device()
+        self.c = DtBlockPool(page, self.n_blocks, self.max_blocks,
+                             _dev(block_table, _I32, self.device, "block_table"),
+                             _dev(n_owned, _I32, self.device, "n_owned", self.B),
+                             _dev(free_list, _I32, self.device, "free_list"),
+                             _dev(free_count, _I32, self.device, "free_count"))
+        self.ref = ctypes.addressof(self.c)
 
     @classmethod
     def empty(cls, B, max_blocks, n_blocks, page, device="cuda"):
         """A pool whose blocks are all free: block 0 is granted first."""
-        i32 = dict(dtype=torch.int32, device=device)
+        i32 = dict(dtype=_I32, device=device)
         return cls(torch.full((B, max_blocks), -1, **i32), torch.zeros((B,), **i32),
                    torch.arange(n_blocks - 1, -1, -1, **i32), torch.full((1,), n_blocks, **i32), page)
 
 
-def _slots_args(B, slots, slot_off, S):
-    p = _dev(slots, torch.int64, "slots")
+def _slots_args(B, dev, slots, slot_off, S):
+    p, n_slots = _dev(slots, _I64, dev, "slots"), slots.numel()
     if slot_off is None:
         if slots.dim() != 2 or slots.shape[0] < B:
             raise ValueError("slots must be [B][S] without slot_off")
-        S = slots.shape[1]
-    elif S is None:
-        S = slots.numel()
-    return p, slots.numel(), S, _dev(slot_off, torch.int32, "slot_off", B + 1)
+        return p, n_slots, slots.shape[1], 0
+    return p, n_slots, n_slots if S is None else S, _dev(slot_off, _I32, dev, "slot_off", B + 1)
 
 
 def dt_kv_reserve(h, pool, seq_len, n_new, slots, n_extra=0, slot_off=None, S=None, stream=None):
     """Pages and slots (int64, [B][S], or packed by slot_off [B+1] with at most S a request) for the next
     n_new + n_extra tokens of every request."""
-    B = n_new.numel()
-    if B > pool.B:
-        raise ValueError("the pool holds fewer requests than n_new")
-    sp, n_slots, S, so = _slots_args(B, slots, slot_off, S)
-    check(lib.dt_kv_reserve(h.h, B, ctypes.byref(pool.c), _dev(seq_len, torch.int32, "seq_len", B),
-                            _dev(n_new, torch.int32, "n_new"), n_extra, sp, n_slots, S, so, _stream(stream)))
+    B, dev = n_new.numel(), _device()
+    if B > pool.B or pool.device != dev:
+        raise ValueError("the pool holds fewer requests than n_new, or is on another device")
+    sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
+    rc = lib.dt_kv_reserve(h.h, B, pool.ref, _dev(seq_len, _I32, dev, "seq_len", B), _dev(n_new, _I32, dev, "n_new"),
+                           n_extra, sp, n_slots, S, so, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
 
 
 def dt_kv_release(h, pool, keep_len, stream=None):
     """Gives back every request's blocks past keep_len tokens (0: all of them)."""
-    if keep_len.numel() > pool.B:
-        raise ValueError("the pool holds fewer requests than keep_len")
-    check(lib.dt_kv_release(h.h, keep_len.numel(), ctypes.byref(pool.c), _dev(keep_len, torch.int32, "keep_len"),
-                            _stream(stream)))
+    B, dev = keep_len.numel(), _device()
+    if B > pool.B or pool.device != dev:
+        raise ValueError("the pool holds fewer requests than keep_len, or is on another device")
+    rc = lib.dt_kv_release(h.h, B, pool.ref, _dev(keep_len, _I32, dev, "keep_len"),
+                           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
 
 
 def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None, row_off=None, n_extra=0,
@@ -345,39 +375,43 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
     """KV rows into pages: tmp [planes][B][P][H][D] or, with row_off [B+1], [planes][rows][H][D] (P: positions a
     request, default all rows); cache [planes][blocks][page][H][D], any strides but the last dimension's (pages
     with the heads first are a transposed view); path [B][D_path] as written by dt_verify, or None (rows 0..n-1)."""
-    B = n_new.numel()
-    lead = 2 if row_off is not None else 3
-    if tmp.dim() != lead + 2 or cache.dim() != 5:
+    B, dev = n_new.numel(), _device()
+    ts, cs, st, sc = tmp.shape, cache.shape, tmp.stride(), cache.stride()
+    if len(ts) != (5 if row_off is None else 4) or len(cs) != 5:
         raise ValueError("tmp needs [planes][B][P][H][D] ([planes][rows][H][D] packed), cache [planes][blocks][page][H][D]")
-    if tmp.shape[-2:] != cache.shape[-2:] or tmp.shape[0] != cache.shape[0]:
+    if ts[-2:] != cs[-2:] or ts[0] != cs[0]:
         raise ValueError("tmp and cache differ in planes, heads or head size")
-    e = tmp.element_size()
-    st, sc = tmp.stride(), cache.stride()
     if row_off is None:
-        if tmp.shape[1] < B or (tmp.shape[1] > 1 and st[1] != tmp.shape[2] * st[2]):
+        if ts[1] < B or (ts[1] > 1 and st[1] != ts[2] * st[2]):
             raise ValueError("tmp [planes][B][P] needs B requests, P rows apart")
-        P, rows = tmp.shape[2], tmp.shape[1] * tmp.shape[2]
+        P, rows = ts[2], ts[1] * ts[2]
     else:
-        rows = tmp.shape[1]
+        rows = ts[1]
         P = rows if P is None else P
-    if path is not None and (path.dim() != 2 or path.shape[0] < B):
-        raise ValueError("path must be [B][D_path]")
-    i32 = torch.int32
-    kv = DtKvRows(_strided(tmp, tmp.dtype, "tmp"), st[0] * e, st[-3] * e, st[-2] * e, rows,
-                  _strided(cache, tmp.dtype, "cache"), sc[0] * e, sc[1] * e, sc[2] * e, sc[3] * e, tmp.shape[0],
-                  tmp.shape[-2], tmp.shape[-1] * e, cache.shape[2], cache.shape[1])
-    sp, n_slots, S, so = _slots_args(B, slots, slot_off, S)
-    check(lib.dt_commit_kv_paged(h.h, B, ctypes.byref(kv), P, _dev(row_off, i32, "row_off", B + 1),
-                                 _dev(path, i32, "path"), 0 if path is None else path.shape[1],
-                                 _dev(n_new, i32, "n_new"), n_extra, sp, n_slots, S, so,
-                                 _dev(seq_len, i32, "seq_len", B), _dev(len_out, i32, "len_out", B), _stream(stream)))
+    dp = 0
+    if path is not None:
+        if path.dim() != 2 or path.shape[0] < B:
+            raise ValueError("path must be [B][D_path]")
+        dp = path.shape[1]
+    e, dtype = tmp.element_size(), tmp.dtype
+    kv = _pack_kv_rows(_strided(tmp, dtype, dev, st, "tmp"), st[0] * e, st[-3] * e, st[-2] * e, rows,
+                       _strided(cache, dtype, dev, sc, "cache"), sc[0] * e, sc[1] * e, sc[2] * e, sc[3] * e, ts[0],
+                       ts[-2], ts[-1] * e, cs[2], cs[1])
+    sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
+    rc = lib.dt_commit_kv_paged(h.h, B, kv, P, _dev(row_off, _I32, dev, "row_off", B + 1),
+                                _dev(path, _I32, dev, "path"), dp, _dev(n_new, _I32, dev, "n_new"), n_extra, sp,
+                                n_slots, S, so, _dev(seq_len, _I32, dev, "seq_len", B),
+                                _dev(len_out, _I32, dev, "len_out", B),
+                                _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
 
 
 def dt_tree_attention_workspace(h, B, P, H_q, H_kv, D, shared=False):
     """A workspace tensor for dt_tree_attention calls of at most these sizes (one call at a time)."""
     n = ctypes.c_int64(0)
     check(lib.dt_tree_attention_workspace(h.h, B, P, H_q, H_kv, D, 1 if shared else 0, ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    return torch.empty(n.value, dtype=_U8, device="cuda")
 
 
 _ATTN_TYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
@@ -389,52 +423,49 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
     [rows][heads][D] with row_off [B+1] (P: positions a request, default the mask's or all rows); k_pages and
     v_pages [blocks][page][H_kv][D], any strides but the last dimension's; block_table [B][max_blocks]; mask
     [B][P][P] uint8 or None (a chain); scale defaults to D ** -0.5."""
-    dtype = q.dtype
+    dtype, dev, B = q.dtype, _device(), n_pos.numel()
     code = _ATTN_TYPES.get(dtype)
     if code is None:
         raise ValueError("q must be bfloat16 or float16")
-    B = n_pos.numel()
-    lead = 1 if row_off is not None else 2
-    H_q, D = q.shape[-2:]
-    rows_shape = q.shape[:lead]
-    H_kv = k_new.shape[-2]
-    if q.dim() != lead + 2 or out.shape != q.shape or k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    qh, nh, ph, th = q.shape, k_new.shape, k_pages.shape, block_table.shape
+    qs, os_, ks, vs, kp, vp_ = q.stride(), out.stride(), k_new.stride(), v_new.stride(), k_pages.stride(), v_pages.stride()
+    if len(qh) != (4 if row_off is None else 3) or out.shape != qh or len(ph) != 4 or v_pages.shape != ph:
         raise ValueError("q and out need [B][P][H][D] ([rows][H][D] packed), pages [blocks][page][H_kv][D]")
-    if k_new.shape != v_new.shape or k_new.shape[:-2] != rows_shape or k_new.shape[-1] != D or \
-            k_pages.shape[-2:] != k_new.shape[-2:]:
+    if v_new.shape != nh or nh[:-2] != qh[:-2] or nh[-1] != qh[-1] or ph[2:] != nh[-2:]:
         raise ValueError("k_new, v_new and the pages must match q's rows and one another's heads and head size")
-    if block_table.dim() != 2 or block_table.shape[0] < B:
+    if len(th) != 2 or th[0] < B:
         raise ValueError("block_table must be [B][max_blocks]")
-    if lead == 2:
-        if q.shape[0] < B:
+    if row_off is None:
+        P, rows = qh[1], qh[0] * qh[1]
+        if qh[0] < B:
             raise ValueError("q holds fewer requests than n_pos")
-        P, rows = q.shape[1], q.shape[0] * q.shape[1]
-        if q.shape[0] > 1:
-            for t in (q, out, k_new, v_new):
-                if t.stride(0) != P * t.stride(1):
-                    raise ValueError("padded rows must be P rows apart")
+        if qh[0] > 1 and not (qs[0] == P * qs[1] and os_[0] == P * os_[1] and ks[0] == P * ks[1] and vs[0] == P * vs[1]):
+            raise ValueError("padded rows must be P rows apart")
     else:
-        rows = q.shape[0]
+        rows = qh[0]
         if P is None:
             P = mask.shape[-1] if mask is not None else min(rows, h.cfg.P_max)
-    if mask is not None and (mask.dim() != 3 or mask.shape[0] < B or mask.shape[1] != P or mask.shape[2] != P):
-        raise ValueError("mask must be [B][P][P]")
-    i32 = torch.int32
-    qs, os_, ks, vs, kp, vp_ = q.stride(), out.stride(), k_new.stride(), v_new.stride(), k_pages.stride(), v_pages.stride()
-    a = DtAttnArgs(B, P, H_q, H_kv, D, code, D ** -0.5 if scale is None else scale, shared_len, rows,
-                   _strided(q, dtype, "q"), qs[-3], qs[-2], _strided(out, dtype, "out"), os_[-3], os_[-2],
-                   _strided(k_new, dtype, "k_new"), _strided(v_new, dtype, "v_new"), ks[-3], ks[-2], vs[-3], vs[-2],
-                   _strided(k_pages, dtype, "k_pages"), _strided(v_pages, dtype, "v_pages"), kp[0], kp[1], kp[2],
-                   vp_[0], vp_[1], vp_[2], k_pages.shape[0], k_pages.shape[1], _dev(block_table, i32, "block_table"),
-                   block_table.shape[1], _dev(seq_len, i32, "seq_len", B), _dev(n_pos, i32, "n_pos"),
-                   _dev(mask, torch.uint8, "mask"), _dev(row_off, i32, "row_off", B + 1),
-                   _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    check(lib.dt_tree_attention(h.h, ctypes.byref(a), _stream(stream)))
+    if mask is not None:
+        mh = mask.shape
+        if len(mh) != 3 or mh[0] < B or mh[1] != P or mh[2] != P:
+            raise ValueError("mask must be [B][P][P]")
+    a = _pack_attn(B, P, qh[-2], nh[-2], qh[-1], code, qh[-1] ** -0.5 if scale is None else scale, shared_len, rows,
+                   _strided(q, dtype, dev, qs, "q"), qs[-3], qs[-2], _strided(out, dtype, dev, os_, "out"), os_[-3],
+                   os_[-2], _strided(k_new, dtype, dev, ks, "k_new"), _strided(v_new, dtype, dev, vs, "v_new"), ks[-3],
+                   ks[-2], vs[-3], vs[-2], _strided(k_pages, dtype, dev, kp, "k_pages"),
+                   _strided(v_pages, dtype, dev, vp_, "v_pages"), kp[0], kp[1], kp[2], vp_[0], vp_[1], vp_[2], ph[0],
+                   ph[1], _dev(block_table, _I32, dev, "block_table"), th[1], _dev(seq_len, _I32, dev, "seq_len", B),
+                   _dev(n_pos, _I32, dev, "n_pos"), _dev(mask, _U8, dev, "mask"),
+                   _dev(row_off, _I32, dev, "row_off", B + 1), _dev(workspace, _U8, dev, "workspace"),
+                   workspace.numel())
+    rc = lib.dt_tree_attention(h.h, a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
 
 
 def dt_count_tokens(h, counts, tokens, n_new, path=None, row_off=None, n_extra=0, prompt=False, P=None, stream=None):
     """Adds tokens ([B][P], or packed by row_off) to the token history counts [B][V] (prompt: marks them)."""
-    B, i32 = n_new.numel(), torch.int32
+    B, dev = n_new.numel(), _device()
     if counts.dim() != 2 or counts.shape[1] != h.cfg.V or counts.shape[0] < B:
         raise ValueError("counts must be [B][V]")
     if row_off is None:
@@ -445,54 +476,64 @@ def dt_count_tokens(h, counts, tokens, n_new, path=None, row_off=None, n_extra=0
         P = max(1, tokens.numel())
     if path is not None and (path.dim() != 2 or path.shape[0] < B):
         raise ValueError("path must be [B][D_path]")
-    check(lib.dt_count_tokens(h.h, B, _dev(counts, i32, "counts"), _dev(tokens, i32, "tokens"), P,
-                              _dev(row_off, i32, "row_off", B + 1), _dev(path, i32, "path"),
-                              0 if path is None else path.shape[1], _dev(n_new, i32, "n_new"), n_extra,
-                              1 if prompt else 0, _stream(stream)))
+    check(lib.dt_count_tokens(h.h, B, _dev(counts, _I32, dev, "counts"), _dev(tokens, _I32, dev, "tokens"), P,
+                              _dev(row_off, _I32, dev, "row_off", B + 1), _dev(path, _I32, dev, "path"),
+                              0 if path is None else path.shape[1], _dev(n_new, _I32, dev, "n_new"), n_extra,
+                              1 if prompt else 0, _raw_stream(dev) if stream is None else stream.cuda_stream))
 
 
 def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=None, counts=None, repetition=None,
                       frequency=None, presence=None, bias_ids=None, bias_vals=None, allow=None, P=None, stream=None):
     """Penalties, biases and grammar masks on target rows: logits and out [B][P][V], or packed [rows][V] with
     row_off (rows may be further apart than V); out may be logits. allow: int32 words, rows as logits."""
-    dtype = torch.bfloat16 if h.cfg.dtype == DT_BF16 else torch.float32
-    B, V, i32, f32 = n_pos.numel(), h.cfg.V, torch.int32, torch.float32
-    lead = 1 if row_off is not None else 2
-    if logits.dim() != lead + 1 or out.shape != logits.shape or logits.shape[-1] != V:
+    cfg = h.cfg
+    dtype = torch.bfloat16 if cfg.dtype == DT_BF16 else _F32
+    B, V, dev = n_pos.numel(), cfg.V, _device()
+    ls, ls_, os_ = logits.shape, logits.stride(), out.stride()
+    if len(ls) != (3 if row_off is None else 2) or out.shape != ls or ls[-1] != V:
         raise ValueError("logits and out need [B][P][V] ([rows][V] packed)")
-    if lead == 2:
-        if logits.shape[0] < B:
+    if row_off is None:
+        P, rows = ls[1], ls[0] * ls[1]
+        if ls[0] < B:
             raise ValueError("logits holds fewer requests than n_pos")
-        P, rows = logits.shape[1], logits.shape[0] * logits.shape[1]
-        for t in (logits, out):
-            if t.shape[0] > 1 and t.stride(0) != P * t.stride(1):
-                raise ValueError("padded rows must be P rows apart")
+        if ls[0] > 1 and not (ls_[0] == P * ls_[1] and os_[0] == P * os_[1]):
+            raise ValueError("padded rows must be P rows apart")
     else:
-        rows = logits.shape[0]
+        rows = ls[0]
         if P is None:
-            P = mask.shape[-1] if mask is not None else tokens.shape[-1] if tokens is not None else min(rows, h.cfg.P_max)
-    if mask is not None and (mask.dim() != 3 or mask.shape[0] < B or mask.shape[1] != P or mask.shape[2] != P):
-        raise ValueError("mask must be [B][P][P]")
-    if tokens is not None and (tokens.dim() != 2 or tokens.shape[0] < B or tokens.shape[1] != P):
-        raise ValueError("tokens must be [B][P]")
-    if counts is not None and (counts.dim() != 2 or counts.shape[0] < B or counts.shape[1] != V):
-        raise ValueError("counts must be [B][V]")
-    if (bias_ids is None) != (bias_vals is None) or (bias_ids is not None and (
-            bias_ids.dim() != 2 or bias_ids.shape[0] < B or bias_vals.shape != bias_ids.shape)):
-        raise ValueError("bias_ids and bias_vals must be [B][n_bias] both")
-    words = 0
+            P = mask.shape[-1] if mask is not None else tokens.shape[-1] if tokens is not None else min(rows, cfg.P_max)
+    if mask is not None:
+        mh = mask.shape
+        if len(mh) != 3 or mh[0] < B or mh[1] != P or mh[2] != P:
+            raise ValueError("mask must be [B][P][P]")
+    if tokens is not None:
+        th = tokens.shape
+        if len(th) != 2 or th[0] < B or th[1] != P:
+            raise ValueError("tokens must be [B][P]")
+    if counts is not None:
+        ch = counts.shape
+        if len(ch) != 2 or ch[0] < B or ch[1] != V:
+            raise ValueError("counts must be [B][V]")
+    n_bias = words = 0
+    if bias_ids is not None or bias_vals is not None:
+        if bias_ids is None or bias_vals is None or bias_ids.dim() != 2 or len(bias_ids) < B or \
+                bias_vals.shape != bias_ids.shape:
+            raise ValueError("bias_ids and bias_vals must be [B][n_bias] both")
+        n_bias = bias_ids.shape[1]
     if allow is not None:
         words = allow.shape[-1]
         if allow.numel() < rows * words or words < (V + 31) // 32:
             raise ValueError("allow needs a row of ceil(V / 32) words for every row of logits")
-    p = DtLogitsParams(P, _dev(n_pos, i32, "n_pos"), _dev(row_off, i32, "row_off", B + 1), rows,
-                       _dev(tokens, i32, "tokens"), _dev(mask, torch.uint8, "mask"), _dev(counts, i32, "counts"),
-                       _dev(repetition, f32, "repetition", B), _dev(frequency, f32, "frequency", B),
-                       _dev(presence, f32, "presence", B), _dev(bias_ids, i32, "bias_ids"),
-                       _dev(bias_vals, f32, "bias_vals"), 0 if bias_ids is None else bias_ids.shape[1],
-                       _dev(allow, i32, "allow"), words)
-    check(lib.dt_logits_process(h.h, B, _strided(logits, dtype, "logits"), logits.stride(-2),
-                                _strided(out, dtype, "out"), out.stride(-2), ctypes.byref(p), _stream(stream)))
+    p = _pack_logits(P, _dev(n_pos, _I32, dev, "n_pos"), _dev(row_off, _I32, dev, "row_off", B + 1), rows,
+                     _dev(tokens, _I32, dev, "tokens"), _dev(mask, _U8, dev, "mask"), _dev(counts, _I32, dev, "counts"),
+                     _dev(repetition, _F32, dev, "repetition", B), _dev(frequency, _F32, dev, "frequency", B),
+                     _dev(presence, _F32, dev, "presence", B), _dev(bias_ids, _I32, dev, "bias_ids", 0),
+                     _dev(bias_vals, _F32, dev, "bias_vals", 0), n_bias, _dev(allow, _I32, dev, "allow"), words)
+    rc = lib.dt_logits_process(h.h, B, _strided(logits, dtype, dev, ls_, "logits"), ls_[-2],
+                               _strided(out, dtype, dev, os_, "out"), os_[-2], p,
+                               _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
 
 
 class Meta:

@@ -147,17 +147,17 @@ def _load():
         "dt_commit_kv": ([vp, vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int64,
                           ctypes.c_int32, ctypes.c_int64, vp, vp, vp, ctypes.c_int32, vp, vp], I),
         "dt_cast_verify_rerank": ([vp, ctypes.POINTER(DtPruneParams), ctypes.POINTER(DtPruneOut), vp, vp], I),
-        "dt_kv_reserve": ([vp, ctypes.c_int32, ctypes.POINTER(DtBlockPool), vp, vp, ctypes.c_int32, vp,
+        "dt_kv_reserve": ([vp, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp,
                            ctypes.c_int64, ctypes.c_int32, vp, vp], I),
-        "dt_kv_release": ([vp, ctypes.c_int32, ctypes.POINTER(DtBlockPool), vp, vp], I),
-        "dt_commit_kv_paged": ([vp, ctypes.c_int32, ctypes.POINTER(DtKvRows), ctypes.c_int32, vp, vp, ctypes.c_int32,
+        "dt_kv_release": ([vp, ctypes.c_int32, vp, vp, vp], I),
+        "dt_commit_kv_paged": ([vp, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, ctypes.c_int32,
                                 vp, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, vp, vp], I),
-        "dt_tree_attention": ([vp, ctypes.POINTER(DtAttnArgs), vp], I),
+        "dt_tree_attention": ([vp, vp, vp], I),
         "dt_tree_attention_workspace": ([vp] + [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int64)], I),
         "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
                              ctypes.c_int32, vp], I),
         "dt_logits_process": ([vp, ctypes.c_int32, vp, ctypes.c_int64, vp, ctypes.c_int64,
-                               ctypes.POINTER(DtLogitsParams), vp], I),
+                               vp, vp], I),
         "dt_row_topk_static": ([vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                 vp, vp, vp, vp], I),
     }
