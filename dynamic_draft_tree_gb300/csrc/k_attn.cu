@@ -48,6 +48,7 @@ struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
 struct AttnParams {
   dt_attn_args a;
   int32_t G, page_shift, tree_box;
+  uint32_t g_magic;   // ceil(2^32 / G): x / G = umulhi(x, g_magic) for x < 2^25 (exact, as x (g_magic G - 2^32) < 2^32)
   float c;            // scale * log2 e
   int32_t ns;         // tiles of the shared prefix
   int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
@@ -104,19 +105,20 @@ struct Plan {
 };
 
 struct Segment {
-  bool shared, whole;
+  int shared, whole;    // whole: an item without other parts, written straight to the result
   int b, h, mp;
-  int t0, t1;           // tiles
-  int tp, len;          // own: prefix tiles, cached tokens; shared: ts, shared_len
-  int n;                // own: positions
-  int64_t base;         // row of the first position
+  int t0, t1;           // tiles; none: the line is at its end
+  int tp, len, tok0;    // prefix tiles, their end and the first one's token
+  int n;                // positions (0 for the shared prefix)
   int rows;             // rows of the item
+  int i0, g0;           // position and head of its row 0
+  int64_t base;         // row of the first position
   int64_t slot;
 };
 
+// One lane walks along the CTA's run.
 struct Walk {
-  int64_t x;
-  int64_t t_b;
+  int64_t x, t_b;
   int b, k_b;
   int loaded;           // request whose extent is held
   Request r;
@@ -129,65 +131,68 @@ struct Walk {
     k_b = pl.k_b;
     loaded = -1;
   }
-  __device__ bool next(const AttnParams& p, const Plan& pl, Segment& s) {
-    if (x >= pl.x1) return false;
+  __device__ __noinline__ void next(const AttnParams& p, const Plan& pl, Segment& s) {
+    s.t0 = s.t1 = 0;
+    if (x >= pl.x1) return;
+    int64_t item;
+    int tt;
     if (x < pl.w_shared) {
-      const int item = (int)(x / pl.ts);
-      s.shared = true;
-      s.whole = false;
+      tt = pl.ts;
+      item = x / tt;
+      s.shared = 1;
       s.b = 0;
-      s.h = item / pl.mp_s;
-      s.mp = item - s.h * pl.mp_s;
-      s.t0 = (int)(x - (int64_t)item * pl.ts);
-      s.t1 = (int)min((int64_t)pl.ts, s.t0 + pl.x1 - x);
-      s.tp = pl.ts;
+      s.h = (int)(item / pl.mp_s);
+      s.mp = (int)item - s.h * pl.mp_s;
+      s.t0 = (int)(x - item * tt);
+      s.tp = tt;
       s.len = p.a.shared_len;
+      s.tok0 = 0;
       s.n = 0;
       s.base = 0;
       s.rows = min(kItemRows, pl.rows_s - s.mp * kItemRows);
       s.slot = item + blockIdx.x;
-      x += s.t1 - s.t0;
-      return true;
-    }
-    const int64_t y = x - pl.w_shared;
-    while (true) {
-      if (b >= p.a.B) return false;
-      if (loaded != b) {
-        r = request_of(p.a, p.page_shift, b);
-        e = extent_of(p, r);
-        loaded = b;
+    } else {
+      const int64_t y = x - pl.w_shared;
+      while (true) {
+        if (b >= p.a.B) return;
+        if (loaded != b) {
+          r = request_of(p.a, p.page_shift, b);
+          e = extent_of(p, r);
+          loaded = b;
+        }
+        const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
+        if (y < t_b + w) break;
+        t_b += w;
+        k_b += p.a.H_kv * e.mp;
+        ++b;
       }
-      const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
-      if (y < t_b + w) break;
-      t_b += w;
-      k_b += p.a.H_kv * e.mp;
-      ++b;
+      tt = e.tt;
+      item = (y - t_b) / tt;
+      s.shared = 0;
+      s.b = b;
+      s.h = (int)item / e.mp;
+      s.mp = (int)item - s.h * e.mp;
+      s.t0 = (int)(y - t_b - item * tt);
+      s.tp = e.tp;
+      s.len = r.len;
+      s.tok0 = p.a.shared_len;
+      s.n = r.n;
+      s.base = r.base;
+      s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
+      s.slot = k_b + item + blockIdx.x;
     }
-    const int item = (int)((y - t_b) / e.tt);
-    s.shared = false;
-    s.b = b;
-    s.h = item / e.mp;
-    s.mp = item - s.h * e.mp;
-    s.t0 = (int)(y - t_b - (int64_t)item * e.tt);
-    s.t1 = (int)min((int64_t)e.tt, s.t0 + pl.x1 - x);
-    s.tp = e.tp;
-    s.len = r.len;
-    s.n = r.n;
-    s.base = r.base;
-    s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
-    s.whole = s.t0 == 0 && s.t1 == e.tt && p.a.shared_len == 0;
-    s.slot = (int64_t)k_b + item + blockIdx.x;
+    s.t1 = (int)min((int64_t)tt, s.t0 + pl.x1 - x);
+    s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
+    s.i0 = s.mp * kItemRows / p.G;
+    s.g0 = s.mp * kItemRows - s.i0 * p.G;
     x += s.t1 - s.t0;
-    return true;
   }
 };
 
 // Tokens or positions of tile t that exist, and whether the tile holds tree positions.
-__device__ __forceinline__ int tile_valid(const AttnParams& p, const Segment& s, int t, bool& tree) {
+__device__ __forceinline__ int tile_valid(const Segment& s, int t, bool& tree) {
   tree = !s.shared && t >= s.tp;
-  if (tree) return min(kTile, s.n - (t - s.tp) * kTile);
-  const int tok = (s.shared ? 0 : p.a.shared_len) + t * kTile;
-  return min(kTile, s.len - tok);
+  return min(kTile, tree ? s.n - (t - s.tp) * kTile : s.len - s.tok0 - t * kTile);
 }
 
 template <int DP>
@@ -198,15 +203,36 @@ struct Smem {
   static constexpr int kBytes = (2 + 2 * kStages) * kBlock + 1024;
 };
 
+constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reader, at most
+
 struct Shared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vfix[4];
   uint64_t sfull[2], pready[2], odone[2], qready[2], mlready;
+  uint64_t segfull[kSegs], segempty[kSegs];
+  Segment seg[kSegs];
   float2 ml[kTile];
   Plan plan;
   int64_t sums[2][12];
   uint32_t tmem;
   int stop, odd_values;
 };
+
+// The roles read the segments that warp 10 puts down, in order. `lead`: the thread that gives the place back.
+struct Segments {
+  uint32_t n = 0;
+  __device__ __forceinline__ bool next(Shared& sh, Segment& s, bool warp, bool lead) {
+    const int at = (int)(n % kSegs);
+    const uint32_t parity = n / kSegs & 1;
+    ++n;
+    if (warp ? !tc::bar_wait_warp(&sh.segfull[at], parity, &sh.stop) : !tc::bar_wait(&sh.segfull[at], parity, &sh.stop))
+      return false;
+    s = sh.seg[at];
+    if (warp) __syncwarp();
+    if (lead) tc::bar_arrive(&sh.segempty[at]);
+    return s.t1 > s.t0;
+  }
+};
+constexpr int kSegReaders = 11;  // eight softmax warps, two loading warps, the issuing thread
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -285,8 +311,12 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
   }
   const int64_t y0 = x0 - w_shared;
   for (int b = b0; b < b1; ++b) {
-    const Extent e = extent_of(p, request_of(p.a, p.page_shift, b));
-    const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
+    int64_t w = tiles, k = items;
+    if (chunk > 1) {
+      const Extent e = extent_of(p, request_of(p.a, p.page_shift, b));
+      w = (int64_t)p.a.H_kv * e.mp * e.tt;
+      k = p.a.H_kv * e.mp;
+    }
     if (y0 > 0 && t_b <= y0 && y0 < t_b + w) {
       sh.plan.b = b;
       sh.plan.t_b = t_b;
@@ -297,7 +327,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
       p.k_pre[b] = (int32_t)k_b;
     }
     t_b += w;
-    k_b += p.a.H_kv * e.mp;
+    k_b += k;
   }
 }
 
@@ -319,15 +349,14 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
   const int shift = p.page_shift, page = p.a.page;
   const int box = min(page, kTile);  // tokens of a page box
   const int box_shift = min(shift, 7);
-  Walk w;
-  w.start(sh.plan);
+  Segments segs;
   Segment s;
   uint32_t n = 0;
   bool ok = true;
   const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
-  while (ok && w.next(p, sh.plan, s)) {
+  while (ok && segs.next(sh, s, true, lane == 0)) {
     const int32_t* table = p.a.block_table + (s.shared ? 0 : (int64_t)s.b * p.a.max_blocks);
-    const int tok0 = s.shared ? 0 : p.a.shared_len;
+    const int tok0 = s.tok0;
     // block id of this lane's box in tile t (-1: none)
     auto block_at = [&](int t) {
       const int tok = tok0 + t * kTile + (part << box_shift);
@@ -349,7 +378,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
       if (!ok) break;
       const uint32_t at = smem + stage * S::kBlock;
       bool tree;
-      const int valid = tile_valid(p, s, t, tree);
+      const int valid = tile_valid(s, t, tree);
       if (tree) {
         // one box of tree_box rows and 64 elements for every tree_box positions that exist
         const int boxes = (valid + p.tree_box - 1) / p.tree_box;
@@ -393,70 +422,74 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint
   constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
   const int steps = (p.a.D + 15) / 16;  // the padding elements of a row are zero
   const uint32_t tm = sh.tmem;
-  Walk w;
-  w.start(sh.plan);
+  // shared memory lies below 2^18 bytes, so offsets add up inside a descriptor's address field
+  const uint64_t q_desc = tc::smem_desc(q_smem, 16, 1024), k_desc = tc::smem_desc(k_smem, 16, 1024),
+                 v_desc = tc::smem_desc(v_smem, S::kHalf, 1024);
+  Segments segs;
   Segment s;
   uint32_t seen = 0;          // tiles of the segments before this one
   uint32_t np[2] = {0, 0};    // units of each group so far (phase of pready)
   uint32_t nq[2] = {0, 0};    // uses of each Q buffer
   uint32_t fix = 0;           // parity of every stage's vfix
-  bool ok = true;
-  while (ok && w.next(p, sh.plan, s)) {
+  while (segs.next(sh, s, false, true)) {
     const bool dual = s.rows > kTile;
     const int tiles = s.t1 - s.t0, units = dual ? 2 * tiles : tiles;
-    ok = tc::bar_wait(&sh.qready[0], nq[0]++ & 1, &sh.stop);
-    if (ok && dual) ok = tc::bar_wait(&sh.qready[1], nq[1]++ & 1, &sh.stop);
-    auto issue_s = [&](int u) {
-      const int k = dual ? u >> 1 : u, g = u & 1;
-      int stage;
-      uint32_t parity;
-      ring<S::kStages>(seen + k, stage, parity);
-      if (!dual || g == 0) {
-        if (!tc::bar_wait(&sh.kfull[stage], parity, &sh.stop)) return false;
-      }
-      tc::fence_after();
-      const uint32_t qa = q_smem + (dual ? g : 0) * S::kBlock, ka = k_smem + stage * S::kBlock;
-      for (int x = 0; x < steps; ++x) {
-        const uint32_t off = (x >> 2) * S::kHalf + (x & 3) * 32;
-        tc::mma_ss(tm + g * kTile, tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(ka + off, 16, 1024), kDescS, x > 0);
-      }
-      tc::mma_commit(&sh.sfull[g]);
-      if (!dual || g == 1) tc::mma_commit(&sh.kempty[stage]);
-      return true;
-    };
-    for (int u = 0; ok && u < min(2, units); ++u) ok = issue_s(u);
-    for (int u = 0; ok && u < units; ++u) {
-      const int k = dual ? u >> 1 : u, g = u & 1, t = s.t0 + k;
-      int stage;
-      uint32_t parity;
-      ring<S::kStages>(seen + k, stage, parity);
-      bool tree;
-      const int valid = tile_valid(p, s, t, tree);
-      if (!dual || g == 0) {
-        ok = tc::bar_wait(&sh.vfull[stage], parity, &sh.stop);
-        if (ok && (tree || valid < kTile)) {
-          ok = tc::bar_wait(&sh.vfix[stage], fix >> stage & 1, &sh.stop);
-          fix ^= 1u << stage;
+    if (!tc::bar_wait(&sh.qready[0], nq[0]++ & 1, &sh.stop)) return;
+    if (dual && !tc::bar_wait(&sh.qready[1], nq[1]++ & 1, &sh.stop)) return;
+    // O += P V of unit v - 2, then S of unit v
+    for (int v = 0; v < units + 2; ++v) {
+      const int g = v & 1;
+      if (v >= 2) {
+        const int u = v - 2, k = dual ? u >> 1 : u;
+        int stage;
+        uint32_t parity;
+        ring<S::kStages>(seen + k, stage, parity);
+        bool tree;
+        const int valid = tile_valid(s, s.t0 + k, tree);
+        if (!dual || g == 0) {
+          if (!tc::bar_wait(&sh.vfull[stage], parity, &sh.stop)) return;
+          if (tree || valid < kTile) {
+            if (!tc::bar_wait(&sh.vfix[stage], fix >> stage & 1, &sh.stop)) return;
+            fix ^= 1u << stage;
+          }
         }
-        if (!ok) break;
+        const uint64_t va = v_desc + (uint32_t)(stage * (S::kBlock >> 4));
+        const uint32_t o = tm + 2 * kTile + g * DP, pr = tm + g * kTile;
+        if (!tc::bar_wait(&sh.pready[g], (g ? np[1]++ : np[0]++) & 1, &sh.stop)) return;
+        tc::fence_after();
+        tc::mma_ts(o, pr, va, kDescO, u >= 2);  // the group's first unit starts its accumulator
+#pragma unroll
+        for (int x = 1; x < kTile / 16; ++x)
+          if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+        tc::mma_commit(&sh.odone[g]);
+        if (!dual || g == 1) tc::mma_commit(&sh.vempty[stage]);
       }
-      ok = tc::bar_wait(&sh.pready[g], np[g]++ & 1, &sh.stop);
-      if (!ok) break;
-      tc::fence_after();
-      const bool first = u < 2;  // the group's first unit starts its accumulator
-      const uint32_t va = v_smem + stage * S::kBlock;
-      for (int x = 0; x < (valid + 15) / 16; ++x)
-        tc::mma_ts(tm + 2 * kTile + g * DP, tm + g * kTile + x * 8, tc::smem_desc(va + x * 2048, S::kHalf, 1024), kDescO,
-                   !(first && x == 0));
-      tc::mma_commit(&sh.odone[g]);
-      if (!dual || g == 1) tc::mma_commit(&sh.vempty[stage]);
-      if (u + 2 < units) ok = issue_s(u + 2);
+      if (v < units) {
+        const int k = dual ? v >> 1 : v;
+        int stage;
+        uint32_t parity;
+        ring<S::kStages>(seen + k, stage, parity);
+        if (!dual || g == 0) {
+          if (!tc::bar_wait(&sh.kfull[stage], parity, &sh.stop)) return;
+        }
+        tc::fence_after();
+        const uint64_t qa = q_desc + (uint32_t)((dual ? g : 0) * (S::kBlock >> 4)), ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
+        const uint32_t d = tm + g * kTile;
+        tc::mma_ss(d, qa, ka, kDescS, false);
+#pragma unroll
+        for (int x = 1; x < DP / 16; ++x) {
+          const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
+          if (x < steps) tc::mma_ss(d, qa + off, ka + off, kDescS, true);
+        }
+        tc::mma_commit(&sh.sfull[g]);
+        if (!dual || g == 1) tc::mma_commit(&sh.kempty[stage]);
+      }
     }
     seen += tiles;
   }
 }
 
-// One warp: value rows past the end of a tile become zero (a weight of zero times what lies there need not be
+// One warp: puts down the segments for the other roles. Value rows past the end of a tile become zero (a weight of zero times what lies there need not be
 // zero), and so do NaN and infinities at tree positions, which only some rows attend to: the rows that do add
 // them in finish_row.
 template <int DP, bool BF16>
@@ -466,11 +499,29 @@ __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int
   Walk w;
   w.start(sh.plan);
   Segment s;
-  uint32_t n = 0;
-  while (w.next(p, sh.plan, s)) {
+  uint32_t n = 0, put = 0;
+  // The segment after the one whose tiles are looked at is put down first: the others work ahead. That waits only
+  // for readers of segments long past, never for tiles of this one.
+  auto put_next = [&]() {
+    const int at = (int)(put % kSegs);
+    const uint32_t parity = put / kSegs & 1;
+    ++put;
+    if (!tc::bar_wait_warp(&sh.segempty[at], parity ^ 1, &sh.stop)) return false;
+    if (lane == 0) {
+      w.next(p, sh.plan, sh.seg[at]);
+      tc::bar_arrive(&sh.segfull[at]);
+    }
+    __syncwarp();
+    return true;
+  };
+  if (!put_next()) return;
+  for (uint32_t seg = 0;; ++seg) {
+    s = sh.seg[seg % kSegs];  // not written again before this warp puts down kSegs more
+    if (s.t1 == s.t0) return;
+    if (!put_next()) return;
     for (int t = s.t0; t < s.t1; ++t, ++n) {
       bool tree;
-      const int valid = tile_valid(p, s, t, tree);
+      const int valid = tile_valid(s, t, tree);
       int stage;
       uint32_t parity;
       ring<S::kStages>(n, stage, parity);
@@ -549,15 +600,32 @@ __device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s,
   }
 }
 
+// Scores of columns that are not attended to become -inf in tensor memory, whatever they were (few tiles of an item
+// need it: a short loop of its own keeps the common path short).
+__device__ __noinline__ void mask_scores(uint32_t s_at, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 16) {
+    uint32_t raw[16];
+    tc::tmem_ld16(s_at + c, raw);
+    const uint32_t w = (c < 64 ? c < 32 ? b0 : b1 : c < 96 ? b2 : b3) >> (c & 16);
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (!(w >> x & 1)) raw[x] = 0xFF800000u;
+    tc::tmem_st16(s_at + c, raw);
+  }
+  tc::wait_st();
+}
+
 // Values that are no numbers at tree positions this row attends to: weight times value, from global memory.
-template <int DP, bool BF16>
-__device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& s, int f, float m, int d0, float* o) {
+template <bool BF16>
+__device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int64_t base, int j0, int j1, int f, float m,
+                                         int d0, float* o) {
   const int i = f / p.G, g = f - i * p.G;
-  const uint16_t* q = (const uint16_t*)p.a.q + (s.base + i) * p.a.q_row + ((int64_t)s.h * p.G + g) * p.a.q_head;
-  for (int j = (max(s.t0, s.tp) - s.tp) * kTile; j < min(s.n, (s.t1 - s.tp) * kTile); ++j) {
-    if (p.a.mask ? p.a.mask[((int64_t)s.b * p.a.P + i) * p.a.P + j] == 0 : j > i) continue;
-    const uint16_t* v = (const uint16_t*)p.a.v_new + (s.base + j) * p.a.vn_row + s.h * p.a.vn_head;
-    const uint16_t* k = (const uint16_t*)p.a.k_new + (s.base + j) * p.a.kn_row + s.h * p.a.kn_head;
+  const uint16_t* q = (const uint16_t*)p.a.q + (base + i) * p.a.q_row + ((int64_t)h * p.G + g) * p.a.q_head;
+  for (int j = j0; j < j1; ++j) {
+    if (p.a.mask ? p.a.mask[((int64_t)b * p.a.P + i) * p.a.P + j] == 0 : j > i) continue;
+    const uint16_t* v = (const uint16_t*)p.a.v_new + (base + j) * p.a.vn_row + h * p.a.vn_head;
+    const uint16_t* k = (const uint16_t*)p.a.k_new + (base + j) * p.a.kn_row + h * p.a.kn_head;
     bool odd = false;
     for (int d = d0; d < min(d0 + 32, p.a.D); ++d) odd |= !isfinite(unpack16<BF16>(v[d]));
     if (!odd) continue;
@@ -571,9 +639,20 @@ __device__ __noinline__ void add_odd_values(const AttnParams& p, const Segment& 
   }
 }
 
+template <int DP, bool BF16>
+__device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segment& s, int f, float m, int d0, float (&o)[32]) {
+  float x[32];  // its own array: one whose address is taken does not stay in registers
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = o[k];
+  add_odd_row<BF16>(p, s.b, s.h, s.base, (max(s.t0, s.tp) - s.tp) * kTile, min(s.n, (s.t1 - s.tp) * kTile), f, m, d0, x);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) o[k] = x[k];
+}
+
 // The segment's rows of a softmax group leave tensor memory. `other`: the second group's accumulator is joined.
 template <int DP, bool BF16>
-__device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool other, uint32_t tm) {
+__device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool other, uint32_t tm,
+                            uint8_t* q_smem) {
   const int wl = threadIdx.x & 127;         // row of the group
   const int r = (s.rows > kTile ? group * kTile : 0) + wl;
   const bool live = r < s.rows;
@@ -588,25 +667,22 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   const int f = s.mp * kItemRows + r;
   const bool odd = *(volatile int*)&sh.odd_values && !s.shared && s.t1 > s.tp;
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // nothing attended to: zeros; NaN stays
-  uint16_t* out = nullptr;
-  float* part = nullptr;
-  if (live) {
-    const int i = f / p.G, g = f - i * p.G;
-    if (s.whole) {
-      out = (uint16_t*)p.a.out + (s.base + i) * p.a.o_row + ((int64_t)s.h * p.G + g) * p.a.o_head;
-    } else if (s.shared) {
-      const int64_t at = s.slot * kItemRows + r;
-      part = p.o_sh + at * p.a.D;
-      p.ml_sh[at] = make_float2(m, l);
-    } else {
-      const int64_t at = s.slot * p.own_rows + r;
-      part = p.o_own + at * p.a.D;
-      p.ml_own[at] = make_float2(m, l);
-    }
+  if (live && !s.whole) {
+    if (s.shared)
+      p.ml_sh[s.slot * kItemRows + r] = make_float2(m, l);
+    else
+      p.ml_own[s.slot * p.own_rows + r] = make_float2(m, l);
   }
   const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
-  const bool any = __any_sync(0xFFFFFFFFu, live);
-  if (!any) return;
+  if (!__any_sync(0xFFFFFFFFu, live)) return;
+  // Through the warp's own 32 rows of the Q buffer (its products are done), 32 elements a turn, so that lanes store
+  // along rows.
+  const int lane = wl & 31;
+  uint8_t* stage = q_smem + group * Smem<DP>::kBlock + (wl >> 5) * 32 * 128;
+  const int row0 = r - lane;                // the warp's first row of the item
+  const float scale = s.whole ? inv : 1.0f;
+  const int log_lanes = s.whole ? 2 : 3;    // lanes along 32 elements of a row: of the result, of partials
+  const int c = lane & ((1 << log_lanes) - 1);
 #pragma unroll 1
   for (int d0 = 0; d0 < p.a.D; d0 += 32) {
     uint32_t raw[32];
@@ -619,24 +695,36 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(raw[k]), f1, o[k]);
     }
-    if (odd && live) {
-      float x[32];  // its own array: one whose address is taken does not stay in registers
-#pragma unroll
-      for (int k = 0; k < 32; ++k) x[k] = o[k];
-      add_odd_values<DP, BF16>(p, s, f, m == -INFINITY ? 0.0f : m, d0, x);
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = x[k];
-    }
-    if (out) {
+    if (odd && live) add_odd_values<DP, BF16>(p, s, f, m == -INFINITY ? 0.0f : m, d0, o);
+    if (s.whole) {
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
-        if (d0 + k < p.a.D)
-          *(uint4*)(out + d0 + k) = make_uint4(pack16<BF16>(o[k] * inv, o[k + 1] * inv), pack16<BF16>(o[k + 2] * inv, o[k + 3] * inv),
-                                               pack16<BF16>(o[k + 4] * inv, o[k + 5] * inv), pack16<BF16>(o[k + 6] * inv, o[k + 7] * inv));
-    } else if (part) {
+        *(uint4*)(stage + lane * 128 + (((k / 8) ^ (lane & 7)) << 4)) =
+            make_uint4(pack16<BF16>(o[k] * scale, o[k + 1] * scale), pack16<BF16>(o[k + 2] * scale, o[k + 3] * scale),
+                       pack16<BF16>(o[k + 4] * scale, o[k + 5] * scale), pack16<BF16>(o[k + 6] * scale, o[k + 7] * scale));
+    } else {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
-        if (d0 + k < p.a.D) *(float4*)(part + d0 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        *(float4*)(stage + lane * 128 + (((k / 4) ^ (lane & 7)) << 4)) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    }
+    __syncwarp();
+    const int d = d0 + (c << (s.whole ? 3 : 2));
+#pragma unroll 1
+    for (int r4 = 0; r4 < 32; r4 += 16) {
+      // sixteen rows of 16-byte pieces: two (result) or four (partials) of them a lane
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int rr = r4 + (u << (5 - log_lanes)) + (lane >> log_lanes), ri = row0 + rr;
+        if ((u << (5 - log_lanes)) < 16 && ri < s.rows && d < p.a.D) {
+          const uint4 x = *(const uint4*)(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+          if (s.whole) {
+            const int v = s.g0 + ri, i = s.i0 + (int)__umulhi((uint32_t)v, p.g_magic);
+            *(uint4*)((uint16_t*)p.a.out + (s.base + i) * p.a.o_row + ((int64_t)s.h * p.G + (v - (i - s.i0) * p.G)) * p.a.o_head + d) = x;
+          } else {
+            *(uint4*)((s.shared ? p.o_sh + (s.slot * kItemRows + ri) * p.a.D : p.o_own + (s.slot * p.own_rows + ri) * p.a.D) + d) = x;
+          }
+        }
+      }
     }
     __syncwarp();
   }
@@ -649,11 +737,10 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
   const int wl = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
   const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
-  Walk w;
-  w.start(sh.plan);
+  Segments segs;
   Segment s;
   uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
-  while (w.next(p, sh.plan, s)) {
+  while (segs.next(sh, s, true, (threadIdx.x & 31) == 0)) {
     const bool dual = s.rows > kTile;
     const int tiles = s.t1 - s.t0;
     const int mine = dual ? tiles : (tiles + 1 - group) / 2;
@@ -661,14 +748,24 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
     const int r = r0 + wl, f = s.mp * kItemRows + r;
     const bool live = r < s.rows;
     if (dual || group == 0) {
-      // Q rows into the swizzled layout, zeros past the end and past D
-      uint8_t* at = q_smem + group * S::kBlock;
-      const int i = f / p.G, g = f - i * p.G;
-      const uint4* q = (const uint4*)((const uint16_t*)p.a.q + (live ? (s.base + i) * p.a.q_row + ((int64_t)s.h * p.G + g) * p.a.q_head : 0));
+      // the warp's 32 Q rows into the swizzled layout, 16 bytes a lane along the rows, zeros past the end and D
+      uint8_t* at = q_smem + group * S::kBlock + (wl >> 5) * 32 * 128;
+      constexpr int kLanes = DP / 8;  // lanes of a row
+      const int lane = wl & 31, c = lane % kLanes;
+      uint4 x[kLanes];
 #pragma unroll
-      for (int c = 0; c < DP / 8; ++c) {
-        const uint4 x = live && c * 8 < p.a.D ? q[c] : make_uint4(0, 0, 0, 0);
-        *(uint4*)(at + (c >> 3) * S::kHalf + wl * 128 + (((c & 7) ^ (wl & 7)) << 4)) = x;
+      for (int u = 0; u < kLanes; ++u) {
+        const int rr = u * (32 / kLanes) + lane / kLanes, ri = r0 + (wl & 96) + rr;
+        const int v = s.g0 + ri, i = s.i0 + (int)__umulhi((uint32_t)v, p.g_magic);
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (ri < s.rows && c * 8 < p.a.D)
+          x[u] = *((const uint4*)((const uint16_t*)p.a.q + (s.base + i) * p.a.q_row +
+                                  ((int64_t)s.h * p.G + (v - (i - s.i0) * p.G)) * p.a.q_head) + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kLanes; ++u) {
+        const int rr = u * (32 / kLanes) + lane / kLanes;
+        *(uint4*)(at + (c >> 3) * S::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[u];
       }
       tc::fence_async_smem();
       tc::fence_before();  // also: the last segment's accumulators have been read
@@ -679,7 +776,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
     for (int k = 0; k < mine; ++k) {
       const int t = s.t0 + (dual ? k : 2 * k + group);
       bool tree;
-      const int valid = tile_valid(p, s, t, tree);
+      const int valid = tile_valid(s, t, tree);
       uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
       const bool masked = tree || valid < kTile;
       if (tree && work) tree_bits(p, s, t - s.tp, f, live, bits);
@@ -695,19 +792,14 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       if (k > 0 && !tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
       tc::fence_after();
       if (work) {
+        if (masked) mask_scores(s_at, bits[0], bits[1], bits[2], bits[3]);
         uint32_t raw[64];
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           tc::tmem_ld64(s_at + hf * 64, raw);
-          if (masked) {
 #pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if (bits[2 * hf + (x >> 5)] >> (x & 31) & 1) top = fmaxf(top, __uint_as_float(raw[x]));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 64; ++x) top = fmaxf(top, __uint_as_float(raw[x]));
-          }
+          for (int x = 0; x < 64; x += 2) top = fmaxf(fmaxf(top, __uint_as_float(raw[x])), __uint_as_float(raw[x + 1]));
         }
         top *= p.c;
         if (k == 0) {
@@ -733,27 +825,19 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
         }
         const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
         float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
+        // both halves of S are read before P overwrites them: P's 64 columns lie over S's first half
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           tc::tmem_ld64(s_at + hf * 64, raw);
           uint32_t pk[32];
 #pragma unroll
           for (int x = 0; x < 64; x += 2) {
-            float a = ex2(fmaf(__uint_as_float(raw[x]), p.c, off)), b = ex2(fmaf(__uint_as_float(raw[x + 1]), p.c, off));
-            if (masked) {
-              if (!(bits[2 * hf + (x >> 5)] >> (x & 31) & 1)) a = 0.0f;
-              if (!(bits[2 * hf + (x >> 5)] >> ((x + 1) & 31) & 1)) b = 0.0f;
-            }
+            const float a = ex2(fmaf(__uint_as_float(raw[x]), p.c, off)), b = ex2(fmaf(__uint_as_float(raw[x + 1]), p.c, off));
             l0 += a;
             l1 += b;
             pk[x >> 1] = pack16<BF16>(a, b);
           }
-          // both halves of S are read before P overwrites the first: P's 64 columns lie over S's first half
-          if (hf == 0) {
-            tc::tmem_st32(s_at, pk);
-          } else {
-            tc::tmem_st32(s_at + 32, pk);
-          }
+          tc::tmem_st32(s_at + hf * 32, pk);
         }
         row.l += l0 + l1;
         tc::wait_st();
@@ -767,7 +851,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       tc::fence_after();
     }
     if (dual) {
-      finish_rows<DP, BF16>(p, sh, s, group, row, false, tm);
+      finish_rows<DP, BF16>(p, sh, s, group, row, false, tm, q_smem);
     } else if (group == 1) {
       if (mine > 0) {
         sh.ml[wl] = make_float2(row.m, row.l);
@@ -780,7 +864,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
         if (!tc::bar_wait_warp(&sh.mlready, nml++ & 1, &sh.stop)) return;
         tc::fence_after();
       }
-      finish_rows<DP, BF16>(p, sh, s, 0, row, other, tm);
+      finish_rows<DP, BF16>(p, sh, s, 0, row, other, tm, q_smem);
     }
   }
 }
@@ -811,6 +895,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc::bar_init(&sh.qready[g], kTile);
     }
     tc::bar_init(&sh.mlready, kTile);
+    for (int i = 0; i < kSegs; ++i) {
+      tc::bar_init(&sh.segfull[i], 1);
+      tc::bar_init(&sh.segempty[i], kSegReaders);
+    }
     tc::bar_init_fence();
     sh.stop = 0;
     sh.odd_values = 0;
@@ -1003,6 +1091,7 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   AttnParams p{};
   p.a = *a;
   p.G = a->H_q / a->H_kv;
+  p.g_magic = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
   while ((1 << p.page_shift) < a->page) ++p.page_shift;
   p.tree_box = 8;  // positions of a tree box: a power of two that covers P, up to a tile
   while (p.tree_box < a->P && p.tree_box < kTile) p.tree_box *= 2;
