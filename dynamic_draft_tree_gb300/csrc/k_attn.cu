@@ -40,9 +40,9 @@ constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves
                                 // small ones stay normal in fp16 for longer; it cancels in the quotient
 
 struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
-  int64_t per;     // tiles of a CTA
-  int64_t w_shared;
-  int32_t ts, mp_s, rows_s, pad;
+  int32_t per;     // units of a CTA
+  int32_t w_shared;
+  int32_t ts, mp_s;
 };
 
 struct AttnParams {
@@ -53,7 +53,7 @@ struct AttnParams {
   int32_t ns;         // tiles of the shared prefix
   int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
   AttnHead* head;
-  int64_t* t_pre;     // [B] tile offset of a request among the own tiles
+  int32_t* t_pre;     // [B] unit offset of a request among the own units
   int32_t* k_pre;     // [B] item offset
   float2* ml_own;     // [slot][own_rows] (m, l)
   float* o_own;       // [slot][own_rows][D]
@@ -83,9 +83,14 @@ __device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_sh
   return r;
 }
 
+// The line in units: an item of t tiles takes kItemCost + t of them, the first kItemCost standing for what an item costs
+// beside its tiles (its rows' loads, an empty pipeline, the rows' way out: about 6 us, a tile of two halves 2 us).
+constexpr int kItemCost = 3;
+
 // Items of a request for all key heads, tiles of one item.
 struct Extent {
   int mp, tp, tt;  // row blocks a head; prefix tiles, all tiles
+  __device__ __forceinline__ int units(int heads) const { return tt > 0 ? heads * mp * (tt + kItemCost) : 0; }
 };
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
   Extent e;
@@ -97,9 +102,9 @@ __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& 
 
 // A CTA's share and where it starts.
 struct Plan {
-  int64_t x0, x1;       // tiles [x0, x1) of the line
-  int64_t w_shared;
-  int64_t t_b;          // own tile offset of request b
+  int32_t x0, x1;       // units [x0, x1) of the line
+  int32_t w_shared;
+  int32_t t_b;          // own unit offset of request b
   int32_t b, k_b;       // first own request, its item offset
   int32_t ts, mp_s, rows_s;
 };
@@ -118,7 +123,7 @@ struct Segment {
 
 // One lane walks along the CTA's run.
 struct Walk {
-  int64_t x, t_b;
+  int x, t_b;
   int b, k_b;
   int loaded;           // request whose extent is held
   Request r;
@@ -131,61 +136,65 @@ struct Walk {
     k_b = pl.k_b;
     loaded = -1;
   }
+  // The next segment that has tiles (a run may end or begin inside an item's first units).
   __device__ __noinline__ void next(const AttnParams& p, const Plan& pl, Segment& s) {
-    s.t0 = s.t1 = 0;
-    if (x >= pl.x1) return;
-    int64_t item;
-    int tt;
-    if (x < pl.w_shared) {
-      tt = pl.ts;
-      item = x / tt;
-      s.shared = 1;
-      s.b = 0;
-      s.h = (int)(item / pl.mp_s);
-      s.mp = (int)item - s.h * pl.mp_s;
-      s.t0 = (int)(x - item * tt);
-      s.tp = tt;
-      s.len = p.a.shared_len;
-      s.tok0 = 0;
-      s.n = 0;
-      s.base = 0;
-      s.rows = min(kItemRows, pl.rows_s - s.mp * kItemRows);
-      s.slot = item + blockIdx.x;
-    } else {
-      const int64_t y = x - pl.w_shared;
-      while (true) {
-        if (b >= p.a.B) return;
-        if (loaded != b) {
-          r = request_of(p.a, p.page_shift, b);
-          e = extent_of(p, r);
-          loaded = b;
+    do {
+      s.t0 = s.t1 = 0;
+      if (x >= pl.x1) return;
+      int item, tt, at;  // item of its kind, its tiles, our place in its units
+      if (x < pl.w_shared) {
+        tt = pl.ts;
+        item = x / (tt + kItemCost);
+        at = x - item * (tt + kItemCost);
+        s.shared = 1;
+        s.b = 0;
+        s.h = item / pl.mp_s;
+        s.mp = item - s.h * pl.mp_s;
+        s.tp = tt;
+        s.len = p.a.shared_len;
+        s.tok0 = 0;
+        s.n = 0;
+        s.base = 0;
+        s.rows = min(kItemRows, pl.rows_s - s.mp * kItemRows);
+        s.slot = item + blockIdx.x;
+      } else {
+        const int y = x - pl.w_shared;
+        while (true) {
+          if (b >= p.a.B) return;
+          if (loaded != b) {
+            r = request_of(p.a, p.page_shift, b);
+            e = extent_of(p, r);
+            loaded = b;
+          }
+          const int w = e.units(p.a.H_kv);
+          if (y < t_b + w) break;
+          t_b += w;
+          k_b += p.a.H_kv * e.mp;
+          ++b;
         }
-        const int64_t w = (int64_t)p.a.H_kv * e.mp * e.tt;
-        if (y < t_b + w) break;
-        t_b += w;
-        k_b += p.a.H_kv * e.mp;
-        ++b;
+        tt = e.tt;
+        item = (y - t_b) / (tt + kItemCost);
+        at = y - t_b - item * (tt + kItemCost);
+        s.shared = 0;
+        s.b = b;
+        s.h = item / e.mp;
+        s.mp = item - s.h * e.mp;
+        s.tp = e.tp;
+        s.len = r.len;
+        s.tok0 = p.a.shared_len;
+        s.n = r.n;
+        s.base = r.base;
+        s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
+        s.slot = (int64_t)k_b + item + blockIdx.x;
       }
-      tt = e.tt;
-      item = (y - t_b) / tt;
-      s.shared = 0;
-      s.b = b;
-      s.h = (int)item / e.mp;
-      s.mp = (int)item - s.h * e.mp;
-      s.t0 = (int)(y - t_b - item * tt);
-      s.tp = e.tp;
-      s.len = r.len;
-      s.tok0 = p.a.shared_len;
-      s.n = r.n;
-      s.base = r.base;
-      s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
-      s.slot = k_b + item + blockIdx.x;
-    }
-    s.t1 = (int)min((int64_t)tt, s.t0 + pl.x1 - x);
-    s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
-    s.i0 = s.mp * kItemRows / p.G;
-    s.g0 = s.mp * kItemRows - s.i0 * p.G;
-    x += s.t1 - s.t0;
+      const int end = min(tt + kItemCost, at + pl.x1 - x);
+      x += end - at;
+      s.t0 = max(0, at - kItemCost);
+      s.t1 = max(0, end - kItemCost);
+      s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
+      s.i0 = s.mp * kItemRows / p.G;
+      s.g0 = s.mp * kItemRows - s.i0 * p.G;
+    } while (s.t1 == s.t0);
   }
 };
 
@@ -212,27 +221,26 @@ struct Shared {
   Segment seg[kSegs];
   float2 ml[kTile];
   Plan plan;
-  int64_t sums[2][12];
+  int32_t sums[2][12];
   uint32_t tmem;
   int stop, odd_values;
 };
 
-// The roles read the segments that warp 10 puts down, in order. `lead`: the thread that gives the place back.
+// The other warps read the segments that warp 10 puts down, in order. `lead`: the lane that gives the place back.
 struct Segments {
   uint32_t n = 0;
-  __device__ __forceinline__ bool next(Shared& sh, Segment& s, bool warp, bool lead) {
+  __device__ __forceinline__ bool next(Shared& sh, Segment& s, bool lead) {
     const int at = (int)(n % kSegs);
     const uint32_t parity = n / kSegs & 1;
     ++n;
-    if (warp ? !tc::bar_wait_warp(&sh.segfull[at], parity, &sh.stop) : !tc::bar_wait(&sh.segfull[at], parity, &sh.stop))
-      return false;
+    if (!tc::bar_wait_warp(&sh.segfull[at], parity, &sh.stop)) return false;
     s = sh.seg[at];
-    if (warp) __syncwarp();
+    __syncwarp();
     if (lead) tc::bar_arrive(&sh.segempty[at]);
     return s.t1 > s.t0;
   }
 };
-constexpr int kSegReaders = 11;  // eight softmax warps, two loading warps, the issuing thread
+constexpr int kSegReaders = 11;  // eight softmax warps, two loading warps, the issuing warp
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -252,26 +260,13 @@ __device__ __forceinline__ float unpack16(uint16_t x) {
 __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (p.a.B + kAttnThreads - 1) / kAttnThreads, b0 = tid * chunk, b1 = min(p.a.B, b0 + chunk);
-  int64_t tiles = 0, items = 0;
+  int units = 0, items = 0;
   for (int b = b0; b < b1; ++b) {
     const Request r = request_of(p.a, p.page_shift, b);
     const Extent e = extent_of(p, r);
-    tiles += (int64_t)p.a.H_kv * e.mp * e.tt;
+    units += e.units(p.a.H_kv);
     items += p.a.H_kv * e.mp;
     if (blockIdx.x == 0 && r.bad) set_status(p.status, DT_DEV_BAD_PAGE);
-  }
-  int64_t st = tiles, si = items;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t a = (int64_t)shfl_u64((uint64_t)st, max(lane - d, 0)), c = (int64_t)shfl_u64((uint64_t)si, max(lane - d, 0));
-    if (lane >= d) {
-      st += a;
-      si += c;
-    }
-  }
-  if (lane == 31) {
-    sh.sums[0][warp] = st;
-    sh.sums[1][warp] = si;
   }
   int64_t rows_used = (int64_t)p.a.B * p.a.P;
   if (p.a.row_off) {
@@ -279,21 +274,36 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     if (blockIdx.x == 0 && tid == 0 && (last < 0 || last > min(rows_used, p.a.rows))) set_status(p.status, DT_DEV_BAD_PAGE);
     rows_used = min(max(last, (int64_t)0), min(rows_used, p.a.rows));
   }
-  __syncthreads();
-  int64_t total = 0, t_b = st - tiles, k_b = si - items;
-  for (int w = 0; w < kAttnThreads / 32; ++w) {
-    if (w < warp) {
-      t_b += sh.sums[0][w];
-      k_b += sh.sums[1][w];
+  int su = units, si = items;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, su, d), c = __shfl_up_sync(0xFFFFFFFFu, si, d);
+    if (lane >= d) {
+      su += a;
+      si += c;
     }
-    total += sh.sums[0][w];
   }
-  const int64_t rows_s = p.ns ? rows_used * p.G : 0;
-  const int mp_s = (int)((rows_s + kItemRows - 1) / kItemRows);
-  const int64_t w_shared = (int64_t)p.a.H_kv * mp_s * p.ns;
+  if (lane == 31) {
+    sh.sums[0][warp] = su;
+    sh.sums[1][warp] = si;
+  }
+  __syncthreads();
+  int total = 0, t_b = su - units, k_b = si - items;
+#pragma unroll
+  for (int w = 0; w < kAttnThreads / 32; ++w) {
+    const int a = sh.sums[0][w], c = sh.sums[1][w];
+    if (w < warp) {
+      t_b += a;
+      k_b += c;
+    }
+    total += a;
+  }
+  const int rows_s = p.ns ? (int)rows_used * p.G : 0;
+  const int mp_s = (rows_s + kItemRows - 1) / kItemRows;
+  const int w_shared = p.ns ? p.a.H_kv * mp_s * (p.ns + kItemCost) : 0;
   total += w_shared;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t x0 = min(total, per * blockIdx.x), x1 = min(total, x0 + per);
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int x0 = min(total, per * (int)blockIdx.x), x1 = min(total, x0 + per);
   if (tid == 0) {
     Plan& pl = sh.plan;
     pl.x0 = x0;
@@ -301,30 +311,30 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     pl.w_shared = w_shared;
     pl.ts = p.ns;
     pl.mp_s = mp_s;
-    pl.rows_s = (int)min(rows_s, (int64_t)0x7FFFFFFF);
+    pl.rows_s = rows_s;
     if (x0 <= w_shared) {  // the own requests from the first
       pl.b = 0;
       pl.t_b = 0;
       pl.k_b = 0;
     }
-    if (blockIdx.x == 0) *p.head = AttnHead{per, w_shared, p.ns, mp_s, pl.rows_s, 0};
+    if (blockIdx.x == 0) *p.head = AttnHead{per, w_shared, p.ns, mp_s};
   }
-  const int64_t y0 = x0 - w_shared;
+  const int y0 = x0 - w_shared;
   for (int b = b0; b < b1; ++b) {
-    int64_t w = tiles, k = items;
+    int w = units, k = items;
     if (chunk > 1) {
       const Extent e = extent_of(p, request_of(p.a, p.page_shift, b));
-      w = (int64_t)p.a.H_kv * e.mp * e.tt;
+      w = e.units(p.a.H_kv);
       k = p.a.H_kv * e.mp;
     }
     if (y0 > 0 && t_b <= y0 && y0 < t_b + w) {
       sh.plan.b = b;
       sh.plan.t_b = t_b;
-      sh.plan.k_b = (int32_t)k_b;
+      sh.plan.k_b = k_b;
     }
     if (blockIdx.x == 0) {
       p.t_pre[b] = t_b;
-      p.k_pre[b] = (int32_t)k_b;
+      p.k_pre[b] = k_b;
     }
     t_b += w;
     k_b += k;
@@ -337,6 +347,7 @@ __device__ __forceinline__ void ring(uint32_t n, int& stage, uint32_t& parity) {
   stage = (int)(n % N);
   parity = (n / N) & 1;
 }
+
 
 // One warp loads the K (or V) tiles of the CTA's line in order.
 template <int DP, bool IS_K>
@@ -354,7 +365,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
   uint32_t n = 0;
   bool ok = true;
   const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
-  while (ok && segs.next(sh, s, true, lane == 0)) {
+  while (ok && segs.next(sh, s, lane == 0)) {
     const int32_t* table = p.a.block_table + (s.shared ? 0 : (int64_t)s.b * p.a.max_blocks);
     const int tok0 = s.tok0;
     // block id of this lane's box in tile t (-1: none)
@@ -414,78 +425,93 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
     }
 }
 
-// One thread issues the matrix instructions of the CTA's line.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// One warp issues the matrix instructions of the CTA's line, all lanes on one path and one thread elected for the
+// instructions themselves, so that descriptors stay in uniform registers.
 template <int DP, bool BF16>
-__device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+__device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int lane) {
   using S = Smem<DP>;
   constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false);
   constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
   const int steps = (p.a.D + 15) / 16;  // the padding elements of a row are zero
-  const uint32_t tm = sh.tmem;
+  const uint32_t tm = uniform(sh.tmem);
   // shared memory lies below 2^18 bytes, so offsets add up inside a descriptor's address field
-  const uint64_t q_desc = tc::smem_desc(q_smem, 16, 1024), k_desc = tc::smem_desc(k_smem, 16, 1024),
-                 v_desc = tc::smem_desc(v_smem, S::kHalf, 1024);
+  const uint64_t q_desc = tc::smem_desc(uniform(q_smem), 16, 1024), k_desc = tc::smem_desc(uniform(k_smem), 16, 1024),
+                 v_desc = tc::smem_desc(uniform(v_smem), S::kHalf, 1024);
+  const bool elected = tc::elect();
   Segments segs;
   Segment s;
-  uint32_t seen = 0;          // tiles of the segments before this one
-  uint32_t np[2] = {0, 0};    // units of each group so far (phase of pready)
-  uint32_t nq[2] = {0, 0};    // uses of each Q buffer
+  uint32_t kn = 0, vn = 0;    // K and V tiles so far
+  uint32_t np0 = 0, np1 = 0;  // units of each group so far (phase of pready)
+  uint32_t nq0 = 0, nq1 = 0;  // uses of each Q buffer
   uint32_t fix = 0;           // parity of every stage's vfix
-  while (segs.next(sh, s, false, true)) {
-    const bool dual = s.rows > kTile;
-    const int tiles = s.t1 - s.t0, units = dual ? 2 * tiles : tiles;
-    if (!tc::bar_wait(&sh.qready[0], nq[0]++ & 1, &sh.stop)) return;
-    if (dual && !tc::bar_wait(&sh.qready[1], nq[1]++ & 1, &sh.stop)) return;
+  while (segs.next(sh, s, lane == 0)) {
+    const bool dual = uniform(s.rows) > kTile;
+    const int t0 = uniform(s.t0), tp = s.shared ? 0x7FFFFFFF : uniform(s.tp), n = uniform(s.n), cached = uniform(s.len - s.tok0);
+    const int units = uniform(s.t1 - s.t0) << (dual ? 1 : 0);
+    if (!tc::bar_wait_warp(&sh.qready[0], nq0++ & 1, &sh.stop)) return;
+    if (dual && !tc::bar_wait_warp(&sh.qready[1], nq1++ & 1, &sh.stop)) return;
+    int t = t0;
     // O += P V of unit v - 2, then S of unit v
     for (int v = 0; v < units + 2; ++v) {
       const int g = v & 1;
       if (v >= 2) {
-        const int u = v - 2, k = dual ? u >> 1 : u;
         int stage;
         uint32_t parity;
-        ring<S::kStages>(seen + k, stage, parity);
-        bool tree;
-        const int valid = tile_valid(s, s.t0 + k, tree);
+        ring<S::kStages>(vn, stage, parity);
+        const bool tree = t >= tp;
+        const int valid = min(kTile, tree ? n - (t - tp) * kTile : cached - t * kTile);
         if (!dual || g == 0) {
-          if (!tc::bar_wait(&sh.vfull[stage], parity, &sh.stop)) return;
+          if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
           if (tree || valid < kTile) {
-            if (!tc::bar_wait(&sh.vfix[stage], fix >> stage & 1, &sh.stop)) return;
+            if (!tc::bar_wait_warp(&sh.vfix[stage], fix >> stage & 1, &sh.stop)) return;
             fix ^= 1u << stage;
           }
         }
         const uint64_t va = v_desc + (uint32_t)(stage * (S::kBlock >> 4));
         const uint32_t o = tm + 2 * kTile + g * DP, pr = tm + g * kTile;
-        if (!tc::bar_wait(&sh.pready[g], (g ? np[1]++ : np[0]++) & 1, &sh.stop)) return;
+        const uint32_t np = g ? np1++ : np0++;
+        if (!tc::bar_wait_warp(&sh.pready[g], np & 1, &sh.stop)) return;
         tc::fence_after();
-        tc::mma_ts(o, pr, va, kDescO, u >= 2);  // the group's first unit starts its accumulator
+        const bool last = !dual || g == 1;
+        if (elected) {
+          tc::mma_ts(o, pr, va, kDescO, v >= 4);  // the group's first unit starts its accumulator
 #pragma unroll
-        for (int x = 1; x < kTile / 16; ++x)
-          if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
-        tc::mma_commit(&sh.odone[g]);
-        if (!dual || g == 1) tc::mma_commit(&sh.vempty[stage]);
+          for (int x = 1; x < kTile / 16; ++x)
+            if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+          tc::mma_commit(&sh.odone[g]);
+          if (last) tc::mma_commit(&sh.vempty[stage]);
+        }
+        if (last) {
+          ++vn;
+          ++t;
+        }
       }
       if (v < units) {
-        const int k = dual ? v >> 1 : v;
         int stage;
         uint32_t parity;
-        ring<S::kStages>(seen + k, stage, parity);
+        ring<S::kStages>(kn, stage, parity);
         if (!dual || g == 0) {
-          if (!tc::bar_wait(&sh.kfull[stage], parity, &sh.stop)) return;
+          if (!tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
         }
         tc::fence_after();
         const uint64_t qa = q_desc + (uint32_t)((dual ? g : 0) * (S::kBlock >> 4)), ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
         const uint32_t d = tm + g * kTile;
-        tc::mma_ss(d, qa, ka, kDescS, false);
+        const bool last = !dual || g == 1;
+        if (elected) {
+          tc::mma_ss(d, qa, ka, kDescS, false);
 #pragma unroll
-        for (int x = 1; x < DP / 16; ++x) {
-          const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
-          if (x < steps) tc::mma_ss(d, qa + off, ka + off, kDescS, true);
+          for (int x = 1; x < DP / 16; ++x) {
+            const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
+            if (x < steps) tc::mma_ss(d, qa + off, ka + off, kDescS, true);
+          }
+          tc::mma_commit(&sh.sfull[g]);
+          if (last) tc::mma_commit(&sh.kempty[stage]);
         }
-        tc::mma_commit(&sh.sfull[g]);
-        if (!dual || g == 1) tc::mma_commit(&sh.kempty[stage]);
+        if (last) ++kn;
       }
     }
-    seen += tiles;
   }
 }
 
@@ -740,7 +766,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
   Segments segs;
   Segment s;
   uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
-  while (segs.next(sh, s, true, (threadIdx.x & 31) == 0)) {
+  while (segs.next(sh, s, (threadIdx.x & 31) == 0)) {
     const bool dual = s.rows > kTile;
     const int tiles = s.t1 - s.t0;
     const int mine = dual ? tiles : (tiles + 1 - group) / 2;
@@ -917,8 +943,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp == 8) {
     load_tiles<DP, true>(p, sh, &k_map, &kn_map, tc::smem_addr(k_smem), lane);
   } else if (warp == 9) {
-    if (lane == 0) issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem));
-    __syncwarp();
+    issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), lane);
   } else if (warp == 10) {
     fix_values<DP, BF16>(p, sh, v_smem, lane);
   } else {
@@ -945,55 +970,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ------------------------------------------------------------------------------- merge ----------
-// A CTA joins the partial results of one position, a warp a head at a time. Partials in the order of the line:
-// the shared prefix's first, then the request's own.
+// A warp joins the partial results of one position and head, in the order of the line: the shared prefix's parts, then
+// the request's own. Lanes take the (m, l) of up to 32 parts at once, then the parts' elements, four a lane.
+constexpr int kMergeWarps = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const AttnParams p) {
   pdl_begin();
-  const int i = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Request rq = request_of(p.a, p.page_shift, b);
-  if (i >= rq.n) return;
+  const int i = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
+  const int x = blockIdx.z * kMergeWarps + (threadIdx.x >> 5);
   const AttnHead hd = *p.head;
+  const int t_b = p.t_pre[b], k_b = p.k_pre[b];
+  const Request rq = request_of(p.a, p.page_shift, b);
+  if (i >= rq.n || x >= p.a.H_q) return;
   const Extent e = extent_of(p, rq);
-  const int64_t t_b = p.t_pre[b];
-  const int k_b = p.k_pre[b];
+  const int h = x / p.G, g = x - h * p.G;
+  const int f = i * p.G + g, item = h * e.mp + f / kItemRows;
+  const int u0 = hd.w_shared + t_b + item * (e.tt + kItemCost) + kItemCost;  // the item's first tile
+  const int c0 = u0 / hd.per, own = (u0 + e.tt - 1) / hd.per - c0 + 1;
+  if (!p.ns && own == 1) return;  // written by the segment itself
+  int is = 0, s0 = 0, parts_s = 0, fs = 0;
+  if (p.ns) {
+    const int64_t fl = (rq.base + i) * p.G + g;
+    is = h * hd.mp_s + (int)(fl / kItemRows);
+    fs = (int)(fl % kItemRows);
+    const int su = is * (hd.ts + kItemCost) + kItemCost;
+    s0 = su / hd.per;
+    parts_s = (su + hd.ts - 1) / hd.per - s0 + 1;
+  }
+  const int parts = parts_s + own;
+  // row of part k among the shared (first parts_s) or own partials
+  auto row_of = [&](int k) {
+    return k < parts_s ? ((int64_t)is + s0 + k) * kItemRows + fs
+                       : ((int64_t)k_b + item + c0 + k - parts_s) * p.own_rows + f % kItemRows;
+  };
   const int d = lane * 4;
-  for (int x = warp; x < p.a.H_q; x += 8) {
-    const int h = x / p.G, g = x - h * p.G;
-    const int f = i * p.G + g, item = h * e.mp + f / kItemRows;
-    const int64_t t0 = hd.w_shared + t_b + (int64_t)item * e.tt;
-    const int64_t c0 = t0 / hd.per, c1 = (t0 + e.tt - 1) / hd.per;
-    if (!p.ns && c0 == c1) continue;  // written by the segment itself
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-    auto join = [&](float2 ml, const float* src) {
-      if (ml.x == -INFINITY && !(ml.y != ml.y)) return;
-      const float4 v = d < p.a.D ? *(const float4*)(src + d) : make_float4(0, 0, 0, 0);
-      const float mm = fmaxf(m, ml.x), a = m == -INFINITY ? 0.0f : exp2f(m - mm), c = exp2f(ml.x - mm);
-      o.x = o.x * a + v.x * c;
-      o.y = o.y * a + v.y * c;
-      o.z = o.z * a + v.z * c;
-      o.w = o.w * a + v.w * c;
-      l = l * a + ml.y * c;
-      m = mm;
-    };
-    if (p.ns) {
-      const int64_t fs = (rq.base + i) * p.G + g, ms = fs / kItemRows;
-      const int64_t is = (int64_t)h * hd.mp_s + ms, s0 = is * hd.ts;
-      for (int64_t c = s0 / hd.per; c <= (s0 + hd.ts - 1) / hd.per; ++c) {
-        const int64_t at = (is + c) * kItemRows + fs - ms * kItemRows;
-        join(p.ml_sh[at], p.o_sh + at * p.a.D);
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0, 0, 0, 0);
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const int cnt = min(32, parts - k0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < cnt) ml = k0 + lane < parts_s ? p.ml_sh[row_of(k0 + lane)] : p.ml_own[row_of(k0 + lane)];
+    float top = fmaxf(m, ml.x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    // a part that attends to nothing has weight 0 (and l = 0); one with NaN keeps it
+    const float wgt = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+    float lw = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ml.y * wgt;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, s);
+    const float old = m == -INFINITY ? 0.0f : exp2f(m - top);
+    o.x *= old;
+    o.y *= old;
+    o.z *= old;
+    o.w *= old;
+    l = l * old + lw;
+    m = top;
+#pragma unroll 4
+    for (int k = 0; k < cnt; ++k) {
+      const float w = __shfl_sync(0xFFFFFFFFu, wgt, k);
+      if (d < p.a.D) {
+        const float* src = (k0 + k < parts_s ? p.o_sh : p.o_own) + row_of(k0 + k) * p.a.D + d;
+        const float4 v = *(const float4*)src;
+        o.x = fmaf(v.x, w, o.x);
+        o.y = fmaf(v.y, w, o.y);
+        o.z = fmaf(v.z, w, o.z);
+        o.w = fmaf(v.w, w, o.w);
       }
     }
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (k_b + item + c) * p.own_rows + f % kItemRows;
-      join(p.ml_own[at], p.o_own + at * p.a.D);
-    }
-    if (d < p.a.D) {
-      const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-      uint16_t* out = (uint16_t*)p.a.out + (rq.base + i) * p.a.o_row + (int64_t)x * p.a.o_head + d;
-      *(uint2*)out = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
-    }
+  }
+  if (d < p.a.D) {
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    uint16_t* out = (uint16_t*)p.a.out + (rq.base + i) * p.a.o_row + (int64_t)x * p.a.o_head + d;
+    *(uint2*)out = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
   }
 }
 
@@ -1016,7 +1064,7 @@ Layout layout_of(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, boo
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  L.t_pre = take(8ll * B);
+  L.t_pre = take(4ll * B);
   L.k_pre = take(4ll * B);
   L.ml_own = take(8 * L.own_slots * L.own_rows);
   L.o_own = take(4 * L.own_slots * L.own_rows * D);
@@ -1064,7 +1112,7 @@ cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cu
   launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  launch_k(attn_merge_kernel<BF16>, dim3(p.a.P, p.a.B), dim3(256), 0, s, p);
+  launch_k(attn_merge_kernel<BF16>, dim3(p.a.P, p.a.B, (p.a.H_q + kMergeWarps - 1) / kMergeWarps), dim3(32 * kMergeWarps), 0, s, p);
   return cudaGetLastError();
 }
 
@@ -1102,7 +1150,7 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.own_slots = L.own_slots;
   p.own_rows = L.own_rows;
   p.head = (AttnHead*)ws;
-  p.t_pre = (int64_t*)(ws + L.t_pre);
+  p.t_pre = (int32_t*)(ws + L.t_pre);
   p.k_pre = (int32_t*)(ws + L.k_pre);
   p.ml_own = (float2*)(ws + L.ml_own);
   p.o_own = (float*)(ws + L.o_own);

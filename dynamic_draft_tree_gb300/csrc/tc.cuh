@@ -150,6 +150,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
 }
 
 // ----------------------------------------------------------------- matrix instructions ----------
+// True in one thread of the (whole) warp. Code that only branches on this keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
 // Shared-memory operand in 128-byte rows swizzled in groups of eight (1024 bytes). K-major: groups of eight rows
 // `sbo` bytes apart. MN-major: a group is 64 elements of the outer dimension by eight of K; groups along K are
 // `sbo` apart, along the outer dimension `lbo`.
