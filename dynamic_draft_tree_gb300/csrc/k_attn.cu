@@ -216,10 +216,10 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vfix[4];
-  uint64_t sfull[2], pready[2], odone[2], qready[2], mlready;
+  uint64_t sfull[2], phalf[2][2], odone[2], qready[2], mlready;
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
-  float2 ml[kTile];
+  float2 ml[2][kTile];
   Plan plan;
   int32_t sums[2][12];
   uint32_t tmem;
@@ -443,7 +443,7 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint
   Segments segs;
   Segment s;
   uint32_t kn = 0, vn = 0;    // K and V tiles so far
-  uint32_t np0 = 0, np1 = 0;  // units of each group so far (phase of pready)
+  uint32_t np0 = 0, np1 = 0;  // units of each group so far (phase of phalf)
   uint32_t nq0 = 0, nq1 = 0;  // uses of each Q buffer
   uint32_t fix = 0;           // parity of every stage's vfix
   while (segs.next(sh, s, lane == 0)) {
@@ -472,13 +472,21 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint
         const uint64_t va = v_desc + (uint32_t)(stage * (S::kBlock >> 4));
         const uint32_t o = tm + 2 * kTile + g * DP, pr = tm + g * kTile;
         const uint32_t np = g ? np1++ : np0++;
-        if (!tc::bar_wait_warp(&sh.pready[g], np & 1, &sh.stop)) return;
-        tc::fence_after();
         const bool last = !dual || g == 1;
+        // the first half's products run while the group works on the second half's weights
+        if (!tc::bar_wait_warp(&sh.phalf[g][0], np & 1, &sh.stop)) return;
+        tc::fence_after();
         if (elected) {
           tc::mma_ts(o, pr, va, kDescO, v >= 4);  // the group's first unit starts its accumulator
 #pragma unroll
-          for (int x = 1; x < kTile / 16; ++x)
+          for (int x = 1; x < kTile / 32; ++x)
+            if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+        }
+        if (!tc::bar_wait_warp(&sh.phalf[g][1], np & 1, &sh.stop)) return;
+        tc::fence_after();
+        if (elected) {
+#pragma unroll
+          for (int x = kTile / 32; x < kTile / 16; ++x)
             if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
           tc::mma_commit(&sh.odone[g]);
           if (last) tc::mma_commit(&sh.vempty[stage]);
@@ -675,16 +683,17 @@ __device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segmen
   for (int k = 0; k < 32; ++k) o[k] = x[k];
 }
 
-// The segment's rows of a softmax group leave tensor memory. `other`: the second group's accumulator is joined.
+// The segment's rows of a softmax group leave tensor memory. `both`: the two groups hold parts of the same rows, and this
+// one takes the even (group 0) or odd blocks of 32 elements.
 template <int DP, bool BF16>
-__device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool other, uint32_t tm,
+__device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool both, uint32_t tm,
                             uint8_t* q_smem) {
   const int wl = threadIdx.x & 127;         // row of the group
   const int r = (s.rows > kTile ? group * kTile : 0) + wl;
   const bool live = r < s.rows;
   float f0 = 1.0f, f1 = 0.0f, m = row.m, l = row.l;
-  if (other) {
-    const float2 o = sh.ml[wl];
+  if (both) {
+    const float2 o = sh.ml[group ^ 1][wl];
     m = fmaxf(row.m, o.x);
     f0 = row.m == -INFINITY ? 0.0f : exp2f(row.m - m);
     f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - m);
@@ -693,7 +702,7 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   const int f = s.mp * kItemRows + r;
   const bool odd = *(volatile int*)&sh.odd_values && !s.shared && s.t1 > s.tp;
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // nothing attended to: zeros; NaN stays
-  if (live && !s.whole) {
+  if (live && !s.whole && !(both && group == 1)) {
     if (s.shared)
       p.ml_sh[s.slot * kItemRows + r] = make_float2(m, l);
     else
@@ -710,13 +719,13 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   const int log_lanes = s.whole ? 2 : 3;    // lanes along 32 elements of a row: of the result, of partials
   const int c = lane & ((1 << log_lanes) - 1);
 #pragma unroll 1
-  for (int d0 = 0; d0 < p.a.D; d0 += 32) {
+  for (int d0 = both ? 32 * group : 0; d0 < p.a.D; d0 += both ? 64 : 32) {
     uint32_t raw[32];
     float o[32];
     tc::tmem_ld32(tm + lanes + 2 * kTile + group * DP + d0, raw);
 #pragma unroll
     for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(raw[k]) * f0;
-    if (other) {
+    if (both) {
       tc::tmem_ld32(tm + lanes + 2 * kTile + (group ^ 1) * DP + d0, raw);
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(raw[k]), f1, o[k]);
@@ -773,7 +782,9 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
     const int r0 = dual ? group * kTile : 0;  // the group's first row of the item
     const int r = r0 + wl, f = s.mp * kItemRows + r;
     const bool live = r < s.rows;
-    if (dual || group == 0) {
+    if (!dual && group == 1) {
+      tc::bar_arrive(&sh.qready[0]);  // done with the last segment's accumulators
+    } else {
       // the warp's 32 Q rows into the swizzled layout, 16 bytes a lane along the rows, zeros past the end and D
       uint8_t* at = q_smem + group * S::kBlock + (wl >> 5) * 32 * 128;
       constexpr int kLanes = DP / 8;  // lanes of a row
@@ -796,6 +807,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       tc::fence_async_smem();
       tc::fence_before();  // also: the last segment's accumulators have been read
       tc::bar_arrive(&sh.qready[group]);
+      if (group == 1) tc::bar_arrive(&sh.qready[0]);
     }
     Row row{-INFINITY, 0.0f};
     const bool work = __any_sync(0xFFFFFFFFu, live);
@@ -850,48 +862,47 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
           }
         }
         const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
-        float l0 = 0.0f, l1 = 0.0f;
-        // both halves of S are read before P overwrites them: P's 64 columns lie over S's first half
+        const float2 c2 = make_float2(p.c, p.c), off2 = make_float2(off, off);
+        float2 l2 = make_float2(0.0f, 0.0f);
+        // P's 64 columns lie over S's first half: the second half of S is read before P reaches it
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           tc::tmem_ld64(s_at + hf * 64, raw);
           uint32_t pk[32];
 #pragma unroll
           for (int x = 0; x < 64; x += 2) {
-            const float a = ex2(fmaf(__uint_as_float(raw[x]), p.c, off)), b = ex2(fmaf(__uint_as_float(raw[x + 1]), p.c, off));
-            l0 += a;
-            l1 += b;
-            pk[x >> 1] = pack16<BF16>(a, b);
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[x]), __uint_as_float(raw[x + 1])), c2, off2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            l2 = __fadd2_rn(l2, e);
+            pk[x >> 1] = pack16<BF16>(e.x, e.y);
           }
           tc::tmem_st32(s_at + hf * 32, pk);
+          tc::wait_st();
+          tc::fence_before();
+          tc::bar_arrive(&sh.phalf[group][hf]);
         }
-        row.l += l0 + l1;
-        tc::wait_st();
+        row.l += l2.x + l2.y;
+      } else {
+        tc::fence_before();
+        tc::bar_arrive(&sh.phalf[group][0]);
+        tc::bar_arrive(&sh.phalf[group][1]);
       }
-      tc::fence_before();
-      tc::bar_arrive(&sh.pready[group]);
     }
     // the group's last product
     if (mine > 0) {
       if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
       tc::fence_after();
     }
-    if (dual) {
-      finish_rows<DP, BF16>(p, sh, s, group, row, false, tm, q_smem);
-    } else if (group == 1) {
-      if (mine > 0) {
-        sh.ml[wl] = make_float2(row.m, row.l);
-        tc::fence_before();
-        tc::bar_arrive(&sh.mlready);
-      }
-    } else {
-      const bool other = tiles > 1;
-      if (other) {
-        if (!tc::bar_wait_warp(&sh.mlready, nml++ & 1, &sh.stop)) return;
-        tc::fence_after();
-      }
-      finish_rows<DP, BF16>(p, sh, s, 0, row, other, tm, q_smem);
+    if (!dual && tiles > 1) {
+      // both groups hold sums over the same rows: each takes half of the elements of the joined ones
+      sh.ml[group][wl] = make_float2(row.m, row.l);
+      tc::fence_before();
+      tc::bar_arrive(&sh.mlready);
+      if (!tc::bar_wait_warp(&sh.mlready, nml++ & 1, &sh.stop)) return;
+      tc::fence_after();
     }
+    if (dual || tiles > 1 || group == 0) finish_rows<DP, BF16>(p, sh, s, group, row, !dual && tiles > 1, tm, q_smem);
   }
 }
 
@@ -916,11 +927,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       tc::bar_init(&sh.sfull[g], 1);
-      tc::bar_init(&sh.pready[g], kTile);
+      tc::bar_init(&sh.phalf[g][0], kTile);
+      tc::bar_init(&sh.phalf[g][1], kTile);
       tc::bar_init(&sh.odone[g], 1);
-      tc::bar_init(&sh.qready[g], kTile);
+      tc::bar_init(&sh.qready[g], g == 0 ? 2 * kTile : kTile);
     }
-    tc::bar_init(&sh.mlready, kTile);
+    tc::bar_init(&sh.mlready, 2 * kTile);
     for (int i = 0; i < kSegs; ++i) {
       tc::bar_init(&sh.segfull[i], 1);
       tc::bar_init(&sh.segempty[i], kSegReaders);
