@@ -33,7 +33,7 @@ namespace dt {
 namespace {
 
 constexpr int kTile = 128;      // tokens of a tile, rows of a group
-constexpr int kItemRows = 256;  // rows of an item
+constexpr int kItemRows = 256;  // rows of an item, at most (whole positions: 2 * (128 / G) * G)
 constexpr int kAttnThreads = 384;
 constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes it by 2^kLazy
 constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
@@ -48,7 +48,8 @@ struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
 struct AttnParams {
   dt_attn_args a;
   int32_t G, page_shift, tree_box;
-  uint32_t g_magic;   // ceil(2^32 / G): x / G = umulhi(x, g_magic) for x < 2^25 (exact, as x (g_magic G - 2^32) < 2^32)
+  int32_t pos, rows2; // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
+  uint32_t g_magic;   // ceil(2^32 / G), for position_of
   float c;            // scale * log2 e
   int32_t ns;         // tiles of the shared prefix
   int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
@@ -61,6 +62,11 @@ struct AttnParams {
   float* o_sh;
   int32_t* status;
 };
+
+// x / G for a row x < 256 of an item: exact, as x (g_magic G - 2^32) < 2^32.
+__device__ __forceinline__ int position_of(const AttnParams& p, int x) {
+  return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.g_magic);
+}
 
 struct Request {
   int len, n;      // cached tokens, positions
@@ -94,7 +100,7 @@ struct Extent {
 };
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
   Extent e;
-  e.mp = (r.n * p.G + kItemRows - 1) / kItemRows;
+  e.mp = (r.n + 2 * p.pos - 1) / (2 * p.pos);
   e.tp = (r.len - p.a.shared_len + kTile - 1) / kTile;
   e.tt = r.n > 0 ? e.tp + (r.n + kTile - 1) / kTile : 0;
   return e;
@@ -116,7 +122,7 @@ struct Segment {
   int tp, len, tok0;    // prefix tiles, their end and the first one's token
   int n;                // positions (0 for the shared prefix)
   int rows;             // rows of the item
-  int i0, g0;           // position and head of its row 0
+  int i0;               // position of its first rows
   int64_t base;         // row of the first position
   int64_t slot;
 };
@@ -137,7 +143,7 @@ struct Walk {
     loaded = -1;
   }
   // The next segment that has tiles (a run may end or begin inside an item's first units).
-  __device__ __noinline__ void next(const AttnParams& p, const Plan& pl, Segment& s) {
+  __device__ __forceinline__ void next(const AttnParams& p, const Plan& pl, Segment& s) {
     do {
       s.t0 = s.t1 = 0;
       if (x >= pl.x1) return;
@@ -155,7 +161,7 @@ struct Walk {
         s.tok0 = 0;
         s.n = 0;
         s.base = 0;
-        s.rows = min(kItemRows, pl.rows_s - s.mp * kItemRows);
+        s.rows = min(p.rows2, pl.rows_s - s.mp * p.rows2);
         s.slot = item + blockIdx.x;
       } else {
         const int y = x - pl.w_shared;
@@ -184,7 +190,7 @@ struct Walk {
         s.tok0 = p.a.shared_len;
         s.n = r.n;
         s.base = r.base;
-        s.rows = min(kItemRows, r.n * p.G - s.mp * kItemRows);
+        s.rows = min(p.rows2, r.n * p.G - s.mp * p.rows2);
         s.slot = (int64_t)k_b + item + blockIdx.x;
       }
       const int end = min(tt + kItemCost, at + pl.x1 - x);
@@ -192,8 +198,7 @@ struct Walk {
       s.t0 = max(0, at - kItemCost);
       s.t1 = max(0, end - kItemCost);
       s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
-      s.i0 = s.mp * kItemRows / p.G;
-      s.g0 = s.mp * kItemRows - s.i0 * p.G;
+      s.i0 = s.mp * 2 * p.pos;
     } while (s.t1 == s.t0);
   }
 };
@@ -216,7 +221,7 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vfix[4];
-  uint64_t sfull[2], phalf[2][2], odone[2], qready[2], mlready;
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready;
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   float2 ml[2][kTile];
@@ -299,7 +304,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     total += a;
   }
   const int rows_s = p.ns ? (int)rows_used * p.G : 0;
-  const int mp_s = (rows_s + kItemRows - 1) / kItemRows;
+  const int mp_s = (rows_s + p.rows2 - 1) / p.rows2;
   const int w_shared = p.ns ? p.a.H_kv * mp_s * (p.ns + kItemCost) : 0;
   total += w_shared;
   const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -430,7 +435,7 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, 
 // One warp issues the matrix instructions of the CTA's line, all lanes on one path and one thread elected for the
 // instructions themselves, so that descriptors stay in uniform registers.
 template <int DP, bool BF16>
-__device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int lane) {
+__device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_map, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int lane) {
   using S = Smem<DP>;
   constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false);
   constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
@@ -444,14 +449,24 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, uint32_t q_smem, uint
   Segment s;
   uint32_t kn = 0, vn = 0;    // K and V tiles so far
   uint32_t np0 = 0, np1 = 0;  // units of each group so far (phase of phalf)
-  uint32_t nq0 = 0, nq1 = 0;  // uses of each Q buffer
+  uint32_t nq = 0;            // segments so far
   uint32_t fix = 0;           // parity of every stage's vfix
   while (segs.next(sh, s, lane == 0)) {
-    const bool dual = uniform(s.rows) > kTile;
+    const bool dual = uniform(s.rows) > p.rows2 >> 1;
     const int t0 = uniform(s.t0), tp = s.shared ? 0x7FFFFFFF : uniform(s.tp), n = uniform(s.n), cached = uniform(s.len - s.tok0);
     const int units = uniform(s.t1 - s.t0) << (dual ? 1 : 0);
-    if (!tc::bar_wait_warp(&sh.qready[0], nq0++ & 1, &sh.stop)) return;
-    if (dual && !tc::bar_wait_warp(&sh.qready[1], nq1++ & 1, &sh.stop)) return;
+    // The rows of Q, once both groups are through with the last segment's (and its accumulators): whole positions of
+    // G heads. Rows past the item's belong to other positions or lie past the buffer (zeros); nobody reads theirs.
+    if (!tc::bar_wait_warp(&sh.qfree, (nq & 1) ^ 1, &sh.stop)) return;
+    if (elected) {
+      constexpr int kHalves = DP / 64;
+      const int groups = dual ? 2 : 1, bytes = p.pos * p.G * 128;
+      tc::bar_expect(&sh.qfull, groups * kHalves * bytes);
+      for (int x = 0; x < groups * kHalves; ++x)
+        tc::tma_load_3d(q_smem + x * S::kHalf, q_map, (x % kHalves) * 64, s.h * p.G, (int)s.base + s.i0 + x / kHalves * p.pos,
+                        &sh.qfull);
+    }
+    if (!tc::bar_wait_warp(&sh.qfull, nq++ & 1, &sh.stop)) return;
     int t = t0;
     // O += P V of unit v - 2, then S of unit v
     for (int v = 0; v < units + 2; ++v) {
@@ -548,11 +563,13 @@ __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int
     __syncwarp();
     return true;
   };
-  if (!put_next()) return;
-  for (uint32_t seg = 0;; ++seg) {
-    s = sh.seg[seg % kSegs];  // not written again before this warp puts down kSegs more
-    if (s.t1 == s.t0) return;
+  for (int seg = -1;; ++seg) {
+    if (seg >= 0) {
+      s = sh.seg[seg % kSegs];  // not written again before this warp puts down kSegs more
+      if (s.t1 == s.t0) return;
+    }
     if (!put_next()) return;
+    if (seg < 0) continue;
     for (int t = s.t0; t < s.t1; ++t, ++n) {
       bool tree;
       const int valid = tile_valid(s, t, tree);
@@ -607,9 +624,9 @@ struct Row {
   float m, l;  // reference maximum (log2 units), sum of weights
 };
 
-// The 128 tree columns that row `f` of the item attends to in tree tile jt, as bits; all lanes of the warp.
-__device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s, int jt, int f, bool live, uint32_t* bits) {
-  const int lane = threadIdx.x & 31, j0 = jt * kTile, i = live ? f / p.G : -1;
+// The 128 tree columns that position i (-1: none) attends to in tree tile jt, as bits; all lanes of the warp.
+__device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s, int jt, int i, uint32_t* bits) {
+  const int lane = threadIdx.x & 31, j0 = jt * kTile;
   bits[0] = bits[1] = bits[2] = bits[3] = 0;
   if (!p.a.mask) {
 #pragma unroll
@@ -652,9 +669,8 @@ __device__ __noinline__ void mask_scores(uint32_t s_at, uint32_t b0, uint32_t b1
 
 // Values that are no numbers at tree positions this row attends to: weight times value, from global memory.
 template <bool BF16>
-__device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int64_t base, int j0, int j1, int f, float m,
-                                         int d0, float* o) {
-  const int i = f / p.G, g = f - i * p.G;
+__device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int64_t base, int j0, int j1, int i, int g,
+                                         float m, float scale, int d0, float* o) {
   const uint16_t* q = (const uint16_t*)p.a.q + (base + i) * p.a.q_row + ((int64_t)h * p.G + g) * p.a.q_head;
   for (int j = j0; j < j1; ++j) {
     if (p.a.mask ? p.a.mask[((int64_t)b * p.a.P + i) * p.a.P + j] == 0 : j > i) continue;
@@ -668,17 +684,19 @@ __device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int6
     const float wgt = exp2f(dot * p.c - m + kShift);
     for (int d = 0; d < min(32, p.a.D - d0); ++d) {
       const float x = unpack16<BF16>(v[d0 + d]);
-      if (!isfinite(x)) o[d] += wgt * x;
+      if (!isfinite(x)) o[d] += wgt * x * scale;
     }
   }
 }
 
 template <int DP, bool BF16>
-__device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segment& s, int f, float m, int d0, float (&o)[32]) {
+__device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segment& s, int r, float m, float scale, int d0,
+                                               float (&o)[32]) {
   float x[32];  // its own array: one whose address is taken does not stay in registers
 #pragma unroll
   for (int k = 0; k < 32; ++k) x[k] = o[k];
-  add_odd_row<BF16>(p, s.b, s.h, s.base, (max(s.t0, s.tp) - s.tp) * kTile, min(s.n, (s.t1 - s.tp) * kTile), f, m, d0, x);
+  add_odd_row<BF16>(p, s.b, s.h, s.base, (max(s.t0, s.tp) - s.tp) * kTile, min(s.n, (s.t1 - s.tp) * kTile), s.i0 + r / p.G,
+                    r % p.G, m, scale, d0, x);
 #pragma unroll
   for (int k = 0; k < 32; ++k) o[k] = x[k];
 }
@@ -688,9 +706,10 @@ __device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segmen
 template <int DP, bool BF16>
 __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, int group, Row row, bool both, uint32_t tm,
                             uint8_t* q_smem) {
-  const int wl = threadIdx.x & 127;         // row of the group
-  const int r = (s.rows > kTile ? group * kTile : 0) + wl;
-  const bool live = r < s.rows;
+  const int wl = threadIdx.x & 127, lane = wl & 31, half = p.rows2 >> 1;
+  const int r = (s.rows > half ? group * half : 0) + wl;  // row of the item
+  const bool live = r < s.rows && wl < half;
+  if (!__any_sync(0xFFFFFFFFu, live)) return;
   float f0 = 1.0f, f1 = 0.0f, m = row.m, l = row.l;
   if (both) {
     const float2 o = sh.ml[group ^ 1][wl];
@@ -699,65 +718,69 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
     f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - m);
     l = row.l * f0 + o.y * f1;
   }
-  const int f = s.mp * kItemRows + r;
   const bool odd = *(volatile int*)&sh.odd_values && !s.shared && s.t1 > s.tp;
-  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // nothing attended to: zeros; NaN stays
-  if (live && !s.whole && !(both && group == 1)) {
-    if (s.shared)
-      p.ml_sh[s.slot * kItemRows + r] = make_float2(m, l);
-    else
-      p.ml_own[s.slot * p.own_rows + r] = make_float2(m, l);
-  }
-  const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
-  if (!__any_sync(0xFFFFFFFFu, live)) return;
-  // Through the warp's own 32 rows of the Q buffer (its products are done), 32 elements a turn, so that lanes store
-  // along rows.
-  const int lane = wl & 31;
+  // 16-byte stores along rows, through the warp's own 32 rows of the Q buffer (its products are done), 32 elements of a
+  // row a turn: four lanes a row of the result, eight of a partial.
+  const int row0 = r - lane, end = min(s.rows - row0, min(32, half - (wl - lane)));  // the warp's first row, its live rows
   uint8_t* stage = q_smem + group * Smem<DP>::kBlock + (wl >> 5) * 32 * 128;
-  const int row0 = r - lane;                // the warp's first row of the item
-  const float scale = s.whole ? inv : 1.0f;
-  const int log_lanes = s.whole ? 2 : 3;    // lanes along 32 elements of a row: of the result, of partials
-  const int c = lane & ((1 << log_lanes) - 1);
+  const uint32_t o_at = tm + ((uint32_t)(threadIdx.x & 96) << 16) + 2 * kTile;
+  float* part = nullptr;
+  uint16_t* out[4];
+  const float inv = !s.whole ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // nothing attended to: zeros; NaN stays
+  if (s.whole) {
+    f0 *= inv;
+    f1 *= inv;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int ri = row0 + u * 8 + (lane >> 2), i = position_of(p, ri);
+      out[u] = (uint16_t*)p.a.out + (s.base + s.i0 + i) * p.a.o_row + ((int64_t)s.h * p.G + ri - i * p.G) * p.a.o_head + (lane & 3) * 8;
+    }
+  } else {
+    const int64_t at = s.shared ? s.slot * kItemRows : s.slot * p.own_rows;
+    if (live && !(both && group == 1)) (s.shared ? p.ml_sh : p.ml_own)[at + r] = make_float2(m, l);
+    part = (s.shared ? p.o_sh : p.o_own) + (at + row0 + (lane >> 3)) * p.a.D + (lane & 7) * 4;
+  }
 #pragma unroll 1
   for (int d0 = both ? 32 * group : 0; d0 < p.a.D; d0 += both ? 64 : 32) {
     uint32_t raw[32];
     float o[32];
-    tc::tmem_ld32(tm + lanes + 2 * kTile + group * DP + d0, raw);
+    tc::tmem_ld32(o_at + group * DP + d0, raw);
 #pragma unroll
     for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(raw[k]) * f0;
     if (both) {
-      tc::tmem_ld32(tm + lanes + 2 * kTile + (group ^ 1) * DP + d0, raw);
+      tc::tmem_ld32(o_at + (group ^ 1) * DP + d0, raw);
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(raw[k]), f1, o[k]);
     }
-    if (odd && live) add_odd_values<DP, BF16>(p, s, f, m == -INFINITY ? 0.0f : m, d0, o);
+    if (odd && live) add_odd_values<DP, BF16>(p, s, r, m == -INFINITY ? 0.0f : m, inv, d0, o);
     if (s.whole) {
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
         *(uint4*)(stage + lane * 128 + (((k / 8) ^ (lane & 7)) << 4)) =
-            make_uint4(pack16<BF16>(o[k] * scale, o[k + 1] * scale), pack16<BF16>(o[k + 2] * scale, o[k + 3] * scale),
-                       pack16<BF16>(o[k + 4] * scale, o[k + 5] * scale), pack16<BF16>(o[k + 6] * scale, o[k + 7] * scale));
+            make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]), pack16<BF16>(o[k + 4], o[k + 5]),
+                       pack16<BF16>(o[k + 6], o[k + 7]));
     } else {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *(float4*)(stage + lane * 128 + (((k / 4) ^ (lane & 7)) << 4)) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
     }
     __syncwarp();
-    const int d = d0 + (c << (s.whole ? 3 : 2));
-#pragma unroll 1
-    for (int r4 = 0; r4 < 32; r4 += 16) {
-      // sixteen rows of 16-byte pieces: two (result) or four (partials) of them a lane
+    if (s.whole) {
+      const int c = lane & 3;
+      if (d0 + c * 8 < p.a.D) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int rr = r4 + (u << (5 - log_lanes)) + (lane >> log_lanes), ri = row0 + rr;
-        if ((u << (5 - log_lanes)) < 16 && ri < s.rows && d < p.a.D) {
-          const uint4 x = *(const uint4*)(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
-          if (s.whole) {
-            const int v = s.g0 + ri, i = s.i0 + (int)__umulhi((uint32_t)v, p.g_magic);
-            *(uint4*)((uint16_t*)p.a.out + (s.base + i) * p.a.o_row + ((int64_t)s.h * p.G + (v - (i - s.i0) * p.G)) * p.a.o_head + d) = x;
-          } else {
-            *(uint4*)((s.shared ? p.o_sh + (s.slot * kItemRows + ri) * p.a.D : p.o_own + (s.slot * p.own_rows + ri) * p.a.D) + d) = x;
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int rr = u * 8 + (lane >> 2);
+          if (rr < end) *(uint4*)(out[u] + d0) = *(const uint4*)(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+        }
+      }
+    } else {
+      const int c = lane & 7;
+      if (d0 + c * 4 < p.a.D) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int rr = u * 4 + (lane >> 3);
+          if (rr < end) *(uint4*)(part + u * 4 * p.a.D + d0) = *(const uint4*)(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
         }
       }
     }
@@ -765,7 +788,7 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   }
 }
 
-// A group of 128 threads: loads its Q rows, then turns every S of its units into weights.
+// A group of 128 threads turns every S of its units into weights.
 template <int DP, bool BF16>
 __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, int group) {
   using S = Smem<DP>;
@@ -776,39 +799,11 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
   Segment s;
   uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
   while (segs.next(sh, s, (threadIdx.x & 31) == 0)) {
-    const bool dual = s.rows > kTile;
+    const bool dual = s.rows > p.rows2 >> 1;
     const int tiles = s.t1 - s.t0;
     const int mine = dual ? tiles : (tiles + 1 - group) / 2;
-    const int r0 = dual ? group * kTile : 0;  // the group's first row of the item
-    const int r = r0 + wl, f = s.mp * kItemRows + r;
-    const bool live = r < s.rows;
-    if (!dual && group == 1) {
-      tc::bar_arrive(&sh.qready[0]);  // done with the last segment's accumulators
-    } else {
-      // the warp's 32 Q rows into the swizzled layout, 16 bytes a lane along the rows, zeros past the end and D
-      uint8_t* at = q_smem + group * S::kBlock + (wl >> 5) * 32 * 128;
-      constexpr int kLanes = DP / 8;  // lanes of a row
-      const int lane = wl & 31, c = lane % kLanes;
-      uint4 x[kLanes];
-#pragma unroll
-      for (int u = 0; u < kLanes; ++u) {
-        const int rr = u * (32 / kLanes) + lane / kLanes, ri = r0 + (wl & 96) + rr;
-        const int v = s.g0 + ri, i = s.i0 + (int)__umulhi((uint32_t)v, p.g_magic);
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (ri < s.rows && c * 8 < p.a.D)
-          x[u] = *((const uint4*)((const uint16_t*)p.a.q + (s.base + i) * p.a.q_row +
-                                  ((int64_t)s.h * p.G + (v - (i - s.i0) * p.G)) * p.a.q_head) + c);
-      }
-#pragma unroll
-      for (int u = 0; u < kLanes; ++u) {
-        const int rr = u * (32 / kLanes) + lane / kLanes;
-        *(uint4*)(at + (c >> 3) * S::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[u];
-      }
-      tc::fence_async_smem();
-      tc::fence_before();  // also: the last segment's accumulators have been read
-      tc::bar_arrive(&sh.qready[group]);
-      if (group == 1) tc::bar_arrive(&sh.qready[0]);
-    }
+    const int r = (dual ? group * (p.rows2 >> 1) : 0) + wl;  // this thread's row of the item
+    const bool live = r < s.rows && wl < p.rows2 >> 1;
     Row row{-INFINITY, 0.0f};
     const bool work = __any_sync(0xFFFFFFFFu, live);
     for (int k = 0; k < mine; ++k) {
@@ -817,7 +812,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       const int valid = tile_valid(s, t, tree);
       uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
       const bool masked = tree || valid < kTile;
-      if (tree && work) tree_bits(p, s, t - s.tp, f, live, bits);
+      if (tree && work) tree_bits(p, s, t - s.tp, live ? s.i0 + position_of(p, r) : -1, bits);
       if (masked) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -903,12 +898,15 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       tc::fence_after();
     }
     if (dual || tiles > 1 || group == 0) finish_rows<DP, BF16>(p, sh, s, group, row, !dual && tiles > 1, tm, q_smem);
+    tc::fence_async_smem();  // the Q rows' memory, written and read above, goes to the next load
+    tc::fence_before();
+    tc::bar_arrive(&sh.qfree);
   }
 }
 
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+    attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map) {
   using S = Smem<DP>;
   extern __shared__ uint8_t dyn[];
@@ -930,8 +928,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc::bar_init(&sh.phalf[g][0], kTile);
       tc::bar_init(&sh.phalf[g][1], kTile);
       tc::bar_init(&sh.odone[g], 1);
-      tc::bar_init(&sh.qready[g], g == 0 ? 2 * kTile : kTile);
     }
+    tc::bar_init(&sh.qfull, 1);
+    tc::bar_init(&sh.qfree, 2 * kTile);
     tc::bar_init(&sh.mlready, 2 * kTile);
     for (int i = 0; i < kSegs; ++i) {
       tc::bar_init(&sh.segfull[i], 1);
@@ -940,6 +939,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::bar_init_fence();
     sh.stop = 0;
     sh.odd_values = 0;
+    tc::tma_prefetch_map(&q_map);
     tc::tma_prefetch_map(&k_map);
     tc::tma_prefetch_map(&v_map);
     tc::tma_prefetch_map(&kn_map);
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp == 8) {
     load_tiles<DP, true>(p, sh, &k_map, &kn_map, tc::smem_addr(k_smem), lane);
   } else if (warp == 9) {
-    issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), lane);
+    issue_mma<DP, BF16>(p, sh, &q_map, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), lane);
   } else if (warp == 10) {
     fix_values<DP, BF16>(p, sh, v_smem, lane);
   } else {
@@ -996,15 +996,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const Attn
   if (i >= rq.n || x >= p.a.H_q) return;
   const Extent e = extent_of(p, rq);
   const int h = x / p.G, g = x - h * p.G;
-  const int f = i * p.G + g, item = h * e.mp + f / kItemRows;
+  const int f = i * p.G + g, item = h * e.mp + f / p.rows2;
   const int u0 = hd.w_shared + t_b + item * (e.tt + kItemCost) + kItemCost;  // the item's first tile
   const int c0 = u0 / hd.per, own = (u0 + e.tt - 1) / hd.per - c0 + 1;
   if (!p.ns && own == 1) return;  // written by the segment itself
   int is = 0, s0 = 0, parts_s = 0, fs = 0;
   if (p.ns) {
     const int64_t fl = (rq.base + i) * p.G + g;
-    is = h * hd.mp_s + (int)(fl / kItemRows);
-    fs = (int)(fl % kItemRows);
+    is = h * hd.mp_s + (int)(fl / p.rows2);
+    fs = (int)(fl % p.rows2);
     const int su = is * (hd.ts + kItemCost) + kItemCost;
     s0 = su / hd.per;
     parts_s = (su + hd.ts - 1) / hd.per - s0 + 1;
@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const Attn
   // row of part k among the shared (first parts_s) or own partials
   auto row_of = [&](int k) {
     return k < parts_s ? ((int64_t)is + s0 + k) * kItemRows + fs
-                       : ((int64_t)k_b + item + c0 + k - parts_s) * p.own_rows + f % kItemRows;
+                       : ((int64_t)k_b + item + c0 + k - parts_s) * p.own_rows + f % p.rows2;
   };
   const int d = lane * 4;
   float m = -INFINITY, l = 0.0f;
@@ -1067,9 +1067,10 @@ Layout layout_of(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, boo
   Layout L{};
   const int64_t G = H_q / H_kv, rows = (int64_t)P * G;
   // a segment's slot is item + CTA: the pair grows along the line, so slots are distinct
-  L.own_slots = (int64_t)B * H_kv * ((rows + kItemRows - 1) / kItemRows) + h->num_sms;
+  const int64_t rows2 = 2 * (kTile / G) * G;
+  L.own_slots = (int64_t)B * H_kv * ((rows + rows2 - 1) / rows2) + h->num_sms;
   L.own_rows = std::min<int64_t>(kItemRows, rows);
-  L.sh_slots = shared ? (int64_t)H_kv * ((B * rows + kItemRows - 1) / kItemRows) + h->num_sms : 0;
+  L.sh_slots = shared ? (int64_t)H_kv * ((B * rows + rows2 - 1) / rows2) + h->num_sms : 0;
   int64_t at = 256;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -1121,7 +1122,7 @@ bool encode(CUtensorMap* m, int dtype, const void* at, int rank, const int64_t* 
 
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
-  launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3]);
+  launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3], m[4]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   launch_k(attn_merge_kernel<BF16>, dim3(p.a.P, p.a.B, (p.a.H_q + kMergeWarps - 1) / kMergeWarps), dim3(32 * kMergeWarps), 0, s, p);
@@ -1151,6 +1152,8 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   AttnParams p{};
   p.a = *a;
   p.G = a->H_q / a->H_kv;
+  p.pos = kTile / p.G;
+  p.rows2 = 2 * p.pos * p.G;
   p.g_magic = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
   while ((1 << p.page_shift) < a->page) ++p.page_shift;
   p.tree_box = 8;  // positions of a tree box: a power of two that covers P, up to a tile
@@ -1169,15 +1172,18 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.ml_sh = (float2*)(ws + L.ml_sh);
   p.o_sh = (float*)(ws + L.o_sh);
   p.status = h->ws.status;
-  CUtensorMap m[4];
+  CUtensorMap m[5];
   const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
   const int64_t ks[4] = {1, a->k_head, a->k_tok, a->k_block}, vs[4] = {1, a->v_head, a->v_tok, a->v_block};
   const int pb[4] = {64, 1, std::min<int>(a->page, kTile), 1};
   const int64_t td[3] = {a->D, a->H_kv, a->rows};
   const int64_t kn[3] = {1, a->kn_head, a->kn_row}, vn[3] = {1, a->vn_head, a->vn_row};
   const int tb[3] = {64, 1, p.tree_box};
-  if (!encode(&m[0], a->dtype, a->k_pages, 4, pd, ks, pb) || !encode(&m[1], a->dtype, a->v_pages, 4, pd, vs, pb) ||
-      !encode(&m[2], a->dtype, a->k_new, 3, td, kn, tb) || !encode(&m[3], a->dtype, a->v_new, 3, td, vn, tb))
+  const int64_t qd[3] = {a->D, a->H_q, a->rows}, qs[3] = {1, a->q_head, a->q_row};
+  const int qb[3] = {64, p.G, p.pos};
+  if (!encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) || !encode(&m[1], a->dtype, a->k_pages, 4, pd, ks, pb) ||
+      !encode(&m[2], a->dtype, a->v_pages, 4, pd, vs, pb) || !encode(&m[3], a->dtype, a->k_new, 3, td, kn, tb) ||
+      !encode(&m[4], a->dtype, a->v_new, 3, td, vn, tb))
     return cudaErrorInvalidValue;
   if (a->D <= 64) return a->dtype == DT_BF16 ? launch_t<64, true>(h, p, m, s) : launch_t<64, false>(h, p, m, s);
   return a->dtype == DT_BF16 ? launch_t<128, true>(h, p, m, s) : launch_t<128, false>(h, p, m, s);

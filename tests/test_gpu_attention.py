@@ -161,6 +161,9 @@ CASES = {
     "group of 128": dict(B=1, P=3, H_kv=1, G=128, D=64, page=16, lens=[90]),
     "more than 256 rows": dict(B=2, P=85, H_kv=2, G=4, D=128, page=16, lens=[513, 20], n_pos=[85, 70]),
     "more than 128 positions": dict(B=2, P=300, H_kv=1, G=2, D=64, page=32, lens=[65, 200], n_pos=[300, 131]),
+    "heads of their own": dict(B=3, P=40, H_kv=5, G=1, D=64, page=16, lens=[70, 0, 300], n_pos=[40, 13, 33]),
+    "heads of their own, shared": dict(B=9, P=40, H_kv=3, G=1, D=128, page=16, lens=[260 + i for i in range(9)],
+                                       shared=256, packed=True, n_pos=[40, 1, 7, 40, 22, 40, 3, 39, 40]),
     "512 positions": dict(B=1, P=512, H_kv=1, G=1, D=128, page=64, lens=[130], tree=False),
     "head size 8": dict(B=2, P=3, H_kv=2, G=2, D=8, page=16, lens=[50, 5]),
     "head size 72": dict(B=2, P=3, H_kv=2, G=2, D=72, page=16, lens=[50, 5], dtype="fp16"),
