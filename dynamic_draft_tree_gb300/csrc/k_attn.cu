@@ -982,78 +982,95 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ------------------------------------------------------------------------------- merge ----------
-// A warp joins the partial results of one position and head, in the order of the line: the shared prefix's parts, then
-// the request's own. Lanes take the (m, l) of up to 32 parts at once, then the parts' elements, four a lane.
 constexpr int kMergeWarps = 4;
-template <bool BF16>
-__global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const AttnParams p) {
+// A warp joins the partial results of HEADS heads of one position: the shared prefix's parts, then the request's own, in
+// the order of the line. 32 / HEADS lanes take the (m, l) of a head's parts at once; then every lane adds up four
+// elements of each part.
+template <bool BF16, int HEADS>
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const __grid_constant__ AttnParams p) {
   pdl_begin();
+  constexpr int kLanes = 32 / HEADS;
   const int i = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
-  const int x = blockIdx.z * kMergeWarps + (threadIdx.x >> 5);
+  const int x0 = (blockIdx.z * kMergeWarps + (threadIdx.x >> 5)) * HEADS;  // the warp's first head
   const AttnHead hd = *p.head;
   const int t_b = p.t_pre[b], k_b = p.k_pre[b];
   const Request rq = request_of(p.a, p.page_shift, b);
-  if (i >= rq.n || x >= p.a.H_q) return;
+  if (i >= rq.n || x0 >= p.a.H_q) return;
   const Extent e = extent_of(p, rq);
-  const int h = x / p.G, g = x - h * p.G;
-  const int f = i * p.G + g, item = h * e.mp + f / p.rows2;
+  // this lane's head: where its parts are
+  const int x = x0 + lane / kLanes, k_lane = lane % kLanes;
+  const int h = x / p.G, f = i * p.G + x - h * p.G, blk = f / p.rows2, item = h * e.mp + blk;
   const int u0 = hd.w_shared + t_b + item * (e.tt + kItemCost) + kItemCost;  // the item's first tile
   const int c0 = u0 / hd.per, own = (u0 + e.tt - 1) / hd.per - c0 + 1;
-  if (!p.ns && own == 1) return;  // written by the segment itself
-  int is = 0, s0 = 0, parts_s = 0, fs = 0;
+  const int64_t own_at = ((int64_t)k_b + item + c0) * p.own_rows + f - blk * p.rows2;
+  int parts_s = 0;
+  int64_t sh_at = 0;
   if (p.ns) {
-    const int64_t fl = (rq.base + i) * p.G + g;
-    is = h * hd.mp_s + (int)(fl / p.rows2);
-    fs = (int)(fl % p.rows2);
-    const int su = is * (hd.ts + kItemCost) + kItemCost;
-    s0 = su / hd.per;
+    const int64_t fl = (rq.base + i) * p.G + x - h * p.G;
+    const int ms = (int)(fl / p.rows2), is = h * hd.mp_s + ms, su = is * (hd.ts + kItemCost) + kItemCost, s0 = su / hd.per;
     parts_s = (su + hd.ts - 1) / hd.per - s0 + 1;
+    sh_at = ((int64_t)is + s0) * kItemRows + fl - (int64_t)ms * p.rows2;
   }
-  const int parts = parts_s + own;
-  // row of part k among the shared (first parts_s) or own partials
-  auto row_of = [&](int k) {
-    return k < parts_s ? ((int64_t)is + s0 + k) * kItemRows + fs
-                       : ((int64_t)k_b + item + c0 + k - parts_s) * p.own_rows + f % p.rows2;
-  };
+  // an unshared item in one part was written by its segment
+  const int parts = x >= p.a.H_q || (!p.ns && own == 1) ? 0 : parts_s + own;
+  const int most = __reduce_max_sync(0xFFFFFFFFu, parts);
   const int d = lane * 4;
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0, 0, 0, 0);
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const int cnt = min(32, parts - k0);
+  float m = -INFINITY, l = 0.0f;  // of this lane's head
+  float4 o[HEADS];
+#pragma unroll
+  for (int q = 0; q < HEADS; ++q) o[q] = make_float4(0, 0, 0, 0);
+  for (int k0 = 0; k0 < most; k0 += kLanes) {
+    const int k = k0 + k_lane;
+    const bool is_shared = k < parts_s;
+    const int64_t at = is_shared ? sh_at + (int64_t)k * kItemRows : own_at + (k - parts_s) * p.own_rows;
     float2 ml = make_float2(-INFINITY, 0.0f);
-    if (lane < cnt) ml = k0 + lane < parts_s ? p.ml_sh[row_of(k0 + lane)] : p.ml_own[row_of(k0 + lane)];
+    if (k < parts) ml = is_shared ? p.ml_sh[at] : p.ml_own[at];
+    const float* src = (is_shared ? p.o_sh : p.o_own) + at * p.a.D;
     float top = fmaxf(m, ml.x);
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    for (int s = kLanes / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
     // a part that attends to nothing has weight 0 (and l = 0); one with NaN keeps it
     const float wgt = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
     float lw = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ml.y * wgt;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, s);
+    for (int s = kLanes / 2; s > 0; s >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, s);
     const float old = m == -INFINITY ? 0.0f : exp2f(m - top);
-    o.x *= old;
-    o.y *= old;
-    o.z *= old;
-    o.w *= old;
     l = l * old + lw;
     m = top;
-#pragma unroll 4
-    for (int k = 0; k < cnt; ++k) {
-      const float w = __shfl_sync(0xFFFFFFFFu, wgt, k);
-      if (d < p.a.D) {
-        const float* src = (k0 + k < parts_s ? p.o_sh : p.o_own) + row_of(k0 + k) * p.a.D + d;
-        const float4 v = *(const float4*)src;
-        o.x = fmaf(v.x, w, o.x);
-        o.y = fmaf(v.y, w, o.y);
-        o.z = fmaf(v.z, w, o.z);
-        o.w = fmaf(v.w, w, o.w);
+    const int here = min(kLanes, parts - k0);  // parts of this lane's head in this turn
+    const int turns = min(kLanes, most - k0);
+    if (k0 > 0) {
+#pragma unroll
+      for (int q = 0; q < HEADS; ++q) {
+        const float c = __shfl_sync(0xFFFFFFFFu, old, q * kLanes);
+        o[q] = make_float4(o[q].x * c, o[q].y * c, o[q].z * c, o[q].w * c);
+      }
+    }
+#pragma unroll 2
+    for (int y = 0; y < turns; ++y) {
+#pragma unroll
+      for (int q = 0; q < HEADS; ++q) {
+        const float w = __shfl_sync(0xFFFFFFFFu, wgt, q * kLanes + y);
+        const float* from = (const float*)shfl_u64((uint64_t)src, q * kLanes + y);
+        const int cnt = __shfl_sync(0xFFFFFFFFu, here, q * kLanes);
+        if (y < cnt && d < p.a.D) {
+          const float4 v = __ldcs((const float4*)(from + d));
+          o[q].x = fmaf(v.x, w, o[q].x);
+          o[q].y = fmaf(v.y, w, o[q].y);
+          o[q].z = fmaf(v.z, w, o[q].z);
+          o[q].w = fmaf(v.w, w, o[q].w);
+        }
       }
     }
   }
-  if (d < p.a.D) {
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    uint16_t* out = (uint16_t*)p.a.out + (rq.base + i) * p.a.o_row + (int64_t)x * p.a.o_head + d;
-    *(uint2*)out = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+#pragma unroll
+  for (int q = 0; q < HEADS; ++q) {
+    const float lq = __shfl_sync(0xFFFFFFFFu, l, q * kLanes);
+    if (__shfl_sync(0xFFFFFFFFu, parts, q * kLanes) > 0 && d < p.a.D) {
+      const float inv = lq > 0.0f ? 1.0f / lq : lq == 0.0f ? 0.0f : lq;
+      uint16_t* out = (uint16_t*)p.a.out + (rq.base + i) * p.a.o_row + (int64_t)(x0 + q) * p.a.o_head + d;
+      *(uint2*)out = make_uint2(pack16<BF16>(o[q].x * inv, o[q].y * inv), pack16<BF16>(o[q].z * inv, o[q].w * inv));
+    }
   }
 }
 
@@ -1125,7 +1142,13 @@ cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cu
   launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3], m[4]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  launch_k(attn_merge_kernel<BF16>, dim3(p.a.P, p.a.B, (p.a.H_q + kMergeWarps - 1) / kMergeWarps), dim3(32 * kMergeWarps), 0, s, p);
+  // Few rows: a warp a head, all of its parts at once; many: four heads a warp.
+  const int heads = (int64_t)p.a.P * p.a.B * p.a.H_q > 16ll * h->num_sms ? 4 : 1;
+  const dim3 grid(p.a.P, p.a.B, (p.a.H_q + kMergeWarps * heads - 1) / (kMergeWarps * heads));
+  if (heads == 4)
+    launch_k(attn_merge_kernel<BF16, 4>, grid, dim3(32 * kMergeWarps), 0, s, p);
+  else
+    launch_k(attn_merge_kernel<BF16, 1>, grid, dim3(32 * kMergeWarps), 0, s, p);
   return cudaGetLastError();
 }
 
