@@ -42,7 +42,7 @@ constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves
 struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
   int32_t per;     // units of a CTA
   int32_t w_shared;
-  int32_t ts, mp_s;
+  int32_t sh_head, mp_s, rows_s;
 };
 
 struct AttnParams {
@@ -89,20 +89,27 @@ __device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_sh
   return r;
 }
 
-// The line in units: an item of t tiles takes kItemCost + t of them, the first kItemCost standing for what an item costs
-// beside its tiles (its rows' loads, an empty pipeline, the rows' way out: about 6 us, a tile of two halves 2 us).
-constexpr int kItemCost = 3;
+// The line in units of about 0.5 us: a tile takes three for two halves of rows and two for one (1.55 and 1.05 us measured),
+// and an item kItemUnits more in front, for what it costs beside its tiles: an empty pipeline at its begin and end, and
+// its rows' way out (about 6 us). Tile t of an item at unit u starts at u + kItemUnits + t * units of a tile, and belongs
+// to the CTA that unit falls to.
+constexpr int kItemUnits = 12;
+__device__ __forceinline__ int tile_units(const AttnParams& p, int rows) { return rows > p.rows2 >> 1 ? 3 : 2; }
 
 // Items of a request for all key heads, tiles of one item.
 struct Extent {
-  int mp, tp, tt;  // row blocks a head; prefix tiles, all tiles
-  __device__ __forceinline__ int units(int heads) const { return tt > 0 ? heads * mp * (tt + kItemCost) : 0; }
+  int mp, tp, tt;        // row blocks a head; prefix tiles, all tiles
+  int full, last;        // units of an item of all its rows, of a head's last item
+  __device__ __forceinline__ int head() const { return (mp - 1) * full + last; }
+  __device__ __forceinline__ int all(int heads) const { return tt > 0 ? heads * head() : 0; }
 };
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
   Extent e;
   e.mp = (r.n + 2 * p.pos - 1) / (2 * p.pos);
   e.tp = (r.len - p.a.shared_len + kTile - 1) / kTile;
   e.tt = r.n > 0 ? e.tp + (r.n + kTile - 1) / kTile : 0;
+  e.full = kItemUnits + 3 * e.tt;
+  e.last = kItemUnits + tile_units(p, r.n * p.G - (e.mp - 1) * p.rows2) * e.tt;
   return e;
 }
 
@@ -112,7 +119,7 @@ struct Plan {
   int32_t w_shared;
   int32_t t_b;          // own unit offset of request b
   int32_t b, k_b;       // first own request, its item offset
-  int32_t ts, mp_s, rows_s;
+  int32_t ts, mp_s, rows_s, sh_head;  // shared: tiles, row blocks, rows, units of a key head
 };
 
 struct Segment {
@@ -150,21 +157,22 @@ struct Walk {
       int item, tt, at;  // item of its kind, its tiles, our place in its units
       if (x < pl.w_shared) {
         tt = pl.ts;
-        item = x / (tt + kItemCost);
-        at = x - item * (tt + kItemCost);
+        const int full = kItemUnits + 3 * tt;
+        s.h = x / pl.sh_head;
+        const int y = x - s.h * pl.sh_head;
+        s.mp = min(y / full, pl.mp_s - 1);
+        at = y - s.mp * full;
+        item = s.h * pl.mp_s + s.mp;
         s.shared = 1;
         s.b = 0;
-        s.h = item / pl.mp_s;
-        s.mp = item - s.h * pl.mp_s;
         s.tp = tt;
         s.len = p.a.shared_len;
         s.tok0 = 0;
         s.n = 0;
         s.base = 0;
         s.rows = min(p.rows2, pl.rows_s - s.mp * p.rows2);
-        s.slot = item + blockIdx.x;
       } else {
-        const int y = x - pl.w_shared;
+        const int z = x - pl.w_shared;
         while (true) {
           if (b >= p.a.B) return;
           if (loaded != b) {
@@ -172,31 +180,33 @@ struct Walk {
             e = extent_of(p, r);
             loaded = b;
           }
-          const int w = e.units(p.a.H_kv);
-          if (y < t_b + w) break;
+          const int w = e.all(p.a.H_kv);
+          if (z < t_b + w) break;
           t_b += w;
           k_b += p.a.H_kv * e.mp;
           ++b;
         }
         tt = e.tt;
-        item = (y - t_b) / (tt + kItemCost);
-        at = y - t_b - item * (tt + kItemCost);
+        s.h = (z - t_b) / e.head();
+        const int y = z - t_b - s.h * e.head();
+        s.mp = min(y / e.full, e.mp - 1);
+        at = y - s.mp * e.full;
+        item = k_b + s.h * e.mp + s.mp;
         s.shared = 0;
         s.b = b;
-        s.h = item / e.mp;
-        s.mp = item - s.h * e.mp;
         s.tp = e.tp;
         s.len = r.len;
         s.tok0 = p.a.shared_len;
         s.n = r.n;
         s.base = r.base;
         s.rows = min(p.rows2, r.n * p.G - s.mp * p.rows2);
-        s.slot = (int64_t)k_b + item + blockIdx.x;
       }
-      const int end = min(tt + kItemCost, at + pl.x1 - x);
+      const int tw = tile_units(p, s.rows);
+      const int end = min(tt * tw + kItemUnits, at + pl.x1 - x);
       x += end - at;
-      s.t0 = max(0, at - kItemCost);
-      s.t1 = max(0, end - kItemCost);
+      s.t0 = (max(0, at - kItemUnits) + tw - 1) / tw;
+      s.t1 = (max(0, end - kItemUnits) + tw - 1) / tw;
+      s.slot = (int64_t)item + blockIdx.x;
       s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
       s.i0 = s.mp * 2 * p.pos;
     } while (s.t1 == s.t0);
@@ -213,14 +223,16 @@ template <int DP>
 struct Smem {
   static constexpr int kHalf = kTile * 128;              // bytes of 64 elements of 128 rows
   static constexpr int kBlock = (DP / 64) * kHalf;       // a tile of Q, K or V
-  static constexpr int kStages = DP == 128 ? 2 : 4;      // tiles of K and of V in flight
-  static constexpr int kBytes = (2 + 2 * kStages) * kBlock + 1024;
+  // tiles of K and of V in flight: a V tile is held longer, from its load until the weights have come
+  static constexpr int kK = DP == 128 ? 2 : 5, kV = DP == 128 ? 3 : 6;
+  static constexpr int kTiles = (2 + kK + kV) * kBlock;
 };
+constexpr int kMostStages = 6;
 
 constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reader, at most
 
 struct Shared {
-  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vfix[4];
+  uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
   uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready;
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
@@ -230,6 +242,10 @@ struct Shared {
   uint32_t tmem;
   int stop, odd_values;
 };
+
+template <int DP>
+constexpr int kSmemBytes = Smem<DP>::kTiles + (int)sizeof(Shared);
+static_assert(kSmemBytes<128> <= 232448 && kSmemBytes<64> <= 232448, "227 KB a CTA");
 
 // The other warps read the segments that warp 10 puts down, in order. `lead`: the lane that gives the place back.
 struct Segments {
@@ -261,6 +277,11 @@ __device__ __forceinline__ float unpack16(uint16_t x) {
   return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
 }
 
+// Units of a key head's items over the shared prefix.
+__device__ __forceinline__ int shared_head(const AttnParams& p, int rows_s, int mp_s, int ts) {
+  return (mp_s - 1) * (kItemUnits + 3 * ts) + kItemUnits + tile_units(p, rows_s - (mp_s - 1) * p.rows2) * ts;
+}
+
 // Every CTA: the line's length and where its own run starts.
 __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -269,7 +290,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
   for (int b = b0; b < b1; ++b) {
     const Request r = request_of(p.a, p.page_shift, b);
     const Extent e = extent_of(p, r);
-    units += e.units(p.a.H_kv);
+    units += e.all(p.a.H_kv);
     items += p.a.H_kv * e.mp;
     if (blockIdx.x == 0 && r.bad) set_status(p.status, DT_DEV_BAD_PAGE);
   }
@@ -305,9 +326,11 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
   }
   const int rows_s = p.ns ? (int)rows_used * p.G : 0;
   const int mp_s = (rows_s + p.rows2 - 1) / p.rows2;
-  const int w_shared = p.ns ? p.a.H_kv * mp_s * (p.ns + kItemCost) : 0;
+  const int sh_head = mp_s > 0 ? shared_head(p, rows_s, mp_s, p.ns) : 0;
+  const int w_shared = p.a.H_kv * sh_head;
   total += w_shared;
-  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  // at least a tile's units: no CTA between an item's first and last one is without a tile
+  const int per = max(3, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const int x0 = min(total, per * (int)blockIdx.x), x1 = min(total, x0 + per);
   if (tid == 0) {
     Plan& pl = sh.plan;
@@ -317,19 +340,20 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     pl.ts = p.ns;
     pl.mp_s = mp_s;
     pl.rows_s = rows_s;
+    pl.sh_head = sh_head;
     if (x0 <= w_shared) {  // the own requests from the first
       pl.b = 0;
       pl.t_b = 0;
       pl.k_b = 0;
     }
-    if (blockIdx.x == 0) *p.head = AttnHead{per, w_shared, p.ns, mp_s};
+    if (blockIdx.x == 0) *p.head = AttnHead{per, w_shared, sh_head, mp_s, rows_s};
   }
   const int y0 = x0 - w_shared;
   for (int b = b0; b < b1; ++b) {
     int w = units, k = items;
     if (chunk > 1) {
       const Extent e = extent_of(p, request_of(p.a, p.page_shift, b));
-      w = e.units(p.a.H_kv);
+      w = e.all(p.a.H_kv);
       k = p.a.H_kv * e.mp;
     }
     if (y0 > 0 && t_b <= y0 && y0 < t_b + w) {
@@ -361,7 +385,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
   using S = Smem<DP>;
   uint64_t* full = IS_K ? sh.kfull : sh.vfull;
   uint64_t* empty = IS_K ? sh.kempty : sh.vempty;
-  constexpr int kHalves = DP / 64;
+  constexpr int kHalves = DP / 64, kStages = IS_K ? S::kK : S::kV;
   const int shift = p.page_shift, page = p.a.page;
   const int box = min(page, kTile);  // tokens of a page box
   const int box_shift = min(shift, 7);
@@ -388,7 +412,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
     for (int t = s.t0; t < s.t1; ++t, ++n) {
       int stage;
       uint32_t parity;
-      ring<S::kStages>(n, stage, parity);
+      ring<kStages>(n, stage, parity);
       const int next_id = t + 1 < s.t1 ? block_at(t + 1) : -1;
       ok = tc::bar_wait_warp(&empty[stage], parity ^ 1, &sh.stop);
       if (!ok) break;
@@ -420,10 +444,10 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
   }
   // after a give-up: no load may land once the CTA is gone
   if (!ok)
-    for (uint32_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k) {
+    for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
       int stage;
       uint32_t parity;
-      ring<S::kStages>(k, stage, parity);
+      ring<kStages>(k, stage, parity);
       const long long t0 = clock64();
       while (!tc::bar_try(&full[stage], parity) && clock64() - t0 < tc::kWaitClocks) {
       }
@@ -474,7 +498,7 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
       if (v >= 2) {
         int stage;
         uint32_t parity;
-        ring<S::kStages>(vn, stage, parity);
+        ring<S::kV>(vn, stage, parity);
         const bool tree = t >= tp;
         const int valid = min(kTile, tree ? n - (t - tp) * kTile : cached - t * kTile);
         if (!dual || g == 0) {
@@ -514,7 +538,7 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
       if (v < units) {
         int stage;
         uint32_t parity;
-        ring<S::kStages>(kn, stage, parity);
+        ring<S::kK>(kn, stage, parity);
         if (!dual || g == 0) {
           if (!tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
         }
@@ -575,7 +599,7 @@ __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int
       const int valid = tile_valid(s, t, tree);
       int stage;
       uint32_t parity;
-      ring<S::kStages>(n, stage, parity);
+      ring<S::kV>(n, stage, parity);
       // every tile is waited for and let go here too, so that the ring never runs ahead of this warp
       if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
       if (!tree && valid == kTile) {
@@ -909,14 +933,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map) {
   using S = Smem<DP>;
-  extern __shared__ uint8_t dyn[];
-  __shared__ Shared sh;
-  uint8_t* smem = dyn + ((1024 - (tc::smem_addr(dyn) & 1023)) & 1023);
-  uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kBlock, *v_smem = k_smem + S::kStages * S::kBlock;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kBlock, *v_smem = k_smem + S::kK * S::kBlock;
+  Shared& sh = *(Shared*)(smem + S::kTiles);
+  if (tc::smem_addr(smem) & 1023) {  // the swizzle goes by address; dynamic shared memory alone starts on 1024
+    if (threadIdx.x == 0) set_status(p.status, DT_DEV_INTERNAL);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 9) tc::tmem_alloc<512>(&sh.tmem);
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       tc::bar_init(&sh.kfull[i], 1);
       tc::bar_init(&sh.kempty[i], 1);
       tc::bar_init(&sh.vfull[i], 1);
@@ -1000,15 +1027,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const __gr
   // this lane's head: where its parts are
   const int x = x0 + lane / kLanes, k_lane = lane % kLanes;
   const int h = x / p.G, f = i * p.G + x - h * p.G, blk = f / p.rows2, item = h * e.mp + blk;
-  const int u0 = hd.w_shared + t_b + item * (e.tt + kItemCost) + kItemCost;  // the item's first tile
-  const int c0 = u0 / hd.per, own = (u0 + e.tt - 1) / hd.per - c0 + 1;
+  const int u0 = hd.w_shared + t_b + h * e.head() + blk * e.full + kItemUnits;  // the item's first tile
+  const int tw = tile_units(p, rq.n * p.G - blk * p.rows2);
+  const int c0 = u0 / hd.per, own = (u0 + (e.tt - 1) * tw) / hd.per - c0 + 1;
   const int64_t own_at = ((int64_t)k_b + item + c0) * p.own_rows + f - blk * p.rows2;
   int parts_s = 0;
   int64_t sh_at = 0;
   if (p.ns) {
     const int64_t fl = (rq.base + i) * p.G + x - h * p.G;
-    const int ms = (int)(fl / p.rows2), is = h * hd.mp_s + ms, su = is * (hd.ts + kItemCost) + kItemCost, s0 = su / hd.per;
-    parts_s = (su + hd.ts - 1) / hd.per - s0 + 1;
+    const int ms = (int)(fl / p.rows2), is = h * hd.mp_s + ms;
+    const int su = h * hd.sh_head + ms * (kItemUnits + 3 * p.ns) + kItemUnits, s0 = su / hd.per;
+    parts_s = (su + (p.ns - 1) * tile_units(p, hd.rows_s - ms * p.rows2)) / hd.per - s0 + 1;
     sh_at = ((int64_t)is + s0) * kItemRows + fl - (int64_t)ms * p.rows2;
   }
   // an unshared item in one part was written by its segment
@@ -1139,7 +1168,7 @@ bool encode(CUtensorMap* m, int dtype, const void* at, int rank, const int64_t* 
 
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
-  launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), Smem<DP>::kBytes, s, p, m[0], m[1], m[2], m[3], m[4]);
+  launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Few rows: a warp a head, all of its parts at once; many: four heads a warp.
@@ -1154,7 +1183,7 @@ cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cu
 
 template <int DP, bool BF16>
 cudaError_t init_t() {
-  return cudaFuncSetAttribute(attn_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP>::kBytes);
+  return cudaFuncSetAttribute(attn_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<DP>);
 }
 
 }  // namespace

@@ -3,7 +3,9 @@
 // Every row is read and written once. A CTA owns a chunk of the vocabulary for one request and goes
 // through a group of that request's rows, so the request's counts and biases of the chunk are read once
 // a group into registers. What differs from row to row is the tree path: the path tokens that fall into
-// the chunk (a few of D <= 17 over V / 2048 chunks) are listed a row in shared memory before the row loop.
+// the chunk (a few of D <= 17 over V / 2048 chunks) are listed a row in shared memory before the row loop, with a
+// bit a token, so that the loop has one multiply-add and two selects an element and only threads with a bit set look
+// at the list. Bound by DRAM: 64 bytes a thread are in flight, the next row's load behind every row's store.
 #include <cuda_bf16.h>
 
 #include "dt_internal.cuh"
@@ -31,16 +33,34 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float y, float& o) { o = y; }
 __device__ __forceinline__ void from_f(float y, __nv_bfloat16& o) { o = __float2bfloat16_rn(y); }
 
+// What the row loop needs of a token: y = x * (x > 0 ? pos : neg) - sub. A token that has not been seen has
+// pos = neg = 1 and sub = -bias; a seen one 1 / repetition, repetition and frequency c + presence - bias.
+struct Token {
+  float pos, neg, sub;
+};
+struct Penalty {
+  float rep, inv, freq, pres;
+};
+__device__ __forceinline__ Token token_of(const Penalty& p, int c, bool prompt, float bias) {
+  const bool seen = c > 0 || prompt;
+  Token t;
+  t.pos = seen ? p.inv : 1.0f;
+  t.neg = seen ? p.rep : 1.0f;
+  t.sub = (c > 0 ? fmaf(p.freq, (float)c, p.pres) : 0.0f) - bias;
+  return t;
+}
+
 // VEC: every row starts on a 16-byte boundary; a thread's tokens are then kLogPer neighbours (one or two
 // 16-byte accesses), else one token in every kLogThreads (coalesced single elements).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kLogThreads) logits_kernel(LogitsArgs a) {
+__global__ void __launch_bounds__(kLogThreads, 3) logits_kernel(LogitsArgs a) {
   extern __shared__ char dyn[];
   const int P = a.p.P;
   int32_t* path_tok = (int32_t*)dyn;               // [P] chunk offset of a position's token, its position
   int32_t* path_pos = path_tok + P;                // [P]
   uint16_t* row_list = (uint16_t*)(path_pos + P);  // [kLogRows][P] chunk offsets of the row's path tokens
-  __shared__ int n_path, n_row[kLogRows], n_bias_s;
+  __shared__ int n_path, n_row[kLogRows];
+  __shared__ uint32_t hit[kLogRows][kLogChunk / 32];  // bit = the token is on the row's path
   __shared__ float bias_s[kLogChunk];
   pdl_begin();
   const int tid = threadIdx.x, b = blockIdx.y;
@@ -54,8 +74,31 @@ __global__ void __launch_bounds__(kLogThreads) logits_kernel(LogitsArgs a) {
     if (tid == 0) set_status(a.status, DT_DEV_BAD_PAGE);
     return;
   }
+  auto place = [&](int u) { return VEC ? tid * kLogPer + u : tid + u * kLogThreads; };  // in the chunk
+  // the first rows are on their way while the tables are made
+  constexpr int kTurn = VEC && sizeof(T) == 4 ? 2 : 4;  // rows in flight: 64 bytes a thread
+  const bool full = VEC && v0 + (tid + 1) * kLogPer <= a.V;
+  T in[kTurn][kLogPer];
+  auto load = [&](int r, T* x) {
+    const T* src = (const T*)a.logits + (base + row0 + r) * a.ld;
+    if (full) {
+      constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
+      uint4 q[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) q[k] = __ldcs((const uint4*)(src + v0 + tid * kLogPer) + k);
+      memcpy(x, q, sizeof(q));
+    } else {
+#pragma unroll
+      for (int u = 0; u < kLogPer; ++u)
+        if (v0 + place(u) < a.V) x[u] = src[v0 + place(u)];
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kTurn; ++k)
+    if (k < rows) load(k, in[k]);
   if (tid == 0) n_path = 0;
   if (tid < kLogRows) n_row[tid] = 0;
+  for (int i = tid; i < kLogRows * (kLogChunk / 32); i += kLogThreads) (&hit[0][0])[i] = 0;
   const bool with_bias = a.p.bias_ids != nullptr && a.p.n_bias > 0;
   if (with_bias)
     for (int i = tid; i < kLogChunk; i += kLogThreads) bias_s[i] = 0.0f;
@@ -81,10 +124,10 @@ __global__ void __launch_bounds__(kLogThreads) logits_kernel(LogitsArgs a) {
         if (blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TOKEN);
         id = -1;
       }
-      const bool in = id >= v0 && id - v0 < kLogChunk;
-      const float val = in ? a.p.bias_vals[(int64_t)b * a.p.n_bias + k] : 0.0f;
-      for (uint32_t m = __ballot_sync(0xFFFFFFFFu, in); m; m &= m - 1) {
-        if (tid == __ffs(m) - 1) bias_s[id - v0] = __fadd_rn(bias_s[id - v0], val);
+      const bool inside = id >= v0 && id - v0 < kLogChunk;
+      const float val = inside ? a.p.bias_vals[(int64_t)b * a.p.n_bias + k] : 0.0f;
+      for (uint32_t m = __ballot_sync(0xFFFFFFFFu, inside); m; m &= m - 1) {
+        if (tid == __ffs(m) - 1) bias_s[id - v0] += val;
         __syncwarp();
       }
     }
@@ -94,92 +137,97 @@ __global__ void __launch_bounds__(kLogThreads) logits_kernel(LogitsArgs a) {
   for (int x = tid; x < np * rows; x += kLogThreads) {
     const int r = x / np, k = x - r * np, i = row0 + r, j = path_pos[k];
     const bool on = a.p.mask ? a.p.mask[((int64_t)b * P + i) * P + j] != 0 : j <= i;
-    if (on) row_list[r * P + atomicAdd(&n_row[r], 1)] = (uint16_t)path_tok[k];
+    if (on) {
+      const int off = path_tok[k];
+      row_list[r * P + atomicAdd(&n_row[r], 1)] = (uint16_t)off;
+      atomicOr(&hit[r][off >> 5], 1u << (off & 31));
+    }
   }
-  // a thread's counts and biases
-  int cnt[kLogPer];
-  float bias[kLogPer];
-  uint32_t prompt = 0;
+  Penalty pen;
+  pen.rep = a.p.repetition ? a.p.repetition[b] : 1.0f;
+  pen.inv = 1.0f / pen.rep;
+  pen.freq = a.p.frequency ? a.p.frequency[b] : 0.0f;
+  pen.pres = a.p.presence ? a.p.presence[b] : 0.0f;
+  Token tok[kLogPer];
+  const int32_t* counts = a.p.counts ? a.p.counts + (int64_t)b * a.V + v0 : nullptr;
 #pragma unroll
   for (int u = 0; u < kLogPer; ++u) {
-    const int off = VEC ? tid * kLogPer + u : tid + u * kLogThreads;
-    const int v = v0 + off;
-    const int c = (a.p.counts && v < a.V) ? a.p.counts[(int64_t)b * a.V + v] : 0;
-    cnt[u] = c & (DT_SEEN_PROMPT - 1);
-    if (c & DT_SEEN_PROMPT) prompt |= 1u << u;
-    bias[u] = with_bias ? bias_s[off] : 0.0f;
+    const int c = counts && v0 + place(u) < a.V ? counts[place(u)] : 0;
+    tok[u] = token_of(pen, c & (DT_SEEN_PROMPT - 1), c & DT_SEEN_PROMPT, with_bias ? bias_s[place(u)] : 0.0f);
   }
-  const float rep = a.p.repetition ? a.p.repetition[b] : 1.0f;
-  const float freq = a.p.frequency ? a.p.frequency[b] : 0.0f;
-  const float pres = a.p.presence ? a.p.presence[b] : 0.0f;
   __syncthreads();
-  for (int r = 0; r < rows; ++r) {
-    const int64_t row = base + row0 + r;
-    const T* x = (const T*)a.logits + row * a.ld;
-    T* y = (T*)a.out + row * a.ld_out;
-    uint32_t allow = 0xFFu;
-    if (a.p.allow) {
-      const uint32_t* w = a.p.allow + row * a.p.allow_ld;
-      if (VEC) {
-        const int v = v0 + tid * kLogPer;
-        allow = v < a.V ? (w[v >> 5] >> (v & 31)) & 0xFFu : 0u;
-      } else {
-        allow = 0;
+  const int lane = tid & 31, warp = tid >> 5;
+  for (int r0 = 0; r0 < rows; r0 += kTurn) {
 #pragma unroll
-        for (int u = 0; u < kLogPer; ++u) {
-          const int v = v0 + tid + u * kLogThreads;
-          if (v < a.V) allow |= ((w[v >> 5] >> (v & 31)) & 1u) << u;
+    for (int k = 0; k < kTurn; ++k) {
+      const int r = r0 + k;
+      if (r >= rows) break;
+      const int64_t row = base + row0 + r;
+      // bit u: the thread's token u may be said
+      uint32_t allow = 0xFFu;
+      if (a.p.allow) {
+        const uint32_t* w = a.p.allow + row * a.p.allow_ld + (v0 >> 5);
+        if (VEC) {
+          allow = v0 + tid * kLogPer < a.V ? w[tid >> 2] >> (8 * (tid & 3)) : 0u;
+        } else {
+          // the warp's tokens of u are the 32 of one word
+          const uint32_t word = lane < kLogPer && v0 + lane * kLogThreads + warp * 32 < a.V ? w[lane * (kLogThreads / 32) + warp] : 0u;
+          allow = 0;
+#pragma unroll
+          for (int u = 0; u < kLogPer; ++u) allow |= (__shfl_sync(0xFFFFFFFFu, word, u) >> lane & 1u) << u;
         }
       }
-    }
-    T in[kLogPer];
-    if (VEC && v0 + (tid + 1) * kLogPer <= a.V) {
-      constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
-      uint4 q[kVec];
+      // tokens on the row's path, past the history
+      uint32_t on_path = 0;
+      if (np > 0) {
+        if (VEC) {
+          on_path = hit[r][tid >> 2] >> (8 * (tid & 3)) & 0xFFu;
+        } else {
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) q[k] = __ldcs((const uint4*)(x + v0 + tid * kLogPer) + k);
-      memcpy(in, q, sizeof(in));
-    } else {
+          for (int u = 0; u < kLogPer; ++u) on_path |= (hit[r][u * (kLogThreads / 32) + warp] >> lane & 1u) << u;
+        }
+      }
+      T res[kLogPer];
 #pragma unroll
       for (int u = 0; u < kLogPer; ++u) {
-        const int v = v0 + (VEC ? tid * kLogPer + u : tid + u * kLogThreads);
-        if (v < a.V) in[u] = x[v];
+        const float x = to_f(in[k][u]);
+        float y = fmaf(x, x > 0.0f ? tok[u].pos : tok[u].neg, -tok[u].sub);
+        if (!(allow >> u & 1)) y = -INFINITY;
+        from_f(y, res[u]);
       }
-    }
-    int add[kLogPer];
+      if (on_path) {
+        const int nr = n_row[r];
+        for (uint32_t m = on_path; m; m &= m - 1) {
+          const int u = __ffs(m) - 1, off = place(u);
+          int c = counts ? counts[off] : 0;
+          const bool prompt = c & DT_SEEN_PROMPT;
+          c &= DT_SEEN_PROMPT - 1;
+          for (int q = 0; q < nr; ++q) c += row_list[r * P + q] == off;
+          const Token t = token_of(pen, c, prompt, with_bias ? bias_s[off] : 0.0f);
+          T o;
+          float x = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kLogPer; ++u) add[u] = 0;
-    const int nr = n_row[r];
-    for (int k = 0; k < nr; ++k) {
-      const int off = row_list[r * P + k];
+          for (int q = 0; q < kLogPer; ++q)
+            if (q == u) x = to_f(in[k][q]);
+          from_f(allow >> u & 1 ? fmaf(x, x > 0.0f ? t.pos : t.neg, -t.sub) : -INFINITY, o);
 #pragma unroll
-      for (int u = 0; u < kLogPer; ++u) add[u] += off == (VEC ? tid * kLogPer + u : tid + u * kLogThreads);
-    }
-    T res[kLogPer];
-#pragma unroll
-    for (int u = 0; u < kLogPer; ++u) {
-      float f = to_f(in[u]);
-      const int c = cnt[u] + add[u];
-      if (c > 0 || (prompt >> u & 1)) {
-        f = f > 0.0f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
-        if (c > 0) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)c)), pres);
+          for (int q = 0; q < kLogPer; ++q)
+            if (q == u) res[q] = o;
+        }
       }
-      if (with_bias) f = __fadd_rn(f, bias[u]);
-      if (!(allow >> u & 1)) f = -INFINITY;
-      from_f(f, res[u]);
-    }
-    if (VEC && v0 + (tid + 1) * kLogPer <= a.V) {
-      constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
-      uint4 q[kVec];
-      memcpy(q, res, sizeof(res));
+      T* dst = (T*)a.out + row * a.ld_out + v0;
+      if (full) {
+        constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
+        uint4 q[kVec];
+        memcpy(q, res, sizeof(q));
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) __stcs((uint4*)(y + v0 + tid * kLogPer) + k, q[k]);
-    } else {
+        for (int c = 0; c < kVec; ++c) ((uint4*)(dst + tid * kLogPer))[c] = q[c];
+      } else {
 #pragma unroll
-      for (int u = 0; u < kLogPer; ++u) {
-        const int v = v0 + (VEC ? tid * kLogPer + u : tid + u * kLogThreads);
-        if (v < a.V) y[v] = res[u];
+        for (int u = 0; u < kLogPer; ++u)
+          if (v0 + place(u) < a.V) dst[place(u)] = res[u];
       }
+      if (r + kTurn < rows) load(r + kTurn, in[k]);
     }
   }
 }
