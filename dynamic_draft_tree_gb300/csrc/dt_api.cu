@@ -120,6 +120,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   const size_t o_bkey = cv.take<unsigned long long>(c.B_max);
   const size_t o_bcnt = cv.take<int32_t>(c.B_max);
   const size_t o_status = cv.take<int32_t>(1);
+  const size_t o_ticket = cv.take<unsigned>(1);
   const size_t total = cv.off;
 
   void* base = nullptr;
@@ -167,6 +168,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   w.bonus_key = reinterpret_cast<unsigned long long*>(bp + o_bkey);
   w.bonus_counter = reinterpret_cast<int32_t*>(bp + o_bcnt);
   w.status = reinterpret_cast<int32_t*>(bp + o_status);
+  w.ticket = reinterpret_cast<unsigned*>(bp + o_ticket);
   h->alloc = base;
   h->alloc_bytes = total;
   *out = h;

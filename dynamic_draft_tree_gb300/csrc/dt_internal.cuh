@@ -92,6 +92,7 @@ struct Workspace {
   unsigned long long* bonus_key;  // [B_max]
   int32_t* bonus_counter;         // [B_max]
   int32_t* status;
+  unsigned* ticket;      // arrivals of a page call's CTAs; zero between calls
 };
 
 }  // namespace dt

@@ -2,20 +2,19 @@
 //
 // Every row is read and written once. A CTA owns a chunk of the vocabulary for one request and goes
 // through a group of that request's rows, so the request's counts and biases of the chunk are read once
-// a group into registers. What differs from row to row is the tree path: the path tokens that fall into
-// the chunk (a few of D <= 17 over V / 2048 chunks) are listed a row in shared memory before the row loop, with a
-// bit a token, so that the loop has one multiply-add and two selects an element and only threads with a bit set look
-// at the list. Bound by DRAM: 64 bytes a thread are in flight, the next row's load behind every row's store.
-#include <cuda_bf16.h>
-
+// a group into registers. What differs from row to row is the tree path: the path tokens that fall into the chunk (a few
+// of D <= 17 over V / 2048 chunks) have a bit a row in shared memory, made before the row loop, so that the loop has one
+// multiply-add and two selects an element and only threads with a bit set look further. Bound by DRAM.
 #include "dt_internal.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kLogThreads = 256;
-constexpr int kLogPer = 8;                       // tokens of a thread
-constexpr int kLogChunk = kLogThreads * kLogPer;  // tokens of a CTA
+constexpr int kLogThreads = 128;
+constexpr int kPer = 8;                          // tokens of a thread
+constexpr int kLogChunk = kLogThreads * kPer;    // tokens of a CTA
+template <typename T>
+constexpr int kWords = kPer * (int)sizeof(T) / 4;  // 32-bit words of a row that a thread holds
 constexpr int kLogRows = 16;                     // rows of a CTA
 
 struct LogitsArgs {
@@ -25,211 +24,316 @@ struct LogitsArgs {
   void* out;
   int64_t ld_out;
   int32_t V;
+  bool counts16;  // every counts row starts on a 16-byte boundary
   int32_t* status;
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float y, float& o) { o = y; }
-__device__ __forceinline__ void from_f(float y, __nv_bfloat16& o) { o = __float2bfloat16_rn(y); }
+template <typename T>
+__device__ __forceinline__ float element(const uint32_t* w, int u) {
+  if (sizeof(T) == 4) return __uint_as_float(w[u]);
+  return u & 1 ? bf16_hi(w[u >> 1]) : bf16_lo(w[u >> 1]);
+}
+template <typename T>
+__device__ __forceinline__ void pack_words(const float* y, uint32_t* w) {
+#pragma unroll
+  for (int k = 0; k < kWords<T>; ++k) {
+    if constexpr (sizeof(T) == 4)
+      w[k] = __float_as_uint(y[k]);
+    else
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(y[2 * k + 1]), "f"(y[2 * k]));
+  }
+}
 
-// What the row loop needs of a token: y = x * (x > 0 ? pos : neg) - sub. A token that has not been seen has
-// pos = neg = 1 and sub = -bias; a seen one 1 / repetition, repetition and frequency c + presence - bias.
-struct Token {
-  float pos, neg, sub;
-};
 struct Penalty {
   float rep, inv, freq, pres;
 };
-__device__ __forceinline__ Token token_of(const Penalty& p, int c, bool prompt, float bias) {
-  const bool seen = c > 0 || prompt;
-  Token t;
-  t.pos = seen ? p.inv : 1.0f;
-  t.neg = seen ? p.rep : 1.0f;
-  t.sub = (c > 0 ? fmaf(p.freq, (float)c, p.pres) : 0.0f) - bias;
-  return t;
+// y = x * factor + add: a token that has not been seen has factor 1 and add = bias; a seen one 1 / repetition or, where
+// x is not positive, repetition, and add = bias - frequency c - presence.
+__device__ __forceinline__ float factor_of(const Penalty& p, bool seen, float x) {
+  const float f = x > 0.0f ? p.inv : p.rep;
+  return seen ? f : 1.0f;
+}
+__device__ __forceinline__ float add_of(const Penalty& p, int c, float bias) {
+  return bias - (c > 0 ? fmaf(p.freq, (float)c, p.pres) : 0.0f);
 }
 
-// VEC: every row starts on a 16-byte boundary; a thread's tokens are then kLogPer neighbours (one or two
-// 16-byte accesses), else one token in every kLogThreads (coalesced single elements).
+// 128 bytes a thread on their way.
+template <typename T>
+constexpr int kRingRows = sizeof(T) == 2 ? 8 : 4;
+template <typename T>
+constexpr int kRingBytes = kRingRows<T> * (kWords<T> + 1) * kLogThreads * 4;
+
+__device__ __forceinline__ void copy16(uint32_t* dst, const void* src, int bytes) {  // the rest of the 16 becomes zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// VEC: every row starts on a 16-byte boundary; a thread's tokens are then neighbours (two 16-byte
+// accesses), else one token in every kLogThreads (coalesced single elements; bf16 ones are too small for an
+// asynchronous copy and are loaded one row ahead of their use).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kLogThreads, 3) logits_kernel(LogitsArgs a) {
-  extern __shared__ char dyn[];
+__global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
+  // A row's elements wait in shared memory, kDepth rows ahead, every thread's in places of its own (asynchronous copies
+  // that only the thread itself waits for), and the allow word that holds (VEC) or lends its warp their bits.
+  constexpr int W = kWords<T>, kDepth = kRingRows<T>;
+  extern __shared__ __align__(16) uint32_t dyn[];
   const int P = a.p.P;
-  int32_t* path_tok = (int32_t*)dyn;               // [P] chunk offset of a position's token, its position
-  int32_t* path_pos = path_tok + P;                // [P]
-  uint16_t* row_list = (uint16_t*)(path_pos + P);  // [kLogRows][P] chunk offsets of the row's path tokens
-  __shared__ int n_path, n_row[kLogRows];
+  uint32_t* ring = dyn;                                          // [kDepth][W][kLogThreads]
+  uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][kLogThreads]
+  int32_t* path_tok = (int32_t*)(said + kDepth * kLogThreads);   // [P] chunk offset of a position's token, its position
+  int32_t* path_pos = path_tok + P;                              // [P]
+  __shared__ int n_path, twice;
   __shared__ uint32_t hit[kLogRows][kLogChunk / 32];  // bit = the token is on the row's path
   __shared__ float bias_s[kLogChunk];
+  __shared__ uint32_t biased[kLogChunk / 32];
   pdl_begin();
-  const int tid = threadIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
   const int v0 = blockIdx.x * kLogChunk;
   const int row0 = blockIdx.z * kLogRows;
+  // everything that depends on the request alone is asked for at once
+  const bool with_bias = a.p.bias_ids != nullptr && a.p.n_bias > 0;
+  const int32_t* ids = a.p.bias_ids + (int64_t)b * a.p.n_bias;
+  const float* vals = a.p.bias_vals + (int64_t)b * a.p.n_bias;
   const int n = min(max(a.p.n_pos[b], 0), P);
+  const int64_t base = a.p.row_off ? (int64_t)a.p.row_off[b] : (int64_t)b * P;
+  constexpr int kTok = kMaxP / kLogThreads;
+  int path[kTok];
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    const int j = tid + k * kLogThreads;
+    path[k] = a.p.tokens && j < P ? a.p.tokens[(int64_t)b * P + j] : -1;
+  }
+  const int id0 = with_bias && tid < a.p.n_bias ? ids[tid] : -1;
+  const float val0 = with_bias && tid < a.p.n_bias ? vals[tid] : 0.0f;
+  Penalty pen;
+  pen.rep = a.p.repetition ? a.p.repetition[b] : 1.0f;
+  pen.freq = a.p.frequency ? a.p.frequency[b] : 0.0f;
+  pen.pres = a.p.presence ? a.p.presence[b] : 0.0f;
   if (row0 >= n) return;
   const int rows = min(kLogRows, n - row0);
-  int64_t base = a.p.row_off ? (int64_t)a.p.row_off[b] : (int64_t)b * P;
   if (base < 0 || base + n > a.p.rows) {
     if (tid == 0) set_status(a.status, DT_DEV_BAD_PAGE);
     return;
   }
-  auto place = [&](int u) { return VEC ? tid * kLogPer + u : tid + u * kLogThreads; };  // in the chunk
-  // the first rows are on their way while the tables are made
-  constexpr int kTurn = VEC && sizeof(T) == 4 ? 2 : 4;  // rows in flight: 64 bytes a thread
-  const bool full = VEC && v0 + (tid + 1) * kLogPer <= a.V;
-  T in[kTurn][kLogPer];
-  auto load = [&](int r, T* x) {
-    const T* src = (const T*)a.logits + (base + row0 + r) * a.ld;
-    if (full) {
-      constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
-      uint4 q[kVec];
+  auto place = [&](int u) { return VEC ? tid * kPer + u : tid + u * kLogThreads; };  // in the chunk
+  constexpr bool kHalves = !VEC && W < kPer;  // strided bf16
+  const T* src = (const T*)a.logits + (base + row0) * a.ld + v0 + (VEC ? tid * kPer : tid);  // the next row to fetch
+  T* dst = (T*)a.out + (base + row0) * a.ld_out + v0 + (VEC ? tid * kPer : tid);
+  const int word_at = VEC ? tid * kPer >> 5 : lane * (kLogThreads / 32) + warp;
+  const int word_shift = tid * kPer & 31;  // VEC: this thread's first bit
+  const bool word_in = a.p.allow && (VEC ? v0 + tid * kPer < a.V : lane < kPer && v0 + word_at * 32 < a.V);
+  const uint32_t* allow_at = a.p.allow + (base + row0) * a.p.allow_ld + (v0 >> 5) + word_at;
+  const int left = (a.V - v0 - tid * kPer) * (int)sizeof(T);  // VEC: bytes of the row from this thread's first token
+  uint32_t* mine = ring + tid * (VEC ? 4 : 1);
+  auto fetch = [&](int r) {
+    if (r < rows) {
+      uint32_t* to = mine + (r % kDepth) * W * kLogThreads;
+      if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) q[k] = __ldcs((const uint4*)(src + v0 + tid * kLogPer) + k);
-      memcpy(x, q, sizeof(q));
-    } else {
+        for (int c = 0; c < W / 4; ++c)
+          if (left > 16 * c) copy16(to + c * kLogThreads * 4, (const char*)src + 16 * c, min(16, left - 16 * c));
+      } else if constexpr (!kHalves) {
 #pragma unroll
-      for (int u = 0; u < kLogPer; ++u)
-        if (v0 + place(u) < a.V) x[u] = src[v0 + place(u)];
+        for (int u = 0; u < kPer; ++u)
+          if (v0 + place(u) < a.V) copy4(to + u * kLogThreads, src + u * kLogThreads);
+      }
+      if (word_in) copy4(said + (r % kDepth) * kLogThreads + tid, allow_at);
+      if constexpr (!kHalves) src += a.ld;
+      allow_at += a.p.allow_ld;
+    }
+    copies_close();
+  };
+  uint16_t half[kPer];  // strided bf16: the next row's
+  auto load_halves = [&]() {
+    if constexpr (kHalves) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        if (v0 + place(u) < a.V) half[u] = src[u * kLogThreads];
+      src += a.ld;
     }
   };
+  // the first rows and the counts are on their way while the tables are made
+#pragma unroll 1
+  for (int k = 0; k < kDepth; ++k) fetch(k);
+  load_halves();
+  const int32_t* counts = a.p.counts ? a.p.counts + (int64_t)b * a.V + v0 : nullptr;
+  int cnt[kPer];
+  if (counts && VEC && a.counts16 && left >= kPer * (int)sizeof(T)) {
+    const int4 lo = ((const int4*)counts)[2 * tid], hi = ((const int4*)counts)[2 * tid + 1];
+    cnt[0] = lo.x, cnt[1] = lo.y, cnt[2] = lo.z, cnt[3] = lo.w, cnt[4] = hi.x, cnt[5] = hi.y, cnt[6] = hi.z, cnt[7] = hi.w;
+  } else {
 #pragma unroll
-  for (int k = 0; k < kTurn; ++k)
-    if (k < rows) load(k, in[k]);
-  if (tid == 0) n_path = 0;
-  if (tid < kLogRows) n_row[tid] = 0;
+    for (int u = 0; u < kPer; ++u) cnt[u] = counts && v0 + place(u) < a.V ? counts[place(u)] : 0;
+  }
+  if (tid == 0) n_path = twice = 0;
   for (int i = tid; i < kLogRows * (kLogChunk / 32); i += kLogThreads) (&hit[0][0])[i] = 0;
-  const bool with_bias = a.p.bias_ids != nullptr && a.p.n_bias > 0;
-  if (with_bias)
+  if (with_bias) {
     for (int i = tid; i < kLogChunk; i += kLogThreads) bias_s[i] = 0.0f;
+    if (tid < kLogChunk / 32) biased[tid] = 0;
+  }
   __syncthreads();
-  if (a.p.tokens) {
-    for (int j = tid; j < n; j += kLogThreads) {
-      const int t = a.p.tokens[(int64_t)b * P + j];
-      if (t < -1 || t >= a.V) {
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    const int j = tid + k * kLogThreads, at = path[k];
+    if (j < n && at != -1) {
+      if (at < 0 || at >= a.V) {
         if (blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TOKEN);
-      } else if (t >= v0 && t - v0 < kLogChunk) {
-        const int k = atomicAdd(&n_path, 1);
-        path_tok[k] = t - v0;
-        path_pos[k] = j;
+      } else if (at >= v0 && at - v0 < kLogChunk) {
+        const int q = atomicAdd(&n_path, 1);
+        path_tok[q] = at - v0;
+        path_pos[q] = j;
       }
     }
   }
-  if (with_bias && tid < 32) {
-    // warp 0 goes through the list in order; equal ids add up in list order
-    for (int k0 = 0; k0 < a.p.n_bias; k0 += 32) {
-      const int k = k0 + tid;
-      int id = k < a.p.n_bias ? a.p.bias_ids[(int64_t)b * a.p.n_bias + k] : -1;
+  if (with_bias) {
+    for (int k = tid; k < a.p.n_bias; k += kLogThreads) {
+      const int id = k == tid ? id0 : ids[k];
+      const float val = k == tid ? val0 : vals[k];
       if (id < -1 || id >= a.V) {
         if (blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TOKEN);
-        id = -1;
-      }
-      const bool inside = id >= v0 && id - v0 < kLogChunk;
-      const float val = inside ? a.p.bias_vals[(int64_t)b * a.p.n_bias + k] : 0.0f;
-      for (uint32_t m = __ballot_sync(0xFFFFFFFFu, inside); m; m &= m - 1) {
-        if (tid == __ffs(m) - 1) bias_s[id - v0] += val;
-        __syncwarp();
+      } else if (id >= v0 && id - v0 < kLogChunk) {
+        const int off = id - v0;
+        if (atomicOr(&biased[off >> 5], 1u << (off & 31)) >> (off & 31) & 1)
+          twice = 1;
+        else
+          bias_s[off] = val;
       }
     }
   }
   __syncthreads();
+  if (with_bias && twice) {
+    // ids that come twice add up in list order: once more, by one warp that goes through the list
+    for (int i = tid; i < kLogChunk; i += kLogThreads) bias_s[i] = 0.0f;
+    __syncthreads();
+    if (warp == 0) {
+      for (int k0 = 0; k0 < a.p.n_bias; k0 += 32) {
+        const int k = k0 + lane, id = k < a.p.n_bias ? ids[k] : -1;
+        const bool inside = id >= v0 && id - v0 < kLogChunk && id < a.V;
+        const float val = inside ? vals[k] : 0.0f;
+        for (uint32_t m = __ballot_sync(0xFFFFFFFFu, inside); m; m &= m - 1) {
+          if (lane == __ffs(m) - 1) bias_s[id - v0] += val;
+          __syncwarp();
+        }
+      }
+    }
+    __syncthreads();
+  }
   const int np = n_path;
+  auto on_path_of = [&](int r, int k) {  // is path entry k on row r's path
+    const int i = row0 + r, j = path_pos[k];
+    return a.p.mask ? a.p.mask[((int64_t)b * P + i) * P + j] != 0 : j <= i;
+  };
   for (int x = tid; x < np * rows; x += kLogThreads) {
-    const int r = x / np, k = x - r * np, i = row0 + r, j = path_pos[k];
-    const bool on = a.p.mask ? a.p.mask[((int64_t)b * P + i) * P + j] != 0 : j <= i;
-    if (on) {
-      const int off = path_tok[k];
-      row_list[r * P + atomicAdd(&n_row[r], 1)] = (uint16_t)off;
-      atomicOr(&hit[r][off >> 5], 1u << (off & 31));
-    }
+    const int r = x / np, k = x - r * np;
+    if (on_path_of(r, k)) atomicOr(&hit[r][path_tok[k] >> 5], 1u << (path_tok[k] & 31));
   }
-  Penalty pen;
-  pen.rep = a.p.repetition ? a.p.repetition[b] : 1.0f;
   pen.inv = 1.0f / pen.rep;
-  pen.freq = a.p.frequency ? a.p.frequency[b] : 0.0f;
-  pen.pres = a.p.presence ? a.p.presence[b] : 0.0f;
-  Token tok[kLogPer];
-  const int32_t* counts = a.p.counts ? a.p.counts + (int64_t)b * a.V + v0 : nullptr;
+  float add[kPer];
+  uint32_t seen = 0;
 #pragma unroll
-  for (int u = 0; u < kLogPer; ++u) {
-    const int c = counts && v0 + place(u) < a.V ? counts[place(u)] : 0;
-    tok[u] = token_of(pen, c & (DT_SEEN_PROMPT - 1), c & DT_SEEN_PROMPT, with_bias ? bias_s[place(u)] : 0.0f);
+  for (int u = 0; u < kPer; ++u) {
+    add[u] = with_bias ? bias_s[place(u)] : 0.0f;
+    if (cnt[u]) add[u] = add_of(pen, cnt[u] & (DT_SEEN_PROMPT - 1), add[u]);
+    seen |= (cnt[u] != 0 ? 1u : 0u) << u;
   }
   __syncthreads();
-  const int lane = tid & 31, warp = tid >> 5;
-  for (int r0 = 0; r0 < rows; r0 += kTurn) {
+  for (int r = 0; r < rows; ++r) {
+    copies_wait<kDepth - 1>();
+    uint32_t in[W];
+    const uint32_t* from = mine + (r % kDepth) * W * kLogThreads;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) {
-      const int r = r0 + k;
-      if (r >= rows) break;
-      const int64_t row = base + row0 + r;
-      // bit u: the thread's token u may be said
-      uint32_t allow = 0xFFu;
-      if (a.p.allow) {
-        const uint32_t* w = a.p.allow + row * a.p.allow_ld + (v0 >> 5);
-        if (VEC) {
-          allow = v0 + tid * kLogPer < a.V ? w[tid >> 2] >> (8 * (tid & 3)) : 0u;
-        } else {
-          // the warp's tokens of u are the 32 of one word
-          const uint32_t word = lane < kLogPer && v0 + lane * kLogThreads + warp * 32 < a.V ? w[lane * (kLogThreads / 32) + warp] : 0u;
-          allow = 0;
-#pragma unroll
-          for (int u = 0; u < kLogPer; ++u) allow |= (__shfl_sync(0xFFFFFFFFu, word, u) >> lane & 1u) << u;
-        }
+      for (int c = 0; c < W / 4; ++c) {
+        const uint4 q = *(const uint4*)(from + c * kLogThreads * 4);
+        in[4 * c] = q.x;
+        in[4 * c + 1] = q.y;
+        in[4 * c + 2] = q.z;
+        in[4 * c + 3] = q.w;
       }
-      // tokens on the row's path, past the history
+    } else if constexpr (!kHalves) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) in[u] = from[u * kLogThreads];
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) in[k] = (uint32_t)half[2 * k] | (uint32_t)half[2 * k + 1] << 16;
+      if (r + 1 < rows) load_halves();
+    }
+    // bit u: the thread's token u may be said
+    uint32_t allow = 0xFFFFFFFFu;
+    if (a.p.allow) {
+      const uint32_t word = said[(r % kDepth) * kLogThreads + tid];
+      if (VEC) {
+        allow = word >> word_shift;
+      } else {  // the warp's tokens of u are the 32 of one word
+        allow = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) allow |= (__shfl_sync(0xFFFFFFFFu, word, u) >> lane & 1u) << u;
+      }
+    }
+    float y[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const float x = element<T>(in, u);
+      y[u] = fmaf(x, factor_of(pen, seen & 1u << u, x), add[u]);
+    }
+    if (np > 0) {  // tokens on the row's path count beside the history
       uint32_t on_path = 0;
-      if (np > 0) {
-        if (VEC) {
-          on_path = hit[r][tid >> 2] >> (8 * (tid & 3)) & 0xFFu;
-        } else {
-#pragma unroll
-          for (int u = 0; u < kLogPer; ++u) on_path |= (hit[r][u * (kLogThreads / 32) + warp] >> lane & 1u) << u;
-        }
-      }
-      T res[kLogPer];
-#pragma unroll
-      for (int u = 0; u < kLogPer; ++u) {
-        const float x = to_f(in[k][u]);
-        float y = fmaf(x, x > 0.0f ? tok[u].pos : tok[u].neg, -tok[u].sub);
-        if (!(allow >> u & 1)) y = -INFINITY;
-        from_f(y, res[u]);
-      }
-      if (on_path) {
-        const int nr = n_row[r];
-        for (uint32_t m = on_path; m; m &= m - 1) {
-          const int u = __ffs(m) - 1, off = place(u);
-          int c = counts ? counts[off] : 0;
-          const bool prompt = c & DT_SEEN_PROMPT;
-          c &= DT_SEEN_PROMPT - 1;
-          for (int q = 0; q < nr; ++q) c += row_list[r * P + q] == off;
-          const Token t = token_of(pen, c, prompt, with_bias ? bias_s[off] : 0.0f);
-          T o;
-          float x = 0.0f;
-#pragma unroll
-          for (int q = 0; q < kLogPer; ++q)
-            if (q == u) x = to_f(in[k][q]);
-          from_f(allow >> u & 1 ? fmaf(x, x > 0.0f ? t.pos : t.neg, -t.sub) : -INFINITY, o);
-#pragma unroll
-          for (int q = 0; q < kLogPer; ++q)
-            if (q == u) res[q] = o;
-        }
-      }
-      T* dst = (T*)a.out + row * a.ld_out + v0;
-      if (full) {
-        constexpr int kVec = (int)sizeof(T) * kLogPer / 16;
-        uint4 q[kVec];
-        memcpy(q, res, sizeof(q));
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) ((uint4*)(dst + tid * kLogPer))[c] = q[c];
+      if (VEC) {
+        on_path = hit[r][word_at] >> word_shift & ((1u << kPer) - 1);
       } else {
 #pragma unroll
-        for (int u = 0; u < kLogPer; ++u)
-          if (v0 + place(u) < a.V) dst[place(u)] = res[u];
+        for (int u = 0; u < kPer; ++u) on_path |= (hit[r][u * (kLogThreads / 32) + warp] >> lane & 1u) << u;
       }
-      if (r + kTurn < rows) load(r + kTurn, in[k]);
+      for (; on_path; on_path &= on_path - 1) {
+        const int u = __ffs(on_path) - 1, off = place(u);
+        int c = counts ? counts[off] & (DT_SEEN_PROMPT - 1) : 0;
+        for (int q = 0; q < np; ++q) c += path_tok[q] == off && on_path_of(r, q);
+        const float plus = add_of(pen, c, with_bias ? bias_s[off] : 0.0f);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          if (q == u) {
+            const float x = element<T>(in, q);
+            y[q] = fmaf(x, factor_of(pen, true, x), plus);
+          }
+        }
+      }
     }
+    if (a.p.allow) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        if (!(allow & 1u << u)) y[u] = -INFINITY;
+    }
+    uint32_t res[W];
+    pack_words<T>(y, res);
+    if (VEC && left >= kPer * (int)sizeof(T)) {
+#pragma unroll
+      for (int c = 0; c < W; c += 4) ((uint4*)dst)[c / 4] = make_uint4(res[c], res[c + 1], res[c + 2], res[c + 3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        if (v0 + place(u) < a.V) {
+          T* to = dst + (VEC ? u : u * kLogThreads);
+          if constexpr (sizeof(T) == 4)
+            *(uint32_t*)to = res[u];
+          else
+            *(uint16_t*)to = (uint16_t)(res[u >> 1] >> (16 * (u & 1)));
+        }
+      }
+    }
+    dst += a.ld_out;
+    fetch(r + kDepth);
   }
+  copies_wait<0>();
 }
 
 struct CountArgs {
@@ -274,7 +378,10 @@ __global__ void __launch_bounds__(kLogThreads) count_kernel(CountArgs a) {
   }
 }
 
-size_t logits_smem(int P) { return (size_t)P * 8 + (size_t)kLogRows * P * 2; }
+template <typename T>
+size_t logits_smem(int P) {
+  return kRingBytes<T> + (size_t)P * 8;
+}
 
 template <typename T>
 cudaError_t launch_logits_t(dt_handle* h, int B, const LogitsArgs& a, cudaStream_t s) {
@@ -282,9 +389,9 @@ cudaError_t launch_logits_t(dt_handle* h, int B, const LogitsArgs& a, cudaStream
   const bool vec = a.ld % per16 == 0 && a.ld_out % per16 == 0 && ((uintptr_t)a.logits | (uintptr_t)a.out) % 16 == 0;
   const dim3 grid((a.V + kLogChunk - 1) / kLogChunk, B, (a.p.P + kLogRows - 1) / kLogRows);
   if (vec)
-    launch_k(logits_kernel<T, true>, grid, dim3(kLogThreads), logits_smem(a.p.P), s, a);
+    launch_k(logits_kernel<T, true>, grid, dim3(kLogThreads), logits_smem<T>(a.p.P), s, a);
   else
-    launch_k(logits_kernel<T, false>, grid, dim3(kLogThreads), logits_smem(a.p.P), s, a);
+    launch_k(logits_kernel<T, false>, grid, dim3(kLogThreads), logits_smem<T>(a.p.P), s, a);
   return cudaGetLastError();
 }
 
@@ -292,8 +399,8 @@ cudaError_t launch_logits_t(dt_handle* h, int B, const LogitsArgs& a, cudaStream
 
 cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                           const dt_logits_params* p, cudaStream_t s) {
-  LogitsArgs a{*p, logits, ld, out, ld_out, h->cfg.V, h->ws.status};
-  return h->cfg.dtype == DT_BF16 ? launch_logits_t<__nv_bfloat16>(h, B, a, s) : launch_logits_t<float>(h, B, a, s);
+  LogitsArgs a{*p, logits, ld, out, ld_out, h->cfg.V, h->cfg.V % 4 == 0 && (uintptr_t)p->counts % 16 == 0, h->ws.status};
+  return h->cfg.dtype == DT_BF16 ? launch_logits_t<uint16_t>(h, B, a, s) : launch_logits_t<float>(h, B, a, s);
 }
 
 cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int P,

@@ -4,8 +4,9 @@
 // Who gets which block follows from sums over the requests before: request b lacks
 //   need_b = max(0, ceil((len_b + n_b) / page) - owned_b)
 // blocks, and takes entries [sum_{b'<b} need, sum_{b'<=b} need) counted from the end of the free list when
-// they exist. Every CTA sums the requests before its own one (three loads a request, B <= 4096), so no
-// CTA waits for another; the lengths and counts that the others read change in a second launch.
+// they exist. Every CTA sums the requests before its own one (three loads a request, B <= 4096), so no CTA waits
+// for another; the counts that all of them read are changed by the CTA that finishes last (a ticket in the
+// handle's workspace that returns to zero by itself).
 #include <algorithm>
 
 #include "dt_internal.cuh"
@@ -14,7 +15,12 @@ namespace dt {
 namespace {
 
 constexpr int kPageThreads = 256;
-constexpr int kSlotsPerCta = 2048;  // slots of one request that a CTA writes
+constexpr int kSlotsPerCta = 512;  // slots of one request that a CTA writes at a time: two independent chains a thread
+// Up to this many CTAs the last one changes the counts; more of them queue up at the ticket, and a second launch is
+// faster. Reserve + release, 64 requests of up to 8000 slots: 13.0 us with two launches each, 15.0 with the ticket;
+// 8 requests of 9 slots: 8.2 and 8.3 us on the device, but two launches take 3 us more on the host.
+constexpr int kTicketCtas = 64;
+
 
 struct ReserveArgs {
   dt_block_pool pool;
@@ -28,6 +34,7 @@ struct ReserveArgs {
   int32_t S;
   const int32_t* slot_off;
   int32_t* status;
+  unsigned* ticket;  // null: the counts change in a launch of their own
 };
 
 // What request b asks for. status: DT_DEV_* bits of a request that cannot be served at all.
@@ -72,9 +79,56 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* smem) {
   return t;
 }
 
+// True in every thread of the CTA that comes last: what the others read and wrote before is done.
+__device__ __forceinline__ bool comes_last(unsigned* ticket, unsigned ctas) {
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicInc(ticket, ctas - 1) == ctas - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  return last;
+}
+
 __device__ __forceinline__ int free_blocks(const dt_block_pool& p) { return min(max(p.free_count[0], 0), p.n_blocks); }
 
-// CTA (c, b): slots [c * kSlotsPerCta, ...) of request b and its share of the new table entries.
+// One CTA: owned counts of the requests that were served, and the free count.
+__device__ void reserve_counts(const ReserveArgs& a, int nfree) {
+  __shared__ int64_t wsum[kPageThreads / 32];
+  __shared__ int64_t taken_s;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (a.B + kPageThreads - 1) / kPageThreads, b0 = tid * per;
+  if (tid == 0) taken_s = 0;
+  int64_t mine = 0;
+  for (int b = b0; b < min(a.B, b0 + per); ++b) mine += ask_of(a, b).need;
+  int64_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = (int64_t)shfl_u64((uint64_t)inc, max(lane - d, 0));
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) wsum[w] = inc;
+  __syncthreads();
+  int64_t upto = inc - mine;
+  for (int i = 0; i < w; ++i) upto += wsum[i];
+  int64_t taken = 0;
+  for (int b = b0; b < min(a.B, b0 + per); ++b) {
+    const Ask r = ask_of(a, b);
+    upto += r.need;
+    if (r.need > 0 && upto <= nfree) {
+      a.pool.n_owned[b] = (int32_t)r.want;
+      taken = upto;
+    }
+  }
+  if (taken > 0) atomicMax((long long*)&taken_s, (long long)taken);
+  __syncthreads();
+  if (tid == 0 && taken_s > 0) a.pool.free_count[0] = nfree - (int32_t)taken_s;
+}
+
+// CTA (c, b): slots [c * kSlotsPerCta, ...) of request b, then gridDim.x * kSlotsPerCta further, and its share of the
+// new table entries.
 __global__ void __launch_bounds__(kPageThreads) reserve_kernel(ReserveArgs a) {
   __shared__ int64_t red[kPageThreads / 32];
   pdl_begin();
@@ -98,55 +152,30 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(ReserveArgs a) {
       table[e] = id;
     }
   }
-  const int64_t lo = (int64_t)blockIdx.x * kSlotsPerCta;
-  const int64_t hi = min(min(lo + kSlotsPerCta, (int64_t)a.S), r.room);
-  for (int64_t j = lo + tid; j < hi; j += kPageThreads) {
-    int64_t slot = -1;
-    if (!status && j < r.n) {
-      const int64_t pos = r.len + j, e = pos >> a.page_shift;
-      const int32_t id = e < r.owned ? table[e] : granted(e);
-      if (id >= 0 && id < a.pool.n_blocks)
-        slot = ((int64_t)id << a.page_shift) + (pos & (a.pool.page - 1));
-      else
-        set_status(a.status, DT_DEV_BAD_PAGE);
+  const int64_t hi = min((int64_t)a.S, r.room);
+  for (int64_t lo = (int64_t)blockIdx.x * kSlotsPerCta; lo < hi; lo += (int64_t)gridDim.x * kSlotsPerCta) {
+#pragma unroll
+    for (int u = 0; u < kSlotsPerCta / kPageThreads; ++u) {
+      const int64_t j = lo + tid + u * kPageThreads;
+      if (j >= hi) break;
+      int64_t slot = -1;
+      if (!status && j < r.n) {
+        const int64_t pos = r.len + j, e = pos >> a.page_shift;
+        const int32_t id = e < r.owned ? table[e] : granted(e);
+        if (id >= 0 && id < a.pool.n_blocks)
+          slot = ((int64_t)id << a.page_shift) + (pos & (a.pool.page - 1));
+        else
+          set_status(a.status, DT_DEV_BAD_PAGE);
+      }
+      a.slots[r.first + j] = slot;
     }
-    a.slots[r.first + j] = slot;
   }
+  if (a.ticket && comes_last(a.ticket, gridDim.x * gridDim.y)) reserve_counts(a, nfree);
 }
 
-// One CTA: owned counts of the requests that were served, and the free count.
-__global__ void __launch_bounds__(1024) reserve_counts_kernel(ReserveArgs a) {
-  __shared__ int64_t wsum[32];
-  __shared__ int64_t taken_s;
+__global__ void __launch_bounds__(kPageThreads) reserve_counts_kernel(ReserveArgs a) {
   pdl_begin();
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int nfree = free_blocks(a.pool);
-  const int per = (a.B + 1023) / 1024, b0 = tid * per;
-  if (tid == 0) taken_s = 0;
-  int64_t mine = 0;
-  for (int b = b0; b < min(a.B, b0 + per); ++b) mine += ask_of(a, b).need;
-  int64_t inc = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = (int64_t)shfl_u64((uint64_t)inc, max(lane - d, 0));
-    if (lane >= d) inc += o;
-  }
-  if (lane == 31) wsum[w] = inc;
-  __syncthreads();
-  int64_t upto = inc - mine;
-  for (int i = 0; i < w; ++i) upto += wsum[i];
-  int64_t taken = 0;
-  for (int b = b0; b < min(a.B, b0 + per); ++b) {
-    const Ask r = ask_of(a, b);
-    upto += r.need;
-    if (r.need > 0 && upto <= nfree) {
-      a.pool.n_owned[b] = (int32_t)r.want;
-      taken = upto;
-    }
-  }
-  atomicMax((long long*)&taken_s, (long long)taken);
-  __syncthreads();
-  if (tid == 0 && taken_s > 0) a.pool.free_count[0] = nfree - (int32_t)taken_s;
+  reserve_counts(a, free_blocks(a.pool));
 }
 
 struct ReleaseArgs {
@@ -155,6 +184,7 @@ struct ReleaseArgs {
   int32_t B;
   const int32_t* keep_len;
   int32_t* status;
+  unsigned* ticket;  // null: the counts change in a launch of their own
 };
 
 // Blocks that request b keeps; `back` the ones it gives back (0 for a corrupt count).
@@ -168,6 +198,17 @@ __device__ __forceinline__ int keep_of(const ReleaseArgs& a, int b, int& back, b
   const int keep = (int)min((int64_t)owned, ((int64_t)keep_len + a.pool.page - 1) >> a.page_shift);
   back = owned - keep;
   return keep;
+}
+
+// One CTA: owned counts and the free count after `total` blocks have come back.
+__device__ void release_counts(const ReleaseArgs& a, int nfree, int64_t total) {
+  for (int i = threadIdx.x; i < a.B; i += kPageThreads) {
+    int back;
+    bool bad;
+    const int kept = keep_of(a, i, back, bad);
+    if (back) a.pool.n_owned[i] = kept;
+  }
+  if (threadIdx.x == 0 && total > 0) a.pool.free_count[0] = (int32_t)min(nfree + total, (int64_t)a.pool.n_blocks);
 }
 
 // CTA b: the r-th block given back, counted over requests and then entries in ascending order, goes to
@@ -195,22 +236,20 @@ __global__ void __launch_bounds__(kPageThreads) release_kernel(ReleaseArgs a) {
     if (at < a.pool.n_blocks) a.pool.free_list[at] = table[keep + e];
     table[keep + e] = -1;
   }
+  if (a.ticket && comes_last(a.ticket, gridDim.x)) release_counts(a, nfree, total);
 }
 
-__global__ void __launch_bounds__(1024) release_counts_kernel(ReleaseArgs a) {
-  __shared__ int64_t red[32];
+__global__ void __launch_bounds__(kPageThreads) release_counts_kernel(ReleaseArgs a) {
+  __shared__ int64_t red[kPageThreads / 32];
   pdl_begin();
   int64_t total = 0;
-  for (int b = threadIdx.x; b < a.B; b += 1024) {
+  for (int i = threadIdx.x; i < a.B; i += kPageThreads) {
     int back;
     bool bad;
-    const int keep = keep_of(a, b, back, bad);
+    keep_of(a, i, back, bad);
     total += back;
-    if (back) a.pool.n_owned[b] = keep;
   }
-  total = block_sum(total, red);
-  if (threadIdx.x == 0 && total > 0)
-    a.pool.free_count[0] = (int32_t)min((int64_t)free_blocks(a.pool) + total, (int64_t)a.pool.n_blocks);
+  release_counts(a, free_blocks(a.pool), block_sum(total, red));
 }
 
 // ------------------------------------------------------------------------------- commit --------
@@ -231,33 +270,10 @@ struct PagedCommitArgs {
 
 constexpr int kMaxTok = 64;  // tokens of a CTA
 
-// CTA (c, b, p): tokens [c * T, (c + 1) * T) of request b in plane p.
-__global__ void __launch_bounds__(kPageThreads) commit_paged_kernel(PagedCommitArgs a) {
-  __shared__ const char* src_s[kMaxTok];
-  __shared__ char* dst_s[kMaxTok];
-  pdl_begin();
-  const int b = blockIdx.y, plane = blockIdx.z, tid = threadIdx.x;
-  const int64_t n64 = (int64_t)a.n_new[b] + a.n_extra;
-  int64_t first = (int64_t)b * a.S, room = a.S;
-  int status = 0;
-  if (a.slot_off) {
-    first = a.slot_off[b];
-    room = (int64_t)a.slot_off[b + 1] - first;
-    if (first < 0 || room < 0 || first + room > a.n_slots) status = DT_DEV_BAD_PAGE;
-  }
-  if (n64 < 0) status = DT_DEV_BAD_PAGE;
-  if (!status && (n64 > min((int64_t)a.S, room) || (a.path && n64 > a.D_path))) status = DT_DEV_KV_FULL;
-  const int n = (int)n64;
-  if (!status && n > 0 && (a.slots[first] < 0 || a.slots[first + n - 1] < 0)) status = DT_DEV_KV_FULL;
-  const bool lead = plane == 0 && blockIdx.x == 0 && tid == 0;
-  if (lead) {
-    if (status) set_status(a.status, status);
-    const int32_t len = a.seq_len[b];
-    a.len_out[b] = status ? len : len + n;
-  }
-  const int t0 = blockIdx.x * a.tok_per_cta;
-  if (status || t0 >= n) return;
-  const int cnt = min(a.tok_per_cta, n - t0);
+// Tokens [t0, t0 + cnt) of request b in one plane; all threads of the CTA.
+__device__ __forceinline__ void commit_rows(const PagedCommitArgs& a, int b, int plane, int64_t first, int t0, int cnt,
+                                            const char** src_s, char** dst_s) {
+  const int tid = threadIdx.x;
   if (tid < cnt) {
     const int j = t0 + tid;
     const int64_t slot = a.slots[first + j];
@@ -304,6 +320,38 @@ __global__ void __launch_bounds__(kPageThreads) commit_paged_kernel(PagedCommitA
   }
 }
 
+// CTA (c, b, p): tokens [c * T, (c + 1) * T) of request b in plane p, then gridDim.x * T further.
+__global__ void __launch_bounds__(kPageThreads) commit_paged_kernel(PagedCommitArgs a) {
+  __shared__ const char* src_s[kMaxTok];
+  __shared__ char* dst_s[kMaxTok];
+  pdl_begin();
+  const int b = blockIdx.y, plane = blockIdx.z, tid = threadIdx.x;
+  const int64_t n64 = (int64_t)a.n_new[b] + a.n_extra;
+  int64_t first = (int64_t)b * a.S, room = a.S;
+  int status = 0;
+  if (a.slot_off) {
+    first = a.slot_off[b];
+    room = (int64_t)a.slot_off[b + 1] - first;
+    if (first < 0 || room < 0 || first + room > a.n_slots) status = DT_DEV_BAD_PAGE;
+  }
+  if (n64 < 0) status = DT_DEV_BAD_PAGE;
+  if (!status && (n64 > min((int64_t)a.S, room) || (a.path && n64 > a.D_path))) status = DT_DEV_KV_FULL;
+  const int n = (int)n64;
+  if (!status && n > 0 && (a.slots[first] < 0 || a.slots[first + n - 1] < 0)) status = DT_DEV_KV_FULL;
+  const bool lead = plane == 0 && blockIdx.x == 0 && tid == 0;
+  if (lead) {
+    if (status) set_status(a.status, status);
+    const int32_t len = a.seq_len[b];
+    a.len_out[b] = status ? len : len + n;
+  }
+  if (status) return;
+  const int64_t begin = (int64_t)blockIdx.x * a.tok_per_cta;
+  for (int64_t t0 = begin; t0 < n; t0 += (int64_t)gridDim.x * a.tok_per_cta) {
+    if (t0 != begin) __syncthreads();  // the addresses of the last turn have been used
+    commit_rows(a, b, plane, first, (int)t0, (int)min((int64_t)a.tok_per_cta, n - t0), src_s, dst_s);
+  }
+}
+
 int shift_of(int page) {
   int s = 0;
   while ((1 << s) < page) ++s;
@@ -312,25 +360,35 @@ int shift_of(int page) {
 
 }  // namespace
 
+// CTAs of a request that has at most S of the slots, `each` at a time. Packed slots leave S loose: four times a
+// request's mean share bounds them there, and longer requests take several turns.
+static int chunks_of(int S, int64_t n_slots, int B, int each, bool packed) {
+  const int64_t most = ((int64_t)S + each - 1) / each;
+  if (!packed) return (int)most;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 4 * ((n_slots + (int64_t)each * B - 1) / ((int64_t)each * B))));
+}
+
 cudaError_t launch_kv_reserve(dt_handle* h, int B, const dt_block_pool* pool, const int32_t* seq_len,
                               const int32_t* n_new, int n_extra, int64_t* slots, int64_t n_slots, int S,
                               const int32_t* slot_off, cudaStream_t s) {
-  ReserveArgs a{*pool, shift_of(pool->page), B, seq_len, n_new, n_extra, slots, n_slots, S, slot_off, h->ws.status};
-  const int chunks = (S + kSlotsPerCta - 1) / kSlotsPerCta;
+  ReserveArgs a{*pool, shift_of(pool->page), B, seq_len, n_new, n_extra, slots, n_slots, S, slot_off, h->ws.status, h->ws.ticket};
+  const int chunks = chunks_of(S, n_slots, B, kSlotsPerCta, slot_off != nullptr);
+  if ((int64_t)chunks * B > kTicketCtas) a.ticket = nullptr;
   launch_k(reserve_kernel, dim3(chunks, B), dim3(kPageThreads), 0, s, a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  launch_k(reserve_counts_kernel, dim3(1), dim3(1024), 0, s, a);
+  if (e != cudaSuccess || a.ticket) return e;
+  launch_k(reserve_counts_kernel, dim3(1), dim3(kPageThreads), 0, s, a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_release(dt_handle* h, int B, const dt_block_pool* pool, const int32_t* keep_len,
                               cudaStream_t s) {
-  ReleaseArgs a{*pool, shift_of(pool->page), B, keep_len, h->ws.status};
+  ReleaseArgs a{*pool, shift_of(pool->page), B, keep_len, h->ws.status, h->ws.ticket};
+  if (B > kTicketCtas) a.ticket = nullptr;
   launch_k(release_kernel, dim3(B), dim3(kPageThreads), 0, s, a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  launch_k(release_counts_kernel, dim3(1), dim3(1024), 0, s, a);
+  if (e != cudaSuccess || a.ticket) return e;
+  launch_k(release_counts_kernel, dim3(1), dim3(kPageThreads), 0, s, a);
   return cudaGetLastError();
 }
 
@@ -356,7 +414,7 @@ cudaError_t launch_commit_kv_paged(dt_handle* h, int B, const dt_kv_rows* kv, in
   a.seq_len = seq_len;
   a.len_out = len_out;
   a.status = h->ws.status;
-  launch_k(commit_paged_kernel, dim3((S + a.tok_per_cta - 1) / a.tok_per_cta, B, kv->planes), dim3(kPageThreads), 0,
+  launch_k(commit_paged_kernel, dim3(chunks_of(S, n_slots, B, a.tok_per_cta, slot_off != nullptr), B, kv->planes), dim3(kPageThreads), 0,
            s, a);
   return cudaGetLastError();
 }

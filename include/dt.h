@@ -427,7 +427,7 @@ typedef struct {
  *   slot_off NULL: [B][S]; else (device [B+1]) packed: request b's at slot_off[b] .. slot_off[b+1] - 1,
  *   at most S of them; entries past slot_off[B] are left as they were.
  * n_slots: entries of the slots buffer (offsets beyond it set DT_DEV_BAD_PAGE, the request gets none).
- * Two launches, or one for a few slots. seq_len is read only (dt_commit_kv_paged advances it). */
+ * One launch. seq_len is read only (dt_commit_kv_paged advances it). */
 int dt_kv_reserve(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* seq_len, const int32_t* n_new,
                   int32_t n_extra, int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
                   cudaStream_t s);
