@@ -100,7 +100,7 @@ class RoundRunner:
         self.prune_out = make_prune_out(width=self.width, stop=self.stop)
         self.verify_out = make_prune_out(m=self.m_dev)
 
-    def run(self, roots, draft_rows, target_rows, seed=0, rnd=0, M=None, n0=0, timing=None):
+    def run(self, roots, draft_rows, target_rows, seed=0, rnd=0, M=None, n0=0, timing=None, kv=None, tokens=None):
         """Launch one round; returns nothing (outputs live in this object's tensors).
 
         ``timing`` (optional): an object with ``start(kind)`` and ``stop(kind)``; the composite
@@ -108,6 +108,10 @@ class RoundRunner:
         dt_verify_rows + dt_verify_accept: the same kernels) and each part is bracketed by
         start/stop with kind "expand", "prune_select", "verify_rows" or "verify_accept", e.g. to
         record events around them.
+        ``tokens`` (optional, paged.TokenState): the target rows get its penalties, biases and grammar words in
+        place before they are verified, and the accepted tokens are counted afterwards.
+        ``kv`` (optional, paged.PagedCache, packed like the rows): the accepted positions' rows of kv.tmp, which
+        ``target_rows`` fills, move into the pages after the verify.
         """
         h = self.h
         pol = self.policy
@@ -190,6 +194,8 @@ class RoundRunner:
         else:
             dt_build_tree_meta(h, self.selected, self.m_cap, self.meta, self.pos_offset)
         logits = target_rows(self.meta)
+        if tokens is not None:
+            tokens.process(logits, self.meta, self.packed)
         mode = (DT_SAMPLE if self.T == 1 else DT_GREEDY) | (DT_VERIFY_PACKED if self.packed else 0)
         if self.draw:
             if timing is not None:
@@ -211,3 +217,7 @@ class RoundRunner:
                       self.top8)
         if pol == "graft":
             dt_adj_update(h, M, self.meta, self.top8)
+        if tokens is not None:
+            tokens.commit(self.accept_len, self.accept_path, self.meta)
+        if kv is not None:
+            kv.commit(self.accept_len, self.accept_path, self.meta)

@@ -1,0 +1,191 @@
+"""Rounds with a paged cache and processed rows, as a serving loop runs them.
+
+Every round the target's "forward" draws keys, values and queries for the tree's positions, attends layer by layer through
+``PagedCache`` and makes its rows from the result; ``RoundRunner`` processes, verifies, counts and commits. A shadow of
+the state is kept in plain form (dense keys and values a request, a count table); attention and processed rows are compared
+with the definitions in 64 bits, pages, lengths and counts exactly. Tolerances as in the operators' own tests: for bf16 with
+u = 2^-8, 2.1 u sum p |v| + u |o| covers the rounded weights, the rounded result and the fp32 sums (under 2^-11 of
+sum p |v| here); rows 8 * 2^-24 of the largest intermediate plus half a step.
+"""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+SEEN = 0x40000000
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as t
+
+    if not t.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+
+    __graft_entry__.build()
+    return t
+
+
+@pytest.mark.parametrize("packed,T", [(False, 0), (True, 1)])
+def test_rounds_with_pages_and_penalties(torch, packed, T):
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache, TokenState
+    from dynamic_draft_tree_gb300.rounds import RoundRunner
+
+    B, V, K, k, D, m, layers, H_q, H_kv, Dh, page = 3, 1500, 4, 4, 3, 16, 2, 8, 2, 64, 16
+    P, D_path = m + 1, D + 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5 + T)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    run = RoundRunner("eagle", B, V, K, k, D, P, D_path, m, dt.DT_F32, T=T, packed=packed)
+    h = run.h
+    kv = PagedCache(h, B, P, layers, H_q, H_kv, Dh, n_blocks=40, max_blocks=12, page=page, D_path=D_path, packed=packed)
+    rep = torch.tensor([1.3, 1.0, 0.9], device="cuda")
+    freq = torch.tensor([0.2, 0.0, 0.5], device="cuda")
+    bias_ids = torch.randint(0, V, (B, 5), generator=g, **i32)
+    bias_vals = torch.randn(B, 5, generator=g, device="cuda")
+    allow = torch.randint(-2 ** 31, 2 ** 31, (B * P, (V + 31) // 32), generator=g, device="cuda",
+                          dtype=torch.int64).to(torch.int32)
+    state = TokenState(h, B, repetition=rep, frequency=freq, bias_ids=bias_ids, bias_vals=bias_vals,
+                       allow=allow if packed else allow.view(B, P, -1))
+    # prompts
+    n0 = [37, 0, 16]
+    off = [0, 37, 37, 53]
+    d_off, d_n0 = torch.tensor(off, **i32), torch.tensor(n0, **i32)
+    prompt_kv = torch.randn(2 * layers, 53, H_kv, Dh, generator=g, device="cuda").bfloat16()
+    prompt_tok = torch.randint(0, V, (53,), generator=g, **i32)
+    kv.prefill(prompt_kv, d_n0, d_off)
+    state.prompt(prompt_tok, d_n0, row_off=d_off)
+    dense = [prompt_kv[:, off[b]:off[b + 1]] for b in range(B)]
+    counts = torch.zeros(B, V, dtype=torch.int64)
+    for b in range(B):
+        for t in prompt_tok[off[b]:off[b + 1]].tolist():
+            counts[b, t] |= SEEN
+    roots = torch.randint(0, V, (B,), generator=g, **i32)
+    out_w = torch.randn(H_q * Dh, V, generator=g, device="cuda") * 0.3
+    seen = {}
+
+    def draft_rows(d, ftok):
+        return torch.randn(B, 1 if d == 1 else k, V, generator=g, device="cuda")
+
+    def target_rows(meta):
+        shape = (B * P,) if packed else (B, P)
+        x = 0.0
+        seen["attn"] = []
+        for layer in range(layers):
+            q = torch.randn(*shape, H_q, Dh, generator=g, device="cuda").bfloat16()
+            kv.tmp[2 * layer:2 * layer + 2] = torch.randn(2, *shape, H_kv, Dh, generator=g, device="cuda").bfloat16()
+            o = torch.zeros(*shape, H_q, Dh, device="cuda", dtype=torch.bfloat16)
+            kv.attend(layer, q, o, meta)
+            seen["attn"].append((q, o))
+            x = x + o.float()
+        rows = x.flatten(-2) @ out_w
+        seen["rows"], seen["logits"] = rows.clone(), rows
+        return rows
+
+    for rnd in range(4):
+        tmp_before = [x.shape[1] for x in dense]
+        run.run(roots, draft_rows, target_rows, seed=11, rnd=rnd, kv=kv, tokens=state)
+        assert dt.dt_get_status(h) in (0, dt.DT_DEV_BAD_LOGITS)  # a grammar may leave a verified row nothing
+        meta = run.meta.numpy()
+        acc, path = run.accept_len.tolist(), run.accept_path.tolist()
+        flat = lambda x: x if packed else x.flatten(0, 1)  # noqa: E731
+        for b in range(B):
+            n = int(meta["n_pos"][b])
+            r0 = int(meta["row_off"][b]) if packed else b * P
+            mask = torch.from_numpy(meta["mask"][b, :n, :n].copy()).cuda().bool()
+            L = tmp_before[b]
+            for layer, (q, o) in enumerate(seen["attn"]):
+                tk, tv = (flat(kv.tmp[2 * layer + j])[r0:r0 + n] for j in (0, 1))
+                key = torch.cat([dense[b][2 * layer], tk]).double().repeat_interleave(H_q // H_kv, 1)
+                val = torch.cat([dense[b][2 * layer + 1], tv]).double().repeat_interleave(H_q // H_kv, 1)
+                ok = torch.cat([torch.ones(n, L, dtype=torch.bool, device="cuda"), mask], 1)
+                z = torch.einsum("ihd,jhd->hij", flat(q)[r0:r0 + n].double(), key) * Dh ** -0.5
+                p = torch.softmax(z.masked_fill(~ok, -math.inf), -1)
+                want = torch.einsum("hij,jhd->ihd", p, val)
+                size = torch.einsum("hij,jhd->ihd", p, val.abs())
+                got = flat(o)[r0:r0 + n].double()
+                assert float(((got - want).abs() - (2.1 * size + want.abs()) * 2.0 ** -8).max()) <= 0
+            for i in range(n):
+                x = flat(seen["rows"])[r0 + i].double().cpu()
+                c = (counts[b] & (SEEN - 1)).clone()
+                for j in range(n):
+                    if meta["mask"][b, i, j] and meta["tokens"][b, j] >= 0:
+                        c[int(meta["tokens"][b, j])] += 1
+                known = (c > 0) | (counts[b] >= SEEN)
+                r = float(rep[b])
+                y = torch.where(known, torch.where(x > 0, x / r, x * r), x) - float(freq[b]) * c
+                extra = torch.zeros(V, dtype=torch.float64)
+                for t, v in zip(bias_ids[b].tolist(), bias_vals[b].tolist()):
+                    y[t] += v
+                    extra[t] += abs(v)
+                words = allow[r0 + i].cpu()
+                v = torch.arange(V)
+                can = (words[v >> 5] >> (v & 31)) & 1 == 1
+                got = flat(seen["logits"])[r0 + i].double().cpu()
+                assert torch.isinf(got[~can]).all() and (got[~can] < 0).all()
+                tol = 8 * 2.0 ** -24 * (x.abs() * max(r, 1 / r) + float(freq[b]) * c + extra) + 2.0 ** -24 * y.abs()
+                assert float(((got - y).abs() - tol)[can].max()) <= 0
+            # commits
+            rows = [r0 + p_ for p_ in path[b][:acc[b] + 1]]
+            dense[b] = torch.cat([dense[b], kv.tmp[:, rows] if packed else
+                                  kv.tmp[:, b, path[b][:acc[b] + 1]]], 1)
+            for p_ in path[b][:acc[b] + 1]:
+                counts[b, int(meta["tokens"][b, p_])] += 1
+        assert kv.seq_len.tolist() == [x.shape[1] for x in dense]
+        assert torch.equal(state.counts.cpu().long(), counts)
+        for b in range(B):
+            n = dense[b].shape[1]
+            blocks = kv.pool.block_table[b, :-(-n // page)].long()
+            assert (blocks >= 0).all()
+            have = kv.pages[:, blocks].flatten(1, 2)[:, :n]
+            assert torch.equal(have, dense[b])
+        roots = run.bonus.clone()
+    # every request ends: all pages come back
+    kv.release(torch.zeros(B, **i32))
+    assert int(kv.pool.free_count) == 40 and sorted(kv.pool.free_list.tolist()) == list(range(40))
+    h.close()
+
+
+def test_committed_round_in_a_graph(torch):
+    """Reserve, commit and count captured once and replayed: lengths, pages and counts advance with every replay."""
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache, TokenState
+
+    B, P, V = 2, 5, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    h = dt.Handle(B, V, 1, 1, 1, P)
+    kv = PagedCache(h, B, P, 1, 2, 1, 64, n_blocks=12, max_blocks=6, page=8, D_path=4)
+    state = TokenState(h, B)
+    meta = dt.Meta(B, P, 4)
+    meta.tokens.copy_(torch.arange(B * P, **i32).view(B, P))
+    acc = torch.tensor([3, 0], **i32)
+    path = torch.tensor([[0, 1, 3, 4], [0, -1, -1, -1]], **i32)
+
+    def commit():
+        state.commit(acc, path, meta)
+        kv.commit(acc, path, meta)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        commit()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        commit()
+    seen = [kv.tmp.clone()]
+    for rnd in range(4):
+        kv.tmp.copy_(torch.randn_like(kv.tmp))
+        seen.append(kv.tmp.clone())
+        g.replay()
+    torch.cuda.synchronize()
+    assert dt.dt_get_status(h) == 0
+    assert kv.seq_len.tolist() == [20, 5]
+    assert state.counts[0, [0, 1, 3, 4]].tolist() == [5] * 4 and int(state.counts.sum()) == 25
+    for b, rows in ((0, [0, 1, 3, 4]), (1, [0])):
+        want = torch.cat([x[:, b, rows] for x in seen], 1)
+        n = want.shape[1]
+        have = kv.pages[:, kv.pool.block_table[b, :-(-n // 8)].long()].flatten(1, 2)[:, :n]
+        assert torch.equal(have, want)
+    h.close()
