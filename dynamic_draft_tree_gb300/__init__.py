@@ -449,15 +449,22 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
         mh = mask.shape
         if len(mh) != 3 or mh[0] < B or mh[1] != P or mh[2] != P:
             raise ValueError("mask must be [B][P][P]")
+    if not (out.dtype is dtype and k_new.dtype is dtype and v_new.dtype is dtype and k_pages.dtype is dtype
+            and v_pages.dtype is dtype):
+        raise ValueError(f"q, k_new, v_new, k_pages, v_pages and out must all be {dtype}")
+    if not (q.get_device() == dev and out.get_device() == dev and k_new.get_device() == dev and v_new.get_device() == dev
+            and k_pages.get_device() == dev and v_pages.get_device() == dev):
+        raise ValueError("q, k_new, v_new, k_pages, v_pages and out must be on the current CUDA device")
+    if not (qs[-1] == 1 and os_[-1] == 1 and ks[-1] == 1 and vs[-1] == 1 and kp[3] == 1 and vp_[3] == 1):
+        raise ValueError("q, k_new, v_new, k_pages, v_pages and out need a contiguous last dimension")
     a = _pack_attn(B, P, qh[-2], nh[-2], qh[-1], code, qh[-1] ** -0.5 if scale is None else scale, shared_len, rows,
-                   _strided(q, dtype, dev, qs, "q"), qs[-3], qs[-2], _strided(out, dtype, dev, os_, "out"), os_[-3],
-                   os_[-2], _strided(k_new, dtype, dev, ks, "k_new"), _strided(v_new, dtype, dev, vs, "v_new"), ks[-3],
-                   ks[-2], vs[-3], vs[-2], _strided(k_pages, dtype, dev, kp, "k_pages"),
-                   _strided(v_pages, dtype, dev, vp_, "v_pages"), kp[0], kp[1], kp[2], vp_[0], vp_[1], vp_[2], ph[0],
-                   ph[1], _dev(block_table, _I32, dev, "block_table"), th[1], _dev(seq_len, _I32, dev, "seq_len", B),
-                   _dev(n_pos, _I32, dev, "n_pos"), _dev(mask, _U8, dev, "mask"),
-                   _dev(row_off, _I32, dev, "row_off", B + 1), _dev(workspace, _U8, dev, "workspace"),
-                   workspace.numel())
+                   q.data_ptr(), qs[-3], qs[-2], out.data_ptr(), os_[-3], os_[-2], k_new.data_ptr(), v_new.data_ptr(),
+                   ks[-3], ks[-2], vs[-3], vs[-2], k_pages.data_ptr(), v_pages.data_ptr(), kp[0], kp[1], kp[2], vp_[0],
+                   vp_[1], vp_[2], ph[0], ph[1], _dev(block_table, _I32, dev, "block_table"), th[1],
+                   _dev(seq_len, _I32, dev, "seq_len", B), _dev(n_pos, _I32, dev, "n_pos"),
+                   0 if mask is None else _dev(mask, _U8, dev, "mask"),
+                   0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
+                   _dev(workspace, _U8, dev, "workspace"), workspace.numel())
     rc = lib.dt_tree_attention(h.h, a, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)

@@ -48,6 +48,7 @@ struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
 struct AttnParams {
   dt_attn_args a;
   int32_t G, page_shift, tree_box;
+  int32_t test_stop;  // test only: every wait that is not over at once gives up
   int32_t pos, rows2; // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
   uint32_t g_magic;   // ceil(2^32 / G), for position_of
   float c;            // scale * log2 e
@@ -448,9 +449,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
       int stage;
       uint32_t parity;
       ring<kStages>(k, stage, parity);
-      const long long t0 = clock64();
-      while (!tc::bar_try(&full[stage], parity) && clock64() - t0 < tc::kWaitClocks) {
-      }
+      tc::bar_drain(&full[stage], parity);
     }
 }
 
@@ -490,7 +489,11 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
         tc::tma_load_3d(q_smem + x * S::kHalf, q_map, (x % kHalves) * 64, s.h * p.G, (int)s.base + s.i0 + x / kHalves * p.pos,
                         &sh.qfull);
     }
-    if (!tc::bar_wait_warp(&sh.qfull, nq++ & 1, &sh.stop)) return;
+    if (!tc::bar_wait_warp(&sh.qfull, nq & 1, &sh.stop)) {
+      tc::bar_drain(&sh.qfull, nq & 1);  // no load may land once the CTA is gone
+      return;
+    }
+    ++nq;
     int t = t0;
     // O += P V of unit v - 2, then S of unit v
     for (int v = 0; v < units + 2; ++v) {
@@ -822,7 +825,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
   Segments segs;
   Segment s;
   uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
-  while (segs.next(sh, s, (threadIdx.x & 31) == 0)) {
+  for (uint32_t seg = 0; segs.next(sh, s, (threadIdx.x & 31) == 0); ++seg) {
     const bool dual = s.rows > p.rows2 >> 1;
     const int tiles = s.t1 - s.t0;
     const int mine = dual ? tiles : (tiles + 1 - group) / 2;
@@ -908,6 +911,9 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
         tc::bar_arrive(&sh.phalf[group][1]);
       }
     }
+    // A group without a unit in this segment still comes along: its arrival on qfree below must not fall into the last
+    // segment's phase, which is over once this segment's Q has been loaded.
+    if (mine == 0 && !tc::bar_wait_warp(&sh.qfull, seg & 1, &sh.stop)) return;
     // the group's last product
     if (mine > 0) {
       if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
@@ -964,7 +970,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc::bar_init(&sh.segempty[i], kSegReaders);
     }
     tc::bar_init_fence();
-    sh.stop = 0;
+    sh.stop = p.test_stop;
     sh.odd_values = 0;
     tc::tma_prefetch_map(&q_map);
     tc::tma_prefetch_map(&k_map);
@@ -993,14 +999,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc::fence_after();
   if (warp == 9) {
     if (sh.stop) {  // products in flight end before their memory goes
-      if (lane == 0) {
+      if (tc::elect()) {  // the thread that issued them
         set_status(p.status, DT_DEV_TIMEOUT);
         tc::bar_init(&sh.mlready, 1);
         tc::bar_init_fence();
         tc::mma_commit(&sh.mlready);
-        const long long t0 = clock64();
-        while (!tc::bar_try(&sh.mlready, 0) && clock64() - t0 < tc::kWaitClocks) {
-        }
+        tc::bar_drain(&sh.mlready, 0);
       }
       __syncwarp();
     }
@@ -1224,6 +1228,7 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.ml_sh = (float2*)(ws + L.ml_sh);
   p.o_sh = (float*)(ws + L.o_sh);
   p.status = h->ws.status;
+  p.test_stop = h->cfg.flags & DT_FLAG_TEST_TIMEOUT ? 1 : 0;
   CUtensorMap m[5];
   const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
   const int64_t ks[4] = {1, a->k_head, a->k_tok, a->k_block}, vs[4] = {1, a->v_head, a->v_tok, a->v_block};

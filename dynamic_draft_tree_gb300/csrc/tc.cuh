@@ -51,6 +51,13 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, vo
   return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, stop));
 }
 
+// After a give-up: waits (again at most kWaitClocks) for what is still on its way to this phase.
+__device__ __forceinline__ void bar_drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {
+  }
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------- TMA loads ------

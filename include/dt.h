@@ -78,7 +78,9 @@ enum {
 enum { DT_FLAG_TEST_TIMEOUT = 1 }; /* test only: the expansion row scans (dt_expand_layer and the
                                       calls built on it, dt_block_expand) give their first bounded
                                       copy wait a limit of zero, so it runs out; the verify streaming
-                                      pass behaves as if its reads had timed out (reads nothing).
+                                      pass behaves as if its reads had timed out (reads nothing);
+                                      dt_tree_attention gives up every wait that is not over at
+                                      once, after its copies in flight have landed.
                                       Either way empty results and DT_DEV_TIMEOUT, no fault */
 
 typedef struct dt_handle dt_handle;

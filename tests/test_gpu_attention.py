@@ -171,6 +171,10 @@ CASES = {
     "heads first": dict(B=2, P=7, H_kv=4, G=2, D=128, page=32, lens=[190, 33], heads_first=True),
     "long": dict(B=2, P=3, H_kv=1, G=4, D=128, page=64, lens=[8191, 5000]),
     "many requests": dict(B=67, P=2, H_kv=1, G=2, D=64, page=16, lens=[(7 * i) % 150 for i in range(67)]),
+    "more requests than threads": dict(B=801, P=2, H_kv=1, G=2, D=64, page=16, lens=[(11 * i) % 97 for i in range(801)],
+                                       n_pos=[1 + i % 2 for i in range(801)], packed=True),
+    "more requests than threads, shared": dict(B=500, P=1, H_kv=2, G=1, D=64, page=16, tree=False,
+                                               lens=[64 + i % 40 for i in range(500)], shared=64),
     "shared": dict(B=5, P=21, H_kv=2, G=4, D=128, page=32, lens=[256, 257, 300, 400, 256], shared=256, packed=True,
                    n_pos=[21, 3, 10, 21, 1]),
     "shared, odd pages": dict(B=4, P=9, H_kv=2, G=5, D=80, page=16, lens=[48, 49, 200, 112], shared=48, dtype="fp16"),
@@ -312,6 +316,28 @@ def test_bad_tables_are_reported(torch):
     pr.call(dt, h, ws)
     assert dt.dt_get_status(h) & dt.DT_DEV_BAD_PAGE
     h.close()
+
+
+def test_waits_that_run_out_are_reported(torch):
+    """With DT_FLAG_TEST_TIMEOUT no wait is taken: the call ends, says so, and the context stays usable."""
+    import dynamic_draft_tree_gb300 as dt
+
+    for case in ("cast tree packed", "one token", "shared"):
+        pr = Problem(torch, **CASES[case])
+        h = dt.Handle(pr.B, 2, 1, 1, 1, pr.P, flags=dt.DT_FLAG_TEST_TIMEOUT)
+        _, ws = pr.handle(dt)
+        ws.zero_()
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) & dt.DT_DEV_TIMEOUT
+        h.close()
+        h, ws = pr.handle(dt)
+        pr.out.fill_(7.0)
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == 0
+        got = pr.out.clone()
+        pr.out.fill_(7.0)
+        _check(pr, got)
+        h.close()
 
 
 def test_refusals(torch):
