@@ -431,7 +431,9 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
     qs, os_, ks, vs, kp, vp_ = q.stride(), out.stride(), k_new.stride(), v_new.stride(), k_pages.stride(), v_pages.stride()
     if len(qh) != (4 if row_off is None else 3) or out.shape != qh or len(ph) != 4 or v_pages.shape != ph:
         raise ValueError("q and out need [B][P][H][D] ([rows][H][D] packed), pages [blocks][page][H_kv][D]")
-    if v_new.shape != nh or nh[:-2] != qh[:-2] or nh[-1] != qh[-1] or ph[2:] != nh[-2:]:
+    D = qh[-1]
+    if v_new.shape != nh or len(nh) != len(qh) or nh[0] != qh[0] or nh[-3] != qh[-3] or nh[-1] != D or ph[2] != nh[-2] \
+            or ph[3] != D:
         raise ValueError("k_new, v_new and the pages must match q's rows and one another's heads and head size")
     if len(th) != 2 or th[0] < B:
         raise ValueError("block_table must be [B][max_blocks]")
@@ -457,14 +459,20 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
         raise ValueError("q, k_new, v_new, k_pages, v_pages and out must be on the current CUDA device")
     if not (qs[-1] == 1 and os_[-1] == 1 and ks[-1] == 1 and vs[-1] == 1 and kp[3] == 1 and vp_[3] == 1):
         raise ValueError("q, k_new, v_new, k_pages, v_pages and out need a contiguous last dimension")
-    a = _pack_attn(B, P, qh[-2], nh[-2], qh[-1], code, qh[-1] ** -0.5 if scale is None else scale, shared_len, rows,
+    if not (block_table.dtype is _I32 and seq_len.dtype is _I32 and n_pos.dtype is _I32 and workspace.dtype is _U8
+            and block_table.get_device() == dev and seq_len.get_device() == dev and n_pos.get_device() == dev
+            and workspace.get_device() == dev and block_table.is_contiguous() and seq_len.is_contiguous()
+            and n_pos.is_contiguous() and workspace.is_contiguous() and len(seq_len) >= B):
+        for t, kind, name, n in ((block_table, _I32, "block_table", B), (seq_len, _I32, "seq_len", B),
+                                 (n_pos, _I32, "n_pos", 1), (workspace, _U8, "workspace", 1)):
+            _dev(t, kind, dev, name, n)
+    a = _pack_attn(B, P, qh[-2], nh[-2], D, code, D ** -0.5 if scale is None else scale, shared_len, rows,
                    q.data_ptr(), qs[-3], qs[-2], out.data_ptr(), os_[-3], os_[-2], k_new.data_ptr(), v_new.data_ptr(),
                    ks[-3], ks[-2], vs[-3], vs[-2], k_pages.data_ptr(), v_pages.data_ptr(), kp[0], kp[1], kp[2], vp_[0],
-                   vp_[1], vp_[2], ph[0], ph[1], _dev(block_table, _I32, dev, "block_table"), th[1],
-                   _dev(seq_len, _I32, dev, "seq_len", B), _dev(n_pos, _I32, dev, "n_pos"),
+                   vp_[1], vp_[2], ph[0], ph[1], block_table.data_ptr(), th[1], seq_len.data_ptr(), n_pos.data_ptr(),
                    0 if mask is None else _dev(mask, _U8, dev, "mask"),
-                   0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
-                   _dev(workspace, _U8, dev, "workspace"), workspace.numel())
+                   0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1), workspace.data_ptr(),
+                   workspace.numel())
     rc = lib.dt_tree_attention(h.h, a, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)

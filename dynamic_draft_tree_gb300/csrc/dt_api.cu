@@ -121,6 +121,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   const size_t o_bcnt = cv.take<int32_t>(c.B_max);
   const size_t o_status = cv.take<int32_t>(1);
   const size_t o_ticket = cv.take<unsigned>(1);
+  const size_t o_atick = cv.take<unsigned>(h->num_sms);
   const size_t total = cv.off;
 
   void* base = nullptr;
@@ -169,6 +170,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   w.bonus_counter = reinterpret_cast<int32_t*>(bp + o_bcnt);
   w.status = reinterpret_cast<int32_t*>(bp + o_status);
   w.ticket = reinterpret_cast<unsigned*>(bp + o_ticket);
+  w.attn_tickets = reinterpret_cast<unsigned*>(bp + o_atick);
   h->alloc = base;
   h->alloc_bytes = total;
   *out = h;
@@ -219,6 +221,8 @@ int dt_get_status(dt_handle* h, cudaStream_t s, int32_t* bits) {
 int dt_clear_status(dt_handle* h, cudaStream_t s) {
   if (!h) return fail(DT_ERR_ARG, "dt_clear_status: null handle");
   cudaError_t e = cudaMemsetAsync(h->ws.status, 0, sizeof(int32_t), s);
+  // a call that gave up may have left arrivals behind
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws.attn_tickets, 0, sizeof(unsigned) * h->num_sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "dt_clear_status");
   return DT_OK;
 }

@@ -93,6 +93,7 @@ struct Workspace {
   int32_t* bonus_counter;         // [B_max]
   int32_t* status;
   unsigned* ticket;      // arrivals of a page call's CTAs; zero between calls
+  unsigned* attn_tickets;  // [num_sms] arrivals at split items of dt_tree_attention; zero between calls
 };
 
 }  // namespace dt

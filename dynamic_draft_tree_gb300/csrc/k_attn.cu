@@ -48,6 +48,8 @@ struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
 struct AttnParams {
   dt_attn_args a;
   int32_t G, page_shift, tree_box;
+  int32_t join;       // split items are joined by the CTA that comes last (items of at most kJoinRows rows, unshared)
+  unsigned* tickets;  // [CTAs] arrivals at the split item whose first CTA this is; zero between calls
   int32_t test_stop;  // test only: every wait that is not over at once gives up
   int32_t pos, rows2; // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
   uint32_t g_magic;   // ceil(2^32 / G), for position_of
@@ -116,7 +118,7 @@ __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& 
 
 // A CTA's share and where it starts.
 struct Plan {
-  int32_t x0, x1;       // units [x0, x1) of the line
+  int32_t x0, x1, per;  // units [x0, x1) of the line, units of a CTA
   int32_t w_shared;
   int32_t t_b;          // own unit offset of request b
   int32_t b, k_b;       // first own request, its item offset
@@ -131,6 +133,7 @@ struct Segment {
   int n;                // positions (0 for the shared prefix)
   int rows;             // rows of the item
   int i0;               // position of its first rows
+  int c0, parts;        // first CTA of the item and how many have tiles of it
   int64_t base;         // row of the first position
   int64_t slot;
 };
@@ -203,7 +206,9 @@ struct Walk {
         s.rows = min(p.rows2, r.n * p.G - s.mp * p.rows2);
       }
       const int tw = tile_units(p, s.rows);
-      const int end = min(tt * tw + kItemUnits, at + pl.x1 - x);
+      const int end = min(tt * tw + kItemUnits, at + pl.x1 - x), u0 = x - at + kItemUnits;
+      s.c0 = u0 / pl.per;
+      s.parts = (u0 + (tt - 1) * tw) / pl.per - s.c0 + 1;
       x += end - at;
       s.t0 = (max(0, at - kItemUnits) + tw - 1) / tw;
       s.t1 = (max(0, end - kItemUnits) + tw - 1) / tw;
@@ -234,14 +239,14 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
-  uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready;
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready, parts_in, ticket_in;
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   float2 ml[2][kTile];
   Plan plan;
   int32_t sums[2][12];
   uint32_t tmem;
-  int stop, odd_values;
+  int stop, odd_values, last;
 };
 
 template <int DP>
@@ -337,6 +342,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     Plan& pl = sh.plan;
     pl.x0 = x0;
     pl.x1 = x1;
+    pl.per = per;
     pl.w_shared = w_shared;
     pl.ts = p.ns;
     pl.mp_s = mp_s;
@@ -815,6 +821,108 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   }
 }
 
+// Items of few rows: the CTA that comes last to a split item joins its parts, so that no second launch is needed. Both
+// groups; returns false after a give-up. Eight lanes hold a row, a warp four of them; with fewer rows than that the
+// warps share the parts out and add up through shared memory (the Q rows' memory).
+constexpr int kJoinRows = 32;
+template <int DP, bool BF16>
+__device__ bool join_parts(const AttnParams& p, Shared& sh, const Segment& s, uint8_t* q_smem, uint32_t& n_in, uint32_t& n_ticket) {
+  __threadfence();  // this thread's part of the rows
+  tc::bar_arrive(&sh.parts_in);
+  if (threadIdx.x < 32) {
+    if (!tc::bar_wait_warp(&sh.parts_in, n_in & 1, &sh.stop)) return false;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      sh.last = atomicInc(&p.tickets[s.c0], s.parts - 1) == s.parts - 1;
+      __threadfence();
+      tc::bar_arrive(&sh.ticket_in);
+    }
+    __syncwarp();
+  }
+  ++n_in;
+  if (!tc::bar_wait_warp(&sh.ticket_in, n_ticket++ & 1, &sh.stop)) return false;
+  if (!*(volatile int*)&sh.last) return true;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7;
+  int blocks = 1;  // of four rows: 1, 2, 4 or 8
+  while (blocks * 4 < s.rows) blocks *= 2;
+  const int r = (warp & (blocks - 1)) * 4 + (lane >> 3), k0 = warp / blocks, step = 8 / blocks;
+  const bool live = r < s.rows;
+  const int64_t at = (s.slot - (int)blockIdx.x + s.c0) * p.own_rows + r;  // part 0's row
+  float m = -INFINITY, l = 0.0f;
+  float4 o[DP / 32];
+#pragma unroll
+  for (int j = 0; j < DP / 32; ++j) o[j] = make_float4(0, 0, 0, 0);
+  if (live) {
+#pragma unroll 4
+    for (int k = k0; k < s.parts; k += step) m = fmaxf(m, __ldcg((const float*)(p.ml_own + at + k * p.own_rows)));
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll 2
+    for (int k = k0; k < s.parts; k += step) {
+      const float2 x = __ldcg(p.ml_own + at + k * p.own_rows);
+      const float w = exp2f(x.x - ref);  // a part that attends to nothing: 0
+      l += x.x == -INFINITY && x.y == 0.0f ? 0.0f : x.y * w;
+      const float* src = p.o_own + (at + k * p.own_rows) * p.a.D + c * 4;
+#pragma unroll
+      for (int j = 0; j < DP / 32; ++j) {
+        if (j * 32 + c * 4 < p.a.D) {
+          const float4 v = __ldcg((const float4*)(src + j * 32));
+          o[j].x = fmaf(v.x, w, o[j].x);
+          o[j].y = fmaf(v.y, w, o[j].y);
+          o[j].z = fmaf(v.z, w, o[j].z);
+          o[j].w = fmaf(v.w, w, o[j].w);
+        }
+      }
+    }
+  }
+  // warps of the same rows: through shared memory to the first of them
+  constexpr int kRowFloats = DP + 2;
+  float* mine = (float*)q_smem + (warp * 4 + (lane >> 3)) * kRowFloats;
+  if (step > 1) {
+    if (k0 > 0) {
+#pragma unroll
+      for (int j = 0; j < DP / 32; ++j) {
+        float* d = mine + j * 32 + c * 4;
+        d[0] = o[j].x;
+        d[1] = o[j].y;
+        d[2] = o[j].z;
+        d[3] = o[j].w;
+      }
+      if (c == 0) {
+        mine[DP] = m;
+        mine[DP + 1] = l;
+      }
+    }
+    tc::bar_arrive(&sh.parts_in);
+    if (!tc::bar_wait_warp(&sh.parts_in, n_in++ & 1, &sh.stop)) return false;
+    if (k0 > 0) return true;
+    for (int y = 1; y < step; ++y) {
+      const float* other = mine + y * blocks * 4 * kRowFloats;
+      const float mo = other[DP], lo = other[DP + 1], top = fmaxf(m, mo), ref = top == -INFINITY ? 0.0f : top;
+      const float a = exp2f(m - ref), w = exp2f(mo - ref);
+      l = l * a + lo * w;
+      m = top;
+#pragma unroll
+      for (int j = 0; j < DP / 32; ++j) {
+        const float* d = other + j * 32 + c * 4;
+        o[j].x = fmaf(d[0], w, o[j].x * a);
+        o[j].y = fmaf(d[1], w, o[j].y * a);
+        o[j].z = fmaf(d[2], w, o[j].z * a);
+        o[j].w = fmaf(d[3], w, o[j].w * a);
+      }
+    }
+  }
+  if (live) {
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    const int i = position_of(p, r);
+    uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0 + i) * p.a.o_row + ((int64_t)s.h * p.G + r - i * p.G) * p.a.o_head + c * 4;
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j)
+      if (j * 32 + c * 4 < p.a.D)
+        *(uint2*)(out + j * 32) = make_uint2(pack16<BF16>(o[j].x * inv, o[j].y * inv), pack16<BF16>(o[j].z * inv, o[j].w * inv));
+  }
+  return true;
+}
+
 // A group of 128 threads turns every S of its units into weights.
 template <int DP, bool BF16>
 __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, int group) {
@@ -825,6 +933,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
   Segments segs;
   Segment s;
   uint32_t ns = 0, no = 0, nml = 0;  // phases of sfull and odone of this group; of mlready
+  uint32_t n_in = 0, n_ticket = 0;   // of parts_in and ticket_in
   for (uint32_t seg = 0; segs.next(sh, s, (threadIdx.x & 31) == 0); ++seg) {
     const bool dual = s.rows > p.rows2 >> 1;
     const int tiles = s.t1 - s.t0;
@@ -928,6 +1037,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       tc::fence_after();
     }
     if (dual || tiles > 1 || group == 0) finish_rows<DP, BF16>(p, sh, s, group, row, !dual && tiles > 1, tm, q_smem);
+    if (p.join && !s.whole && !join_parts<DP, BF16>(p, sh, s, q_smem, n_in, n_ticket)) return;
     tc::fence_async_smem();  // the Q rows' memory, written and read above, goes to the next load
     tc::fence_before();
     tc::bar_arrive(&sh.qfree);
@@ -965,6 +1075,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::bar_init(&sh.qfull, 1);
     tc::bar_init(&sh.qfree, 2 * kTile);
     tc::bar_init(&sh.mlready, 2 * kTile);
+    tc::bar_init(&sh.parts_in, 2 * kTile);
+    tc::bar_init(&sh.ticket_in, 1);
     for (int i = 0; i < kSegs; ++i) {
       tc::bar_init(&sh.segfull[i], 1);
       tc::bar_init(&sh.segempty[i], kSegReaders);
@@ -1174,7 +1286,7 @@ template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const AttnParams& p, const CUtensorMap* m, cudaStream_t s) {
   launch_k(attn_kernel<DP, BF16>, dim3(h->num_sms), dim3(kAttnThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4]);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.join) return e;
   // Few rows: a warp a head, all of its parts at once; many: four heads a warp.
   const int heads = (int64_t)p.a.P * p.a.B * p.a.H_q > 16ll * h->num_sms ? 4 : 1;
   const dim3 grid(p.a.P, p.a.B, (p.a.H_q + kMergeWarps * heads - 1) / (kMergeWarps * heads));
@@ -1228,6 +1340,8 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.ml_sh = (float2*)(ws + L.ml_sh);
   p.o_sh = (float*)(ws + L.o_sh);
   p.status = h->ws.status;
+  p.join = a->shared_len == 0 && (int64_t)a->P * p.G <= kJoinRows;
+  p.tickets = h->ws.attn_tickets;
   p.test_stop = h->cfg.flags & DT_FLAG_TEST_TIMEOUT ? 1 : 0;
   CUtensorMap m[5];
   const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};

@@ -477,7 +477,8 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
  * seq_len < shared_len sets DT_DEV_BAD_PAGE and its rows are computed as if seq_len = shared_len.
  * Types: DT_BF16 or DT_F16 for all of q, k, v, out; scores, softmax statistics and sums in fp32, the softmax
  * weights rounded to the input type for the second product. D: a multiple of 8, up to 128. H_q / H_kv <= 128.
- * Strides in elements, multiples of 8; pointers 16-byte aligned. */
+ * Strides in elements, multiples of 8; pointers 16-byte aligned. After DT_DEV_TIMEOUT, dt_clear_status also makes the
+ * handle fit for the next call. */
 typedef struct {
   int32_t B, P, H_q, H_kv, D, dtype;
   float scale;
@@ -498,8 +499,9 @@ typedef struct {
   const int32_t* n_pos;         /* [B] */
   const uint8_t* mask;          /* [B][P][P] or NULL */
   const int32_t* row_off;       /* [B+1] or NULL     */
-  void* workspace;              /* dt_tree_attention_workspace bytes, 256-byte aligned; used by this call
-                                   until it has run: calls that may overlap need one each */
+  void* workspace;              /* dt_tree_attention_workspace bytes, 256-byte aligned, no initial value; used
+                                   until the call has run (calls that may overlap need a handle and a
+                                   workspace each) */
   int64_t workspace_bytes;
 } dt_attn_args;
 int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
