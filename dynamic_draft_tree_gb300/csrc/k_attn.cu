@@ -824,6 +824,8 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
 // Items of few rows: the CTA that comes last to a split item joins its parts, so that no second launch is needed. Both
 // groups; returns false after a give-up. Eight lanes hold a row, a warp four of them; with fewer rows than that the
 // warps share the parts out and add up through shared memory (the Q rows' memory).
+// One request, eight key heads of 128, 2000 cached tokens, joined here or by a second launch: 32 rows 15.8 and 18.7 us,
+// 68 rows 22.5 and 18.3 us (one CTA's rows against all CTAs').
 constexpr int kJoinRows = 32;
 template <int DP, bool BF16>
 __device__ bool join_parts(const AttnParams& p, Shared& sh, const Segment& s, uint8_t* q_smem, uint32_t& n_in, uint32_t& n_ticket) {
