@@ -338,12 +338,15 @@ class BlockPool:
 
 
 def _slots_args(B, dev, slots, slot_off, S):
-    p, n_slots = _dev(slots, _I64, dev, "slots"), slots.numel()
+    n_slots = slots.numel()
+    if not (slots.dtype is _I64 and slots.get_device() == dev and slots.is_contiguous()):
+        _dev(slots, _I64, dev, "slots")
     if slot_off is None:
-        if slots.dim() != 2 or slots.shape[0] < B:
+        sh = slots.shape
+        if len(sh) != 2 or sh[0] < B:
             raise ValueError("slots must be [B][S] without slot_off")
-        return p, n_slots, slots.shape[1], 0
-    return p, n_slots, n_slots if S is None else S, _dev(slot_off, _I32, dev, "slot_off", B + 1)
+        return slots.data_ptr(), n_slots, sh[1], 0
+    return slots.data_ptr(), n_slots, n_slots if S is None else S, _dev(slot_off, _I32, dev, "slot_off", B + 1)
 
 
 def dt_kv_reserve(h, pool, seq_len, n_new, slots, n_extra=0, slot_off=None, S=None, stream=None):
@@ -353,8 +356,12 @@ def dt_kv_reserve(h, pool, seq_len, n_new, slots, n_extra=0, slot_off=None, S=No
     if B > pool.B or pool.device != dev:
         raise ValueError("the pool holds fewer requests than n_new, or is on another device")
     sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
-    rc = lib.dt_kv_reserve(h.h, B, pool.ref, _dev(seq_len, _I32, dev, "seq_len", B), _dev(n_new, _I32, dev, "n_new"),
-                           n_extra, sp, n_slots, S, so, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if not (seq_len.dtype is _I32 and n_new.dtype is _I32 and seq_len.get_device() == dev and n_new.get_device() == dev
+            and seq_len.is_contiguous() and n_new.is_contiguous() and len(seq_len) >= B):
+        _dev(seq_len, _I32, dev, "seq_len", B)
+        _dev(n_new, _I32, dev, "n_new")
+    rc = lib.dt_kv_reserve(h.h, B, pool.ref, seq_len.data_ptr(), n_new.data_ptr(), n_extra, sp, n_slots, S, so,
+                           _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 
@@ -379,7 +386,8 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
     ts, cs, st, sc = tmp.shape, cache.shape, tmp.stride(), cache.stride()
     if len(ts) != (5 if row_off is None else 4) or len(cs) != 5:
         raise ValueError("tmp needs [planes][B][P][H][D] ([planes][rows][H][D] packed), cache [planes][blocks][page][H][D]")
-    if ts[-2:] != cs[-2:] or ts[0] != cs[0]:
+    H, D = ts[-2], ts[-1]
+    if H != cs[3] or D != cs[4] or ts[0] != cs[0]:
         raise ValueError("tmp and cache differ in planes, heads or head size")
     if row_off is None:
         if ts[1] < B or (ts[1] > 1 and st[1] != ts[2] * st[2]):
@@ -390,18 +398,25 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
         P = rows if P is None else P
     dp = 0
     if path is not None:
-        if path.dim() != 2 or path.shape[0] < B:
+        if path.dim() != 2 or len(path) < B:
             raise ValueError("path must be [B][D_path]")
         dp = path.shape[1]
     e, dtype = tmp.element_size(), tmp.dtype
-    kv = _pack_kv_rows(_strided(tmp, dtype, dev, st, "tmp"), st[0] * e, st[-3] * e, st[-2] * e, rows,
-                       _strided(cache, dtype, dev, sc, "cache"), sc[0] * e, sc[1] * e, sc[2] * e, sc[3] * e, ts[0],
-                       ts[-2], ts[-1] * e, cs[2], cs[1])
+    if not (cache.dtype is dtype and tmp.get_device() == dev and cache.get_device() == dev and st[-1] == 1
+            and sc[4] == 1):
+        _strided(tmp, dtype, dev, st, "tmp")
+        _strided(cache, dtype, dev, sc, "cache")
+    if not (n_new.dtype is _I32 and seq_len.dtype is _I32 and len_out.dtype is _I32 and n_new.get_device() == dev
+            and seq_len.get_device() == dev and len_out.get_device() == dev and n_new.is_contiguous()
+            and seq_len.is_contiguous() and len_out.is_contiguous() and len(seq_len) >= B and len(len_out) >= B):
+        for t, name in ((n_new, "n_new"), (seq_len, "seq_len"), (len_out, "len_out")):
+            _dev(t, _I32, dev, name, B)
+    kv = _pack_kv_rows(tmp.data_ptr(), st[0] * e, st[-3] * e, st[-2] * e, rows, cache.data_ptr(), sc[0] * e, sc[1] * e,
+                       sc[2] * e, sc[3] * e, ts[0], H, D * e, cs[2], cs[1])
     sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
-    rc = lib.dt_commit_kv_paged(h.h, B, kv, P, _dev(row_off, _I32, dev, "row_off", B + 1),
-                                _dev(path, _I32, dev, "path"), dp, _dev(n_new, _I32, dev, "n_new"), n_extra, sp,
-                                n_slots, S, so, _dev(seq_len, _I32, dev, "seq_len", B),
-                                _dev(len_out, _I32, dev, "len_out", B),
+    rc = lib.dt_commit_kv_paged(h.h, B, kv, P, 0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
+                                0 if path is None else _dev(path, _I32, dev, "path"), dp, n_new.data_ptr(), n_extra, sp,
+                                n_slots, S, so, seq_len.data_ptr(), len_out.data_ptr(),
                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
@@ -539,13 +554,21 @@ def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=Non
         words = allow.shape[-1]
         if allow.numel() < rows * words or words < (V + 31) // 32:
             raise ValueError("allow needs a row of ceil(V / 32) words for every row of logits")
-    p = _pack_logits(P, _dev(n_pos, _I32, dev, "n_pos"), _dev(row_off, _I32, dev, "row_off", B + 1), rows,
-                     _dev(tokens, _I32, dev, "tokens"), _dev(mask, _U8, dev, "mask"), _dev(counts, _I32, dev, "counts"),
-                     _dev(repetition, _F32, dev, "repetition", B), _dev(frequency, _F32, dev, "frequency", B),
-                     _dev(presence, _F32, dev, "presence", B), _dev(bias_ids, _I32, dev, "bias_ids", 0),
-                     _dev(bias_vals, _F32, dev, "bias_vals", 0), n_bias, _dev(allow, _I32, dev, "allow"), words)
-    rc = lib.dt_logits_process(h.h, B, _strided(logits, dtype, dev, ls_, "logits"), ls_[-2],
-                               _strided(out, dtype, dev, os_, "out"), os_[-2], p,
+    if not (logits.dtype is dtype and out.dtype is dtype and logits.get_device() == dev and out.get_device() == dev
+            and ls_[-1] == 1 and os_[-1] == 1):
+        _strided(logits, dtype, dev, ls_, "logits")
+        _strided(out, dtype, dev, os_, "out")
+    p = _pack_logits(P, _dev(n_pos, _I32, dev, "n_pos"), 0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
+                     rows, 0 if tokens is None else _dev(tokens, _I32, dev, "tokens"),
+                     0 if mask is None else _dev(mask, _U8, dev, "mask"),
+                     0 if counts is None else _dev(counts, _I32, dev, "counts"),
+                     0 if repetition is None else _dev(repetition, _F32, dev, "repetition", B),
+                     0 if frequency is None else _dev(frequency, _F32, dev, "frequency", B),
+                     0 if presence is None else _dev(presence, _F32, dev, "presence", B),
+                     0 if bias_ids is None else _dev(bias_ids, _I32, dev, "bias_ids", 0),
+                     0 if bias_vals is None else _dev(bias_vals, _F32, dev, "bias_vals", 0), n_bias,
+                     0 if allow is None else _dev(allow, _I32, dev, "allow"), words)
+    rc = lib.dt_logits_process(h.h, B, logits.data_ptr(), ls_[-2], out.data_ptr(), os_[-2], p,
                                _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
