@@ -285,16 +285,16 @@ def _refuse(t, dtype, dev, name, n):
         raise ValueError(f"{name} must be {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if t.dim() < 1 or t.shape[0] < n:
+    if t.numel() < n:
         raise ValueError(f"{name} has fewer than {n} entries")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _dev(t, dtype, dev, name, n=1):
-    """Pointer of a contiguous tensor on device `dev` with this dtype and at least n (leading) entries; 0 for None."""
+    """Pointer of a contiguous tensor on device `dev` with this dtype and at least n entries; 0 for None."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (t.numel() if n == 1 else len(t)) < n:
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < n:
         _refuse(t, dtype, dev, name, n)
     return t.data_ptr()
 
@@ -357,7 +357,7 @@ def dt_kv_reserve(h, pool, seq_len, n_new, slots, n_extra=0, slot_off=None, S=No
         raise ValueError("the pool holds fewer requests than n_new, or is on another device")
     sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
     if not (seq_len.dtype is _I32 and n_new.dtype is _I32 and seq_len.get_device() == dev and n_new.get_device() == dev
-            and seq_len.is_contiguous() and n_new.is_contiguous() and len(seq_len) >= B):
+            and seq_len.is_contiguous() and n_new.is_contiguous() and seq_len.numel() >= B):
         _dev(seq_len, _I32, dev, "seq_len", B)
         _dev(n_new, _I32, dev, "n_new")
     rc = lib.dt_kv_reserve(h.h, B, pool.ref, seq_len.data_ptr(), n_new.data_ptr(), n_extra, sp, n_slots, S, so,
@@ -398,7 +398,7 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
         P = rows if P is None else P
     dp = 0
     if path is not None:
-        if path.dim() != 2 or len(path) < B:
+        if path.dim() != 2 or path.shape[0] < B:
             raise ValueError("path must be [B][D_path]")
         dp = path.shape[1]
     e, dtype = tmp.element_size(), tmp.dtype
@@ -408,7 +408,7 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
         _strided(cache, dtype, dev, sc, "cache")
     if not (n_new.dtype is _I32 and seq_len.dtype is _I32 and len_out.dtype is _I32 and n_new.get_device() == dev
             and seq_len.get_device() == dev and len_out.get_device() == dev and n_new.is_contiguous()
-            and seq_len.is_contiguous() and len_out.is_contiguous() and len(seq_len) >= B and len(len_out) >= B):
+            and seq_len.is_contiguous() and len_out.is_contiguous() and seq_len.numel() >= B and len_out.numel() >= B):
         for t, name in ((n_new, "n_new"), (seq_len, "seq_len"), (len_out, "len_out")):
             _dev(t, _I32, dev, name, B)
     kv = _pack_kv_rows(tmp.data_ptr(), st[0] * e, st[-3] * e, st[-2] * e, rows, cache.data_ptr(), sc[0] * e, sc[1] * e,
@@ -477,7 +477,7 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
     if not (block_table.dtype is _I32 and seq_len.dtype is _I32 and n_pos.dtype is _I32 and workspace.dtype is _U8
             and block_table.get_device() == dev and seq_len.get_device() == dev and n_pos.get_device() == dev
             and workspace.get_device() == dev and block_table.is_contiguous() and seq_len.is_contiguous()
-            and n_pos.is_contiguous() and workspace.is_contiguous() and len(seq_len) >= B):
+            and n_pos.is_contiguous() and workspace.is_contiguous() and seq_len.numel() >= B):
         for t, kind, name, n in ((block_table, _I32, "block_table", B), (seq_len, _I32, "seq_len", B),
                                  (n_pos, _I32, "n_pos", 1), (workspace, _U8, "workspace", 1)):
             _dev(t, kind, dev, name, n)
@@ -546,7 +546,7 @@ def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=Non
             raise ValueError("counts must be [B][V]")
     n_bias = words = 0
     if bias_ids is not None or bias_vals is not None:
-        if bias_ids is None or bias_vals is None or bias_ids.dim() != 2 or len(bias_ids) < B or \
+        if bias_ids is None or bias_vals is None or bias_ids.dim() != 2 or bias_ids.shape[0] < B or \
                 bias_vals.shape != bias_ids.shape:
             raise ValueError("bias_ids and bias_vals must be [B][n_bias] both")
         n_bias = bias_ids.shape[1]
