@@ -15,7 +15,7 @@ constexpr int kPer = 8;                          // tokens of a thread
 constexpr int kLogChunk = kLogThreads * kPer;    // tokens of a CTA
 template <typename T>
 constexpr int kWords = kPer * (int)sizeof(T) / 4;  // 32-bit words of a row that a thread holds
-constexpr int kLogRows = 16;                     // rows of a CTA
+constexpr int kLogRows = 16;                     // rows of a CTA (at most 32: bits of a word)
 
 struct LogitsArgs {
   dt_logits_params p;
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][kLogThreads]
   int32_t* path_tok = (int32_t*)(said + kDepth * kLogThreads);   // [P] chunk offset of a position's token, its position
   int32_t* path_pos = path_tok + P;                              // [P]
+  uint32_t* on_rows = (uint32_t*)(path_pos + P);                 // [P] bit r: on row r's path
   __shared__ int n_path, twice;
   __shared__ uint32_t hit[kLogRows][kLogChunk / 32];  // bit = the token is on the row's path
   __shared__ float bias_s[kLogChunk];
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
         const int q = atomicAdd(&n_path, 1);
         path_tok[q] = at - v0;
         path_pos[q] = j;
+        on_rows[q] = 0;
       }
     }
   }
@@ -233,18 +235,27 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     const int i = row0 + r, j = path_pos[k];
     return a.p.mask ? a.p.mask[((int64_t)b * P + i) * P + j] != 0 : j <= i;
   };
-  for (int x = tid; x < np * rows; x += kLogThreads) {
-    const int r = x / np, k = x - r * np;
-    if (on_path_of(r, k)) atomicOr(&hit[r][path_tok[k] >> 5], 1u << (path_tok[k] & 31));
-  }
+  // bits of the rows' path tokens: the first mask byte of a thread travels while the additions are made up
+  auto mark = [&](int r, int k) {
+    atomicOr(&hit[r][path_tok[k] >> 5], 1u << (path_tok[k] & 31));
+    atomicOr(&on_rows[k], 1u << r);
+  };
+  const int r1 = np > 0 ? tid / np : 0, k1 = tid - r1 * np;
+  const bool on1 = tid < np * rows && on_path_of(r1, k1);
   pen.inv = 1.0f / pen.rep;
   float add[kPer];
-  uint32_t seen = 0;
+  uint32_t seen = 0, made = 0;  // bits: in the history at all; generated before
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     add[u] = with_bias ? bias_s[place(u)] : 0.0f;
     if (cnt[u]) add[u] = add_of(pen, cnt[u] & (DT_SEEN_PROMPT - 1), add[u]);
     seen |= (cnt[u] != 0 ? 1u : 0u) << u;
+    made |= (cnt[u] & (DT_SEEN_PROMPT - 1) ? 1u : 0u) << u;
+  }
+  if (on1) mark(r1, k1);
+  for (int x = tid + kLogThreads; x < np * rows; x += kLogThreads) {
+    const int r = x / np, k = x - r * np;
+    if (on_path_of(r, k)) mark(r, k);
   }
   __syncthreads();
   for (int r = 0; r < rows; ++r) {
@@ -296,14 +307,14 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
       }
       for (; on_path; on_path &= on_path - 1) {
         const int u = __ffs(on_path) - 1, off = place(u);
-        int c = counts ? counts[off] & (DT_SEEN_PROMPT - 1) : 0;
-        for (int q = 0; q < np; ++q) c += path_tok[q] == off && on_path_of(r, q);
-        const float plus = add_of(pen, c, with_bias ? bias_s[off] : 0.0f);
+        int c = 0;  // occurrences on the path
+        for (int q = 0; q < np; ++q) c += path_tok[q] == off && on_rows[q] >> r & 1;
+        const float more = fmaf(pen.freq, (float)c, made & 1u << u ? 0.0f : pen.pres);
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
           if (q == u) {
             const float x = element<T>(in, q);
-            y[q] = fmaf(x, factor_of(pen, true, x), plus);
+            y[q] = fmaf(x, factor_of(pen, true, x), add[q] - more);
           }
         }
       }
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(kLogThreads) count_kernel(CountArgs a) {
 
 template <typename T>
 size_t logits_smem(int P) {
-  return kRingBytes<T> + (size_t)P * 8;
+  return kRingBytes<T> + (size_t)P * 12;
 }
 
 template <typename T>
