@@ -680,9 +680,7 @@ int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
       return fail(DT_ERR_ARG, "dt_tree_attention: strides must be multiples of 8 elements, at least D");
   if (!aligned(a->block_table, 4) || !aligned(a->seq_len, 4) || !aligned(a->n_pos, 4) || !aligned(a->row_off, 4))
     return fail(DT_ERR_ARG, "dt_tree_attention: int32 arrays must be 4-byte aligned");
-  // places on the line of work are 32-bit
-  const double rows_g = (double)a->P * (a->H_q / a->H_kv), tiles = (double)a->max_blocks * a->page / 128 + 16;
-  if ((double)a->B * a->H_kv * (rows_g / 256 + 2) * tiles > 2.0e9)
+  if (!dt::attn_line_fits(a))
     return fail(DT_ERR_ARG, "dt_tree_attention: B * H_kv * rows * max_blocks * page too large");
   if (!aligned(a->workspace, 256) ||
       a->workspace_bytes < dt::attn_workspace_bytes(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0))

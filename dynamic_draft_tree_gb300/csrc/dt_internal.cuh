@@ -190,6 +190,7 @@ cudaError_t launch_commit_kv_paged(dt_handle* h, int B, const dt_kv_rows* kv, in
                                    const int64_t* slots, int64_t n_slots, int S, const int32_t* slot_off,
                                    const int32_t* seq_len, int32_t* len_out, cudaStream_t s);
 cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
+bool attn_line_fits(const dt_attn_args* a);  // places on the kernel's line of work are 32-bit
 int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared);
 cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                           const dt_logits_params* p, cudaStream_t s);

@@ -11,16 +11,25 @@
 // request's own cached tokens and then its tree positions. All tiles in item order form one line that the CTAs
 // (one a SM) cut into equal runs, whatever the lengths; a CTA's run of one item is a segment. A segment that is a
 // whole item of an unshared call writes the result; others leave sum, maximum and unnormalised result in
-// fp32, and attn_merge_kernel joins them in a fixed order. Every CTA derives the cuts from the lengths on the
-// device, so a captured call follows them.
+// fp32, joined in a fixed order by the CTA that comes last to the item (few rows, no shared prefix) or by
+// attn_merge_kernel. Every CTA derives the cuts from the lengths on the device, so a captured call follows them.
 //
 // A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads K tiles, warp 11 V tiles (TMA, one
-// box a page and 64 elements), warp 9 issues the matrix instructions, warp 10 clears value rows past the end.
+// box a page and 64 elements), warp 9 loads Q rows and issues the matrix instructions, warp 10 walks along the line
+// and clears value rows past the end. Every wait is bounded (DT_DEV_TIMEOUT).
 // The line of work is a sequence of units u = 0, 1, ... for groups u & 1: with more than 128 rows a tile gives two
 // units, one for each half of the rows; with fewer, tiles alternate between the groups, whose results are
 // joined at the end. S = Q K^T of unit u + 2 is issued right behind O += P V of unit u, so the tensor cores
-// work for one group while the other takes its softmax. S (fp32) and P (16-bit, over S) and O live in tensor
-// memory.
+// work for one group while the other takes its softmax; P goes over in halves. S (fp32), P (16-bit, over S) and O
+// live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
+//
+// What bounds it, at D = 128 on one GB300: few rows, the cache's bytes (64 requests, 5100 cached tokens on average:
+// 6.4 TB/s, 0.95 of the measured copy peak); a shared prefix, the chain of one group's softmax (about 1500 clocks a tile
+// of 128 x 128) and its two products (1024), of which the tensor cores are busy 2048 of 2780 clocks; small calls,
+// latency (11 us: 1.3 for the plan, 1 for the first segment, 2.5 for the first tiles, 1.1 softmax, 3 for the join).
+// One issuing thread behind `if (lane == 0)` instead of the uniform path cost 70 clocks an instruction (attend to 64
+// requests behind a prefix: 436 against 294 us); fully unrolled softmax code for masked and unmasked tiles missed the
+// instruction cache and made a segment's ends 4 to 12 us long instead of 2 to 3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -571,9 +580,9 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
   }
 }
 
-// One warp: puts down the segments for the other roles. Value rows past the end of a tile become zero (a weight of zero times what lies there need not be
-// zero), and so do NaN and infinities at tree positions, which only some rows attend to: the rows that do add
-// them in finish_row.
+// One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
+// (a weight of zero times what lies there need not be zero), and so do NaN and infinities at tree positions, which only
+// some rows attend to: the rows that do add them in finish_rows.
 template <int DP, bool BF16>
 __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int lane) {
   using S = Smem<DP>;
@@ -1312,6 +1321,14 @@ cudaError_t init_attn_attributes() {
   if (e == cudaSuccess) e = init_t<128, true>();
   if (e == cudaSuccess) e = init_t<128, false>();
   return e;
+}
+
+bool attn_line_fits(const dt_attn_args* a) {
+  const int pos2 = 2 * (kTile / (a->H_q / a->H_kv));  // positions of an item
+  const double own_tiles = ((double)a->max_blocks * a->page + a->P) / kTile + 2, sh_tiles = (double)a->shared_len / kTile + 1;
+  const double own = (double)a->B * a->H_kv * ((a->P + pos2 - 1) / pos2) * (kItemUnits + 3 * own_tiles);
+  const double sh = a->shared_len > 0 ? a->H_kv * ((double)a->B * a->P / pos2 + 1) * (kItemUnits + 3 * sh_tiles) : 0.0;
+  return own + sh < 2.0e9;
 }
 
 int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared) {
