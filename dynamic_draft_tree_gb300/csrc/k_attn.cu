@@ -63,7 +63,8 @@ struct AttnParams {
   int32_t pos, rows2; // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
   uint32_t g_magic;   // ceil(2^32 / G), for position_of
   float c;            // scale * log2 e
-  int32_t ns;         // tiles of the shared prefix
+  int32_t ns;         // tiles of the shared prefix as items of its own; 0: requests read it with their own tokens
+  int32_t skip;       // tokens that a request's own items leave to it
   int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
   AttnHead* head;
   int32_t* t_pre;     // [B] unit offset of a request among the own units
@@ -118,12 +119,18 @@ struct Extent {
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
   Extent e;
   e.mp = (r.n + 2 * p.pos - 1) / (2 * p.pos);
-  e.tp = (r.len - p.a.shared_len + kTile - 1) / kTile;
+  e.tp = (r.len - p.skip + kTile - 1) / kTile;
   e.tt = r.n > 0 ? e.tp + (r.n + kTile - 1) / kTile : 0;
   e.full = kItemUnits + 3 * e.tt;
   e.last = kItemUnits + tile_units(p, r.n * p.G - (e.mp - 1) * p.rows2) * e.tt;
   return e;
 }
+
+// Items of its own for a shared prefix cost a launch to join them and an item's ends; they pay from about ten units an SM
+// that the requests' own items would have more. 8 key heads of 128, groups of 4, as items of their own against with the
+// requests' tokens: 8 requests behind 512 tokens (2.7 units an SM) 17.0 and 15.2 us, 20 behind 1024 (7.2) 21.6 and 18.5,
+// 8 behind 2048 (10.9) 19.1 and 20.2, 32 behind 1024 (26) 25 and 32, 64 behind 2048 (105) 40 and 75.
+constexpr int kShareUnits = 10;
 
 // A CTA's share and where it starts.
 struct Plan {
@@ -209,7 +216,7 @@ struct Walk {
         s.b = b;
         s.tp = e.tp;
         s.len = r.len;
-        s.tok0 = p.a.shared_len;
+        s.tok0 = p.skip;
         s.n = r.n;
         s.base = r.base;
         s.rows = min(p.rows2, r.n * p.G - s.mp * p.rows2);
@@ -411,13 +418,13 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
   bool ok = true;
   const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
   while (ok && segs.next(sh, s, lane == 0)) {
-    const int32_t* table = p.a.block_table + (s.shared ? 0 : (int64_t)s.b * p.a.max_blocks);
+    const int32_t* table = p.a.block_table + (int64_t)s.b * p.a.max_blocks;
     const int tok0 = s.tok0;
     // block id of this lane's box in tile t (-1: none)
     auto block_at = [&](int t) {
       const int tok = tok0 + t * kTile + (part << box_shift);
       if (t >= s.tp || (part << box_shift) >= kTile || tok >= s.len) return -1;
-      int id = table[tok >> shift];
+      int id = (tok < p.a.shared_len ? p.a.block_table : table)[tok >> shift];
       if (id < 0 || id >= p.a.n_blocks) {
         set_status(p.status, DT_DEV_BAD_PAGE);
         id = p.a.n_blocks;  // outside the tensor: zeros
@@ -1347,6 +1354,11 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   while (p.tree_box < a->P && p.tree_box < kTile) p.tree_box *= 2;
   p.c = a->scale * kLog2e;
   p.ns = (a->shared_len + kTile - 1) / kTile;
+  // units that the requests' own items would have more if they read the prefix with their own tokens
+  const int64_t blocks = (a->P + 2 * p.pos - 1) / (2 * p.pos), blocks_s = ((int64_t)a->B * a->P + 2 * p.pos - 1) / (2 * p.pos);
+  const int64_t more = (int64_t)a->H_kv * p.ns * (a->B * blocks * (a->P * p.G > p.rows2 / 2 ? 3 : 2) - blocks_s * 3);
+  if (more < kShareUnits * h->num_sms) p.ns = 0;
+  p.skip = p.ns ? a->shared_len : 0;
   const Layout L = layout_of(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0);
   char* ws = (char*)a->workspace;
   p.own_slots = L.own_slots;
@@ -1359,7 +1371,7 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.ml_sh = (float2*)(ws + L.ml_sh);
   p.o_sh = (float*)(ws + L.o_sh);
   p.status = h->ws.status;
-  p.join = a->shared_len == 0 && (int64_t)a->P * p.G <= kJoinRows;
+  p.join = p.ns == 0 && (int64_t)a->P * p.G <= kJoinRows;
   p.tickets = h->ws.attn_tickets;
   p.test_stop = h->cfg.flags & DT_FLAG_TEST_TIMEOUT ? 1 : 0;
   CUtensorMap m[5];

@@ -49,7 +49,10 @@ class Problem:
         for b in range(B):
             table.append(perm[:ns] + perm[at:at + need[b]] + [-1] * (self.max_blocks - ns - need[b]))
             at += need[b]
+        for b in range(1, B):  # only the first request's entries of shared pages are read
+            table[b][:ns] = [-1 - b] * ns
         self.table = t.tensor(table, dtype=t.int32, device="cuda")
+        table = [table[0][:ns] + row[ns:] for row in table]
         nan = float("nan")
         shape = (n_blocks, H_kv, page, D) if heads_first else (n_blocks, page, H_kv, D)
         pages = [t.full(shape, nan, dtype=dt_, device="cuda") for _ in range(2)]
@@ -181,6 +184,11 @@ CASES = {
     "shared, one token": dict(B=40, P=1, H_kv=2, G=4, D=128, page=64, lens=[640 + i for i in range(40)], shared=640,
                               tree=False),
     "shared long": dict(B=9, P=33, H_kv=1, G=4, D=64, page=16, lens=[2048 + 9 * i for i in range(9)], shared=2048),
+    "shared, read with the own tokens": dict(B=3, P=5, H_kv=2, G=4, D=128, page=16, lens=[64, 100, 64], shared=64),
+    "shared, many rows": dict(B=48, P=9, H_kv=4, G=3, D=64, page=32, lens=[1024 + 5 * i for i in range(48)], shared=1024,
+                              n_pos=[1 + i % 9 for i in range(48)], packed=True),
+    "shared, long and few": dict(B=4, P=1, H_kv=1, G=8, D=128, page=64, lens=[8192, 8200, 8300, 8192], shared=8192,
+                                 tree=False),
     "weak scores": dict(B=2, P=9, H_kv=2, G=2, D=128, page=16, lens=[900, 30], q_scale=0.01),
     "sharp scores": dict(B=2, P=9, H_kv=2, G=2, D=128, page=16, lens=[900, 30], q_scale=40.0),
 }
