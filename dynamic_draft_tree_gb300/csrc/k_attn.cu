@@ -110,8 +110,11 @@ constexpr int kItemUnits = 12;
 __device__ __forceinline__ int tile_units(const AttnParams& p, int rows) { return rows > p.rows2 >> 1 ? 3 : 2; }
 
 // Items of a request for all key heads, tiles of one item.
+// The tree's positions begin a tile of their own or, where the last cached tokens and all positions fit into one, stand
+// in that tile behind the tokens' pages: position 0 is column `col` of tile `tree`.
 struct Extent {
-  int mp, tp, tt;        // row blocks a head; prefix tiles, all tiles
+  int mp, tt;            // row blocks a head; tiles
+  int tree, col;
   int full, last;        // units of an item of all its rows, of a head's last item
   __device__ __forceinline__ int head() const { return (mp - 1) * full + last; }
   __device__ __forceinline__ int all(int heads) const { return tt > 0 ? heads * head() : 0; }
@@ -119,8 +122,13 @@ struct Extent {
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Request& r) {
   Extent e;
   e.mp = (r.n + 2 * p.pos - 1) / (2 * p.pos);
-  e.tp = (r.len - p.skip + kTile - 1) / kTile;
-  e.tt = r.n > 0 ? e.tp + (r.n + kTile - 1) / kTile : 0;
+  const int cached = r.len - p.skip, rest = cached & (kTile - 1), box = min(p.a.page, kTile);
+  e.tree = (cached + kTile - 1) / kTile;
+  e.col = (rest + box - 1) & -box;  // pages are loaded whole
+  const bool with = rest > 0 && e.col + ((r.n + p.tree_box - 1) & -p.tree_box) <= kTile;
+  if (with) --e.tree;
+  else e.col = 0;
+  e.tt = r.n > 0 ? e.tree + (e.col + r.n + kTile - 1) / kTile : 0;
   e.full = kItemUnits + 3 * e.tt;
   e.last = kItemUnits + tile_units(p, r.n * p.G - (e.mp - 1) * p.rows2) * e.tt;
   return e;
@@ -145,7 +153,8 @@ struct Segment {
   int shared, whole;    // whole: an item without other parts, written straight to the result
   int b, h, mp;
   int t0, t1;           // tiles; none: the line is at its end
-  int tp, len, tok0;    // prefix tiles, their end and the first one's token
+  int len, tok0;        // cached tokens, the first tile's first one
+  int tree, col;        // tile and column of position 0
   int n;                // positions (0 for the shared prefix)
   int rows;             // rows of the item
   int i0;               // position of its first rows
@@ -185,7 +194,8 @@ struct Walk {
         item = s.h * pl.mp_s + s.mp;
         s.shared = 1;
         s.b = 0;
-        s.tp = tt;
+        s.tree = tt;
+        s.col = 0;
         s.len = p.a.shared_len;
         s.tok0 = 0;
         s.n = 0;
@@ -214,7 +224,8 @@ struct Walk {
         item = k_b + s.h * e.mp + s.mp;
         s.shared = 0;
         s.b = b;
-        s.tp = e.tp;
+        s.tree = e.tree;
+        s.col = e.col;
         s.len = r.len;
         s.tok0 = p.skip;
         s.n = r.n;
@@ -235,10 +246,14 @@ struct Walk {
   }
 };
 
-// Tokens or positions of tile t that exist, and whether the tile holds tree positions.
+// Columns of tile t that are in use, and whether it holds tree positions.
 __device__ __forceinline__ int tile_valid(const Segment& s, int t, bool& tree) {
-  tree = !s.shared && t >= s.tp;
-  return min(kTile, tree ? s.n - (t - s.tp) * kTile : s.len - s.tok0 - t * kTile);
+  tree = t >= s.tree;  // (a shared prefix: never)
+  return min(kTile, tree ? s.col + s.n - (t - s.tree) * kTile : s.len - s.tok0 - t * kTile);
+}
+// Its columns of cached tokens.
+__device__ __forceinline__ int tile_cached(const Segment& s, int t) {
+  return max(0, min(kTile, s.len - s.tok0 - t * kTile));
 }
 
 template <int DP>
@@ -423,7 +438,7 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
     // block id of this lane's box in tile t (-1: none)
     auto block_at = [&](int t) {
       const int tok = tok0 + t * kTile + (part << box_shift);
-      if (t >= s.tp || (part << box_shift) >= kTile || tok >= s.len) return -1;
+      if ((part << box_shift) >= kTile || tok >= s.len) return -1;
       int id = (tok < p.a.shared_len ? p.a.block_table : table)[tok >> shift];
       if (id < 0 || id >= p.a.n_blocks) {
         set_status(p.status, DT_DEV_BAD_PAGE);
@@ -442,25 +457,20 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
       const uint32_t at = smem + stage * S::kBlock;
       bool tree;
       const int valid = tile_valid(s, t, tree);
-      if (tree) {
-        // one box of tree_box rows and 64 elements for every tree_box positions that exist
-        const int boxes = (valid + p.tree_box - 1) / p.tree_box;
-        if (lane == 0) tc::bar_expect(&full[stage], boxes * kHalves * p.tree_box * 128);
-        __syncwarp();
-        for (int k = lane; k < boxes * kHalves; k += 32) {
-          const int hf = k & (kHalves - 1), i = k / kHalves * p.tree_box;
-          tc::tma_load_3d(at + hf * S::kHalf + i * 128, tree_map, hf * 64, s.h, (int)s.base + (t - s.tp) * kTile + i,
-                          &full[stage]);
-        }
-      } else {
-        const int boxes = (valid + box - 1) >> box_shift;
-        if (lane == 0) tc::bar_expect(&full[stage], boxes * kHalves * box * 128);
-        __syncwarp();
-        if (part < boxes) {
-          const int tok = tok0 + t * kTile + (part << box_shift);
-          tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id,
-                          &full[stage]);
-        }
+      // page boxes of the cached tokens, then boxes of tree_box positions
+      const int boxes = (tile_cached(s, t) + box - 1) >> box_shift, col = t == s.tree ? s.col : 0;
+      const int tree_boxes = tree ? (valid - col + p.tree_box - 1) / p.tree_box : 0;
+      if (lane == 0) tc::bar_expect(&full[stage], kHalves * 128 * (boxes * box + tree_boxes * p.tree_box));
+      __syncwarp();
+      if (part < boxes) {
+        const int tok = tok0 + t * kTile + (part << box_shift);
+        tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id,
+                        &full[stage]);
+      }
+      for (int k = lane; k < tree_boxes * kHalves; k += 32) {
+        const int hf = k & (kHalves - 1), i = k / kHalves * p.tree_box;
+        tc::tma_load_3d(at + hf * S::kHalf + (col + i) * 128, tree_map, hf * 64, s.h,
+                        (int)s.base + (t - s.tree) * kTile - s.col + col + i, &full[stage]);
       }
       id = next_id;
     }
@@ -498,7 +508,7 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
   uint32_t fix = 0;           // parity of every stage's vfix
   while (segs.next(sh, s, lane == 0)) {
     const bool dual = uniform(s.rows) > p.rows2 >> 1;
-    const int t0 = uniform(s.t0), tp = s.shared ? 0x7FFFFFFF : uniform(s.tp), n = uniform(s.n), cached = uniform(s.len - s.tok0);
+    const int t0 = uniform(s.t0), first = uniform(s.tree), n = uniform(s.col + s.n), cached = uniform(s.len - s.tok0);
     const int units = uniform(s.t1 - s.t0) << (dual ? 1 : 0);
     // The rows of Q, once both groups are through with the last segment's (and its accumulators): whole positions of
     // G heads. Rows past the item's belong to other positions or lie past the buffer (zeros); nobody reads theirs.
@@ -524,8 +534,8 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
         int stage;
         uint32_t parity;
         ring<S::kV>(vn, stage, parity);
-        const bool tree = t >= tp;
-        const int valid = min(kTile, tree ? n - (t - tp) * kTile : cached - t * kTile);
+        const bool tree = t >= first;  // as tile_valid
+        const int valid = min(kTile, tree ? n - (t - first) * kTile : cached - t * kTile);
         if (!dual || g == 0) {
           if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
           if (tree || valid < kTile) {
@@ -632,12 +642,14 @@ __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int
         continue;
       }
       uint8_t* at = v_smem + stage * S::kBlock;
-      const int upto = (valid + 15) / 16 * 16;
+      const int upto = (valid + 15) / 16 * 16, cached = tree ? tile_cached(s, t) : valid;
+      const int col = tree && t == s.tree ? s.col : tree ? 0 : upto;  // clear: between tokens and positions, and behind
       for (int hf = 0; hf < DP / 64; ++hf) {
-        for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(at + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+        for (int c = cached * 8 + lane; c < col * 8; c += 32) *(uint4*)(at + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
         if (tree) {
+          for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(at + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
           bool odd = false;
-          for (int c = lane; c < valid * 8; c += 32) {
+          for (int c = col * 8 + lane; c < valid * 8; c += 32) {
             uint4 q = *(uint4*)(at + hf * S::kHalf + c * 16);
             uint32_t* e = &q.x;
             bool mine = false;
@@ -673,15 +685,20 @@ struct Row {
   float m, l;  // reference maximum (log2 units), sum of weights
 };
 
-// The 128 tree columns that position i (-1: none) attends to in tree tile jt, as bits; all lanes of the warp.
-__device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s, int jt, int i, uint32_t* bits) {
-  const int lane = threadIdx.x & 31, j0 = jt * kTile;
-  bits[0] = bits[1] = bits[2] = bits[3] = 0;
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// The 128 columns of tile t, which holds tree positions, that position i (-1: none) attends to, as bits; all lanes of the
+// warp.
+__device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s, int t, int i, uint32_t* bits) {
+  const int lane = threadIdx.x & 31, j0 = (t - s.tree) * kTile - s.col;  // position of column 0
+  const int cached = t == s.tree && s.col > 0 ? tile_cached(s, t) : 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) bits[w] = low_bits(cached - 32 * w);
   if (!p.a.mask) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int k = i - (j0 + 32 * w);
-      bits[w] = i < 0 || k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
+      const int c = j0 + 32 * w;  // positions max(c, 0) .. i
+      if (i >= 0) bits[w] |= low_bits(i + 1 - c) & ~low_bits(-c);
     }
     return;
   }
@@ -694,8 +711,8 @@ __device__ __forceinline__ void tree_bits(const AttnParams& p, const Segment& s,
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int j = j0 + 32 * w + lane;
-      const uint32_t word = __ballot_sync(0xFFFFFFFFu, j < s.n && m[(int64_t)x * p.a.P + j] != 0);
-      if (x == i) bits[w] = word;
+      const uint32_t word = __ballot_sync(0xFFFFFFFFu, j >= 0 && j < s.n && m[(int64_t)x * p.a.P + j] != 0);
+      if (x == i) bits[w] |= word;
     }
   }
 }
@@ -744,7 +761,8 @@ __device__ __forceinline__ void add_odd_values(const AttnParams& p, const Segmen
   float x[32];  // its own array: one whose address is taken does not stay in registers
 #pragma unroll
   for (int k = 0; k < 32; ++k) x[k] = o[k];
-  add_odd_row<BF16>(p, s.b, s.h, s.base, (max(s.t0, s.tp) - s.tp) * kTile, min(s.n, (s.t1 - s.tp) * kTile), s.i0 + r / p.G,
+  add_odd_row<BF16>(p, s.b, s.h, s.base, max(0, (max(s.t0, s.tree) - s.tree) * kTile - s.col),
+                    min(s.n, (s.t1 - s.tree) * kTile - s.col), s.i0 + r / p.G,
                     r % p.G, m, scale, d0, x);
 #pragma unroll
   for (int k = 0; k < 32; ++k) o[k] = x[k];
@@ -767,7 +785,7 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
     f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - m);
     l = row.l * f0 + o.y * f1;
   }
-  const bool odd = *(volatile int*)&sh.odd_values && !s.shared && s.t1 > s.tp;
+  const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.tree;
   // 16-byte stores along rows, through the warp's own 32 rows of the Q buffer (its products are done), 32 elements of a
   // row a turn: four lanes a row of the result, eight of a partial.
   const int row0 = r - lane, end = min(s.rows - row0, min(32, half - (wl - lane)));  // the warp's first row, its live rows
@@ -966,13 +984,10 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       const int valid = tile_valid(s, t, tree);
       uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
       const bool masked = tree || valid < kTile;
-      if (tree && work) tree_bits(p, s, t - s.tp, live ? s.i0 + position_of(p, r) : -1, bits);
+      if (tree && work) tree_bits(p, s, t, live ? s.i0 + position_of(p, r) : -1, bits);
       if (masked) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int left = valid - 32 * x;
-          bits[x] &= left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
-        }
+        for (int x = 0; x < 4; ++x) bits[x] &= low_bits(valid - 32 * x);
       }
       if (!tc::bar_wait_warp(&sh.sfull[group], ns++ & 1, &sh.stop)) return;
       // the unit before this one has been added up (S of this one was issued behind it)

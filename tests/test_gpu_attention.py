@@ -155,6 +155,12 @@ CASES = {
     "page 8": dict(B=3, P=2, H_kv=2, G=3, D=64, page=8, lens=[7, 8, 200], tree=False),
     "page 256": dict(B=2, P=5, H_kv=1, G=8, D=128, page=256, lens=[255, 700]),
     "page 128": dict(B=2, P=5, H_kv=2, G=2, D=128, page=128, lens=[128, 515], dtype="fp16"),
+    "tree behind the last tokens": dict(B=7, P=9, H_kv=2, G=2, D=128, page=8, lens=[1, 8, 9, 111, 112, 113, 239]),
+    "tree behind the last tokens, boxes that do not fit": dict(B=5, P=61, H_kv=1, G=4, D=64, page=16,
+                                                               lens=[63, 64, 65, 48, 193], n_pos=[61, 61, 3, 61, 64 - 3]),
+    "chain behind the last tokens": dict(B=6, P=30, H_kv=1, G=2, D=64, page=32, lens=[1, 31, 33, 95, 96, 97], tree=False,
+                                         n_pos=[30, 1, 17, 30, 30, 30], dtype="fp16"),
+    "tree behind the last tokens, shared": dict(B=4, P=9, H_kv=2, G=2, D=64, page=16, lens=[50, 49, 100, 48], shared=48),
     "pr1 tree": dict(B=1, P=17, H_kv=8, G=4, D=128, page=16, lens=[515]),
     "cast tree packed": dict(B=4, P=61, H_kv=2, G=4, D=128, page=64, lens=[1000, 3, 0, 64], n_pos=[61, 17, 40, 1],
                              packed=True),
