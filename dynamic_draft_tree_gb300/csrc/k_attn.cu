@@ -65,7 +65,7 @@ struct AttnParams {
   float c;            // scale * log2 e
   int32_t ns;         // tiles of the shared prefix as items of its own; 0: requests read it with their own tokens
   int32_t skip;       // tokens that a request's own items leave to it
-  int64_t own_slots, own_rows;  // partials of own items: slots and rows of a slot
+  int64_t own_rows;   // rows of an own item's partials
   AttnHead* head;
   int32_t* t_pre;     // [B] unit offset of a request among the own units
   int32_t* k_pre;     // [B] item offset
@@ -87,6 +87,12 @@ struct Request {
   bool bad;
 };
 
+// Rows that belong to requests.
+__device__ __forceinline__ int64_t rows_used(const dt_attn_args& a) {
+  const int64_t padded = (int64_t)a.B * a.P;
+  return a.row_off ? min(max((int64_t)a.row_off[a.B], (int64_t)0), min(padded, a.rows)) : padded;
+}
+
 __device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_shift, int b) {
   Request r;
   const int len = a.seq_len[b], n = a.n_pos[b];
@@ -95,7 +101,8 @@ __device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_sh
   r.len = (int)min((int64_t)max(len, a.shared_len), most);
   r.n = min(max(n, 0), a.P);
   r.bad = len < a.shared_len || len > most || n < 0 || n > a.P;
-  if (r.base < 0 || r.base + r.n > a.rows) {
+  // the rows behind a packed batch's end are no request's (and no shared item's)
+  if (r.base < 0 || r.base + r.n > rows_used(a)) {
     r.bad = true;
     r.n = 0;
   }
@@ -331,11 +338,9 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     items += p.a.H_kv * e.mp;
     if (blockIdx.x == 0 && r.bad) set_status(p.status, DT_DEV_BAD_PAGE);
   }
-  int64_t rows_used = (int64_t)p.a.B * p.a.P;
-  if (p.a.row_off) {
+  if (p.a.row_off && blockIdx.x == 0 && tid == 0) {
     const int64_t last = p.a.row_off[p.a.B];
-    if (blockIdx.x == 0 && tid == 0 && (last < 0 || last > min(rows_used, p.a.rows))) set_status(p.status, DT_DEV_BAD_PAGE);
-    rows_used = min(max(last, (int64_t)0), min(rows_used, p.a.rows));
+    if (last < 0 || last > min((int64_t)p.a.B * p.a.P, p.a.rows)) set_status(p.status, DT_DEV_BAD_PAGE);
   }
   int su = units, si = items;
 #pragma unroll
@@ -361,7 +366,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Shared& sh) {
     }
     total += a;
   }
-  const int rows_s = p.ns ? (int)rows_used * p.G : 0;
+  const int rows_s = p.ns ? (int)rows_used(p.a) * p.G : 0;
   const int mp_s = (rows_s + p.rows2 - 1) / p.rows2;
   const int sh_head = mp_s > 0 ? shared_head(p, rows_s, mp_s, p.ns) : 0;
   const int w_shared = p.a.H_kv * sh_head;
@@ -414,7 +419,6 @@ __device__ __forceinline__ void ring(uint32_t n, int& stage, uint32_t& parity) {
   stage = (int)(n % N);
   parity = (n / N) & 1;
 }
-
 
 // One warp loads the K (or V) tiles of the CTA's line in order.
 template <int DP, bool IS_K>
@@ -1376,7 +1380,6 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.skip = p.ns ? a->shared_len : 0;
   const Layout L = layout_of(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0);
   char* ws = (char*)a->workspace;
-  p.own_slots = L.own_slots;
   p.own_rows = L.own_rows;
   p.head = (AttnHead*)ws;
   p.t_pre = (int32_t*)(ws + L.t_pre);

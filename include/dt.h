@@ -470,8 +470,9 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
  * positions j < n_pos[b] with mask[b][i][j] != 0 (mask NULL: j <= i, a chain, so that P = 1 is a plain
  * decode step). out = softmax(scale * q k^T) v for query head x with key head x / (H_q / H_kv). A position
  * that attends to nothing gets zeros. Rows of tmp buffers (q, k_new, v_new, out) as in DT_VERIFY_PACKED:
- * b*P + i, or row_off[b] + i; rows of no position are left as they were. K and V of tokens past seq_len, of
- * positions past n_pos and of masked positions may hold anything (NaN and infinities too).
+ * b*P + i, or row_off[b] + i (a request whose rows do not end by row_off[B] sets DT_DEV_BAD_PAGE and gets none);
+ * rows of no position are left as they were. K and V of tokens past seq_len, of positions past n_pos and of
+ * masked positions may hold anything (NaN and infinities too).
  * shared_len: the first shared_len tokens (a multiple of page) of every request are the same blocks, those of
  * block_table[0] (the other rows' entries for them are not read): where it pays, their attention is computed for
  * the rows of all requests together, so that they are read once; a request with seq_len < shared_len sets

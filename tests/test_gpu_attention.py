@@ -332,6 +332,38 @@ def test_bad_tables_are_reported(torch):
     h.close()
 
 
+@pytest.mark.parametrize("shared", [0, 2048])
+def test_rows_past_a_packed_batchs_end(torch, shared):
+    """A request whose rows do not end within the packed batch (row_off[B]) sets the status and writes nothing; the
+    others keep their results. Behind a prefix read once for all rows, such rows are no item's."""
+    import dynamic_draft_tree_gb300 as dt
+
+    B = 32 if shared else 3
+    pr = Problem(torch, B=B, P=17, H_kv=8, G=4, D=64, page=16, lens=[shared + 5 + b for b in range(B)], packed=True,
+                 shared=shared)
+    h, ws = pr.handle(dt)
+    pr.row_off[B] = pr.off[B] - 1
+    pr.call(dt, h, ws)
+    assert dt.dt_get_status(h) == dt.DT_DEV_BAD_PAGE
+    dt.dt_clear_status(h)
+    got = pr.out.clone()
+    assert bool((got[pr.off[B - 1]:] == 7.0).all())
+    pr.out.fill_(7.0)
+    want, tol = pr.reference()
+    n = pr.off[B - 1]
+    assert bool(((got[:n].double() - want[:n]).abs() <= tol[:n]).all())
+    # a first row far behind the batch, within the buffers
+    far = 40 * n
+    big = [torch.zeros(far + 17, *x.shape[1:], dtype=x.dtype, device="cuda") for x in (pr.q, pr.kn, pr.vn, pr.out)]
+    pr.q, pr.kn, pr.vn, pr.out = big
+    pr.row_off[B] = pr.off[B]
+    pr.row_off[B - 1] = far
+    pr.call(dt, h, ws)
+    assert dt.dt_get_status(h) == dt.DT_DEV_BAD_PAGE
+    assert bool((pr.out[n:] == 0.0).all())
+    h.close()
+
+
 def test_waits_that_run_out_are_reported(torch):
     """With DT_FLAG_TEST_TIMEOUT no wait is taken: the call ends, says so, and the context stays usable."""
     import dynamic_draft_tree_gb300 as dt
