@@ -100,7 +100,8 @@ __device__ __forceinline__ Request request_of(const dt_attn_args& a, int page_sh
   const int64_t most = min((int64_t)a.max_blocks << page_shift, (int64_t)0x7FFFFF00);
   r.len = (int)min((int64_t)max(len, a.shared_len), most);
   r.n = min(max(n, 0), a.P);
-  r.bad = len < a.shared_len || len > most || n < 0 || n > a.P;
+  // one without positions (an idle place in the batch) needs no prefix
+  r.bad = (n != 0 && len < a.shared_len) || len > most || n < 0 || n > a.P;
   // the rows behind a packed batch's end are no request's (and no shared item's)
   if (r.base < 0 || r.base + r.n > rows_used(a)) {
     r.bad = true;

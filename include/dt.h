@@ -475,8 +475,8 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
  * masked positions may hold anything (NaN and infinities too).
  * shared_len: the first shared_len tokens (a multiple of page) of every request are the same blocks, those of
  * block_table[0] (the other rows' entries for them are not read): where it pays, their attention is computed for
- * the rows of all requests together, so that they are read once; a request with seq_len < shared_len sets
- * DT_DEV_BAD_PAGE and its rows are computed as if seq_len = shared_len.
+ * the rows of all requests together, so that they are read once; a request with positions and
+ * seq_len < shared_len sets DT_DEV_BAD_PAGE and its rows are computed as if seq_len = shared_len.
  * Types: DT_BF16 or DT_F16 for all of q, k, v, out; scores, softmax statistics and sums in fp32, the softmax
  * weights rounded to the input type for the second product. D: a multiple of 8, up to 128. H_q / H_kv <= 128.
  * Strides in elements, multiples of 8; pointers 16-byte aligned. After DT_DEV_TIMEOUT, dt_clear_status also makes the

@@ -332,6 +332,27 @@ def test_bad_tables_are_reported(torch):
     h.close()
 
 
+def test_idle_places_need_no_shared_prefix(torch):
+    """A place without positions and tokens among requests behind a shared prefix is no error; one with positions is."""
+    import dynamic_draft_tree_gb300 as dt
+
+    for shared in (64, 4096):
+        pr = Problem(torch, B=6, P=5, H_kv=8, G=4, D=64, page=16, lens=[shared + 9 * b for b in range(6)],
+                     n_pos=[5, 0, 3, 5, 0, 1], shared=shared)
+        h, ws = pr.handle(dt)
+        pr.seq_len[1] = 0
+        pr.seq_len[4] = 0
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == 0
+        got = pr.out.clone()
+        pr.out.fill_(7.0)
+        _check(pr, got)
+        pr.seq_len[5] = shared - 1
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == dt.DT_DEV_BAD_PAGE
+        h.close()
+
+
 @pytest.mark.parametrize("shared", [0, 2048])
 def test_rows_past_a_packed_batchs_end(torch, shared):
     """A request whose rows do not end within the packed batch (row_off[B]) sets the status and writes nothing; the
