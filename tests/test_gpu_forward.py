@@ -189,3 +189,27 @@ def test_committed_round_in_a_graph(torch):
         have = kv.pages[:, kv.pool.block_table[b, :-(-n // 8)].long()].flatten(1, 2)[:, :n]
         assert torch.equal(have, want)
     h.close()
+
+
+def test_prefill_on_another_stream_keeps_its_slots(torch):
+    """Memory that the current stream allocates while a prefill waits on another stream is not the prefill's."""
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache
+
+    n = 100000
+    h = dt.Handle(1, 50, 1, 1, 1, 4)
+    kv = PagedCache(h, 1, 4, 1, 1, 1, 16, n_blocks=n // 16 + 1, max_blocks=n // 16 + 1, page=16)
+    rows = torch.randn(2, n, 1, 16, device="cuda").bfloat16()
+    n_new, off = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, n]))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # tens of milliseconds
+    kv.prefill(rows, n_new, off, stream=side)
+    later = [torch.full((n,), -7, dtype=torch.int64, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((x == -7).all()) for x in later)
+    assert dt.dt_get_status(h) == 0 and kv.seq_len.tolist() == [n]
+    table = kv.pool.block_table[0, :n // 16].long()
+    assert torch.equal(kv.pages[:, table].view(2, -1, 1, 16)[:, :n], rows)
+    h.close()
