@@ -506,7 +506,7 @@ def dt_count_tokens(h, counts, tokens, n_new, path=None, row_off=None, n_extra=0
         P = max(1, tokens.numel())
     if path is not None and (path.dim() != 2 or path.shape[0] < B):
         raise ValueError("path must be [B][D_path]")
-    check(lib.dt_count_tokens(h.h, B, _dev(counts, _I32, dev, "counts"), _dev(tokens, _I32, dev, "tokens"), P,
+    check(lib.dt_count_tokens(h.h, B, _dev(counts, _I32, dev, "counts"), _dev(tokens, _I32, dev, "tokens"), tokens.numel(), P,
                               _dev(row_off, _I32, dev, "row_off", B + 1), _dev(path, _I32, dev, "path"),
                               0 if path is None else path.shape[1], _dev(n_new, _I32, dev, "n_new"), n_extra,
                               1 if prompt else 0, _raw_stream(dev) if stream is None else stream.cuda_stream))

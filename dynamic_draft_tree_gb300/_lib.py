@@ -154,7 +154,7 @@ def _load():
                                 vp, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, vp, vp], I),
         "dt_tree_attention": ([vp, vp, vp], I),
         "dt_tree_attention_workspace": ([vp] + [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int64)], I),
-        "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
+        "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
                              ctypes.c_int32, vp], I),
         "dt_logits_process": ([vp, ctypes.c_int32, vp, ctypes.c_int64, vp, ctypes.c_int64,
                                vp, vp], I),

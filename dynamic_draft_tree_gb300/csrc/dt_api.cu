@@ -690,16 +690,18 @@ int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
   return DT_OK;
 }
 
-int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int32_t P, const int32_t* row_off,
-                    const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra, int32_t prompt,
+int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int32_t P,
+                    const int32_t* row_off, const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra, int32_t prompt,
                     cudaStream_t s) {
   const int rc = check_batch(h, "dt_count_tokens", B);
   if (rc != DT_OK) return rc;
   if (!counts || !tokens || !n_new) return fail(DT_ERR_ARG, "dt_count_tokens: null argument");
   if (P < 1 || n_extra < 0 || (path && D_path < 1)) return fail(DT_ERR_ARG, "dt_count_tokens: P, D_path >= 1 and n_extra >= 0");
+  if (n_tokens < 1 || (!row_off && n_tokens < (int64_t)B * P))
+    return fail(DT_ERR_ARG, "dt_count_tokens: tokens holds fewer than B * P entries");
   if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(n_new, 4) || !aligned(path, 4) || !aligned(row_off, 4))
     return fail(DT_ERR_ARG, "dt_count_tokens: int32 arrays must be 4-byte aligned");
-  cudaError_t e = dt::launch_count_tokens(h, B, counts, tokens, P, row_off, path, D_path, n_new, n_extra,
+  cudaError_t e = dt::launch_count_tokens(h, B, counts, tokens, n_tokens, P, row_off, path, D_path, n_new, n_extra,
                                           prompt ? 1 : 0, s);
   if (e != cudaSuccess) return cuda_fail(e, "dt_count_tokens");
   return DT_OK;

@@ -194,7 +194,7 @@ bool attn_line_fits(const dt_attn_args* a);  // places on the kernel's line of w
 int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared);
 cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                           const dt_logits_params* p, cudaStream_t s);
-cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int P,
+cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int P,
                                 const int32_t* row_off, const int32_t* path, int D_path, const int32_t* n_new,
                                 int n_extra, int prompt, cudaStream_t s);
 cudaError_t launch_row_topk_static(const void* logits, int64_t ld, int rows, int V, int K, int dtype, float* logp,

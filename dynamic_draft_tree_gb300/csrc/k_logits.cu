@@ -3,7 +3,7 @@
 // Every row is read and written once. A CTA owns a chunk of the vocabulary for one request and goes
 // through a group of that request's rows, so the request's counts and biases of the chunk are read once
 // a group into registers. What differs from row to row is the tree path: the path tokens that fall into the chunk (a few
-// of D <= 17 over V / 2048 chunks) have a bit a row in shared memory, made before the row loop, so that the loop has one
+// of D <= 17 over V / 1024 chunks) have a bit a row in shared memory, made before the row loop, so that the loop has one
 // multiply-add and two selects an element and only threads with a bit set look further. Rows wait in a ring of
 // asynchronous copies that every thread fills and waits for by itself. Bound by DRAM in large calls: 330 rows of 128256
 // bf16 with a grammar mask 38 us (4.7 TB/s of what has to move; a plain device copy of the rows takes 55), 766 MB of fp32
@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
 struct CountArgs {
   int32_t* counts;
   const int32_t* tokens;
+  int64_t n_tokens;
   int32_t P;
   const int32_t* row_off;
   const int32_t* path;
@@ -367,24 +368,20 @@ struct CountArgs {
   int32_t* status;
 };
 
-// CTA (c, b): every gridDim.x-th group of 256 tokens of request b. Integer atomics: order does not matter.
+// CTA (c, b): every gridDim.x-th group of kLogThreads tokens of request b. Integer atomics: order does not matter.
 __global__ void __launch_bounds__(kLogThreads) count_kernel(CountArgs a) {
   pdl_begin();
   const int b = blockIdx.y;
   const int64_t n = (int64_t)a.n_new[b] + a.n_extra;
-  const int64_t room = a.path ? a.D_path : a.row_off ? (int64_t)a.row_off[b + 1] - a.row_off[b] : a.P;
-  if (n < 0 || n > room) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TREE);
-    return;
-  }
   const int64_t base = a.row_off ? (int64_t)a.row_off[b] : (int64_t)b * a.P;
-  if (base < 0) {
+  const int64_t rows = a.row_off ? (int64_t)a.row_off[b + 1] - base : a.P;  // the request's
+  if (n < 0 || n > (a.path ? (int64_t)a.D_path : rows)) {
     if (threadIdx.x == 0 && blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TREE);
     return;
   }
   for (int64_t j = (int64_t)blockIdx.x * kLogThreads + threadIdx.x; j < n; j += (int64_t)gridDim.x * kLogThreads) {
     const int pos = a.path ? a.path[(int64_t)b * a.D_path + j] : (int)j;
-    if (pos < 0 || (a.path && pos >= a.P)) {
+    if (pos < 0 || pos >= rows || (a.path && pos >= a.P) || base < 0 || base + pos >= a.n_tokens) {
       set_status(a.status, DT_DEV_BAD_TREE);
       continue;
     }
@@ -430,10 +427,10 @@ cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, v
   return h->cfg.dtype == DT_BF16 ? launch_logits_t<uint16_t>(h, B, a, s) : launch_logits_t<float>(h, B, a, s);
 }
 
-cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int P,
+cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int P,
                                 const int32_t* row_off, const int32_t* path, int D_path, const int32_t* n_new,
                                 int n_extra, int prompt, cudaStream_t s) {
-  CountArgs a{counts, tokens, P, row_off, path, D_path, n_new, n_extra, prompt, h->cfg.V, h->ws.status};
+  CountArgs a{counts, tokens, n_tokens, P, row_off, path, D_path, n_new, n_extra, prompt, h->cfg.V, h->ws.status};
   const int64_t most = path ? D_path : P;
   const int chunks = (int)min((int64_t)64, max((int64_t)1, (most + kLogThreads - 1) / kLogThreads));
   launch_k(count_kernel, dim3(chunks, B), dim3(kLogThreads), 0, s, a);

@@ -429,7 +429,7 @@ typedef struct {
  *   slot_off NULL: [B][S]; else (device [B+1]) packed: request b's at slot_off[b] .. slot_off[b+1] - 1,
  *   at most S of them; entries past slot_off[B] are left as they were.
  * n_slots: entries of the slots buffer (offsets beyond it set DT_DEV_BAD_PAGE, the request gets none).
- * One launch. seq_len is read only (dt_commit_kv_paged advances it). */
+ * seq_len is read only (dt_commit_kv_paged advances it). */
 int dt_kv_reserve(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* seq_len, const int32_t* n_new,
                   int32_t n_extra, int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
                   cudaStream_t s);
@@ -514,19 +514,20 @@ int dt_tree_attention_workspace(dt_handle* h, int32_t B, int32_t P, int32_t H_q,
  * DT_SEEN_PROMPT when v is in the prompt. A new request's row is cleared by the caller. */
 enum { DT_SEEN_PROMPT = 0x40000000 };
 /* Adds request b's tokens tokens[(row_off ? row_off[b] : b*P) + (path ? path[b*D_path + j] : j)],
- * j < n_new[b] + n_extra, to counts [B][V] (prompt != 0: marks them instead): after a verify, tokens =
- * dt_tree_meta.tokens, path = accept_path, n_new = accept_len, n_extra = 1 add the root and the accepted
- * tokens, the ones whose KV dt_commit_kv commits. A token outside [0, V) sets DT_DEV_BAD_TOKEN and is
- * skipped; n past D_path (with a path) or P (without row_off) sets DT_DEV_BAD_TREE and adds nothing. */
-int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int32_t P, const int32_t* row_off,
-                    const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra, int32_t prompt,
-                    cudaStream_t s);
+ * j < n_new[b] + n_extra, to counts [B][V] (prompt != 0: marks them instead); n_tokens: entries of tokens.
+ * After a verify, tokens = dt_tree_meta.tokens, path = accept_path, n_new = accept_len, n_extra = 1 add the root
+ * and the accepted tokens, the ones whose KV dt_commit_kv commits. A token outside [0, V) sets DT_DEV_BAD_TOKEN
+ * and is skipped; n past D_path (with a path), P or the request's row_off[b + 1] - row_off[b] (without) sets
+ * DT_DEV_BAD_TREE and adds nothing; a position outside [0, P), its rows or tokens sets it and is skipped. */
+int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int32_t P,
+                    const int32_t* row_off, const int32_t* path, int32_t D_path, const int32_t* n_new,
+                    int32_t n_extra, int32_t prompt, cudaStream_t s);
 
 /* Target rows prepared for dt_verify: penalties for repeated tokens, biases and grammar masks, in one pass.
  * For every used row (b, i) (padded b*P + i, or row_off[b] + i) and token v, in fp32, rounded once:
  *   c = (counts[b][v] without DT_SEEN_PROMPT) + occurrences of v among the tokens on i's path (the tree
  *       positions j with mask[b][i][j] != 0; mask NULL: j <= i), seen = c > 0 or DT_SEEN_PROMPT;
- *   y = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x;
+ *   y = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x;   (x / r as x times the fp32 1 / r)
  *   y = y - frequency[b] * c - (c > 0 ? presence[b] : 0);
  *   y = y + the sum of bias_vals[b][k] over bias_ids[b][k] == v in list order (-1: unused entry);
  *   out = allow bit v of the row's words (bit v & 31 of word v >> 5) ? y : -inf.

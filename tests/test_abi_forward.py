@@ -28,7 +28,7 @@ def test_null_handle_is_refused(libdt):
     assert lib.dt_commit_kv_paged(None, 1, None, 1, None, None, 0, None, 0, None, 0, 1, None, None, None, None) == bad
     assert lib.dt_tree_attention(None, None, None) == bad
     assert lib.dt_tree_attention_workspace(None, 1, 1, 1, 1, 64, 0, ctypes.byref(n)) == bad
-    assert lib.dt_count_tokens(None, 1, None, None, 1, None, None, 0, None, 0, 0, None) == bad
+    assert lib.dt_count_tokens(None, 1, None, None, 0, 1, None, None, 0, None, 0, 0, None) == bad
     assert lib.dt_logits_process(None, 1, None, 0, None, 0, None, None) == bad
     assert "null" in lib.dt_last_error_string().decode()
 

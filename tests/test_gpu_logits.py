@@ -266,6 +266,23 @@ def test_count_tokens(torch):
     dt.dt_count_tokens(h, counts, torch.tensor(tok, **i32), torch.full((B,), P + 1, **i32))
     assert dt.dt_get_status(h) == dt.DT_DEV_BAD_TREE
     assert torch.equal(before, counts)
+    dt.dt_clear_status(h)
+    # packed rows: a path out of the request's rows, rows that do not end in the buffer
+    two, one = torch.tensor([0, 3, 5], **i32), torch.ones(2, **i32)
+    few = torch.tensor([1, 2, 3, 4, 5], **i32)
+    for path, off in (([[3], [0]], two), ([[-1], [0]], two), ([[0], [2]], torch.tensor([0, 3, 6], **i32)),
+                      ([[0], [0]], torch.tensor([0, 1 << 30, (1 << 30) + 2], **i32)),
+                      ([[0], [0]], torch.tensor([-3, 0, 2], **i32)),
+                      ([[0], [0]], torch.tensor([0, 3, 2], **i32))):
+        counts.zero_()
+        dt.dt_count_tokens(h, counts, few, one, path=torch.tensor(path, **i32), row_off=off, P=3)
+        assert dt.dt_get_status(h) == dt.DT_DEV_BAD_TREE
+        dt.dt_clear_status(h)
+        assert int(counts.sum()) == 1
+    counts.zero_()
+    dt.dt_count_tokens(h, counts, few, torch.tensor([3, 3], **i32), row_off=torch.tensor([0, 3, 6], **i32))
+    assert dt.dt_get_status(h) == dt.DT_DEV_BAD_TREE
+    assert int(counts.sum()) == 5  # the sixth lies past the buffer
     h.close()
 
 
