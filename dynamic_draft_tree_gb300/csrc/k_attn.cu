@@ -1001,14 +1001,17 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
       if (work) {
         if (masked) mask_scores(s_at, bits[0], bits[1], bits[2], bits[3]);
         uint32_t raw[64];
-        float top = -INFINITY;
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           tc::tmem_ld64(s_at + hf * 64, raw);
 #pragma unroll
-          for (int x = 0; x < 64; x += 2) top = fmaxf(fmaxf(top, __uint_as_float(raw[x])), __uint_as_float(raw[x + 1]));
+          for (int x = 0; x < 64; x += 8) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
+          }
         }
-        top *= p.c;
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
         if (k == 0) {
           row.m = top;
         } else {
