@@ -24,8 +24,9 @@
 // live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
 //
 // What bounds it, at D = 128 on one GB300: few rows, the cache's bytes (64 requests, 5100 cached tokens on average:
-// 6.4 TB/s, 0.95 of the measured copy peak); a shared prefix, the chain of one group's softmax (about 1500 clocks a tile
-// of 128 x 128) and its two products (1024), of which the tensor cores are busy 2048 of 2780 clocks; small calls,
+// 6.3 TB/s, 0.93 of the measured copy peak); a shared prefix, the chain of one group's softmax (about 1400 clocks a tile
+// of 128 x 128, 450 of them for 64 columns' powers, where the unit for them would need 260) and its two products (1030),
+// of which the tensor cores are busy 2060 of 2750 clocks; small calls,
 // latency (11 us: 1.3 for the plan, 1 for the first segment, 2.5 for the first tiles, 1.1 softmax, 3 for the join).
 // One issuing thread behind `if (lane == 0)` instead of the uniform path cost 70 clocks an instruction (attend to 64
 // requests behind a prefix: 436 against 294 us); fully unrolled softmax code for masked and unmasked tiles missed the
@@ -567,7 +568,7 @@ __device__ void issue_mma(const AttnParams& p, Shared& sh, const CUtensorMap* q_
 #pragma unroll
           for (int x = kTile / 32; x < kTile / 16; ++x)
             if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
-          tc::mma_commit(&sh.odone[g]);
+          if (v >= units) tc::mma_commit(&sh.odone[g]);  // else S's commit says so too
           if (last) tc::mma_commit(&sh.vempty[stage]);
         }
         if (last) {
@@ -995,8 +996,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
         for (int x = 0; x < 4; ++x) bits[x] &= low_bits(valid - 32 * x);
       }
       if (!tc::bar_wait_warp(&sh.sfull[group], ns++ & 1, &sh.stop)) return;
-      // the unit before this one has been added up (S of this one was issued behind it)
-      if (k > 0 && !tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
+      // the unit before this one has been added up too: S of this one was issued behind it
       tc::fence_after();
       if (work) {
         if (masked) mask_scores(s_at, bits[0], bits[1], bits[2], bits[3]);
@@ -1064,7 +1064,7 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
     // A group without a unit in this segment still comes along: its arrival on qfree below must not fall into the last
     // segment's phase, which is over once this segment's Q has been loaded.
     if (mine == 0 && !tc::bar_wait_warp(&sh.qfull, seg & 1, &sh.stop)) return;
-    // the group's last product
+    // the group's last product, with no S behind it
     if (mine > 0) {
       if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
       tc::fence_after();
