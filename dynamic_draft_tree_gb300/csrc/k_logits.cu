@@ -22,6 +22,10 @@ constexpr int kPer = 8;                          // tokens of a thread
 constexpr int kLogChunk = kLogThreads * kPer;    // tokens of a CTA
 template <typename T>
 constexpr int kWords = kPer * (int)sizeof(T) / 4;  // 32-bit words of a row that a thread holds
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);        // tokens of 16 bytes
+template <typename T>
+constexpr int kChunks = kPer / kVec<T>;
 constexpr int kLogRows = 16;                     // rows of a CTA, at most (bits of a word)
 
 struct LogitsArgs {
@@ -69,7 +73,7 @@ __device__ __forceinline__ float add_of(const Penalty& p, int c, float bias) {
 template <typename T>
 constexpr int kRingRows = sizeof(T) == 2 ? 8 : 4;
 template <typename T>
-constexpr int kRingBytes = kRingRows<T> * (kWords<T> + 1) * kLogThreads * 4;
+constexpr int kRingBytes = kRingRows<T> * (kWords<T> + kChunks<T>) * kLogThreads * 4;
 
 __device__ __forceinline__ void copy16(uint32_t* dst, const void* src, int bytes) {  // the rest of the 16 becomes zero
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
@@ -86,19 +90,20 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups ar
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// VEC: every row starts on a 16-byte boundary; a thread's tokens are then neighbours (two 16-byte
-// accesses), else one token in every kLogThreads (coalesced single elements; bf16 ones are too small for an
-// asynchronous copy and are loaded one row ahead of their use).
+// VEC: every row starts on a 16-byte boundary; a thread's tokens are then 16 bytes in every 16 kLogThreads (a warp's
+// accesses are whole lines; fp32 tokens of a thread as one run of 32 bytes, half lines an access: 16 x up to 65 rows of
+// 128256 149 us, so 110 us), else one token in every kLogThreads (coalesced single elements; bf16 ones are too small for
+// an asynchronous copy and are loaded one row ahead of their use).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   // A row's elements wait in shared memory, kDepth rows ahead, every thread's in places of its own (asynchronous copies
   // that only the thread itself waits for), and the allow word that holds (VEC) or lends its warp their bits.
-  constexpr int W = kWords<T>, kDepth = kRingRows<T>;
+  constexpr int W = kWords<T>, kDepth = kRingRows<T>, E = kVec<T>, C = kChunks<T>;
   extern __shared__ __align__(16) uint32_t dyn[];
   const int P = a.p.P;
   uint32_t* ring = dyn;                                          // [kDepth][W][kLogThreads]
-  uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][kLogThreads]
-  int32_t* path_tok = (int32_t*)(said + kDepth * kLogThreads);   // [P] chunk offset of a position's token, its position
+  uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][C][kLogThreads]
+  int32_t* path_tok = (int32_t*)(said + kDepth * C * kLogThreads);  // [P] chunk offset of a position's token, its position
   int32_t* path_pos = path_tok + P;                              // [P]
   uint32_t* on_rows = (uint32_t*)(path_pos + P);                 // [P] bit r: on row r's path
   __shared__ int n_path, twice;
@@ -134,15 +139,17 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     if (tid == 0) set_status(a.status, DT_DEV_BAD_PAGE);
     return;
   }
-  auto place = [&](int u) { return VEC ? tid * kPer + u : tid + u * kLogThreads; };  // in the chunk
+  auto place = [&](int u) { return VEC ? u / E * E * kLogThreads + tid * E + u % E : tid + u * kLogThreads; };  // in the chunk
   constexpr bool kHalves = !VEC && W < kPer;  // strided bf16
-  const T* src = (const T*)a.logits + (base + row0) * a.ld + v0 + (VEC ? tid * kPer : tid);  // the next row to fetch
-  T* dst = (T*)a.out + (base + row0) * a.ld_out + v0 + (VEC ? tid * kPer : tid);
-  const int word_at = VEC ? tid * kPer >> 5 : lane * (kLogThreads / 32) + warp;
-  const int word_shift = tid * kPer & 31;  // VEC: this thread's first bit
-  const bool word_in = a.p.allow && (VEC ? v0 + tid * kPer < a.V : lane < kPer && v0 + word_at * 32 < a.V);
+  const T* src = (const T*)a.logits + (base + row0) * a.ld + v0 + (VEC ? tid * E : tid);  // the next row to fetch
+  T* dst = (T*)a.out + (base + row0) * a.ld_out + v0 + (VEC ? tid * E : tid);
+  constexpr int kWordStep = E * kLogThreads / 32;  // VEC: words from one 16 bytes' bits to the next
+  const int word_at = VEC ? tid * E >> 5 : lane * (kLogThreads / 32) + warp;
+  const int word_shift = tid * E & 31;  // VEC: this thread's first bit
+  const bool word_in = a.p.allow && (VEC ? v0 + tid * E < a.V : lane < kPer && v0 + word_at * 32 < a.V);
   const uint32_t* allow_at = a.p.allow + (base + row0) * a.p.allow_ld + (v0 >> 5) + word_at;
-  const int left = (a.V - v0 - tid * kPer) * (int)sizeof(T);  // VEC: bytes of the row from this thread's first token
+  const int left = (a.V - v0 - tid * E) * (int)sizeof(T);  // VEC: bytes of the row from this thread's first token
+  constexpr int kStep = 16 * kLogThreads;                  // VEC: bytes from one 16 to the next
   uint32_t* mine = ring + tid * (VEC ? 4 : 1);
   auto fetch = [&](int r) {
     if (r < rows) {
@@ -150,13 +157,15 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
       if constexpr (VEC) {
 #pragma unroll
         for (int c = 0; c < W / 4; ++c)
-          if (left > 16 * c) copy16(to + c * kLogThreads * 4, (const char*)src + 16 * c, min(16, left - 16 * c));
+          if (left > kStep * c) copy16(to + c * kLogThreads * 4, (const char*)src + kStep * c, min(16, left - kStep * c));
       } else if constexpr (!kHalves) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u)
           if (v0 + place(u) < a.V) copy4(to + u * kLogThreads, src + u * kLogThreads);
       }
-      if (word_in) copy4(said + (r % kDepth) * kLogThreads + tid, allow_at);
+      if (word_in) copy4(said + (r % kDepth) * C * kLogThreads + tid, allow_at);
+      if constexpr (VEC && C > 1)
+        if (a.p.allow && left > kStep) copy4(said + ((r % kDepth) * C + 1) * kLogThreads + tid, allow_at + kWordStep);
       if constexpr (!kHalves) src += a.ld;
       allow_at += a.p.allow_ld;
     }
@@ -177,12 +186,15 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   load_halves();
   const int32_t* counts = a.p.counts ? a.p.counts + (int64_t)b * a.V + v0 : nullptr;
   int cnt[kPer];
-  if (counts && VEC && a.counts16 && left >= kPer * (int)sizeof(T)) {
-    const int4 lo = ((const int4*)counts)[2 * tid], hi = ((const int4*)counts)[2 * tid + 1];
-    cnt[0] = lo.x, cnt[1] = lo.y, cnt[2] = lo.z, cnt[3] = lo.w, cnt[4] = hi.x, cnt[5] = hi.y, cnt[6] = hi.z, cnt[7] = hi.w;
-  } else {
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) cnt[u] = counts && v0 + place(u) < a.V ? counts[place(u)] : 0;
+  for (int u = 0; u < kPer; u += 4) {
+    if (counts && VEC && a.counts16 && v0 + place(u) < a.V) {  // (V is a multiple of 4)
+      const int4 q = *(const int4*)(counts + place(u));
+      cnt[u] = q.x, cnt[u + 1] = q.y, cnt[u + 2] = q.z, cnt[u + 3] = q.w;
+    } else {
+#pragma unroll
+      for (int k = u; k < u + 4; ++k) cnt[k] = counts && v0 + place(k) < a.V ? counts[place(k)] : 0;
+    }
   }
   if (tid == 0) n_path = twice = 0;
   for (int i = tid; i < kLogRows * (kLogChunk / 32); i += kLogThreads) (&hit[0][0])[i] = 0;
@@ -290,9 +302,11 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     // bit u: the thread's token u may be said
     uint32_t allow = 0xFFFFFFFFu;
     if (a.p.allow) {
-      const uint32_t word = said[(r % kDepth) * kLogThreads + tid];
+      const uint32_t word = said[(r % kDepth) * C * kLogThreads + tid];
       if (VEC) {
         allow = word >> word_shift;
+        if constexpr (C > 1)
+          allow = (allow & ((1u << E) - 1)) | said[((r % kDepth) * C + 1) * kLogThreads + tid] >> word_shift << E;
       } else {  // the warp's tokens of u are the 32 of one word
         allow = 0;
 #pragma unroll
@@ -308,7 +322,8 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     if (np > 0) {  // tokens on the row's path count beside the history
       uint32_t on_path = 0;
       if (VEC) {
-        on_path = hit[r][word_at] >> word_shift & ((1u << kPer) - 1);
+#pragma unroll
+        for (int c = 0; c < C; ++c) on_path |= (hit[r][word_at + c * kWordStep] >> word_shift & ((1u << E) - 1)) << c * E;
       } else {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) on_path |= (hit[r][u * (kLogThreads / 32) + warp] >> lane & 1u) << u;
@@ -334,14 +349,15 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     }
     uint32_t res[W];
     pack_words<T>(y, res);
-    if (VEC && left >= kPer * (int)sizeof(T)) {
+    if (VEC && left >= kStep * (C - 1) + 16) {
 #pragma unroll
-      for (int c = 0; c < W; c += 4) ((uint4*)dst)[c / 4] = make_uint4(res[c], res[c + 1], res[c + 2], res[c + 3]);
+      for (int c = 0; c < C; ++c)
+        *(uint4*)((char*)dst + kStep * c) = make_uint4(res[4 * c], res[4 * c + 1], res[4 * c + 2], res[4 * c + 3]);
     } else {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         if (v0 + place(u) < a.V) {
-          T* to = dst + (VEC ? u : u * kLogThreads);
+          T* to = dst + (VEC ? u / E * E * kLogThreads + u % E : u * kLogThreads);
           if constexpr (sizeof(T) == 4)
             *(uint32_t*)to = res[u];
           else
