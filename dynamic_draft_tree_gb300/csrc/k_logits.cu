@@ -7,8 +7,10 @@
 // multiply-add and two selects an element and only threads with a bit set look further. Rows wait in a ring of
 // asynchronous copies that every thread fills and waits for by itself. Bound by DRAM in large calls: 330 rows of 128256
 // bf16 with a grammar mask 38 us (4.7 TB/s of what has to move; a plain device copy of the rows takes 55), 766 MB of fp32
-// rows 146 us (5.2 TB/s). Loads into registers instead of the ring: 48 us (more registers, fewer CTAs); 16 tokens
+// rows of an odd vocabulary 131 us (5.8 TB/s), of a vocabulary of whole 16 bytes 6.1 TB/s. Loads into registers instead of the ring: 48 us (more registers, fewer CTAs); 16 tokens
 // a thread instead of 8: 52 us; 8 CTAs an SM instead of 6 (spills): 58 us.
+#include <algorithm>
+
 #include "dt_internal.cuh"
 
 namespace dt {
@@ -28,6 +30,22 @@ template <typename T>
 constexpr int kChunks = kPer / kVec<T>;
 constexpr int kLogRows = 16;                     // rows of a CTA, at most (bits of a word)
 
+// How a row's tokens are divided among the threads.
+// kAligned: every row starts on a 16-byte boundary; a thread's tokens are 16 bytes in every 16 kLogThreads (a warp's
+//   accesses are whole lines; fp32 tokens of a thread as one run of 32 bytes, half lines an access: 16 x up to 65 rows of
+//   128256 149 us, so 110 us).
+// kShifted: rows start anywhere, but every `step`-th row equally far from a 16-byte boundary, in the logits and in the
+//   output. A CTA takes such rows, and its chunk begins that far in front of the vocabulary's, so that accesses are those of
+//   aligned rows (what lies in front of a row is read, never used or written; 16 aligned bytes do not begin before an
+//   allocation).
+// kSingle: one token in every kLogThreads (single elements; bf16 ones are too small for an asynchronous copy and are loaded
+//   one row ahead of their use): logits and output that differ in alignment, and few rows, whose tables weigh more the
+//   fewer rows a CTA has of its kind: kShiftRows. Single and shifted, 16 requests: fp32, every fourth row alike, 128255
+//   tokens: 16 positions 40 and 47 us, 32 66.5 and 68, 48 105 and 96, 65 146 and 131; bf16, every second row alike, 128252
+//   tokens: 8 positions 21 and 24 us, 24 44 and 40, 65 98 and 80; every eighth, 128255 tokens, 65 positions: 108 and 111 us.
+enum { kSingle, kAligned, kShifted };
+constexpr int kShiftRows = 10;
+
 struct LogitsArgs {
   dt_logits_params p;
   const void* logits;
@@ -36,6 +54,7 @@ struct LogitsArgs {
   int64_t ld_out;
   int32_t V;
   int32_t rows;   // rows of a CTA
+  int32_t step;   // kShifted: from one of its rows to the next, else 1
   bool counts16;  // every counts row starts on a 16-byte boundary
   int32_t* status;
 };
@@ -72,8 +91,10 @@ __device__ __forceinline__ float add_of(const Penalty& p, int c, float bias) {
 // 128 bytes a thread on their way.
 template <typename T>
 constexpr int kRingRows = sizeof(T) == 2 ? 8 : 4;
-template <typename T>
-constexpr int kRingBytes = kRingRows<T> * (kWords<T> + kChunks<T>) * kLogThreads * 4;
+template <typename T, int MODE>
+constexpr int kSaid = (MODE == kShifted ? 2 : 1) * kChunks<T>;  // allow words that a thread has of a row
+template <typename T, int MODE>
+constexpr int kRingBytes = kRingRows<T> * (kWords<T> + kSaid<T, MODE>) * kLogThreads * 4;
 
 __device__ __forceinline__ void copy16(uint32_t* dst, const void* src, int bytes) {  // the rest of the 16 becomes zero
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
@@ -90,20 +111,17 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups ar
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// VEC: every row starts on a 16-byte boundary; a thread's tokens are then 16 bytes in every 16 kLogThreads (a warp's
-// accesses are whole lines; fp32 tokens of a thread as one run of 32 bytes, half lines an access: 16 x up to 65 rows of
-// 128256 149 us, so 110 us), else one token in every kLogThreads (coalesced single elements; bf16 ones are too small for
-// an asynchronous copy and are loaded one row ahead of their use).
-template <typename T, bool VEC>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   // A row's elements wait in shared memory, kDepth rows ahead, every thread's in places of its own (asynchronous copies
-  // that only the thread itself waits for), and the allow word that holds (VEC) or lends its warp their bits.
-  constexpr int W = kWords<T>, kDepth = kRingRows<T>, E = kVec<T>, C = kChunks<T>;
+  // that only the thread itself waits for), and the allow words that hold (VEC) or lend its warp their bits.
+  constexpr bool VEC = MODE != kSingle, SHIFT = MODE == kShifted;
+  constexpr int W = kWords<T>, kDepth = kRingRows<T>, E = kVec<T>, C = kChunks<T>, A = kSaid<T, MODE>;
   extern __shared__ __align__(16) uint32_t dyn[];
   const int P = a.p.P;
   uint32_t* ring = dyn;                                          // [kDepth][W][kLogThreads]
-  uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][C][kLogThreads]
-  int32_t* path_tok = (int32_t*)(said + kDepth * C * kLogThreads);  // [P] chunk offset of a position's token, its position
+  uint32_t* said = ring + kDepth * W * kLogThreads;              // [kDepth][A][kLogThreads]
+  int32_t* path_tok = (int32_t*)(said + kDepth * A * kLogThreads);  // [P] chunk offset of a position's token, its position
   int32_t* path_pos = path_tok + P;                              // [P]
   uint32_t* on_rows = (uint32_t*)(path_pos + P);                 // [P] bit r: on row r's path
   __shared__ int n_path, twice;
@@ -112,8 +130,8 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   __shared__ uint32_t biased[kLogChunk / 32];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
-  const int v0 = blockIdx.x * kLogChunk;
-  const int row0 = blockIdx.z * a.rows;
+  const int step = SHIFT ? a.step : 1;
+  const int row0 = SHIFT ? (int)(blockIdx.z % step + blockIdx.z / step * a.rows * step) : (int)blockIdx.z * a.rows;
   // everything that depends on the request alone is asked for at once
   const bool with_bias = a.p.bias_ids != nullptr && a.p.n_bias > 0;
   const int32_t* ids = a.p.bias_ids + (int64_t)b * a.p.n_bias;
@@ -134,11 +152,13 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   pen.freq = a.p.frequency ? a.p.frequency[b] : 0.0f;
   pen.pres = a.p.presence ? a.p.presence[b] : 0.0f;
   if (row0 >= n) return;
-  const int rows = min(a.rows, n - row0);
+  const int rows = min(a.rows, (n - row0 + step - 1) / step);
   if (base < 0 || base + n > a.p.rows) {
     if (tid == 0) set_status(a.status, DT_DEV_BAD_PAGE);
     return;
   }
+  int v0 = blockIdx.x * kLogChunk;  // token of the chunk's first place
+  if (SHIFT) v0 -= (int)(((uint64_t)(uintptr_t)a.logits / sizeof(T) + (uint64_t)(base + row0) * a.ld) % E);
   auto place = [&](int u) { return VEC ? u / E * E * kLogThreads + tid * E + u % E : tid + u * kLogThreads; };  // in the chunk
   constexpr bool kHalves = !VEC && W < kPer;  // strided bf16
   const T* src = (const T*)a.logits + (base + row0) * a.ld + v0 + (VEC ? tid * E : tid);  // the next row to fetch
@@ -147,7 +167,8 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   const int word_at = VEC ? tid * E >> 5 : lane * (kLogThreads / 32) + warp;
   const int word_shift = tid * E & 31;  // VEC: this thread's first bit
   const bool word_in = a.p.allow && (VEC ? v0 + tid * E < a.V : lane < kPer && v0 + word_at * 32 < a.V);
-  const uint32_t* allow_at = a.p.allow + (base + row0) * a.p.allow_ld + (v0 >> 5) + word_at;
+  const int allow_shift = SHIFT ? (v0 + tid * E) & 31 : word_shift;  // where its bits begin in the allow word
+  const uint32_t* allow_at = a.p.allow + (base + row0) * a.p.allow_ld + (SHIFT ? (v0 + tid * E) >> 5 : (v0 >> 5) + word_at);
   const int left = (a.V - v0 - tid * E) * (int)sizeof(T);  // VEC: bytes of the row from this thread's first token
   constexpr int kStep = 16 * kLogThreads;                  // VEC: bytes from one 16 to the next
   uint32_t* mine = ring + tid * (VEC ? 4 : 1);
@@ -163,11 +184,23 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
         for (int u = 0; u < kPer; ++u)
           if (v0 + place(u) < a.V) copy4(to + u * kLogThreads, src + u * kLogThreads);
       }
-      if (word_in) copy4(said + (r % kDepth) * C * kLogThreads + tid, allow_at);
-      if constexpr (VEC && C > 1)
-        if (a.p.allow && left > kStep) copy4(said + ((r % kDepth) * C + 1) * kLogThreads + tid, allow_at + kWordStep);
-      if constexpr (!kHalves) src += a.ld;
-      allow_at += a.p.allow_ld;
+      uint32_t* word = said + (r % kDepth) * A * kLogThreads + tid;
+      if constexpr (SHIFT) {  // the bits of 16 bytes may lie in two words
+        if (a.p.allow) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int v = v0 + c * E * kLogThreads + tid * E;
+            if (v >= 0 && v < a.V) copy4(word + 2 * c * kLogThreads, allow_at + c * kWordStep);
+            if (allow_shift > 32 - E && (v | 31) + 1 < a.V) copy4(word + (2 * c + 1) * kLogThreads, allow_at + c * kWordStep + 1);
+          }
+        }
+      } else {
+        if (word_in) copy4(word, allow_at);
+        if constexpr (VEC && C > 1)
+          if (a.p.allow && left > kStep) copy4(word + kLogThreads, allow_at + kWordStep);
+      }
+      if constexpr (!kHalves) src += step * a.ld;
+      allow_at += step * a.p.allow_ld;
     }
     copies_close();
   };
@@ -177,7 +210,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u)
         if (v0 + place(u) < a.V) half[u] = src[u * kLogThreads];
-      src += a.ld;
+      src += a.ld;  // (step 1)
     }
   };
   // the first rows and the counts are on their way while the tables are made
@@ -188,12 +221,12 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   int cnt[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; u += 4) {
-    if (counts && VEC && a.counts16 && v0 + place(u) < a.V) {  // (V is a multiple of 4)
+    if (counts && VEC && !SHIFT && a.counts16 && v0 + place(u) < a.V) {  // (V is a multiple of 4)
       const int4 q = *(const int4*)(counts + place(u));
       cnt[u] = q.x, cnt[u + 1] = q.y, cnt[u + 2] = q.z, cnt[u + 3] = q.w;
     } else {
 #pragma unroll
-      for (int k = u; k < u + 4; ++k) cnt[k] = counts && v0 + place(k) < a.V ? counts[place(k)] : 0;
+      for (int k = u; k < u + 4; ++k) cnt[k] = counts && v0 + place(k) < a.V && (!SHIFT || v0 + place(k) >= 0) ? counts[place(k)] : 0;
     }
   }
   if (tid == 0) n_path = twice = 0;
@@ -223,7 +256,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
       const float val = k == tid ? val0 : vals[k];
       if (id < -1 || id >= a.V) {
         if (blockIdx.x == 0) set_status(a.status, DT_DEV_BAD_TOKEN);
-      } else if (id >= v0 && id - v0 < kLogChunk) {
+      } else if (id >= max(v0, 0) && id - v0 < kLogChunk) {
         const int off = id - v0;
         if (atomicOr(&biased[off >> 5], 1u << (off & 31)) >> (off & 31) & 1)
           twice = 1;
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     if (warp == 0) {
       for (int k0 = 0; k0 < a.p.n_bias; k0 += 32) {
         const int k = k0 + lane, id = k < a.p.n_bias ? ids[k] : -1;
-        const bool inside = id >= v0 && id - v0 < kLogChunk && id < a.V;
+        const bool inside = id >= max(v0, 0) && id - v0 < kLogChunk && id < a.V;
         const float val = inside ? vals[k] : 0.0f;
         for (uint32_t m = __ballot_sync(0xFFFFFFFFu, inside); m; m &= m - 1) {
           if (lane == __ffs(m) - 1) bias_s[id - v0] += val;
@@ -252,7 +285,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
   }
   const int np = n_path;
   auto on_path_of = [&](int r, int k) {  // is path entry k on row r's path
-    const int i = row0 + r, j = path_pos[k];
+    const int i = row0 + r * step, j = path_pos[k];
     return a.p.mask ? a.p.mask[((int64_t)b * P + i) * P + j] != 0 : j <= i;
   };
   // bits of the rows' path tokens: the first mask byte of a thread travels while the additions are made up
@@ -302,11 +335,16 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     // bit u: the thread's token u may be said
     uint32_t allow = 0xFFFFFFFFu;
     if (a.p.allow) {
-      const uint32_t word = said[(r % kDepth) * C * kLogThreads + tid];
-      if (VEC) {
+      const uint32_t* words = said + (r % kDepth) * A * kLogThreads + tid;
+      const uint32_t word = words[0];
+      if constexpr (SHIFT) {
+        allow = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          allow |= (__funnelshift_r(words[2 * c * kLogThreads], words[(2 * c + 1) * kLogThreads], allow_shift) & ((1u << E) - 1)) << c * E;
+      } else if constexpr (VEC) {
         allow = word >> word_shift;
-        if constexpr (C > 1)
-          allow = (allow & ((1u << E) - 1)) | said[((r % kDepth) * C + 1) * kLogThreads + tid] >> word_shift << E;
+        if constexpr (C > 1) allow = (allow & ((1u << E) - 1)) | words[kLogThreads] >> word_shift << E;
       } else {  // the warp's tokens of u are the 32 of one word
         allow = 0;
 #pragma unroll
@@ -349,14 +387,14 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     }
     uint32_t res[W];
     pack_words<T>(y, res);
-    if (VEC && left >= kStep * (C - 1) + 16) {
+    if (VEC && left >= kStep * (C - 1) + 16 && (!SHIFT || v0 + tid * E >= 0)) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
         *(uint4*)((char*)dst + kStep * c) = make_uint4(res[4 * c], res[4 * c + 1], res[4 * c + 2], res[4 * c + 3]);
     } else {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
-        if (v0 + place(u) < a.V) {
+        if (v0 + place(u) < a.V && (!SHIFT || v0 + place(u) >= 0)) {
           T* to = dst + (VEC ? u / E * E * kLogThreads + u % E : u * kLogThreads);
           if constexpr (sizeof(T) == 4)
             *(uint32_t*)to = res[u];
@@ -365,7 +403,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
         }
       }
     }
-    dst += a.ld_out;
+    dst += step * a.ld_out;
     fetch(r + kDepth);
   }
   copies_wait<0>();
@@ -414,32 +452,37 @@ __global__ void __launch_bounds__(kLogThreads) count_kernel(CountArgs a) {
   }
 }
 
-template <typename T>
-size_t logits_smem(int P) {
-  return kRingBytes<T> + (size_t)P * 12;
+template <typename T, int MODE>
+cudaError_t launch_logits_m(dt_handle* h, int B, LogitsArgs a, cudaStream_t s) {
+  const int chunks = (a.V + (MODE == kShifted ? kVec<T> - 1 : 0) + kLogChunk - 1) / kLogChunk;
+  // a CTA's tables pay over many rows, but few CTAs leave SMs idle
+  const int classes = std::min(a.step, a.p.P), most = (a.p.P + a.step - 1) / a.step;
+  auto groups = [&]() { return (most + a.rows - 1) / a.rows; };
+  a.rows = kLogRows;
+  while (a.rows > 1 && (int64_t)chunks * B * classes * groups() < h->num_sms * kLogFill) a.rows /= 2;
+  const size_t smem = kRingBytes<T, MODE> + (size_t)a.p.P * 12;
+  launch_k(logits_kernel<T, MODE>, dim3(chunks, B, (groups() - 1) * a.step + classes), dim3(kLogThreads), smem, s, a);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_logits_t(dt_handle* h, int B, LogitsArgs a, cudaStream_t s) {
-  const int per16 = 16 / (int)sizeof(T);
-  const bool vec = a.ld % per16 == 0 && a.ld_out % per16 == 0 && ((uintptr_t)a.logits | (uintptr_t)a.out) % 16 == 0;
-  const int chunks = (a.V + kLogChunk - 1) / kLogChunk;
-  // a CTA's tables pay over many rows, but few CTAs leave SMs idle
-  a.rows = kLogRows;
-  while (a.rows > 1 && (int64_t)chunks * B * ((a.p.P + a.rows - 1) / a.rows) < h->num_sms * kLogFill) a.rows /= 2;
-  const dim3 grid(chunks, B, (a.p.P + a.rows - 1) / a.rows);
-  if (vec)
-    launch_k(logits_kernel<T, true>, grid, dim3(kLogThreads), logits_smem<T>(a.p.P), s, a);
-  else
-    launch_k(logits_kernel<T, false>, grid, dim3(kLogThreads), logits_smem<T>(a.p.P), s, a);
-  return cudaGetLastError();
+  constexpr int E = kVec<T>;
+  const uintptr_t in = (uintptr_t)a.logits, out = (uintptr_t)a.out;
+  a.step = 1;
+  if (a.ld % E == 0 && a.ld_out % E == 0 && (in | out) % 16 == 0) return launch_logits_m<T, kAligned>(h, B, a, s);
+  int step = 1;
+  while (step * a.ld % E != 0) step *= 2;
+  if ((in - out) % 16 != 0 || (a.ld - a.ld_out) % E != 0 || a.p.P < kShiftRows * step) return launch_logits_m<T, kSingle>(h, B, a, s);
+  a.step = step;
+  return launch_logits_m<T, kShifted>(h, B, a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                           const dt_logits_params* p, cudaStream_t s) {
-  LogitsArgs a{*p, logits, ld, out, ld_out, h->cfg.V, 0, h->cfg.V % 4 == 0 && (uintptr_t)p->counts % 16 == 0, h->ws.status};
+  LogitsArgs a{*p, logits, ld, out, ld_out, h->cfg.V, 0, 1, h->cfg.V % 4 == 0 && (uintptr_t)p->counts % 16 == 0, h->ws.status};
   return h->cfg.dtype == DT_BF16 ? launch_logits_t<uint16_t>(h, B, a, s) : launch_logits_t<float>(h, B, a, s);
 }
 

@@ -188,6 +188,50 @@ def test_matches_definition(torch, name):
     h.close()
 
 
+# dtype, V, elements between rows and in front of the first one: logits, output (None: in place)
+ALIGNMENTS = [("bf16", 4099, (4099, 0), (4099, 0)), ("bf16", 4099, (4101, 3), (4101, 3)), ("bf16", 1021, (1030, 5), (1046, 13)),
+              ("bf16", 2052, (2052, 1), None), ("bf16", 2048, (2048, 7), (2048, 7)), ("bf16", 1024, (1025, 2), (1024, 2)),
+              ("bf16", 3, (3, 0), (3, 0)), ("bf16", 7, (11, 4), None), ("fp32", 4099, (4099, 0), (4099, 0)),
+              ("fp32", 2047, (2050, 1), (2054, 5)), ("fp32", 3000, (3001, 3), None), ("fp32", 1024, (1024, 2), (1024, 2)),
+              ("fp32", 2, (2, 0), (2, 0)), ("fp32", 513, (513, 1), (516, 0))]
+
+
+@pytest.mark.parametrize("dtype,V,src,dst", ALIGNMENTS)
+@pytest.mark.parametrize("P,packed", [(19, True), (85, False), (85, True)])
+def test_alignments(torch, dtype, V, src, dst, P, packed):
+    """Rows that start anywhere: the definition's values, and nothing but the rows' tokens is written."""
+    import dynamic_draft_tree_gb300 as dt
+
+    n_pos = [P, 7, 1]
+    pr = Problem(torch, B=3, P=P, V=V, dtype=dtype, packed=packed, n_pos=n_pos, n_bias=9, seed=4)
+    rows = pr.x.shape[0]
+    h = dt.Handle(3, V, 1, 1, 1, P, dt.DT_BF16 if dtype == "bf16" else dt.DT_F32)
+
+    def place(ld, at, fill):
+        flat = torch.full((at + rows * ld + 9,), fill, dtype=pr.x.dtype, device="cuda")
+        return flat, flat[at:at + rows * ld].view(rows, ld)[:, :V]
+
+    x_flat, x = place(*src, 5.0)
+    x.copy_(pr.x)
+    pr.x = x
+    out_flat, out = place(*(dst or src), 7.0)
+    want, tol = pr.reference(out if dst else x.clone())
+    if dst is None:
+        out_flat, out = x_flat, x
+    before = out_flat.clone()
+    pr.call(dt, h, out, logits=x)
+    assert dt.dt_get_status(h) == 0
+    used = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for b in range(3):
+        used[pr.base[b]:pr.base[b] + n_pos[b]] = True
+    _compare(torch, out[used], want[used], tol[used])
+    out[used] = 0
+    ld, at = dst or src
+    before[at:at + rows * ld].view(rows, ld)[:, :V][used] = 0
+    assert torch.equal(out_flat, before)
+    h.close()
+
+
 def test_special_values(torch):
     """-inf, +inf, NaN and zeros in the rows; a forbidden token is -inf whatever it held."""
     import dynamic_draft_tree_gb300 as dt
