@@ -34,13 +34,12 @@ constexpr int kLogRows = 16;                     // rows of a CTA, at most (bits
 // kAligned: every row starts on a 16-byte boundary; a thread's tokens are 16 bytes in every 16 kLogThreads (a warp's
 //   accesses are whole lines; fp32 tokens of a thread as one run of 32 bytes, half lines an access: 16 x up to 65 rows of
 //   128256 149 us, so 110 us).
-// kShifted: rows start anywhere, but every `step`-th row equally far from a 16-byte boundary, in the logits and in the
-//   output. A CTA takes such rows, and its chunk begins that far in front of the vocabulary's, so that accesses are those of
-//   aligned rows (what lies in front of a row is read, never used or written; 16 aligned bytes do not begin before an
-//   allocation).
+// kShifted: the first row starts on a 16-byte boundary, and every `step`-th one equally far from one, in the logits and in
+//   the output. A CTA takes such rows, and its chunk begins that far in front of the vocabulary's, so that accesses are those
+//   of aligned rows (the end of the row before is read with a row's first tokens, never used or written).
 // kSingle: one token in every kLogThreads (single elements; bf16 ones are too small for an asynchronous copy and are loaded
-//   one row ahead of their use): logits and output that differ in alignment, and few rows, whose tables weigh more the
-//   fewer rows a CTA has of its kind: kShiftRows. Single and shifted, 16 requests: fp32, every fourth row alike, 128255
+//   one row ahead of their use): rows of other alignments, and few rows, whose tables weigh more the fewer rows a CTA has of
+//   its kind: kShiftRows. Single and shifted, 16 requests: fp32, every fourth row alike, 128255
 //   tokens: 16 positions 40 and 47 us, 32 66.5 and 68, 48 105 and 96, 65 146 and 131; bf16, every second row alike, 128252
 //   tokens: 8 positions 21 and 24 us, 24 44 and 40, 65 98 and 80; every eighth, 128255 tokens, 65 positions: 108 and 111 us.
 enum { kSingle, kAligned, kShifted };
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kLogThreads, 6) logits_kernel(LogitsArgs a) {
     return;
   }
   int v0 = blockIdx.x * kLogChunk;  // token of the chunk's first place
-  if (SHIFT) v0 -= (int)(((uint64_t)(uintptr_t)a.logits / sizeof(T) + (uint64_t)(base + row0) * a.ld) % E);
+  if (SHIFT) v0 -= (int)((uint64_t)(base + row0) * a.ld % E);
   auto place = [&](int u) { return VEC ? u / E * E * kLogThreads + tid * E + u % E : tid + u * kLogThreads; };  // in the chunk
   constexpr bool kHalves = !VEC && W < kPer;  // strided bf16
   const T* src = (const T*)a.logits + (base + row0) * a.ld + v0 + (VEC ? tid * E : tid);  // the next row to fetch
@@ -473,7 +472,7 @@ cudaError_t launch_logits_t(dt_handle* h, int B, LogitsArgs a, cudaStream_t s) {
   if (a.ld % E == 0 && a.ld_out % E == 0 && (in | out) % 16 == 0) return launch_logits_m<T, kAligned>(h, B, a, s);
   int step = 1;
   while (step * a.ld % E != 0) step *= 2;
-  if ((in - out) % 16 != 0 || (a.ld - a.ld_out) % E != 0 || a.p.P < kShiftRows * step) return launch_logits_m<T, kSingle>(h, B, a, s);
+  if ((in | out) % 16 != 0 || (a.ld - a.ld_out) % E != 0 || a.p.P < kShiftRows * step) return launch_logits_m<T, kSingle>(h, B, a, s);
   a.step = step;
   return launch_logits_m<T, kShifted>(h, B, a, s);
 }

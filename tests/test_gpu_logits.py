@@ -193,7 +193,9 @@ ALIGNMENTS = [("bf16", 4099, (4099, 0), (4099, 0)), ("bf16", 4099, (4101, 3), (4
               ("bf16", 2052, (2052, 1), None), ("bf16", 2048, (2048, 7), (2048, 7)), ("bf16", 1024, (1025, 2), (1024, 2)),
               ("bf16", 3, (3, 0), (3, 0)), ("bf16", 7, (11, 4), None), ("fp32", 4099, (4099, 0), (4099, 0)),
               ("fp32", 2047, (2050, 1), (2054, 5)), ("fp32", 3000, (3001, 3), None), ("fp32", 1024, (1024, 2), (1024, 2)),
-              ("fp32", 2, (2, 0), (2, 0)), ("fp32", 513, (513, 1), (516, 0))]
+              ("fp32", 2, (2, 0), (2, 0)), ("fp32", 513, (513, 1), (516, 0)), ("bf16", 1021, (1030, 0), (1046, 0)),
+              ("bf16", 7, (11, 0), None), ("bf16", 2052, (2052, 0), (2052, 0)), ("fp32", 2047, (2050, 0), (2054, 0)),
+              ("fp32", 3000, (3001, 0), None)]
 
 
 @pytest.mark.parametrize("dtype,V,src,dst", ALIGNMENTS)
