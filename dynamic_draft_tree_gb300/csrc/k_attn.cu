@@ -481,14 +481,14 @@ __device__ void load_tiles(const AttnParams& p, Shared& sh, const CUtensorMap* p
       id = next_id;
     }
   }
-  // after a give-up: no load may land once the CTA is gone
-  if (!ok)
-    for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
-      int stage;
-      uint32_t parity;
-      ring<kStages>(k, stage, parity);
-      tc::bar_drain(&full[stage], parity);
-    }
+  // No load may land once the CTA is gone, and any wait, here or of a reader, may be the one that gave up: the last tiles
+  // are waited for whatever ended the loop (in a call that runs through, the products wait for them too).
+  for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
+    int stage;
+    uint32_t parity;
+    ring<kStages>(k, stage, parity);
+    tc::bar_drain(&full[stage], parity);
+  }
 }
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
