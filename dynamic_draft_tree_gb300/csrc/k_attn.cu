@@ -279,7 +279,7 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
-  uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready, parts_in, ticket_in;
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull, qfree, mlready, parts_in, ticket_in, drained;
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   float2 ml[2][kTile];
@@ -1118,6 +1118,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::bar_init(&sh.mlready, 2 * kTile);
     tc::bar_init(&sh.parts_in, 2 * kTile);
     tc::bar_init(&sh.ticket_in, 1);
+    tc::bar_init(&sh.drained, 1);
     for (int i = 0; i < kSegs; ++i) {
       tc::bar_init(&sh.segfull[i], 1);
       tc::bar_init(&sh.segempty[i], kSegReaders);
@@ -1154,10 +1155,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (sh.stop) {  // products in flight end before their memory goes
       if (tc::elect()) {  // the thread that issued them
         set_status(p.status, DT_DEV_TIMEOUT);
-        tc::bar_init(&sh.mlready, 1);
-        tc::bar_init_fence();
-        tc::mma_commit(&sh.mlready);
-        tc::bar_drain(&sh.mlready, 0);
+        tc::mma_commit(&sh.drained);
+        tc::bar_drain(&sh.drained, 0);
       }
       __syncwarp();
     }

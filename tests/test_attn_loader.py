@@ -5,6 +5,7 @@ from the kernel's source as it stands, its barriers and loads are replaced by re
 phases of all loads must have been waited for.
 """
 import os
+import re
 import subprocess
 
 import pytest
@@ -136,3 +137,10 @@ def leave(tmp_path_factory):
 def test_loads_have_landed_at_every_way_out(leave):
     r = subprocess.run([str(leave)], capture_output=True, text=True)
     assert r.returncode == 0, [x for x in r.stdout.splitlines() if not x.endswith(" 0 not waited for")]
+
+
+def test_barriers_are_made_once():
+    """A barrier that is in use is not initialised again: its memory holds one for the CTA's whole life."""
+    text = open(os.path.join(CSRC, "k_attn.cu")).read()
+    made = re.findall(r"bar_init\(&sh\.(\w+(?:\[[^\]]*\])*)", text)
+    assert len(made) == len(set(made)) and made.count("drained") == 1, made
