@@ -33,9 +33,9 @@ class PagedCache:
 
     def prefill(self, tmp, n_new, row_off, stream=None):
         """Appends the prompts' KV rows: tmp [2 * layers][rows][H_kv][D], request b's n_new[b] rows at row_off[b]."""
-        slots = torch.empty((tmp.shape[1],), dtype=torch.int64, device=tmp.device)
-        if stream is not None:
-            slots.record_stream(stream)  # its memory goes to nobody else before the two calls have run
+        # memory of the stream that the calls run on: nothing queued elsewhere still uses it, nor will before they have run
+        with torch.cuda.stream(stream):
+            slots = torch.empty((tmp.shape[1],), dtype=torch.int64, device=tmp.device)
         dt_kv_reserve(self.h, self.pool, self.seq_len, n_new, slots, slot_off=row_off, stream=stream)
         dt_commit_kv_paged(self.h, tmp, self.pages, slots, n_new, self.seq_len, self.seq_len, row_off=row_off,
                            slot_off=row_off, stream=stream)

@@ -213,3 +213,34 @@ def test_prefill_on_another_stream_keeps_its_slots(torch):
     table = kv.pool.block_table[0, :n // 16].long()
     assert torch.equal(kv.pages[:, table].view(2, -1, 1, 16)[:, :n], rows)
     h.close()
+
+
+def test_prefill_takes_no_memory_that_another_stream_still_writes(torch):
+    """A freed tensor of the current stream, which a delayed kernel there still writes, does not become the slots of a
+    prefill on another stream."""
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache
+
+    n = 100000
+    h = dt.Handle(1, 50, 1, 1, 1, 4)
+    kv = PagedCache(h, 1, 4, 1, 1, 1, 16, n_blocks=n // 16 + 1, max_blocks=n // 16 + 1, page=16)
+    rows = torch.randn(2, n, 1, 16, device="cuda").bfloat16()
+    n_new, off = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, n]))
+    side = torch.cuda.Stream()
+    old = [torch.empty((n,), dtype=torch.int64, device="cuda") for _ in range(4)]
+    places = {x.data_ptr() for x in old}
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)  # tens of milliseconds
+    for x in old:
+        x.fill_(0)  # a slot inside the pages
+    x = None
+    del old
+    again = torch.empty((n,), dtype=torch.int64, device="cuda")
+    assert again.data_ptr() in places  # such memory is what an allocation of the current stream gets
+    del again
+    kv.prefill(rows, n_new, off, stream=side)
+    torch.cuda.synchronize()
+    assert dt.dt_get_status(h) == 0 and kv.seq_len.tolist() == [n]
+    table = kv.pool.block_table[0, :n // 16].long()
+    assert torch.equal(kv.pages[:, table].view(2, -1, 1, 16)[:, :n], rows)
+    h.close()
