@@ -111,10 +111,12 @@ class RoundRunner:
         ``tokens`` (optional, paged.TokenState): the target rows get its penalties, biases and grammar words in
         place before they are verified, and the accepted tokens are counted afterwards.
         ``kv`` (optional, paged.PagedCache, packed like the rows): the accepted positions' rows of kv.tmp, which
-        ``target_rows`` fills, move into the pages after the verify.
+        ``target_rows`` fills, move into the pages after the verify. The tree's root stands behind the cached
+        tokens: meta.position_ids are kv.seq_len + depth (without kv, self.pos_offset + depth).
         """
         h = self.h
         pol = self.policy
+        pos_offset = self.pos_offset if kv is None else kv.seq_len
         if pol == "cast":
             self.set_n0(n0)
         if pol == "graft":  # the checkpoints only ever set stop; CAST writes every entry, EAGLE none
@@ -188,11 +190,11 @@ class RoundRunner:
                                   selected=self.selected, m_cap=self.m_cap, ret_anchor=self.ret_anchor)
             else:
                 torch.cuda.current_stream().wait_event(self.retrieved)
-            dt_build_tree_meta(h, self.selected, self.m_cap, self.meta, self.pos_offset, self.ret_token,
+            dt_build_tree_meta(h, self.selected, self.m_cap, self.meta, pos_offset, self.ret_token,
                                self.ret_parent, self.ret_count, self.R_cap, ret_anchor=self.ret_anchor,
                                K_total=self.graft["K_total"])
         else:
-            dt_build_tree_meta(h, self.selected, self.m_cap, self.meta, self.pos_offset)
+            dt_build_tree_meta(h, self.selected, self.m_cap, self.meta, pos_offset)
         logits = target_rows(self.meta)
         if tokens is not None:
             tokens.process(logits, self.meta, self.packed)

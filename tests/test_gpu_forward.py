@@ -244,3 +244,54 @@ def test_prefill_takes_no_memory_that_another_stream_still_writes(torch):
     table = kv.pool.block_table[0, :n // 16].long()
     assert torch.equal(kv.pages[:, table].view(2, -1, 1, 16)[:, :n], rows)
     h.close()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_positions_of_a_round_start_behind_the_cache(torch, packed):
+    """position_ids = seq_len + depth in every round, captured and replayed too: the root follows the cached tokens."""
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache
+    from dynamic_draft_tree_gb300.rounds import RoundRunner
+
+    B, V, K, k, D, m = 3, 700, 4, 4, 3, 12
+    P, D_path = m + 1, D + 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    run = RoundRunner("eagle", B, V, K, k, D, P, D_path, m, dt.DT_F32, packed=packed)
+    kv = PagedCache(run.h, B, P, 1, 2, 1, 32, n_blocks=60, max_blocks=12, page=16, D_path=D_path, packed=packed)
+    n0 = [33, 0, 16]
+    kv.prefill(torch.randn(2, 49, 1, 32, device="cuda").bfloat16(), torch.tensor(n0, **i32),
+               torch.tensor([0, 33, 33, 49], **i32))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    draft = [torch.randn(B, k, V, generator=g, device="cuda") for _ in range(D + 1)]
+    rows = torch.randn(*((B * P,) if packed else (B, P)), V, generator=g, device="cuda")
+    roots = torch.randint(0, V, (B,), generator=g, **i32)
+
+    def one():
+        run.run(roots, lambda d, t: draft[d][:, :1].contiguous() if d == 1 else draft[d], lambda meta: rows, kv=kv)
+
+    def check(before):
+        assert dt.dt_get_status(run.h) == 0
+        meta = run.meta.numpy()
+        for b in range(B):
+            n = int(meta["n_pos"][b])
+            assert meta["position_ids"][b, :n].tolist() == [before[b] + int(d) for d in meta["depth"][b, :n]]
+            assert (meta["position_ids"][b, n:] == -1).all()
+        after = kv.seq_len.tolist()
+        assert after == [x + a + 1 for x, a in zip(before, run.accept_len.tolist())]
+        return after
+
+    before = n0
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        one()
+    side.synchronize()
+    before = check(before)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        before = check(before)
+    run.h.close()

@@ -64,3 +64,39 @@ def test_prefill_allocates_on_the_stream_it_runs_on(calls, monkeypatch):
     assert made == [side, "default"]
     assert [c[0] for c in calls] == ["dt_kv_reserve", "dt_commit_kv_paged"] * 2
     assert [c[2]["stream"] for c in calls] == [side, side, None, None]
+
+
+class _Anything:
+    """Stands for a handle, device buffers and outputs that only pass through."""
+
+    def __getattr__(self, name):
+        return _Anything()
+
+
+def _runner(monkeypatch, log, policy="eagle", B=2, P=4, packed=False):
+    """A RoundRunner without its constructor, whose library calls are records."""
+    from dynamic_draft_tree_gb300 import DT_ANCHOR_TAIL, rounds
+
+    for name in [n for n in vars(rounds) if n.startswith("dt_")]:
+        monkeypatch.setattr(rounds, name, lambda *a, _n=name, **k: log.append((_n, a, k)))
+    r = rounds.RoundRunner.__new__(rounds.RoundRunner)
+    for name in ("h", "meta", "selected", "m_dev", "width", "stop", "frontier_token", "params", "prune_out", "ret_token",
+                 "ret_parent", "ret_count", "ret_anchor", "accept_len", "accept_path", "bonus", "pos_offset"):
+        setattr(r, name, _Anything())
+    r.policy, r.B, r.P, r.D, r.D_path, r.k, r.m_cap, r.T, r.R_cap = policy, B, P, 2, 5, 2, 3, 0, 2
+    r.packed, r.fused, r.block, r.draw, r.top8 = packed, True, False, False, None
+    r.stop = types.SimpleNamespace(zero_=lambda: None)
+    r.template, r.graft = types.SimpleNamespace(anchor=DT_ANCHOR_TAIL), {"K_total": 4}
+    return r
+
+
+@pytest.mark.parametrize("policy", ["eagle", "graft"])
+def test_a_rounds_positions_start_behind_the_cache(calls, monkeypatch, policy):
+    run = _runner(monkeypatch, calls, policy)
+    kv = _cache()
+    offsets = []
+    for cache in (kv, None):
+        run.run(None, lambda d, t: None, lambda meta: None, kv=cache)
+        offsets += [a[4] for n, a, k in calls if n == "dt_build_tree_meta"]
+        calls.clear()
+    assert offsets[0] is kv.seq_len and offsets[1] is run.pos_offset
