@@ -378,10 +378,11 @@ def dt_kv_release(h, pool, keep_len, stream=None):
 
 
 def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None, row_off=None, n_extra=0,
-                       slot_off=None, S=None, P=None, stream=None):
+                       slot_off=None, S=None, P=None, committed=None, stream=None):
     """KV rows into pages: tmp [planes][B][P][H][D] or, with row_off [B+1], [planes][rows][H][D] (P: positions a
     request, default all rows); cache [planes][blocks][page][H][D], any strides but the last dimension's (pages
-    with the heads first are a transposed view); path [B][D_path] as written by dt_verify, or None (rows 0..n-1)."""
+    with the heads first are a transposed view); path [B][D_path] as written by dt_verify, or None (rows 0..n-1);
+    committed [B] (optional) gets the number of tokens appended, 0 for a refused request."""
     B, dev = n_new.numel(), _device()
     ts, cs, st, sc = tmp.shape, cache.shape, tmp.stride(), cache.stride()
     if len(ts) != (5 if row_off is None else 4) or len(cs) != 5:
@@ -412,7 +413,7 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
         for t, name in ((n_new, "n_new"), (seq_len, "seq_len"), (len_out, "len_out")):
             _dev(t, _I32, dev, name, B)
     kv = _pack_kv_rows(tmp.data_ptr(), st[0] * e, st[-3] * e, st[-2] * e, rows, cache.data_ptr(), sc[0] * e, sc[1] * e,
-                       sc[2] * e, sc[3] * e, ts[0], H, D * e, cs[2], cs[1])
+                       sc[2] * e, sc[3] * e, ts[0], H, D * e, cs[2], cs[1], 0 if committed is None else _dev(committed, _I32, dev, "committed", B))
     sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
     rc = lib.dt_commit_kv_paged(h.h, B, kv, P, 0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
                                 0 if path is None else _dev(path, _I32, dev, "path"), dp, n_new.data_ptr(), n_extra, sp,

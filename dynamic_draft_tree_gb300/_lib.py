@@ -82,7 +82,7 @@ class DtKvRows(ctypes.Structure):
                 ("tmp_head", ctypes.c_int64), ("rows", ctypes.c_int64), ("cache", vp),
                 ("cache_plane", ctypes.c_int64), ("cache_block", ctypes.c_int64), ("cache_tok", ctypes.c_int64),
                 ("cache_head", ctypes.c_int64), ("planes", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("head_bytes", ctypes.c_int64), ("page", ctypes.c_int32), ("n_blocks", ctypes.c_int32)]
+                ("head_bytes", ctypes.c_int64), ("page", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("committed", vp)]
 
 
 class DtAttnArgs(ctypes.Structure):

@@ -627,7 +627,7 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
   if (n_slots < 0 || (!slot_off && n_slots < (int64_t)B * S))
     return fail(DT_ERR_ARG, "dt_commit_kv_paged: slots holds fewer than B * S entries");
   if (!aligned(slots, 8) || !aligned(seq_len, 4) || !aligned(len_out, 4) || !aligned(n_new, 4) || !aligned(path, 4) ||
-      !aligned(row_off, 4) || !aligned(slot_off, 4))
+      !aligned(row_off, 4) || !aligned(slot_off, 4) || !aligned(kv->committed, 4))
     return fail(DT_ERR_ARG, "dt_commit_kv_paged: misaligned array");
   cudaError_t e = dt::launch_commit_kv_paged(h, B, kv, P, row_off, path, D_path, n_new, n_extra, slots, n_slots, S,
                                              slot_off, seq_len, len_out, s);

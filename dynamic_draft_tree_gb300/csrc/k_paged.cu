@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kPageThreads) commit_paged_kernel(PagedCommitA
     if (status) set_status(a.status, status);
     const int32_t len = a.seq_len[b];
     a.len_out[b] = status ? len : len + n;
+    if (a.kv.committed) a.kv.committed[b] = status ? 0 : n;
   }
   if (status) return;
   const int64_t begin = (int64_t)blockIdx.x * a.tok_per_cta;

@@ -29,6 +29,7 @@ class PagedCache:
         self.pool = BlockPool.empty(B, max_blocks, n_blocks, page, device)
         self.seq_len = torch.zeros((B,), dtype=torch.int32, device=device)
         self.slots = torch.empty((B, D_path), dtype=torch.int64, device=device)
+        self.committed = torch.zeros((B,), dtype=torch.int32, device=device)  # tokens that the last commit appended
         self.workspace = dt_tree_attention_workspace(h, B, P, H_q, H_kv, D, shared=shared_len > 0)
 
     def prefill(self, tmp, n_new, row_off, stream=None):
@@ -48,11 +49,12 @@ class PagedCache:
                           shared_len=self.shared_len, scale=scale, stream=stream)
 
     def commit(self, accept_len, accept_path, meta=None, stream=None):
-        """Appends the root's and the accepted positions' rows of tmp (after dt_verify); meta with ``packed``."""
+        """Appends the root's and the accepted positions' rows of tmp (after dt_verify); meta with ``packed``. A request
+        that finds no pages keeps its length, and its entry of ``committed`` is 0."""
         dt_kv_reserve(self.h, self.pool, self.seq_len, accept_len, self.slots, n_extra=1, stream=stream)
         dt_commit_kv_paged(self.h, self.tmp, self.pages, self.slots, accept_len, self.seq_len, self.seq_len,
                            path=accept_path, n_extra=1, row_off=meta.row_off if self.packed else None,
-                           P=self.P if self.packed else None, stream=stream)
+                           P=self.P if self.packed else None, committed=self.committed, stream=stream)
 
     def release(self, keep_len, stream=None):
         """Gives back every request's pages past keep_len tokens (0 ends a request); the lengths are the caller's."""
@@ -82,6 +84,8 @@ class TokenState:
                           bias_vals=self.bias_vals, allow=self.allow, P=meta.P, stream=stream)
         return out
 
-    def commit(self, accept_len, accept_path, meta, stream=None):
-        """Counts the root's and the accepted positions' tokens, the ones whose KV is committed."""
-        dt_count_tokens(self.h, self.counts, meta.tokens, accept_len, path=accept_path, n_extra=1, stream=stream)
+    def commit(self, accept_len, accept_path, meta, committed=None, stream=None):
+        """Counts the root's and the accepted positions' tokens; with ``committed`` (PagedCache.committed after its
+        commit) only those whose KV is in the pages, so that a refused request keeps its history as it keeps its length."""
+        n_new, n_extra = (accept_len, 1) if committed is None else (committed[:accept_len.numel()], 0)
+        dt_count_tokens(self.h, self.counts, meta.tokens, n_new, path=accept_path, n_extra=n_extra, stream=stream)

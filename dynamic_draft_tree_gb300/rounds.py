@@ -109,7 +109,8 @@ class RoundRunner:
         start/stop with kind "expand", "prune_select", "verify_rows" or "verify_accept", e.g. to
         record events around them.
         ``tokens`` (optional, paged.TokenState): the target rows get its penalties, biases and grammar words in
-        place before they are verified, and the accepted tokens are counted afterwards.
+        place before they are verified, and the accepted tokens are counted afterwards (with ``kv``, those of
+        requests whose rows found pages: one that did not, DT_DEV_KV_FULL, keeps its length and its history).
         ``kv`` (optional, paged.PagedCache, packed like the rows): the accepted positions' rows of kv.tmp, which
         ``target_rows`` fills, move into the pages after the verify. The tree's root stands behind the cached
         tokens: meta.position_ids are kv.seq_len + depth (without kv, self.pos_offset + depth).
@@ -219,7 +220,7 @@ class RoundRunner:
                       self.top8)
         if pol == "graft":
             dt_adj_update(h, M, self.meta, self.top8)
-        if tokens is not None:
-            tokens.commit(self.accept_len, self.accept_path, self.meta)
         if kv is not None:
             kv.commit(self.accept_len, self.accept_path, self.meta)
+        if tokens is not None:
+            tokens.commit(self.accept_len, self.accept_path, self.meta, None if kv is None else kv.committed)

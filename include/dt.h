@@ -452,6 +452,7 @@ typedef struct {
   int32_t planes, heads;
   int64_t head_bytes;
   int32_t page, n_blocks;
+  int32_t* committed;     /* [B] or NULL: tokens that the call appended, 0 for a refused request */
 } dt_kv_rows;
 
 /* dt_commit_kv into pages: the KV row of token j < n = n_new[b] + n_extra of request b, at row
@@ -516,7 +517,8 @@ enum { DT_SEEN_PROMPT = 0x40000000 };
 /* Adds request b's tokens tokens[(row_off ? row_off[b] : b*P) + (path ? path[b*D_path + j] : j)],
  * j < n_new[b] + n_extra, to counts [B][V] (prompt != 0: marks them instead); n_tokens: entries of tokens.
  * After a verify, tokens = dt_tree_meta.tokens, path = accept_path, n_new = accept_len, n_extra = 1 add the root
- * and the accepted tokens, the ones whose KV dt_commit_kv commits. A token outside [0, V) sets DT_DEV_BAD_TOKEN
+ * and the accepted tokens, the ones whose KV dt_commit_kv commits (with pages, n_new = dt_kv_rows.committed and
+ * n_extra = 0 leave out requests whose commit was refused). A token outside [0, V) sets DT_DEV_BAD_TOKEN
  * and is skipped; n past D_path (with a path), P or the request's row_off[b + 1] - row_off[b] (without) sets
  * DT_DEV_BAD_TREE and adds nothing; a position outside [0, P), its rows or tokens sets it and is skipped. */
 int dt_count_tokens(dt_handle* h, int32_t B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int32_t P,

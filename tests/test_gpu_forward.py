@@ -295,3 +295,39 @@ def test_positions_of_a_round_start_behind_the_cache(torch, packed):
         torch.cuda.synchronize()
         before = check(before)
     run.h.close()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_request_without_pages_keeps_its_length_and_its_history(torch, packed):
+    """One request's commits find no free page: neither its length nor its counts move, the other's both do."""
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache, TokenState
+    from dynamic_draft_tree_gb300.rounds import RoundRunner
+
+    B, V, K, k, D, m, page = 2, 400, 4, 4, 2, 8, 8
+    P, D_path = m + 1, D + 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    run = RoundRunner("eagle", B, V, K, k, D, P, D_path, m, dt.DT_F32, packed=packed)
+    # request 0 has room in its page for two rounds and more; request 1's page is full, and there is no third one
+    kv = PagedCache(run.h, B, P, 1, 2, 1, 32, n_blocks=2, max_blocks=4, page=page, D_path=D_path, packed=packed)
+    state = TokenState(run.h, B, repetition=torch.full((B,), 1.2, device="cuda"))
+    kv.prefill(torch.randn(2, 9, 1, 32, device="cuda").bfloat16(), torch.tensor([1, 8], **i32), torch.tensor([0, 1, 9], **i32))
+    assert kv.seq_len.tolist() == [1, 8] and int(kv.pool.free_count) == 0
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    roots = torch.tensor([5, 6], **i32)
+    want = torch.zeros(B, V, dtype=torch.int64)
+    length = 1
+    for rnd in range(2):
+        run.run(roots, lambda d, t: torch.randn(B, 1 if d == 1 else k, V, generator=g, device="cuda"),
+                lambda meta: torch.randn(*((B * P,) if packed else (B, P)), V, generator=g, device="cuda"), rnd=rnd, kv=kv,
+                tokens=state)
+        assert dt.dt_get_status(run.h) == dt.DT_DEV_KV_FULL
+        dt.dt_clear_status(run.h)
+        acc, path, tok = int(run.accept_len[0]), run.accept_path[0].tolist(), run.meta.tokens[0].tolist()
+        for p in path[:acc + 1]:
+            want[0, tok[p]] += 1
+        length += acc + 1
+        assert kv.seq_len.tolist() == [length, 8] and kv.committed.tolist() == [acc + 1, 0]
+        assert torch.equal(state.counts.cpu().long(), want)
+    run.h.close()

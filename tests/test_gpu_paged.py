@@ -286,3 +286,27 @@ def test_refusals(torch):
     no(dt.DtError, dt.dt_commit_kv_paged, **dict(good, tmp=tmp[..., :4], cache=cache[..., :4]))
     dt.dt_commit_kv_paged(**good)
     h.close()
+
+
+def test_commit_says_what_it_appended(torch):
+    """committed: the tokens of served requests; 0 where slots are missing, the path is too short, n is 0 or negative."""
+    import dynamic_draft_tree_gb300 as dt
+
+    B, S, page = 5, 4, 8
+    i32 = dict(dtype=torch.int32, device="cuda")
+    h = dt.Handle(B, 2, 1, 1, 1, 8)
+    slots = torch.arange(B * S, dtype=torch.int64, device="cuda").view(B, S)
+    slots[1, 2:] = -1
+    acc, seq = torch.tensor([3, 2, 4, -1, -5], **i32), torch.tensor([4, 5, 6, 7, 8], **i32)
+    path = torch.arange(S, **i32).expand(B, S).contiguous()
+    tmp = torch.randn(2, B, 8, 1, 16, device="cuda").bfloat16()
+    cache = torch.zeros(2, 3, page, 1, 16, device="cuda").bfloat16()
+    done, out = torch.full((B + 1,), -7, **i32), torch.zeros(B, **i32)
+    dt.dt_commit_kv_paged(h, tmp, cache, slots, acc, seq, out, path=path, n_extra=1, committed=done)
+    assert done.tolist() == [4, 0, 0, 0, 0, -7] and out.tolist() == [8, 5, 6, 7, 8]
+    assert dt.dt_get_status(h) == dt.DT_DEV_KV_FULL | dt.DT_DEV_BAD_PAGE
+    with pytest.raises(ValueError):
+        dt.dt_commit_kv_paged(h, tmp, cache, slots, acc, seq, out, path=path, n_extra=1, committed=done[:B - 1])
+    with pytest.raises(ValueError):
+        dt.dt_commit_kv_paged(h, tmp, cache, slots, acc, seq, out, path=path, n_extra=1, committed=done.long())
+    h.close()

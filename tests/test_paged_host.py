@@ -32,6 +32,7 @@ def _cache(**over):
     kv.tmp = torch.zeros(2, 2, 4, 1, 16)
     kv.seq_len = torch.zeros(2, dtype=torch.int32)
     kv.slots = torch.zeros(2, 5, dtype=torch.int64)
+    kv.committed = torch.zeros(2, dtype=torch.int32)
     kv.pool = types.SimpleNamespace(page=16, block_table=torch.full((2, 4), -1, dtype=torch.int32),
                                     n_owned=torch.zeros(2, dtype=torch.int32))
     for k, v in over.items():
@@ -100,3 +101,27 @@ def test_a_rounds_positions_start_behind_the_cache(calls, monkeypatch, policy):
         offsets += [a[4] for n, a, k in calls if n == "dt_build_tree_meta"]
         calls.clear()
     assert offsets[0] is kv.seq_len and offsets[1] is run.pos_offset
+
+
+def test_tokens_are_counted_after_their_rows_are_in_the_pages(calls, monkeypatch):
+    """The count takes what the commit appended, not what was accepted; without a cache, what was accepted."""
+    from dynamic_draft_tree_gb300.paged import TokenState
+
+    run = _runner(monkeypatch, calls)
+    run.accept_len = torch.zeros(2, dtype=torch.int32)
+    state = TokenState.__new__(TokenState)
+    state.h = state.counts = state.repetition = state.frequency = state.presence = None
+    state.bias_ids = state.bias_vals = state.allow = None
+    kv = _cache(committed=torch.zeros(3, dtype=torch.int32))
+    for cache in (kv, None):
+        run.run(None, lambda d, t: None, lambda meta: None, kv=cache, tokens=state)
+        order = [n for n, a, k in calls if n in ("dt_commit_kv_paged", "dt_count_tokens")]
+        count = [(a, k) for n, a, k in calls if n == "dt_count_tokens"][0]
+        if cache is None:
+            assert order == ["dt_count_tokens"] and count[0][3] is run.accept_len and count[1]["n_extra"] == 1
+        else:
+            assert order == ["dt_commit_kv_paged", "dt_count_tokens"]
+            assert [k for n, a, k in calls if n == "dt_commit_kv_paged"][0]["committed"] is kv.committed
+            assert count[0][3].data_ptr() == kv.committed.data_ptr() and count[0][3].numel() == 2
+            assert count[1]["n_extra"] == 0
+        calls.clear()
