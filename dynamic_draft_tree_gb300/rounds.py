@@ -117,6 +117,8 @@ class RoundRunner:
         """
         h = self.h
         pol = self.policy
+        if kv is not None and (kv.packed != self.packed or kv.P < self.P or kv.B < self.B):
+            raise ValueError("kv must hold the round's rows: the same packed, at least its P positions and B requests")
         pos_offset = self.pos_offset if kv is None else kv.seq_len
         if pol == "cast":
             self.set_n0(n0)

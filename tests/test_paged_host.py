@@ -125,3 +125,13 @@ def test_tokens_are_counted_after_their_rows_are_in_the_pages(calls, monkeypatch
             assert count[0][3].data_ptr() == kv.committed.data_ptr() and count[0][3].numel() == 2
             assert count[1]["n_extra"] == 0
         calls.clear()
+
+
+@pytest.mark.parametrize("over", [dict(packed=True), dict(P=3), dict(B=1)])
+def test_a_cache_of_other_rows_is_refused_before_the_round(calls, monkeypatch, over):
+    run = _runner(monkeypatch, calls)
+    with pytest.raises(ValueError):
+        run.run(None, lambda d, t: None, lambda meta: None, kv=_cache(**over))
+    assert calls == []
+    run.run(None, lambda d, t: None, lambda meta: None, kv=_cache(P=run.P + 1, B=run.B + 1))  # more room is no fault
+    assert "dt_commit_kv_paged" in [c[0] for c in calls]
