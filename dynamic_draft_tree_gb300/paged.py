@@ -17,10 +17,14 @@ class PagedCache:
     pages [2 * layers][n_blocks][page][H_kv][D]: plane 2 l holds layer l's keys, plane 2 l + 1 its values.
     tmp: the verify forward's keys and values, [2 * layers][B][P][H_kv][D], or [2 * layers][B * P][H_kv][D] with
     ``packed`` (row meta.row_off[b] + i), written by the forward before it attends.
+    shared_len: tokens, a multiple of the page, of a prefix that all requests share (``prefix`` fills it once). Its pages
+    are in the pool once, stand first in every request's table, and stay there when requests end.
     """
 
     def __init__(self, h, B, P, layers, H_q, H_kv, D, n_blocks, max_blocks, page=16, D_path=64, dtype=torch.bfloat16,
                  packed=False, shared_len=0, device="cuda"):
+        if shared_len < 0 or shared_len % page or shared_len > max_blocks * page:
+            raise ValueError("shared_len must be a multiple of page within max_blocks")
         self.h, self.B, self.P, self.H_q, self.H_kv, self.D = h, B, P, H_q, H_kv, D
         self.packed, self.shared_len = packed, shared_len
         self.pages = torch.zeros((2 * layers, n_blocks, page, H_kv, D), dtype=dtype, device=device)
@@ -31,6 +35,22 @@ class PagedCache:
         self.slots = torch.empty((B, D_path), dtype=torch.int64, device=device)
         self.committed = torch.zeros((B,), dtype=torch.int32, device=device)  # tokens that the last commit appended
         self.workspace = dt_tree_attention_workspace(h, B, P, H_q, H_kv, D, shared=shared_len > 0)
+
+    def prefix(self, tmp, stream=None):
+        """Fills the shared prefix, before any other call: tmp [2 * layers][shared_len][H_kv][D]. Every request owns its
+        pages from then on and has the length shared_len. Without pages for it (DT_DEV_KV_FULL) nothing changes."""
+        n, blocks = self.shared_len, self.shared_len // self.pool.page
+        if n == 0 or tmp.shape[1] != n:
+            raise ValueError("tmp must hold the shared_len rows of the prefix")
+        with torch.cuda.stream(stream):
+            n_new = torch.full((1,), n, dtype=torch.int32, device=tmp.device)
+            slots = torch.empty((1, n), dtype=torch.int64, device=tmp.device)
+            table, owned, length = self.pool.block_table, self.pool.n_owned, self.seq_len
+            dt_kv_reserve(self.h, self.pool, length[:1], n_new, slots)  # request 0's, then everybody's
+            dt_commit_kv_paged(self.h, tmp.unsqueeze(1), self.pages, slots, n_new, length[:1], length[:1])
+            table[1:, :blocks] = table[:1, :blocks]
+            owned[1:] = owned[:1]
+            length[1:] = length[:1]
 
     def prefill(self, tmp, n_new, row_off, stream=None):
         """Appends the prompts' KV rows: tmp [2 * layers][rows][H_kv][D], request b's n_new[b] rows at row_off[b]."""
@@ -57,7 +77,11 @@ class PagedCache:
                            P=self.P if self.packed else None, committed=self.committed, stream=stream)
 
     def release(self, keep_len, stream=None):
-        """Gives back every request's pages past keep_len tokens (0 ends a request); the lengths are the caller's."""
+        """Gives back every request's pages past keep_len tokens (0 ends a request); the lengths are the caller's. Pages of
+        the shared prefix stay in every table, and a new request's length is shared_len."""
+        if self.shared_len:
+            with torch.cuda.stream(stream):
+                keep_len = keep_len.clamp(min=self.shared_len)
         dt_kv_release(self.h, self.pool, keep_len, stream=stream)
 
 

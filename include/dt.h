@@ -436,7 +436,9 @@ int dt_kv_reserve(dt_handle* h, int32_t B, const dt_block_pool* pool, const int3
 
 /* Gives back the blocks past the first ceil(keep_len[b] / page) of every request (keep_len = seq_len rolls an
  * unused reservation back, 0 ends a request): the entries become -1. Blocks go back so that the
- * reservation that took them last is undone exactly: the last block of the last request lowest. */
+ * reservation that took them last is undone exactly: the last block of the last request lowest. Requests may
+ * share their first blocks (dt_attn_args.shared_len): reserve them for one, give its entries and n_owned to the others,
+ * and keep at least their tokens in every release of any of them; a block given back by two requests would be free twice. */
 int dt_kv_release(dt_handle* h, int32_t B, const dt_block_pool* pool, const int32_t* keep_len, cudaStream_t s);
 
 /* KV rows and pages as strided bytes (every stride, pointer and head_bytes a multiple of 16). A plane is one

@@ -331,3 +331,95 @@ def test_a_request_without_pages_keeps_its_length_and_its_history(torch, packed)
         assert kv.seq_len.tolist() == [length, 8] and kv.committed.tolist() == [acc + 1, 0]
         assert torch.equal(state.counts.cpu().long(), want)
     run.h.close()
+
+
+@pytest.mark.parametrize("B,shared,side", [(3, 32, False), (3, 32, True), (24, 2048, False)])
+def test_requests_behind_a_shared_prefix(torch, B, shared, side):
+    """The prefix is in the pool once, every request attends to it, it outlives the request in place 0, and a request that
+    ends gives back its own pages alone. (24 requests behind 2048 tokens: the prefix as work of its own.)"""
+    import types
+
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache
+
+    H_q, H_kv, D, page, P = 8, 2, 64, 16, 3
+    ns = shared // page
+    r = torch.Generator(device="cuda")
+    r.manual_seed(B)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    h = dt.Handle(B, 2, 1, 1, 1, P)
+    n_blocks = ns + 4 * B
+    kv = PagedCache(h, B, P, 1, H_q, H_kv, D, n_blocks=n_blocks, max_blocks=ns + 4, page=page, D_path=P, shared_len=shared)
+    randn = lambda *s: torch.randn(*s, generator=r, device="cuda").bfloat16()  # noqa: E731
+    stream = torch.cuda.Stream() if side else None
+    prefix = randn(2, shared, H_kv, D)
+    torch.cuda.synchronize()
+    kv.prefix(prefix, stream=stream)
+    torch.cuda.synchronize()
+    assert dt.dt_get_status(h) == 0
+    assert kv.seq_len.tolist() == [shared] * B and int(kv.pool.free_count) == n_blocks - ns
+    dense = [prefix for _ in range(B)]
+    pages_of = lambda x: -(-x.shape[1] // page)  # noqa: E731
+
+    def append(n):
+        off = [0]
+        for x in n:
+            off.append(off[-1] + x)
+        rows = randn(2, off[-1], H_kv, D)
+        torch.cuda.synchronize()
+        kv.prefill(rows, torch.tensor(n, **i32), torch.tensor(off, **i32), stream=stream)
+        torch.cuda.synchronize()
+        for b in range(B):
+            dense[b] = torch.cat([dense[b], rows[:, off[b]:off[b + 1]]], 1)
+
+    def check():
+        meta = types.SimpleNamespace(n_pos=torch.full((B,), P, **i32), mask=None, row_off=None)
+        q, out = randn(B, P, H_q, D), torch.zeros(B, P, H_q, D, device="cuda").bfloat16()
+        kv.tmp.copy_(randn(*kv.tmp.shape))
+        kv.attend(0, q, out, meta)
+        assert dt.dt_get_status(h) == 0
+        assert kv.seq_len.tolist() == [x.shape[1] for x in dense]
+        own = sum(pages_of(x) - ns for x in dense)
+        assert int(kv.pool.free_count) == n_blocks - ns - own
+        used = [kv.pool.block_table[b, ns:pages_of(dense[b])].tolist() for b in range(B)]
+        free = kv.pool.free_list[:int(kv.pool.free_count)].tolist()
+        assert sorted(sum(used, free) + kv.pool.block_table[B - 1, :ns].tolist()) == list(range(n_blocks))
+        for b in range(B):
+            k = torch.cat([dense[b][0], kv.tmp[0, b]]).double().repeat_interleave(H_q // H_kv, 1)
+            v = torch.cat([dense[b][1], kv.tmp[1, b]]).double().repeat_interleave(H_q // H_kv, 1)
+            z = torch.einsum("ihd,jhd->hij", q[b].double(), k) * D ** -0.5
+            L = dense[b].shape[1]
+            ok = torch.ones(P, L + P, dtype=torch.bool, device="cuda").tril(L)
+            p = torch.softmax(z.masked_fill(~ok, -math.inf), -1)
+            want, size = torch.einsum("hij,jhd->ihd", p, v), torch.einsum("hij,jhd->ihd", p, v.abs())
+            assert float(((out[b].double() - want).abs() - (2.1 * size + want.abs()) * 2.0 ** -8).max()) <= 0
+
+    append([5 + b % 30 for b in range(B)])
+    check()
+    # the requests in places 0 and 2 end, others go on; new ones take their places
+    keep = kv.seq_len.clone()
+    keep[0] = keep[2] = 0
+    torch.cuda.synchronize()
+    kv.release(keep, stream=stream)
+    torch.cuda.synchronize()
+    kv.seq_len[0] = kv.seq_len[2] = shared
+    dense[0] = dense[2] = prefix
+    check()
+    append([20 if b in (0, 2) else b % 2 for b in range(B)])
+    check()
+    kv.release(torch.zeros(B, **i32))
+    assert int(kv.pool.free_count) == n_blocks - ns and dt.dt_get_status(h) == 0
+    h.close()
+
+
+def test_a_prefix_without_pages_changes_nothing(torch):
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import PagedCache
+
+    h = dt.Handle(2, 2, 1, 1, 1, 1)
+    kv = PagedCache(h, 2, 1, 1, 1, 1, 16, n_blocks=2, max_blocks=4, page=8, shared_len=24)
+    kv.prefix(torch.ones(2, 24, 1, 16, device="cuda").bfloat16())
+    assert dt.dt_get_status(h) == dt.DT_DEV_KV_FULL
+    assert kv.seq_len.tolist() == [0, 0] and kv.pool.n_owned.tolist() == [0, 0] and int(kv.pool.free_count) == 2
+    assert bool((kv.pool.block_table == -1).all()) and not bool(kv.pages.any())
+    h.close()

@@ -135,3 +135,23 @@ def test_a_cache_of_other_rows_is_refused_before_the_round(calls, monkeypatch, o
     assert calls == []
     run.run(None, lambda d, t: None, lambda meta: None, kv=_cache(P=run.P + 1, B=run.B + 1))  # more room is no fault
     assert "dt_commit_kv_paged" in [c[0] for c in calls]
+
+
+def test_a_release_keeps_the_shared_prefix(calls):
+    keep = torch.tensor([0, 40], dtype=torch.int32)
+    _cache().release(keep)
+    _cache(shared_len=32).release(keep)
+    assert [a[2].tolist() for n, a, k in calls] == [[0, 40], [32, 40]]
+    assert calls[0][1][2] is keep and calls[1][1][2].dtype is torch.int32 and keep.tolist() == [0, 40]
+
+
+def test_a_prefix_has_the_caches_length(calls):
+    from dynamic_draft_tree_gb300.paged import PagedCache
+
+    for shared, rows in ((0, 32), (32, 31)):
+        with pytest.raises(ValueError):
+            _cache(shared_len=shared).prefix(torch.zeros(2, rows, 1, 16))
+    for shared in (-16, 24, 80):
+        with pytest.raises(ValueError):
+            PagedCache(None, 2, 4, 1, 2, 1, 16, n_blocks=8, max_blocks=4, page=16, shared_len=shared, device="cpu")
+    assert calls == []
