@@ -423,3 +423,83 @@ def test_a_prefix_without_pages_changes_nothing(torch):
     assert kv.seq_len.tolist() == [0, 0] and kv.pool.n_owned.tolist() == [0, 0] and int(kv.pool.free_count) == 2
     assert bool((kv.pool.block_table == -1).all()) and not bool(kv.pages.any())
     h.close()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T", [0, 1])
+def test_a_round_verifies_the_processed_rows(torch, packed, T):
+    """Accepted paths and bonus tokens are those of the oracle on rows processed in 64 bits by the definition. The target's
+    favourite among a position's children is one that the grammar forbids for every other row, so that verifying the raw rows
+    would go another way (held on the oracle too). With T = 1 requests with a decision closer than 1e-4 are left out: the
+    kernel's rows are within 1e-5 of the reference here."""
+    import numpy as np
+
+    import dynamic_draft_tree_gb300 as dt
+    from dynamic_draft_tree_gb300.paged import TokenState
+    from dynamic_draft_tree_gb300.rounds import RoundRunner
+    from oracle.verify import verify_greedy, verify_sample
+
+    B, V, K, k, D, m = 8, 1100, 4, 4, 4, 24
+    P, D_path, seed, rnd = m + 1, D + 1, 17, 3
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(40 + T)
+    run = RoundRunner("eagle", B, V, K, k, D, P, D_path, m, dt.DT_F32, T=T, packed=packed)
+    rep, freq = torch.rand(B, generator=g, device="cuda") * 0.4 + 1, torch.rand(B, generator=g, device="cuda")
+    allow = torch.full((B * P, (V + 31) // 32), -1, **i32)
+    state = TokenState(run.h, B, repetition=rep, frequency=freq, allow=allow if packed else allow.view(B, P, -1))
+    seen = {}
+
+    def target_rows(meta):
+        rows = torch.randn(B * P, V, generator=g, device="cuda")
+        mt = meta.numpy()
+        for b in range(B):
+            r0 = int(mt["row_off"][b]) if packed else b * P
+            for i in range(int(mt["n_pos"][b])):
+                kids = [j for j in range(1, int(mt["n_pos"][b])) if mt["parents"][b, j] == i]
+                for rank, j in enumerate(kids[:2]):
+                    t = int(mt["tokens"][b, j])
+                    rows[r0 + i, t] = 14.0 - 3.0 * rank
+                    if rank == 0 and (b + i) % 2:
+                        word = int(allow[r0 + i, t >> 5]) & 0xFFFFFFFF & ~(1 << (t & 31))
+                        allow[r0 + i, t >> 5] = word - 2 ** 32 if word >= 2 ** 31 else word
+        seen["raw"] = rows.clone()
+        return rows if packed else rows.view(B, P, V)
+
+    draft = [torch.randn(B, k, V, generator=g, device="cuda") * 3 for _ in range(D + 1)]
+    roots = torch.randint(0, V, (B,), generator=g, **i32)
+    run.run(roots, lambda d, t: draft[d][:, :1].contiguous() if d == 1 else draft[d], target_rows, seed=seed, rnd=rnd,
+            tokens=state)
+    assert dt.dt_get_status(run.h) == 0
+    mt = run.meta.numpy()
+    raw, words = seen["raw"].double().cpu().numpy(), allow.cpu().numpy()
+    v = np.arange(V)
+    near = {}
+
+    class Gaps:
+        def add(self, kind, gap, scale, b):
+            near[b] = min(near.get(b, 1.0), abs(gap))
+
+    def row_at(b, i):
+        return (int(mt["row_off"][b]) if packed else b * P) + i
+
+    def processed(b, i):
+        x, c = raw[row_at(b, i)], np.zeros(V)
+        for j in range(int(mt["n_pos"][b])):
+            if mt["mask"][b, i, j]:
+                c[mt["tokens"][b, j]] += 1
+        r = float(rep[b])
+        y = np.where(c > 0, np.where(x > 0, x / r, x * r), x) - float(freq[b]) * c
+        can = (words[row_at(b, i)][v >> 5] >> (v & 31)) & 1 == 1
+        return np.where(can, y, -np.inf)
+
+    verify = (lambda rows: verify_greedy(mt, rows)) if T == 0 else (lambda rows: verify_sample(mt, rows, seed, rnd, Gaps()))
+    want = verify(processed)
+    clear = [b for b in range(B) if near.get(b, 1.0) > 1e-4]
+    assert len(clear) > B // 2
+    got = (run.accept_len.cpu().numpy(), run.accept_path.cpu().numpy(), run.bonus.cpu().numpy())
+    for name, a, o in zip(("accept_len", "accept_path", "bonus"), got, want):
+        np.testing.assert_array_equal(a[clear], o[clear], err_msg=name)
+    other = verify(lambda b, i: raw[row_at(b, i)])
+    assert sum(not np.array_equal(want[1][b], other[1][b]) for b in clear) >= 2  # the raw rows go another way
+    run.h.close()
