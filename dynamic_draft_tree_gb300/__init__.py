@@ -16,7 +16,7 @@ from ._lib import (lib, check, DtError, DtConfig, DtTreeView, DtPruneParams, DtP
                    DT_POLICY_CAST_WIDTH_DEPTH, DT_POLICY_CAST_VERIFY, DT_POLICY_GRAFT_CHECKPOINT, DT_POLICY_NONE,
                    DT_DEV_BAD_LOGITS, DT_DEV_BAD_TOKEN, DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_INTERNAL, DT_DEV_KV_FULL,
                    DT_DEV_BAD_PAGE, DT_SEEN_PROMPT, DT_F16, DtBlockPool, DtKvRows, DtAttnArgs, DtLogitsParams,
-                   DT_FLAG_TEST_TIMEOUT, DT_ANCHOR_ROOT, DT_ANCHOR_TAIL, LIB_PATH)
+                   DT_FLAG_TEST_TIMEOUT, DT_FLAG_TEST_ARRIVED, DT_ANCHOR_ROOT, DT_ANCHOR_TAIL, LIB_PATH)
 
 
 def _ptr(t):

@@ -18,7 +18,7 @@ DT_POLICY_CAST_WIDTH_DEPTH, DT_POLICY_CAST_VERIFY, DT_POLICY_GRAFT_CHECKPOINT, D
 DT_DEV_BAD_LOGITS, DT_DEV_BAD_TOKEN, DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_INTERNAL = 1, 2, 4, 8, 16
 DT_DEV_KV_FULL, DT_DEV_BAD_PAGE = 32, 64
 DT_SEEN_PROMPT = 0x40000000
-DT_FLAG_TEST_TIMEOUT = 1
+DT_FLAG_TEST_TIMEOUT, DT_FLAG_TEST_ARRIVED = 1, 2
 DT_ANCHOR_ROOT, DT_ANCHOR_TAIL = 0, 1
 
 EXPORTS = ["dt_last_error_string", "dt_create", "dt_destroy", "dt_get_tree", "dt_get_status",

@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstring>
 #include <new>
+#include <vector>
 
 #include "dt_internal.cuh"
 
@@ -171,6 +172,15 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   w.status = reinterpret_cast<int32_t*>(bp + o_status);
   w.ticket = reinterpret_cast<unsigned*>(bp + o_ticket);
   w.attn_tickets = reinterpret_cast<unsigned*>(bp + o_atick);
+  if (c.flags & DT_FLAG_TEST_ARRIVED) {
+    const std::vector<unsigned> one(h->num_sms, 1u);
+    e = cudaMemcpy(w.attn_tickets, one.data(), sizeof(unsigned) * one.size(), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) {
+      cudaFree(base);
+      delete h;
+      return cuda_fail(e, "cudaMemcpy(workspace)");
+    }
+  }
   h->alloc = base;
   h->alloc_bytes = total;
   *out = h;

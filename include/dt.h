@@ -82,6 +82,9 @@ enum { DT_FLAG_TEST_TIMEOUT = 1 }; /* test only: the expansion row scans (dt_exp
                                       dt_tree_attention gives up every wait that is not over at
                                       once, after its copies in flight have landed.
                                       Either way empty results and DT_DEV_TIMEOUT, no fault */
+enum { DT_FLAG_TEST_ARRIVED = 2 }; /* test only: dt_create leaves one arrival at every split item of
+                                      dt_tree_attention, as a call that gave up may; dt_clear_status
+                                      is needed before the first call                             */
 
 typedef struct dt_handle dt_handle;
 

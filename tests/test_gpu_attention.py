@@ -440,3 +440,22 @@ def test_refusals(torch):
     dt.dt_tree_attention(**args)
     assert dt.dt_get_status(h) == 0
     h.close()
+
+
+def test_clear_status_takes_back_arrivals(torch):
+    """A handle with arrivals left at its split items, as after a call that gave up, is fit again after dt_clear_status."""
+    import dynamic_draft_tree_gb300 as dt
+
+    pr = Problem(torch, B=2, P=2, H_kv=2, G=4, D=64, page=16, lens=[6000, 2500])
+    _, ws = pr.handle(dt)
+    h = dt.Handle(pr.B, 2, 1, 1, 1, pr.P, flags=dt.DT_FLAG_TEST_ARRIVED)
+    dt.dt_clear_status(h)
+    pr.out.fill_(7.0)
+    want, tol = pr.reference()
+    for _ in range(3):
+        ws.fill_(255)  # parts that are read before they are written are no numbers
+        pr.out.fill_(7.0)
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == 0
+        assert bool(((pr.out.double() - want).abs() <= tol).all())
+    h.close()
