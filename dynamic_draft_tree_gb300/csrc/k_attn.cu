@@ -67,6 +67,7 @@ struct AttnParams {
   int32_t ns;         // tiles of the shared prefix as items of its own; 0: requests read it with their own tokens
   int32_t skip;       // tokens that a request's own items leave to it
   int64_t own_rows;   // rows of an own item's partials
+  int32_t by_cut;     // their slots go by the CTA of the first cut instead of by item: layout_of
   AttnHead* head;
   int32_t* t_pre;     // [B] unit offset of a request among the own units
   int32_t* k_pre;     // [B] item offset
@@ -248,7 +249,7 @@ struct Walk {
       x += end - at;
       s.t0 = (max(0, at - kItemUnits) + tw - 1) / tw;
       s.t1 = (max(0, end - kItemUnits) + tw - 1) / tw;
-      s.slot = (int64_t)item + blockIdx.x;
+      s.slot = (int64_t)(p.by_cut ? s.c0 : item) + blockIdx.x;
       s.whole = s.t0 == 0 && s.t1 == tt && p.ns == 0;
       s.i0 = s.mp * 2 * p.pos;
     } while (s.t1 == s.t0);
@@ -1186,7 +1187,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const __gr
   const int u0 = hd.w_shared + t_b + h * e.head() + blk * e.full + kItemUnits;  // the item's first tile
   const int tw = tile_units(p, rq.n * p.G - blk * p.rows2);
   const int c0 = u0 / hd.per, own = (u0 + (e.tt - 1) * tw) / hd.per - c0 + 1;
-  const int64_t own_at = ((int64_t)k_b + item + c0) * p.own_rows + f - blk * p.rows2;
+  const int64_t own_at = ((p.by_cut ? (int64_t)c0 : (int64_t)k_b + item) + c0) * p.own_rows + f - blk * p.rows2;
   int parts_s = 0;
   int64_t sh_at = 0;
   if (p.ns) {
@@ -1261,16 +1262,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const __gr
 
 // ------------------------------------------------------------------------------- host -----------
 struct Layout {
-  int64_t own_slots, own_rows, sh_slots;
+  int64_t items, own_slots, own_rows, sh_slots;
   int64_t t_pre, k_pre, ml_own, o_own, ml_sh, o_sh, total;
 };
 
 Layout layout_of(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, bool shared) {
   Layout L{};
   const int64_t G = H_q / H_kv, rows = (int64_t)P * G;
-  // a segment's slot is item + CTA: the pair grows along the line, so slots are distinct
+  // A segment's slot is item + CTA: the pair grows along the line, so slots are distinct. Without a shared prefix only
+  // items that are cut have parts, and with more items than CTAs a slot is first CTA of the item + CTA: an item in CTAs
+  // a .. a + m, m > 0, takes 2 a .. 2 a + m, and the next cut one begins in CTA a + m or later, from 2 a + 2 m on.
   const int64_t rows2 = 2 * (kTile / G) * G;
-  L.own_slots = (int64_t)B * H_kv * ((rows + rows2 - 1) / rows2) + h->num_sms;
+  L.items = (int64_t)B * H_kv * ((rows + rows2 - 1) / rows2);
+  L.own_slots = h->num_sms + (shared ? L.items : std::min<int64_t>(L.items, h->num_sms));
   L.own_rows = std::min<int64_t>(kItemRows, rows);
   L.sh_slots = shared ? (int64_t)H_kv * ((B * rows + rows2 - 1) / rows2) + h->num_sms : 0;
   int64_t at = 256;
@@ -1384,6 +1388,7 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   const Layout L = layout_of(h, a->B, a->P, a->H_q, a->H_kv, a->D, a->shared_len > 0);
   char* ws = (char*)a->workspace;
   p.own_rows = L.own_rows;
+  p.by_cut = a->shared_len == 0 && L.items > h->num_sms;
   p.head = (AttnHead*)ws;
   p.t_pre = (int32_t*)(ws + L.t_pre);
   p.k_pre = (int32_t*)(ws + L.k_pre);

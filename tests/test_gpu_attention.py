@@ -459,3 +459,48 @@ def test_clear_status_takes_back_arrivals(torch):
         assert dt.dt_get_status(h) == 0
         assert bool(((pr.out.double() - want).abs() <= tol).all())
     h.close()
+
+
+def test_workspace_goes_by_the_cuts(torch):
+    """Without a shared prefix a CTA's run cuts two items at most: a larger batch needs no more room for parts, and what it
+    has is enough, to the byte, for batches whose items are many and long."""
+    import dynamic_draft_tree_gb300 as dt
+
+    h = dt.Handle(1024, 2, 1, 1, 1, 64)
+    need = {B: dt.dt_tree_attention_workspace(h, B, 61, 32, 8, 64).numel() for B in (64, 256, 1024)}
+    assert need[1024] - need[64] <= 2 * 4 * (1024 - 64) + 512 and need[256] <= need[1024]
+    small = dt.dt_tree_attention_workspace(h, 1, 61, 32, 8, 64).numel()  # eight items: one slot each and one a CTA
+    assert small < need[64]
+    h.close()
+    r = __import__("random").Random(4)
+    for B, P, G, page in ((64, 40, 4, 32), (40, 9, 3, 16), (300, 1, 4, 16)):
+        pr = Problem(torch, B=B, P=P, H_kv=8, G=G, D=64, page=page, lens=[r.randint(0, 700) for _ in range(B)], packed=True,
+                     n_pos=[r.randint(0, P) for _ in range(B)])
+        h, ws = pr.handle(dt)
+        room = torch.full((ws.numel() + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        want, tol = pr.reference()
+        pr.call(dt, h, room[:ws.numel()])
+        assert dt.dt_get_status(h) == 0
+        assert bool(((pr.out.double() - want).abs() <= tol).all())
+        assert bool((room[ws.numel():] == 0xA5).all())
+        h.close()
+
+
+def test_results_repeat_exactly(torch):
+    """The cuts follow from the lengths and parts are joined in a fixed order: two calls give the same bits."""
+    import dynamic_draft_tree_gb300 as dt
+
+    for case in (dict(B=2, P=2, H_kv=2, G=4, D=64, page=16, lens=[6000, 2500]),  # joined by the CTA that comes last
+                 dict(B=5, P=40, H_kv=3, G=5, D=80, page=32, lens=[3000, 1, 0, 777, 1500]),  # by the second launch
+                 dict(B=32, P=17, H_kv=8, G=4, D=64, page=16, lens=[2048 + 9 * b for b in range(32)], shared=2048)):
+        pr = Problem(torch, **case)
+        h, ws = pr.handle(dt)
+        pr.call(dt, h, ws)
+        first = pr.out.clone()
+        for _ in range(4):
+            pr.out.fill_(7.0)
+            ws.fill_(255)
+            pr.call(dt, h, ws)
+            assert torch.equal(pr.out.view(torch.int16), first.view(torch.int16))
+        assert dt.dt_get_status(h) == 0
+        h.close()
