@@ -391,11 +391,13 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
     if H != cs[3] or D != cs[4] or ts[0] != cs[0]:
         raise ValueError("tmp and cache differ in planes, heads or head size")
     if row_off is None:
-        if ts[1] < B or (ts[1] > 1 and st[1] != ts[2] * st[2]):
-            raise ValueError("tmp [planes][B][P] needs B requests, P rows apart")
         P, rows = ts[2], ts[1] * ts[2]
+        one = P == 1 and ts[1] > 1  # the requests are the rows (a dimension of one has any stride)
+        row = st[1] if one else st[2]
+        if ts[1] < B or (ts[1] > 1 and not one and st[1] != P * row):
+            raise ValueError("tmp [planes][B][P] needs B requests, P rows apart")
     else:
-        rows = ts[1]
+        rows, row = ts[1], st[1]
         P = rows if P is None else P
     dp = 0
     if path is not None:
@@ -412,7 +414,7 @@ def dt_commit_kv_paged(h, tmp, cache, slots, n_new, seq_len, len_out, path=None,
             and seq_len.is_contiguous() and len_out.is_contiguous() and seq_len.numel() >= B and len_out.numel() >= B):
         for t, name in ((n_new, "n_new"), (seq_len, "seq_len"), (len_out, "len_out")):
             _dev(t, _I32, dev, name, B)
-    kv = _pack_kv_rows(tmp.data_ptr(), st[0] * e, st[-3] * e, st[-2] * e, rows, cache.data_ptr(), sc[0] * e, sc[1] * e,
+    kv = _pack_kv_rows(tmp.data_ptr(), st[0] * e, row * e, st[-2] * e, rows, cache.data_ptr(), sc[0] * e, sc[1] * e,
                        sc[2] * e, sc[3] * e, ts[0], H, D * e, cs[2], cs[1], 0 if committed is None else _dev(committed, _I32, dev, "committed", B))
     sp, n_slots, S, so = _slots_args(B, dev, slots, slot_off, S)
     rc = lib.dt_commit_kv_paged(h.h, B, kv, P, 0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
@@ -453,12 +455,16 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
         raise ValueError("k_new, v_new and the pages must match q's rows and one another's heads and head size")
     if len(th) != 2 or th[0] < B:
         raise ValueError("block_table must be [B][max_blocks]")
+    at = -3  # dimension of the rows
     if row_off is None:
         P, rows = qh[1], qh[0] * qh[1]
         if qh[0] < B:
             raise ValueError("q holds fewer requests than n_pos")
-        if qh[0] > 1 and not (qs[0] == P * qs[1] and os_[0] == P * os_[1] and ks[0] == P * ks[1] and vs[0] == P * vs[1]):
-            raise ValueError("padded rows must be P rows apart")
+        if qh[0] > 1:
+            if P == 1:  # the requests are the rows (a dimension of one has any stride)
+                at = 0
+            elif not (qs[0] == P * qs[1] and os_[0] == P * os_[1] and ks[0] == P * ks[1] and vs[0] == P * vs[1]):
+                raise ValueError("padded rows must be P rows apart")
     else:
         rows = qh[0]
         if P is None:
@@ -483,8 +489,8 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
                                  (n_pos, _I32, "n_pos", 1), (workspace, _U8, "workspace", 1)):
             _dev(t, kind, dev, name, n)
     a = _pack_attn(B, P, qh[-2], nh[-2], D, code, D ** -0.5 if scale is None else scale, shared_len, rows,
-                   q.data_ptr(), qs[-3], qs[-2], out.data_ptr(), os_[-3], os_[-2], k_new.data_ptr(), v_new.data_ptr(),
-                   ks[-3], ks[-2], vs[-3], vs[-2], k_pages.data_ptr(), v_pages.data_ptr(), kp[0], kp[1], kp[2], vp_[0],
+                   q.data_ptr(), qs[at], qs[-2], out.data_ptr(), os_[at], os_[-2], k_new.data_ptr(), v_new.data_ptr(),
+                   ks[at], ks[-2], vs[at], vs[-2], k_pages.data_ptr(), v_pages.data_ptr(), kp[0], kp[1], kp[2], vp_[0],
                    vp_[1], vp_[2], ph[0], ph[1], block_table.data_ptr(), th[1], seq_len.data_ptr(), n_pos.data_ptr(),
                    0 if mask is None else _dev(mask, _U8, dev, "mask"),
                    0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1), workspace.data_ptr(),
@@ -523,12 +529,16 @@ def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=Non
     ls, ls_, os_ = logits.shape, logits.stride(), out.stride()
     if len(ls) != (3 if row_off is None else 2) or out.shape != ls or ls[-1] != V:
         raise ValueError("logits and out need [B][P][V] ([rows][V] packed)")
+    at = -2  # dimension of the rows
     if row_off is None:
         P, rows = ls[1], ls[0] * ls[1]
         if ls[0] < B:
             raise ValueError("logits holds fewer requests than n_pos")
-        if ls[0] > 1 and not (ls_[0] == P * ls_[1] and os_[0] == P * os_[1]):
-            raise ValueError("padded rows must be P rows apart")
+        if ls[0] > 1:
+            if P == 1:  # the requests are the rows (a dimension of one has any stride)
+                at = 0
+            elif not (ls_[0] == P * ls_[1] and os_[0] == P * os_[1]):
+                raise ValueError("padded rows must be P rows apart")
     else:
         rows = ls[0]
         if P is None:
@@ -569,7 +579,7 @@ def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=Non
                      0 if bias_ids is None else _dev(bias_ids, _I32, dev, "bias_ids", 0),
                      0 if bias_vals is None else _dev(bias_vals, _F32, dev, "bias_vals", 0), n_bias,
                      0 if allow is None else _dev(allow, _I32, dev, "allow"), words)
-    rc = lib.dt_logits_process(h.h, B, logits.data_ptr(), ls_[-2], out.data_ptr(), os_[-2], p,
+    rc = lib.dt_logits_process(h.h, B, logits.data_ptr(), ls_[at], out.data_ptr(), os_[at], p,
                                _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)

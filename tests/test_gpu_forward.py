@@ -503,3 +503,62 @@ def test_a_round_verifies_the_processed_rows(torch, packed, T):
     other = verify(lambda b, i: raw[row_at(b, i)])
     assert sum(not np.array_equal(want[1][b], other[1][b]) for b in clear) >= 2  # the raw rows go another way
     run.h.close()
+
+
+def test_one_position_a_request_in_rows_of_any_distance(torch):
+    """P = 1: queries, keys and values cut out of one projection, heads before positions, and the last position of padded
+    logits are rows as they stand; the dimension of one position has any stride."""
+    import dynamic_draft_tree_gb300 as dt
+
+    B, H_q, H_kv, D, page, V = 5, 8, 2, 64, 16, 320
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    h = dt.Handle(B, V, 1, 1, 1, 4)
+    ws = dt.dt_tree_attention_workspace(h, B, 1, H_q, H_kv, D)
+    kp, vp = randn(2 * B, page, H_kv, D), randn(2 * B, page, H_kv, D)
+    table = torch.arange(2 * B, **i32).view(B, 2)
+    lens, one = torch.tensor([0, 1, 17, 30, 32], **i32), torch.ones(B, **i32)
+    fused = randn(B, (H_q + 2 * H_kv) * D)
+    q, k, v = (x.view(B, 1, -1, D) for x in fused.split([H_q * D, H_kv * D, H_kv * D], 1))
+    assert q.stride(0) != q.stride(1)
+    heads_first = torch.zeros(B, H_q, 1, D, device="cuda").bfloat16()
+
+    def attend(q, k, v, out):
+        dt.dt_tree_attention(h, q, k, v, kp, vp, table, lens, one, out, ws)
+        return out
+
+    want = attend(*(x.contiguous().clone() for x in (q, k, v)), torch.zeros(B, 1, H_q, D, device="cuda").bfloat16())
+    assert torch.equal(attend(q, k, v, heads_first.transpose(1, 2)), want)
+    wide = randn(B, 3, H_q, D)
+    before = wide.clone()
+    assert torch.equal(attend(q, k, v, wide[:, 1:2]), want)
+    before[:, 1:2] = want
+    assert torch.equal(wide, before)
+    # rows of logits
+    logits = torch.randn(B, 4, V, generator=g, device="cuda").bfloat16()
+    rep = torch.full((B,), 1.5, device="cuda")
+    tokens = logits[:, -1].argmax(1, keepdim=True).to(torch.int32)
+    flat = torch.zeros(B, 1, V, device="cuda").bfloat16()
+    dt.dt_logits_process(h, logits[:, -1:].clone(), flat, one, tokens=tokens, repetition=rep)
+    assert not torch.equal(flat, logits[:, -1:])
+    before = logits.clone()
+    dt.dt_logits_process(h, logits[:, -1:], logits[:, -1:], one, tokens=tokens, repetition=rep)
+    before[:, -1:] = flat
+    assert torch.equal(logits, before)
+    # rows of keys and values
+    tmp = randn(2, B, 3, H_kv, D)
+    slots = torch.arange(3, 3 + 7 * B, 7, dtype=torch.int64, device="cuda").view(B, 1)
+    caches = [torch.zeros(2, 3, page, H_kv, D, device="cuda").bfloat16() for _ in range(2)]
+    for x, cache in zip((tmp[:, :, 1:2], tmp[:, :, 1:2].clone()), caches):
+        dt.dt_commit_kv_paged(h, x, cache, slots, one, lens, torch.zeros(B, **i32))
+    rows = caches[0].flatten(1, 2)[:, slots.view(-1)]
+    assert torch.equal(rows, tmp[:, :, 1]) and torch.equal(*caches)
+    # more positions are still held against their distance
+    with pytest.raises(ValueError):
+        dt.dt_logits_process(h, logits[:, 1:3], logits[:, 1:3], one)
+    with pytest.raises(ValueError):
+        dt.dt_commit_kv_paged(h, tmp[:, :, :2], caches[0], slots, one, lens, torch.zeros(B, **i32))
+    assert dt.dt_get_status(h) == 0
+    h.close()
