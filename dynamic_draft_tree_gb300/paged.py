@@ -26,7 +26,7 @@ class PagedCache:
         if shared_len < 0 or shared_len % page or shared_len > max_blocks * page:
             raise ValueError("shared_len must be a multiple of page within max_blocks")
         self.h, self.B, self.P, self.H_q, self.H_kv, self.D = h, B, P, H_q, H_kv, D
-        self.packed, self.shared_len = packed, shared_len
+        self.packed, self.shared_len, self.filled = packed, shared_len, False
         self.pages = torch.zeros((2 * layers, n_blocks, page, H_kv, D), dtype=dtype, device=device)
         rows = (B * P,) if packed else (B, P)
         self.tmp = torch.zeros((2 * layers, *rows, H_kv, D), dtype=dtype, device=device)
@@ -40,8 +40,9 @@ class PagedCache:
         """Fills the shared prefix, before any other call: tmp [2 * layers][shared_len][H_kv][D]. Every request owns its
         pages from then on and has the length shared_len. Without pages for it (DT_DEV_KV_FULL) nothing changes."""
         n, blocks = self.shared_len, self.shared_len // self.pool.page
-        if n == 0 or tmp.shape[1] != n:
-            raise ValueError("tmp must hold the shared_len rows of the prefix")
+        if n == 0 or tmp.shape[1] != n or self.filled:
+            raise ValueError("tmp must hold the shared_len rows of the prefix, which is filled once")
+        self.filled = True
         with torch.cuda.stream(stream):
             n_new = torch.full((1,), n, dtype=torch.int32, device=tmp.device)
             slots = torch.empty((1, n), dtype=torch.int64, device=tmp.device)
@@ -108,7 +109,7 @@ class TokenState:
                           bias_vals=self.bias_vals, allow=self.allow, P=meta.P, stream=stream)
         return out
 
-    def commit(self, accept_len, accept_path, meta, committed=None, stream=None):
+    def commit(self, accept_len, accept_path, meta, stream=None, committed=None):
         """Counts the root's and the accepted positions' tokens; with ``committed`` (PagedCache.committed after its
         commit) only those whose KV is in the pages, so that a refused request keeps its history as it keeps its length."""
         n_new, n_extra = (accept_len, 1) if committed is None else (committed[:accept_len.numel()], 0)

@@ -225,4 +225,4 @@ class RoundRunner:
         if kv is not None:
             kv.commit(self.accept_len, self.accept_path, self.meta)
         if tokens is not None:
-            tokens.commit(self.accept_len, self.accept_path, self.meta, None if kv is None else kv.committed)
+            tokens.commit(self.accept_len, self.accept_path, self.meta, committed=None if kv is None else kv.committed)

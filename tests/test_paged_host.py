@@ -27,7 +27,7 @@ def _cache(**over):
     from dynamic_draft_tree_gb300.paged import PagedCache
 
     kv = PagedCache.__new__(PagedCache)
-    kv.h, kv.B, kv.P, kv.H_q, kv.H_kv, kv.D, kv.packed, kv.shared_len = None, 2, 4, 2, 1, 16, False, 0
+    kv.h, kv.B, kv.P, kv.H_q, kv.H_kv, kv.D, kv.packed, kv.shared_len, kv.filled = None, 2, 4, 2, 1, 16, False, 0, False
     kv.pages = torch.zeros(2, 8, 16, 1, 16)
     kv.tmp = torch.zeros(2, 2, 4, 1, 16)
     kv.seq_len = torch.zeros(2, dtype=torch.int32)
@@ -148,9 +148,9 @@ def test_a_release_keeps_the_shared_prefix(calls):
 def test_a_prefix_has_the_caches_length(calls):
     from dynamic_draft_tree_gb300.paged import PagedCache
 
-    for shared, rows in ((0, 32), (32, 31)):
+    for shared, rows, filled in ((0, 32, False), (32, 31, False), (32, 32, True)):
         with pytest.raises(ValueError):
-            _cache(shared_len=shared).prefix(torch.zeros(2, rows, 1, 16))
+            _cache(shared_len=shared, filled=filled).prefix(torch.zeros(2, rows, 1, 16))
     for shared in (-16, 24, 80):
         with pytest.raises(ValueError):
             PagedCache(None, 2, 4, 1, 2, 1, 16, n_blocks=8, max_blocks=4, page=16, shared_len=shared, device="cpu")
