@@ -865,8 +865,11 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
 // Items of few rows: the CTA that comes last to a split item joins its parts, so that no second launch is needed. Both
 // groups; returns false after a give-up. Eight lanes hold a row, a warp four of them; with fewer rows than that the
 // warps share the parts out and add up through shared memory (the Q rows' memory).
-// One request, eight key heads of 128, 2000 cached tokens, joined here or by a second launch: 32 rows 15.8 and 18.7 us,
-// 68 rows 22.5 and 18.3 us (one CTA's rows against all CTAs').
+// Joined here or by a second launch, eight key heads of 128, us: one request of 2000 cached tokens, 4 rows 12.9 and 15.6, 16
+// rows 14.3 and 19.2, 32 rows 16.4 and 19.1; eight requests of 2000, 32 rows 20.4 and 23.6; 64 of 300, 32 rows 31.0 and 35.5;
+// 64 of 2000, 4 rows 90.8 and 92.7, 32 rows 95.3 and 97.2. With 68 rows of one request, when this took any number of
+// rows, 22.5 and 18.3 (one CTA's rows against all CTAs'); not measured for many items of more than 32 rows. Behind a shared
+// prefix a row's parts belong to two items, which one item's arrivals do not count.
 constexpr int kJoinRows = 32;
 template <int DP, bool BF16>
 __device__ bool join_parts(const AttnParams& p, Shared& sh, const Segment& s, uint8_t* q_smem, uint32_t& n_in, uint32_t& n_ticket) {

@@ -478,7 +478,7 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
  * that attends to nothing gets zeros. Rows of tmp buffers (q, k_new, v_new, out) as in DT_VERIFY_PACKED:
  * b*P + i, or row_off[b] + i (a request whose rows do not end by row_off[B] sets DT_DEV_BAD_PAGE and gets none);
  * rows of no position are left as they were. K and V of tokens past seq_len, of positions past n_pos and of
- * masked positions may hold anything (NaN and infinities too).
+ * masked positions may hold anything (NaN and infinities too). out overlaps none of the inputs.
  * shared_len: the first shared_len tokens (a multiple of page) of every request are the same blocks, those of
  * block_table[0] (the other rows' entries for them are not read): where it pays, their attention is computed for
  * the rows of all requests together, so that they are read once; a request with positions and
