@@ -15,7 +15,7 @@ from ._lib import (lib, check, DtError, DtConfig, DtTreeView, DtPruneParams, DtP
                    DT_ERR_DEVICE_TIMEOUT, DT_BF16, DT_F32, DT_GREEDY, DT_SAMPLE, DT_VERIFY_PACKED,
                    DT_POLICY_CAST_WIDTH_DEPTH, DT_POLICY_CAST_VERIFY, DT_POLICY_GRAFT_CHECKPOINT, DT_POLICY_NONE,
                    DT_DEV_BAD_LOGITS, DT_DEV_BAD_TOKEN, DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_INTERNAL, DT_DEV_KV_FULL,
-                   DT_DEV_BAD_PAGE, DT_SEEN_PROMPT, DT_F16, DtBlockPool, DtKvRows, DtAttnArgs, DtLogitsParams,
+                   DT_DEV_BAD_PAGE, DT_SEEN_PROMPT, DT_F16, DtBlockPool, DtKvRows, DtAttnArgs, DtLogitsParams, DtPromptArgs,
                    DT_FLAG_TEST_TIMEOUT, DT_FLAG_TEST_ARRIVED, DT_ANCHOR_ROOT, DT_ANCHOR_TAIL, LIB_PATH)
 
 
@@ -278,6 +278,7 @@ def _packer(struct_type):
 
 
 _pack_kv_rows, _pack_attn, _pack_logits = _packer(DtKvRows), _packer(DtAttnArgs), _packer(DtLogitsParams)
+_pack_prompt = _packer(DtPromptArgs)
 
 
 def _refuse(t, dtype, dev, name, n):
@@ -496,6 +497,63 @@ def dt_tree_attention(h, q, k_new, v_new, k_pages, v_pages, block_table, seq_len
                    0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1), workspace.data_ptr(),
                    workspace.numel())
     rc = lib.dt_tree_attention(h.h, a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
+
+
+def dt_prompt_attention_workspace(h, B, H_q, H_kv, D):
+    """A workspace tensor for dt_prompt_attention calls of this head size (one call at a time)."""
+    n = ctypes.c_int64(0)
+    check(lib.dt_prompt_attention_workspace(h.h, B, H_q, H_kv, D, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=_U8, device="cuda")
+
+
+def dt_prompt_attention(h, q, k_new, v_new, row_off, out, workspace, k_pages=None, v_pages=None, block_table=None,
+                        seq_len=None, scale=None, stream=None):
+    """Causal attention over packed prompts: q and out [rows][H_q][D], k_new and v_new [rows][H_kv][D], request b's rows
+    row_off[b] .. row_off[b + 1] - 1 (row_off [B+1]); behind seq_len[b] cached tokens with k_pages and v_pages
+    [blocks][page][H_kv][D], any strides but the last dimension's, block_table [B][max_blocks] and seq_len [B] (all or
+    none); scale defaults to D ** -0.5."""
+    dtype, dev, B = q.dtype, _device(), row_off.numel() - 1
+    code = _ATTN_TYPES.get(dtype)
+    if code is None:
+        raise ValueError("q must be bfloat16 or float16")
+    qh, nh = q.shape, k_new.shape
+    qs, os_, ks, vs = q.stride(), out.stride(), k_new.stride(), v_new.stride()
+    if len(qh) != 3 or out.shape != qh or len(nh) != 3 or v_new.shape != nh or nh[0] != qh[0] or nh[2] != qh[2]:
+        raise ValueError("q and out need [rows][H_q][D], k_new and v_new [rows][H_kv][D]")
+    if B < 1:
+        raise ValueError("row_off must be [B+1]")
+    rows, H, D = qh
+    if not (out.dtype is dtype and k_new.dtype is dtype and v_new.dtype is dtype):
+        raise ValueError(f"q, k_new, v_new and out must all be {dtype}")
+    if not (q.get_device() == dev and out.get_device() == dev and k_new.get_device() == dev and v_new.get_device() == dev):
+        raise ValueError("q, k_new, v_new and out must be on the current CUDA device")
+    if not (qs[2] == 1 and os_[2] == 1 and ks[2] == 1 and vs[2] == 1):
+        raise ValueError("q, k_new, v_new and out need a contiguous last dimension")
+    if not (row_off.dtype is _I32 and workspace.dtype is _U8 and row_off.get_device() == dev
+            and workspace.get_device() == dev and row_off.is_contiguous() and workspace.is_contiguous()):
+        _dev(row_off, _I32, dev, "row_off")
+        _dev(workspace, _U8, dev, "workspace")
+    pages = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    if k_pages is not None or v_pages is not None or block_table is not None or seq_len is not None:
+        if k_pages is None or v_pages is None or block_table is None or seq_len is None:
+            raise ValueError("k_pages, v_pages, block_table and seq_len come together")
+        ph, th, kp, vp_ = k_pages.shape, block_table.shape, k_pages.stride(), v_pages.stride()
+        if len(ph) != 4 or v_pages.shape != ph or ph[2] != nh[1] or ph[3] != D:
+            raise ValueError("pages must be [blocks][page][H_kv][D] with the heads and the head size of k_new")
+        if len(th) != 2 or th[0] < B:
+            raise ValueError("block_table must be [B][max_blocks]")
+        if not (k_pages.dtype is dtype and v_pages.dtype is dtype and k_pages.get_device() == dev
+                and v_pages.get_device() == dev and kp[3] == 1 and vp_[3] == 1):
+            _strided(k_pages, dtype, dev, kp, "k_pages")
+            _strided(v_pages, dtype, dev, vp_, "v_pages")
+        pages = (k_pages.data_ptr(), v_pages.data_ptr(), kp[0], kp[1], kp[2], vp_[0], vp_[1], vp_[2], ph[0], ph[1],
+                 _dev(block_table, _I32, dev, "block_table"), th[1], _dev(seq_len, _I32, dev, "seq_len", B))
+    a = _pack_prompt(B, H, nh[1], D, code, D ** -0.5 if scale is None else scale, rows, q.data_ptr(), qs[0], qs[1],
+                     out.data_ptr(), os_[0], os_[1], k_new.data_ptr(), v_new.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                     row_off.data_ptr(), *pages, workspace.data_ptr(), workspace.numel())
+    rc = lib.dt_prompt_attention(h.h, a, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 

@@ -28,7 +28,8 @@ EXPORTS = ["dt_last_error_string", "dt_create", "dt_destroy", "dt_get_tree", "dt
            "dt_cast_verify_rerank", "dt_expand_prune_select", "dt_verify_rows", "dt_verify_accept",
            "dt_commit_kv", "dt_block_expand", "dt_expand_layer_sampled", "dt_verify_sampled",
            "dt_kv_reserve", "dt_kv_release", "dt_commit_kv_paged", "dt_tree_attention",
-           "dt_tree_attention_workspace", "dt_count_tokens", "dt_logits_process"]
+           "dt_tree_attention_workspace", "dt_count_tokens", "dt_logits_process", "dt_prompt_attention",
+           "dt_prompt_attention_workspace"]
 
 c_i32p = ctypes.c_void_p
 vp = ctypes.c_void_p
@@ -100,6 +101,20 @@ class DtAttnArgs(ctypes.Structure):
                 ("row_off", vp), ("workspace", vp), ("workspace_bytes", ctypes.c_int64)]
 
 
+class DtPromptArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("rows", ctypes.c_int64),
+                ("q", vp), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("out", vp), ("o_row", ctypes.c_int64), ("o_head", ctypes.c_int64),
+                ("k_new", vp), ("v_new", vp), ("kn_row", ctypes.c_int64), ("kn_head", ctypes.c_int64),
+                ("vn_row", ctypes.c_int64), ("vn_head", ctypes.c_int64), ("row_off", vp),
+                ("k_pages", vp), ("v_pages", vp), ("k_block", ctypes.c_int64), ("k_tok", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_block", ctypes.c_int64), ("v_tok", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("n_blocks", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("block_table", vp), ("max_blocks", ctypes.c_int32), ("seq_len", vp), ("workspace", vp),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 class DtLogitsParams(ctypes.Structure):
     _fields_ = [("P", ctypes.c_int32), ("n_pos", vp), ("row_off", vp), ("rows", ctypes.c_int64), ("tokens", vp),
                 ("mask", vp), ("counts", vp), ("repetition", vp), ("frequency", vp), ("presence", vp),
@@ -154,6 +169,8 @@ def _load():
                                 vp, ctypes.c_int32, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, vp, vp], I),
         "dt_tree_attention": ([vp, vp, vp], I),
         "dt_tree_attention_workspace": ([vp] + [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int64)], I),
+        "dt_prompt_attention": ([vp, vp, vp], I),
+        "dt_prompt_attention_workspace": ([vp] + [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_int64)], I),
         "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
                              ctypes.c_int32, vp], I),
         "dt_logits_process": ([vp, ctypes.c_int32, vp, ctypes.c_int64, vp, ctypes.c_int64,

@@ -81,6 +81,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   if (e == cudaSuccess) e = dt::init_meta_attributes();
   if (e == cudaSuccess) e = dt::init_block_attributes();
   if (e == cudaSuccess) e = dt::init_attn_attributes();
+  if (e == cudaSuccess) e = dt::init_prompt_attributes();
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail(e, "cudaFuncSetAttribute");
@@ -645,15 +646,21 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
   return DT_OK;
 }
 
+static int check_heads(const dt_handle* h, const char* who, int32_t B, int32_t H_q, int32_t H_kv, int32_t D) {
+  const int rc = check_batch(h, who, B);
+  if (rc != DT_OK) return rc;
+  if (H_kv < 1 || H_q < H_kv || H_q % H_kv || H_q / H_kv > 128 || H_q > 4096)
+    return fail(DT_ERR_ARG, "%s: H_q must be a multiple of H_kv, H_q / H_kv <= 128, H_q <= 4096", who);
+  if (D < 8 || D > 128 || D % 8) return fail(DT_ERR_ARG, "%s: D must be a multiple of 8 in [8, 128]", who);
+  return DT_OK;
+}
+
 static int check_attn_sizes(const dt_handle* h, const char* who, int32_t B, int32_t P, int32_t H_q, int32_t H_kv,
                             int32_t D) {
   const int rc = check_batch(h, who, B);
   if (rc != DT_OK) return rc;
   if (P < 1 || P > h->cfg.P_max) return fail(DT_ERR_ARG, "%s: P must be in [1, P_max]", who);
-  if (H_kv < 1 || H_q < H_kv || H_q % H_kv || H_q / H_kv > 128 || H_q > 4096)
-    return fail(DT_ERR_ARG, "%s: H_q must be a multiple of H_kv, H_q / H_kv <= 128, H_q <= 4096", who);
-  if (D < 8 || D > 128 || D % 8) return fail(DT_ERR_ARG, "%s: D must be a multiple of 8 in [8, 128]", who);
-  return DT_OK;
+  return check_heads(h, who, B, H_q, H_kv, D);
 }
 
 int dt_tree_attention_workspace(dt_handle* h, int32_t B, int32_t P, int32_t H_q, int32_t H_kv, int32_t D,
@@ -697,6 +704,46 @@ int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s) {
     return fail(DT_ERR_ARG, "dt_tree_attention: workspace too small (dt_tree_attention_workspace) or not 256-byte aligned");
   cudaError_t e = dt::launch_attention(h, a, s);
   if (e != cudaSuccess) return cuda_fail(e, "dt_tree_attention");
+  return DT_OK;
+}
+
+int dt_prompt_attention_workspace(dt_handle* h, int32_t B, int32_t H_q, int32_t H_kv, int32_t D, int64_t* bytes) {
+  const int rc = check_heads(h, "dt_prompt_attention_workspace", B, H_q, H_kv, D);
+  if (rc != DT_OK) return rc;
+  if (!bytes) return fail(DT_ERR_ARG, "dt_prompt_attention_workspace: null argument");
+  *bytes = dt::prompt_workspace_bytes(h, D);
+  return DT_OK;
+}
+
+int dt_prompt_attention(dt_handle* h, const dt_prompt_args* a, cudaStream_t s) {
+  if (!h || !a) return fail(DT_ERR_ARG, "dt_prompt_attention: null argument");
+  const int rc = check_heads(h, "dt_prompt_attention", a->B, a->H_q, a->H_kv, a->D);
+  if (rc != DT_OK) return rc;
+  if (!a->q || !a->out || !a->k_new || !a->v_new || !a->row_off || !a->workspace)
+    return fail(DT_ERR_ARG, "dt_prompt_attention: null argument");
+  const bool cached = a->seq_len || a->block_table || a->k_pages || a->v_pages;
+  if (cached && (!a->seq_len || !a->block_table || !a->k_pages || !a->v_pages))
+    return fail(DT_ERR_ARG, "dt_prompt_attention: seq_len, block_table, k_pages and v_pages come together");
+  if (a->dtype != DT_BF16 && a->dtype != DT_F16) return fail(DT_ERR_ARG, "dt_prompt_attention: dtype must be DT_BF16 or DT_F16");
+  if (cached && (!good_page(a->page) || a->n_blocks < 1 || a->max_blocks < 1))
+    return fail(DT_ERR_ARG, "dt_prompt_attention: page must be a power of two in [8, 256], n_blocks and max_blocks >= 1");
+  if (!(a->scale >= 1e-30f) || a->scale > 1e30f) return fail(DT_ERR_ARG, "dt_prompt_attention: scale must be in [1e-30, 1e30]");
+  if (a->rows < 1 || a->rows > 0x7FFFFF00ll) return fail(DT_ERR_ARG, "dt_prompt_attention: rows must be in [1, 2^31 - 256]");
+  const void* p16[] = {a->q, a->out, a->k_new, a->v_new, a->k_pages, a->v_pages};
+  for (const void* p : p16)
+    if (!aligned(p, 16)) return fail(DT_ERR_ARG, "dt_prompt_attention: tensors must be 16-byte aligned");
+  const int64_t st[] = {a->q_row,   a->q_head,  a->o_row, a->o_head, a->kn_row,  a->kn_head, a->vn_row,
+                        a->vn_head, a->k_block, a->k_tok, a->k_head, a->v_block, a->v_tok,   a->v_head};
+  for (int k = 0; k < (cached ? 14 : 8); ++k)
+    if (st[k] < a->D || st[k] % 8 || st[k] > (int64_t)1 << 38)
+      return fail(DT_ERR_ARG, "dt_prompt_attention: strides must be multiples of 8 elements, at least D");
+  if (!aligned(a->block_table, 4) || !aligned(a->seq_len, 4) || !aligned(a->row_off, 4))
+    return fail(DT_ERR_ARG, "dt_prompt_attention: int32 arrays must be 4-byte aligned");
+  if (!dt::prompt_line_fits(h, a)) return fail(DT_ERR_ARG, "dt_prompt_attention: H_kv * rows * (max_blocks * page + rows) too large");
+  if (!aligned(a->workspace, 256) || a->workspace_bytes < dt::prompt_workspace_bytes(h, a->D))
+    return fail(DT_ERR_ARG, "dt_prompt_attention: workspace too small (dt_prompt_attention_workspace) or not 256-byte aligned");
+  cudaError_t e = dt::launch_prompt(h, a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_prompt_attention");
   return DT_OK;
 }
 

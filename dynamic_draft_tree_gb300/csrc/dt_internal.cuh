@@ -192,6 +192,9 @@ cudaError_t launch_commit_kv_paged(dt_handle* h, int B, const dt_kv_rows* kv, in
 cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
 bool attn_line_fits(const dt_attn_args* a);  // places on the kernel's line of work are 32-bit
 int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared);
+cudaError_t launch_prompt(dt_handle* h, const dt_prompt_args* a, cudaStream_t s);
+bool prompt_line_fits(const dt_handle* h, const dt_prompt_args* a);  // units of a CTA are 32-bit
+int64_t prompt_workspace_bytes(const dt_handle* h, int D);
 cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                           const dt_logits_params* p, cudaStream_t s);
 cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int P,
@@ -208,6 +211,7 @@ cudaError_t init_select_attributes();
 cudaError_t init_meta_attributes();
 cudaError_t init_block_attributes();
 cudaError_t init_attn_attributes();
+cudaError_t init_prompt_attributes();
 
 
 }  // namespace dt

@@ -38,6 +38,7 @@
 
 #include "dt_internal.cuh"
 #include "tc.cuh"
+#include "tma_map.cuh"
 
 namespace dt {
 namespace {
@@ -1294,39 +1295,6 @@ Layout layout_of(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, boo
   L.o_sh = take(4 * L.sh_slots * kItemRows * D);
   L.total = at;
   return L;
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder (a host function that touches no device state).
-EncodeFn encoder() {
-  static EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (EncodeFn)f;
-  }();
-  return fn;
-}
-
-// 64 elements of `box` rows a copy, 128-byte rows swizzled; strides in elements, the innermost one is 1.
-bool encode(CUtensorMap* m, int dtype, const void* at, int rank, const int64_t* dims, const int64_t* strides,
-            const int* box) {
-  cuuint64_t d[4], st[3];
-  cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = (cuuint64_t)dims[i];
-    bx[i] = (cuuint32_t)box[i];
-    if (i) st[i - 1] = (cuuint64_t)strides[i] * 2;
-  }
-  const EncodeFn fn = encoder();
-  return fn && fn(m, dtype == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                  const_cast<void*>(at), d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP, bool BF16>

@@ -1,0 +1,1047 @@
+// Causal attention over whole prompts, packed one behind the other, each behind the tokens that its request has in pages.
+//
+// For query row f = (position i, head of the group) of request b and key head h, with c = scale * log2 e:
+//   out_f = sum_j 2^(c s_fj - m_f) v_j / sum_j 2^(c s_fj - m_f),  s_fj = q_f k_j,
+// j over the request's cached tokens and its new positions up to i. G = H_q / H_kv rows of one position read the same keys,
+// so a block of 128 rows is 128 / G positions of all G heads: it has the narrowest diagonal, and short prompts fill it.
+//
+// Work. An item is up to 256 rows (two groups of 128) of one key head over tiles of 128 tokens: the cached tokens', then
+// those of the new positions up to the item's last one. Tiles above the diagonal do not exist. All tiles in item order
+// (request, key head, block of positions) form one line that the CTAs, one an SM, cut into equal runs, whatever the lengths;
+// a CTA's run of one item is a segment. An item in one CTA is written by it; of others every CTA leaves sum, maximum and
+// unnormalised result in fp32, joined in the order of the line by join_kernel. Every CTA derives the cuts from the lengths
+// on the device, so a captured call follows them.
+//
+// A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads Q rows and K tiles, warp 11 V tiles (TMA),
+// warp 9 issues the matrix instructions, warp 10 walks along the line and clears value rows. Every wait is bounded
+// (DT_DEV_TIMEOUT). S = Q K^T of a group's next tile is issued right behind O += P V of its last one, over the ends of
+// segments too: Q has a buffer a group that is loaded again when the group's last S of a segment is done, and O leaves
+// while the other group's products run, so the pipeline does not run empty between items. S (fp32), P (16-bit, over S) and O
+// live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "dt_internal.cuh"
+#include "tc.cuh"
+#include "tma_map.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int kTile = 128;      // tokens of a tile, rows of a group
+constexpr int kItemRows = 256;  // rows of an item, at most (whole positions: 2 * (128 / G) * G)
+constexpr int kPromptThreads = 384;
+constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes it by 2^kLazy
+constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
+                                // small ones stay normal in fp16 for longer; it cancels in the quotient
+// Units of the line: a tile takes three for two groups of rows and two for one; an item has kItemUnits more in front for
+// its ends. Tile t of an item at unit u starts at u + kItemUnits + t * units of a tile, and belongs to the CTA that unit
+// falls to.
+constexpr int kItemUnits = 3;
+
+// An item that is cut: left by its first CTA for the join.
+struct Cut {
+  int32_t parts, rows;  // parts 0: none begins in this CTA
+  int32_t h, pad;
+  int64_t row;          // row of its first position
+};
+
+struct PromptParams {
+  dt_prompt_args a;
+  int32_t G, page_shift;
+  int32_t pos, rows2;   // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
+  int32_t w;            // positions of an item, 2 pos
+  uint32_t g_magic;     // ceil(2^32 / G), for position_of
+  float c;              // scale * log2 e
+  int32_t period, step; // w / 128 = step / period in lowest terms, period a power of two
+  int32_t period_shift;
+  int32_t min_per;      // least units of a CTA
+  uint16_t part[128];   // part[r] = sum of ceil(k step / period), k = 1 .. r < period
+  int32_t part_all;     // the same up to r = period
+  Cut* cuts;            // [CTAs]
+  float2* ml;           // [2 CTAs][kItemRows] (m, l)
+  float* o;             // [2 CTAs][kItemRows][D]
+  int32_t* status;
+  int32_t test_stop;    // test only: every wait that is not over at once gives up
+};
+
+// x / G for a row x < 256 of an item: exact, as x (g_magic G - 2^32) < 2^32.
+__device__ __forceinline__ int position_of(const PromptParams& p, int x) {
+  return p.G == 1 ? x : (int)__umulhi((uint32_t)x, p.g_magic);
+}
+
+struct Request {
+  int len, n;    // cached tokens, positions
+  int64_t base;  // row of position 0
+  bool bad;
+};
+
+__device__ __forceinline__ Request request_of(const PromptParams& p, int b) {
+  const dt_prompt_args& a = p.a;
+  Request r;
+  const int64_t r0 = a.row_off[b], r1 = a.row_off[b + 1];
+  const int len = a.seq_len ? a.seq_len[b] : 0;
+  const int64_t most = a.seq_len ? min((int64_t)a.max_blocks << p.page_shift, (int64_t)0x7FFFFF00) : 0;
+  r.base = r0;
+  r.len = (int)min((int64_t)max(len, 0), most);
+  r.bad = len < 0 || len > most || r0 < 0 || r1 < r0 || r1 > a.rows;
+  r.n = r0 < 0 || r1 < r0 || r1 > a.rows ? 0 : (int)(r1 - r0);
+  return r;
+}
+
+// sum of ceil(k w / 128), k = 1 .. m: tiles of new positions in the first m items of a prompt. Whole periods first.
+__device__ __forceinline__ int64_t new_tiles(const PromptParams& p, int m) {
+  const int64_t q = m >> p.period_shift;
+  const int r = m & (p.period - 1);
+  return (int64_t)p.step * p.period * (q * (q - 1) / 2) + q * p.part_all + r * q * p.step + p.part[r];
+}
+
+// Items of a request and key head.
+struct Extent {
+  int items, ct;      // items; tiles of cached tokens
+  int64_t head;       // units of a key head
+  int last_tw;        // units of a tile of the last item
+};
+__device__ __forceinline__ int64_t units_before(const PromptParams& p, int ct, int i) {  // of items 0 .. i - 1, not the last
+  return (int64_t)i * kItemUnits + 3 * ((int64_t)i * ct + new_tiles(p, i));
+}
+__device__ __forceinline__ Extent extent_of(const PromptParams& p, const Request& r) {
+  Extent e;
+  e.items = (r.n + p.w - 1) / p.w;
+  e.ct = (r.len + kTile - 1) / kTile;
+  e.last_tw = r.n - (e.items - 1) * p.w > p.pos ? 3 : 2;
+  e.head = r.n > 0 ? units_before(p, e.ct, e.items - 1) + kItemUnits + (int64_t)e.last_tw * (e.ct + (r.n + kTile - 1) / kTile) : 0;
+  return e;
+}
+
+// A CTA's run.
+struct Plan {
+  int64_t x0, x1;  // units of the line
+  int64_t t_b;     // unit offset of request b
+  int32_t per;     // units of a CTA
+  int32_t b;       // first request
+};
+
+struct Segment {
+  int t0, t1;           // tiles; none: the line is at its end
+  int tiles0, tiles1;   // tiles of the item for each group
+  int tt;               // tiles of the item
+  int b, h;
+  int ct, len;          // tiles of cached tokens, cached tokens
+  int i0, iend;         // the item's positions
+  int rows;             // rows of the item
+  int c0, parts;        // first CTA of the item and how many have tiles of it
+  int64_t base;         // row of position 0
+};
+
+// One lane walks along the CTA's run.
+struct Walk {
+  int64_t x;
+  int64_t z;            // units from x to the current item's first
+  int b, h, i;          // the current item
+  Request r;
+  Extent e;
+
+  __device__ void start(const PromptParams& p, const Plan& pl) {
+    x = pl.x0;
+    if (x >= pl.x1) return;
+    b = pl.b;
+    r = request_of(p, b);
+    e = extent_of(p, r);
+    const int64_t y = x - pl.t_b;
+    h = (int)(y / e.head);
+    const int64_t at = y - h * e.head;
+    int lo = 0, hi = e.items - 1;  // the last item that starts at or before `at`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (units_before(p, e.ct, mid) <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    i = lo;
+    z = at - units_before(p, e.ct, i);
+  }
+  // The next segment that has tiles (a run may end or begin inside an item's first units).
+  __device__ __forceinline__ void next(const PromptParams& p, const Plan& pl, Segment& s) {
+    do {
+      s.t0 = s.t1 = 0;
+      if (x >= pl.x1) return;
+      s.b = b;
+      s.h = h;
+      s.ct = e.ct;
+      s.len = r.len;
+      s.base = r.base;
+      s.i0 = i * p.w;
+      s.iend = min(r.n, s.i0 + p.w);
+      s.rows = (s.iend - s.i0) * p.G;
+      s.tiles0 = e.ct + (min(s.iend, s.i0 + p.pos) + kTile - 1) / kTile;
+      s.tt = e.ct + (s.iend + kTile - 1) / kTile;
+      const bool dual = s.iend - s.i0 > p.pos;
+      s.tiles1 = dual ? s.tt : 0;
+      const int tw = dual ? 3 : 2;
+      const int64_t units = kItemUnits + (int64_t)tw * s.tt, end = min(units, z + pl.x1 - x), u0 = x - z + kItemUnits;
+      s.c0 = (int)(u0 / pl.per);
+      s.parts = (int)((u0 + (int64_t)(s.tt - 1) * tw) / pl.per) - s.c0 + 1;
+      s.t0 = (int)((max((int64_t)0, z - kItemUnits) + tw - 1) / tw);
+      s.t1 = (int)((max((int64_t)0, end - kItemUnits) + tw - 1) / tw);
+      x += end - z;
+      z = end;
+      if (end == units) {
+        z = 0;
+        if (++i == e.items) {
+          i = 0;
+          if (++h == p.a.H_kv) {
+            h = 0;
+            while (x < pl.x1) {  // the next request with positions (units left: there is one)
+              if (++b >= p.a.B) {
+                x = pl.x1;
+                break;
+              }
+              r = request_of(p, b);
+              if (r.n > 0) {
+                e = extent_of(p, r);
+                break;
+              }
+            }
+          }
+        }
+      }
+    } while (s.t1 == s.t0);
+  }
+};
+
+// Columns of tile t that are in use: cached tokens, or new positions up to the item's last one.
+__device__ __forceinline__ int tile_valid(int t, int ct, int len, int iend) {
+  return min(kTile, t < ct ? len - t * kTile : iend - (t - ct) * kTile);
+}
+// Whether value rows of tile t are cleared before it is used: rows past its end, and positions that the item's first rows
+// do not attend to.
+__device__ __forceinline__ bool tile_fixed(int t, int ct, int valid, int i0) {
+  return valid < kTile || (t >= ct && (t - ct) * kTile + valid > i0 + 1);
+}
+
+template <int DP>
+struct Smem {
+  static constexpr int kHalf = kTile * 128;         // bytes of 64 elements of 128 rows
+  static constexpr int kBlock = (DP / 64) * kHalf;  // a tile of Q, K or V
+  // tiles of K and of V in flight: a V tile is held longer, from its load until the weights have come
+  static constexpr int kK = DP == 128 ? 2 : 5, kV = DP == 128 ? 3 : 6;
+  static constexpr int kTiles = (2 + kK + kV) * kBlock;
+};
+constexpr int kMostStages = 6;
+constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reader, at most
+
+struct Shared {
+  uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], drained;
+  uint64_t segfull[kSegs], segempty[kSegs];
+  Segment seg[kSegs];
+  Plan plan;
+  int64_t sums[12];
+  uint32_t tmem;
+  int stop, odd_values, cut;
+};
+
+template <int DP>
+constexpr int kSmemBytes = Smem<DP>::kTiles + (int)sizeof(Shared);
+static_assert(kSmemBytes<128> <= 232448 && kSmemBytes<64> <= 232448, "227 KB a CTA");
+
+// The other warps read the segments that warp 10 puts down, in order. `lead`: the lane that gives the place back.
+struct Segments {
+  uint32_t n = 0;
+  __device__ __forceinline__ bool next(Shared& sh, Segment& s, bool lead) {
+    const int at = (int)(n % kSegs);
+    const uint32_t parity = n / kSegs & 1;
+    ++n;
+    if (!tc::bar_wait_warp(&sh.segfull[at], parity, &sh.stop)) return false;
+    s = sh.seg[at];
+    __syncwarp();
+    if (lead) tc::bar_arrive(&sh.segempty[at]);
+    return s.t1 > s.t0;
+  }
+};
+constexpr int kSegReaders = 11;  // eight softmax warps, two loading warps, the issuing warp
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t d;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ float unpack16(uint16_t x) {
+  return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+
+// Every CTA: the line's length and where its own run starts.
+__device__ __forceinline__ void make_plan(const PromptParams& p, Shared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = (p.a.B + kPromptThreads - 1) / kPromptThreads, b0 = tid * chunk, b1 = min(p.a.B, b0 + chunk);
+  int64_t units = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = request_of(p, b);
+    units += p.a.H_kv * extent_of(p, r).head;
+    if (blockIdx.x == 0 && r.bad) set_status(p.status, DT_DEV_BAD_PAGE);
+  }
+  int64_t su = units;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = (int64_t)shfl_u64((uint64_t)su, max(lane - d, 0));
+    if (lane >= d) su += o;
+  }
+  if (lane == 31) sh.sums[warp] = su;
+  if (tid == 0) sh.cut = 0;
+  __syncthreads();
+  int64_t total = 0, t_b = su - units;
+#pragma unroll
+  for (int w = 0; w < kPromptThreads / 32; ++w) {
+    const int64_t o = sh.sums[w];
+    if (w < warp) t_b += o;
+    total += o;
+  }
+  // at least a tile's units: no CTA between an item's first and last one is without a tile
+  const int64_t per = max((int64_t)p.min_per, (total + (int64_t)gridDim.x - 1) / (int64_t)gridDim.x);
+  const int64_t x0 = min(total, per * (int64_t)blockIdx.x), x1 = min(total, x0 + per);
+  if (tid == 0) {
+    sh.plan.x0 = x0;
+    sh.plan.x1 = x1;
+    sh.plan.per = (int32_t)per;
+  }
+  if (x0 >= x1) return;
+  for (int b = b0; b < b1; ++b) {
+    int64_t u = units;
+    if (chunk > 1) u = p.a.H_kv * extent_of(p, request_of(p, b)).head;
+    if (t_b <= x0 && x0 < t_b + u) {
+      sh.plan.b = b;
+      sh.plan.t_b = t_b;
+    }
+    t_b += u;
+  }
+}
+
+// Ring position of the n-th tile: stage and the parity of its use.
+template <int N>
+__device__ __forceinline__ void ring(uint32_t n, int& stage, uint32_t& parity) {
+  stage = (int)(n % N);
+  parity = (n / N) & 1;
+}
+
+// One warp loads the K (or V) tiles of the CTA's line in order; K's warp also a segment's rows of Q, behind the segment's
+// first K tile, whose place is free earlier.
+template <int DP, bool IS_K>
+__device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap* pages, const CUtensorMap* new_map,
+                           const CUtensorMap* q_map, uint32_t smem, uint32_t q_smem, int lane) {
+  using S = Smem<DP>;
+  uint64_t* full = IS_K ? sh.kfull : sh.vfull;
+  uint64_t* empty = IS_K ? sh.kempty : sh.vempty;
+  constexpr int kHalves = DP / 64, kStages = IS_K ? S::kK : S::kV;
+  const int shift = p.page_shift, page = p.a.page;
+  const int box = min(page, kTile);  // tokens of a page box
+  const int box_shift = min(shift, 7);
+  Segments segs;
+  Segment s;
+  uint32_t n = 0;
+  uint32_t nq0 = 0, nq1 = 0;  // loads of each group's Q so far
+  bool ok = true;
+  const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
+  while (ok && segs.next(sh, s, lane == 0)) {
+    const int32_t* table = p.a.block_table + (int64_t)s.b * p.a.max_blocks;
+    // block id of this lane's box in tile t (-1: none)
+    auto block_at = [&](int t) {
+      const int tok = t * kTile + (part << box_shift);
+      if (t >= s.ct || (part << box_shift) >= kTile || tok >= s.len) return -1;
+      int id = table[tok >> shift];
+      if (id < 0 || id >= p.a.n_blocks) {
+        set_status(p.status, DT_DEV_BAD_PAGE);
+        id = p.a.n_blocks;  // outside the tensor: zeros
+      }
+      return id;
+    };
+    int id = block_at(s.t0);
+    for (int t = s.t0; t < s.t1; ++t, ++n) {
+      int stage;
+      uint32_t parity;
+      ring<kStages>(n, stage, parity);
+      const int next_id = t + 1 < s.t1 ? block_at(t + 1) : -1;
+      ok = tc::bar_wait_warp(&empty[stage], parity ^ 1, &sh.stop);
+      if (!ok) break;
+      const uint32_t at = smem + stage * S::kBlock;
+      if (t < s.ct) {
+        const int boxes = (min(kTile, s.len - t * kTile) + box - 1) >> box_shift;
+        if (lane == 0) tc::bar_expect(&full[stage], kHalves * 128 * boxes * box);
+        __syncwarp();
+        if (part < boxes) {
+          const int tok = t * kTile + (part << box_shift);
+          tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id,
+                          &full[stage]);
+        }
+      } else {  // new positions; rows behind the request's last one are masked
+        if (lane == 0) tc::bar_expect(&full[stage], S::kBlock);
+        __syncwarp();
+        if (lane < kHalves)
+          tc::tma_load_3d(at + lane * S::kHalf, new_map, lane * 64, s.h, (int)s.base + (t - s.ct) * kTile, &full[stage]);
+      }
+      id = next_id;
+      if (IS_K && t == s.t0) {
+        // Whole positions of G heads, once the group's last S of the segment before is done. Rows past the item's belong
+        // to other positions or lie past the buffer (zeros); nobody reads theirs.
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (s.t0 >= (g ? s.tiles1 : s.tiles0)) continue;
+          uint32_t& nq = g ? nq1 : nq0;
+          ok = tc::bar_wait_warp(&sh.qempty[g], (nq & 1) ^ 1, &sh.stop);
+          if (!ok) break;
+          ++nq;
+          if (lane == 0) tc::bar_expect(&sh.qfull[g], kHalves * p.pos * p.G * 128);
+          __syncwarp();
+          if (lane < kHalves)
+            tc::tma_load_3d(q_smem + g * S::kBlock + lane * S::kHalf, q_map, lane * 64, s.h * p.G, (int)s.base + s.i0 + g * p.pos,
+                            &sh.qfull[g]);
+        }
+        if (!ok) {
+          ++n;
+          break;
+        }
+      }
+    }
+  }
+  // No load may land once the CTA is gone, and any wait, here or of a reader, may be the one that gave up: the last tiles
+  // are waited for whatever ended the loop (in a call that runs through, the products wait for them too).
+  for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
+    int stage;
+    uint32_t parity;
+    ring<kStages>(k, stage, parity);
+    tc::bar_drain(&full[stage], parity);
+  }
+  if (IS_K) {
+    if (nq0) tc::bar_drain(&sh.qfull[0], (nq0 - 1) & 1);
+    if (nq1) tc::bar_drain(&sh.qfull[1], (nq1 - 1) & 1);
+  }
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// One warp issues the matrix instructions of the CTA's line, all lanes on one path and one thread elected for the
+// instructions themselves, so that descriptors stay in uniform registers. A step is a tile n of the line: for each group
+// O += P V of the tile before (if the group had it), then S of this one (if it has it).
+template <int DP, bool BF16>
+__device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int lane) {
+  using S = Smem<DP>;
+  constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false);
+  constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
+  const int steps = (p.a.D + 15) / 16;  // the padding elements of a row are zero
+  const uint32_t tm = uniform(sh.tmem);
+  // shared memory lies below 2^18 bytes, so offsets add up inside a descriptor's address field
+  const uint64_t q_desc = tc::smem_desc(uniform(q_smem), 16, 1024), k_desc = tc::smem_desc(uniform(k_smem), 16, 1024),
+                 v_desc = tc::smem_desc(uniform(v_smem), S::kHalf, 1024);
+  const bool elected = tc::elect();
+  Segments segs;
+  Segment s;
+  uint32_t n = 0;             // tiles so far
+  uint32_t np0 = 0, np1 = 0;  // products with V of each group so far (phase of phalf)
+  uint32_t nq0 = 0, nq1 = 0;  // segments of each group so far (phase of qfull)
+  uint32_t fix = 0;           // parity of every stage's vfix
+  // what the groups still owe of the tile before: bit 0 anything, bit 1 it begins the accumulator, bit 2 it ends a segment
+  int owe0 = 0, owe1 = 0;
+  int valid = 0;              // of the tile before
+  bool fixed = false;
+  // O += P V of the tile before for group g; `first`: the tile has not been waited for yet
+  auto add_values = [&](int g, int owe, bool first) {
+    int stage;
+    uint32_t parity;
+    ring<S::kV>(n - 1, stage, parity);
+    if (first) {
+      if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return false;
+      if (fixed) {
+        if (!tc::bar_wait_warp(&sh.vfix[stage], fix >> stage & 1, &sh.stop)) return false;
+        fix ^= 1u << stage;
+      }
+    }
+    const uint64_t va = v_desc + (uint32_t)(stage * (S::kBlock >> 4));
+    const uint32_t o = tm + 2 * kTile + g * DP, pr = tm + g * kTile;
+    const uint32_t np = g ? np1++ : np0++;
+    // the first half's products run while the group works on the second half's weights
+    if (!tc::bar_wait_warp(&sh.phalf[g][0], np & 1, &sh.stop)) return false;
+    tc::fence_after();
+    if (elected) {
+      tc::mma_ts(o, pr, va, kDescO, !(owe & 2));
+#pragma unroll
+      for (int x = 1; x < kTile / 32; ++x)
+        if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+    }
+    if (!tc::bar_wait_warp(&sh.phalf[g][1], np & 1, &sh.stop)) return false;
+    tc::fence_after();
+    if (elected) {
+#pragma unroll
+      for (int x = kTile / 32; x < kTile / 16; ++x)
+        if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+      if (owe & 4) tc::mma_commit(&sh.odone[g]);  // else S's commit says so too
+    }
+    return true;
+  };
+  auto release_values = [&] {
+    if (n > 0 && elected) tc::mma_commit(&sh.vempty[(n - 1) % S::kV]);
+  };
+  while (segs.next(sh, s, lane == 0)) {
+    const int t0 = uniform(s.t0), t1 = uniform(s.t1), ct = uniform(s.ct), len = uniform(s.len), iend = uniform(s.iend),
+              i0 = uniform(s.i0), tiles0 = uniform(s.tiles0), tiles1 = uniform(s.tiles1);
+    for (int t = t0; t < t1; ++t) {
+      int stage;
+      uint32_t parity;
+      ring<S::kK>(n, stage, parity);
+      bool first_k = true;
+      int owe_next0 = 0, owe_next1 = 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int owe = g ? owe1 : owe0;
+        if (owe && !add_values(g, owe, g == 0 || !owe0)) return;
+        const int tiles = g ? tiles1 : tiles0;
+        if (t < tiles) {
+          uint32_t& nq = g ? nq1 : nq0;
+          if (t == t0 && !tc::bar_wait_warp(&sh.qfull[g], nq++ & 1, &sh.stop)) return;
+          if (first_k && !tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
+          first_k = false;
+          tc::fence_after();
+          const uint64_t qa = q_desc + (uint32_t)(g * (S::kBlock >> 4)), ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
+          const uint32_t d = tm + g * kTile;
+          const bool last = t + 1 >= min(t1, tiles);
+          if (elected) {
+            tc::mma_ss(d, qa, ka, kDescS, false);
+#pragma unroll
+            for (int x = 1; x < DP / 16; ++x) {
+              const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
+              if (x < steps) tc::mma_ss(d, qa + off, ka + off, kDescS, true);
+            }
+            tc::mma_commit(&sh.sfull[g]);
+            if (last) tc::mma_commit(&sh.qempty[g]);
+          }
+          (g ? owe_next1 : owe_next0) = 1 | (t == t0 ? 2 : 0) | (last ? 4 : 0);
+        }
+      }
+      release_values();
+      if (elected) tc::mma_commit(&sh.kempty[stage]);
+      owe0 = owe_next0;
+      owe1 = owe_next1;
+      valid = tile_valid(t, ct, len, iend);
+      fixed = tile_fixed(t, ct, valid, i0);
+      ++n;
+    }
+  }
+  if (owe0 && !add_values(0, owe0, true)) return;
+  if (owe1 && !add_values(1, owe1, !owe0)) return;
+  release_values();
+}
+
+// One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
+// (a weight of zero times what lies there need not be zero), and so do NaN and infinities at positions that only some rows
+// of the item attend to: the rows that do add them in finish_rows.
+template <int DP, bool BF16>
+__device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, int lane) {
+  using S = Smem<DP>;
+  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+  Walk w;
+  w.start(p, sh.plan);
+  Segment s;
+  uint32_t n = 0, put = 0;
+  // The segment after the one whose tiles are looked at is put down first: the others work ahead. That waits only
+  // for readers of segments long past, never for tiles of this one.
+  auto put_next = [&]() {
+    const int at = (int)(put % kSegs);
+    const uint32_t parity = put / kSegs & 1;
+    ++put;
+    if (!tc::bar_wait_warp(&sh.segempty[at], parity ^ 1, &sh.stop)) return false;
+    if (lane == 0) {
+      w.next(p, sh.plan, sh.seg[at]);
+      const Segment& q = sh.seg[at];
+      if (q.t0 == 0 && q.t1 > 0 && q.t1 < q.tt) {
+        p.cuts[blockIdx.x] = Cut{q.parts, q.rows, q.h, 0, q.base + q.i0};
+        sh.cut = 1;
+      }
+      if (q.t1 == q.t0 && !sh.cut) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};
+      tc::bar_arrive(&sh.segfull[at]);
+    }
+    __syncwarp();
+    return true;
+  };
+  for (int seg = -1;; ++seg) {
+    if (seg >= 0) {
+      s = sh.seg[seg % kSegs];  // not written again before this warp puts down kSegs more
+      if (s.t1 == s.t0) return;
+    }
+    if (!put_next()) return;
+    if (seg < 0) continue;
+    for (int t = s.t0; t < s.t1; ++t, ++n) {
+      const int valid = tile_valid(t, s.ct, s.len, s.iend);
+      int stage;
+      uint32_t parity;
+      ring<S::kV>(n, stage, parity);
+      // every tile is waited for and let go here too, so that the ring never runs ahead of this warp
+      if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
+      if (!tile_fixed(t, s.ct, valid, s.i0)) {
+        if (lane == 0) tc::bar_arrive(&sh.vempty[stage]);
+        continue;
+      }
+      uint8_t* at = v_smem + stage * S::kBlock;
+      const int upto = (valid + 15) / 16 * 16;
+      const int some = t < s.ct ? valid : max(0, s.i0 + 1 - (t - s.ct) * kTile);  // the first that not all rows attend to
+      bool odd = false;
+      for (int hf = 0; hf < DP / 64; ++hf) {
+        uint8_t* rows = at + hf * S::kHalf;
+        for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(rows + c * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int c = some * 8 + lane; c < valid * 8; c += 32) {
+          uint4 q = *(uint4*)(rows + c * 16);
+          uint32_t* e = &q.x;
+          bool mine = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((e[k] & kExp) == kExp) {
+              e[k] &= 0xFFFF0000u;
+              mine = true;
+            }
+            if ((e[k] >> 16 & kExp) == kExp) {
+              e[k] &= 0xFFFFu;
+              mine = true;
+            }
+          }
+          if (mine) *(uint4*)(rows + c * 16) = q;
+          odd |= mine;
+        }
+      }
+      if (odd) *(volatile int*)&sh.odd_values = 1;
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::bar_arrive(&sh.vfix[stage]);
+        tc::bar_arrive(&sh.vempty[stage]);
+      }
+    }
+  }
+}
+
+// What a softmax thread keeps of its row.
+struct Row {
+  float m, l;  // reference maximum (log2 units), sum of weights
+};
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Scores of the columns from `n` on become -inf in tensor memory, whatever they were (few tiles of an item need it: a
+// short loop of its own keeps the common path short).
+__device__ __noinline__ void mask_scores(uint32_t s_at, int n) {
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 16) {
+    if (__all_sync(0xFFFFFFFFu, n >= c + 16)) continue;
+    uint32_t raw[16];
+    tc::tmem_ld16(s_at + c, raw);
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (c + x >= n) raw[x] = 0xFF800000u;
+    tc::tmem_st16(s_at + c, raw);
+  }
+  tc::wait_st();
+}
+
+// Values that are no numbers at positions j0 .. j1 - 1, which this row attends to: weight times value, from global memory.
+template <bool BF16>
+__device__ __noinline__ void add_odd_row(const PromptParams& p, int h, int64_t base, int j0, int j1, int i, int g, float m,
+                                         float scale, int d0, float* o) {
+  const uint16_t* q = (const uint16_t*)p.a.q + (base + i) * p.a.q_row + ((int64_t)h * p.G + g) * p.a.q_head;
+  for (int j = j0; j < j1; ++j) {
+    const uint16_t* v = (const uint16_t*)p.a.v_new + (base + j) * p.a.vn_row + h * p.a.vn_head;
+    const uint16_t* k = (const uint16_t*)p.a.k_new + (base + j) * p.a.kn_row + h * p.a.kn_head;
+    bool odd = false;
+    for (int d = d0; d < min(d0 + 32, p.a.D); ++d) odd |= !isfinite(unpack16<BF16>(v[d]));
+    if (!odd) continue;
+    float dot = 0.0f;
+    for (int d = 0; d < p.a.D; ++d) dot += unpack16<BF16>(q[d]) * unpack16<BF16>(k[d]);
+    const float wgt = exp2f(dot * p.c - m + kShift);
+    for (int d = 0; d < min(32, p.a.D - d0); ++d) {
+      const float x = unpack16<BF16>(v[d0 + d]);
+      if (!isfinite(x)) o[d] += wgt * x * scale;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void add_odd_values(const PromptParams& p, const Segment& s, int r, float m, float scale, int d0,
+                                               float (&o)[32]) {
+  float x[32];  // its own array: one whose address is taken does not stay in registers
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = o[k];
+  const int i = s.i0 + r / p.G;
+  add_odd_row<BF16>(p, s.h, s.base, max(s.i0 + 1, (max(s.t0, s.ct) - s.ct) * kTile), min(i + 1, (s.t1 - s.ct) * kTile), i,
+                    r % p.G, m, scale, d0, x);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) o[k] = x[k];
+}
+
+// A group's rows of a segment leave tensor memory, every thread its own: 32 elements a turn.
+template <int DP, bool BF16>
+__device__ __forceinline__ void finish_rows(const PromptParams& p, Shared& sh, const Segment& s, int r, bool live, Row row, uint32_t o_at,
+                                            bool some) {
+  const bool whole = s.t0 == 0 && s.t1 == s.tt;
+  const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
+  const float inv = !whole ? 1.0f : row.l > 0.0f ? 1.0f / row.l : row.l == 0.0f ? 0.0f : row.l;  // NaN stays
+  const float ref = row.m == -INFINITY ? 0.0f : row.m;
+  const int i = position_of(p, r);
+  uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0 + i) * p.a.o_row + ((int64_t)s.h * p.G + r - i * p.G) * p.a.o_head;
+  const int64_t at = (int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r;
+  float* part = p.o + at * p.a.D;
+  if (!whole && live) p.ml[at] = make_float2(row.m, row.l);
+  if (!some) return;  // no tile of this segment is the group's: m = -inf, l = 0 say so
+#pragma unroll 1
+  for (int d0 = 0; d0 < p.a.D; d0 += 32) {
+    uint32_t raw[32];
+    float o[32];
+    tc::tmem_ld32(o_at + d0, raw);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(raw[k]) * inv;
+    if (odd && live) add_odd_values<BF16>(p, s, r, ref, inv, d0, o);
+    if (live && whole) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        if (d0 + k < p.a.D)
+          *(uint4*)(out + d0 + k) = make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]),
+                                               pack16<BF16>(o[k + 4], o[k + 5]), pack16<BF16>(o[k + 6], o[k + 7]));
+    } else if (live) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        if (d0 + k < p.a.D) *(float4*)(part + d0 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    }
+    __syncwarp();
+  }
+}
+
+// A group of 128 threads turns every S of its tiles into weights.
+template <int DP, bool BF16>
+__device__ void softmax_group(const PromptParams& p, Shared& sh, int group) {
+  const int wl = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
+  const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
+  const int half = p.rows2 >> 1, r = group * half + wl;  // this thread's row of an item
+  Segments segs;
+  Segment s;
+  uint32_t ns = 0, no = 0;  // phases of sfull and odone of this group
+  while (segs.next(sh, s, (threadIdx.x & 31) == 0)) {
+    const bool live = wl < half && r < s.rows;
+    const int i = live ? s.i0 + position_of(p, r) : -1;  // this thread's position
+    const int tiles = min(s.t1, group ? s.tiles1 : s.tiles0);
+    Row row{-INFINITY, 0.0f};
+    const bool work = __any_sync(0xFFFFFFFFu, live);
+    for (int t = s.t0; t < tiles; ++t) {
+      const int valid = tile_valid(t, s.ct, s.len, s.iend);
+      // columns that this row attends to: all, or up to its own position
+      const int see = !live ? kTile : t < s.ct ? valid : min(valid, i + 1 - (t - s.ct) * kTile);
+      if (!tc::bar_wait_warp(&sh.sfull[group], ns++ & 1, &sh.stop)) return;
+      // the tile before this one has been added up too: S of this one was issued behind it
+      tc::fence_after();
+      if (work) {
+        if (__any_sync(0xFFFFFFFFu, see < kTile)) mask_scores(s_at, see);
+        uint32_t raw[64];
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          tc::tmem_ld64(s_at + hf * 64, raw);
+#pragma unroll
+          for (int x = 0; x < 64; x += 8) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
+          }
+        }
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
+        if (t == s.t0) {
+          row.m = top;
+        } else {
+          const bool up = top > row.m + kLazy;
+          if (__any_sync(0xFFFFFFFFu, up)) {
+            // the accumulator of the tiles so far moves to the new reference
+            const float fac = up ? (row.m == -INFINITY ? 0.0f : exp2f(row.m - top)) : 1.0f;
+            if (up) {
+              row.m = top;
+              row.l *= fac;
+            }
+#pragma unroll 1
+            for (int d0 = 0; d0 < DP; d0 += 32) {
+              tc::tmem_ld32(o_at + d0, raw);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) raw[x] = __float_as_uint(__uint_as_float(raw[x]) * fac);
+              tc::tmem_st32(o_at + d0, raw);
+            }
+            tc::wait_st();
+          }
+        }
+        const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
+        const float2 c2 = make_float2(p.c, p.c), off2 = make_float2(off, off);
+        float2 l2 = make_float2(0.0f, 0.0f);
+        // P's 64 columns lie over S's first half: the second half of S is read before P reaches it
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          tc::tmem_ld64(s_at + hf * 64, raw);
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[x]), __uint_as_float(raw[x + 1])), c2, off2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            l2 = __fadd2_rn(l2, e);
+            pk[x >> 1] = pack16<BF16>(e.x, e.y);
+          }
+          tc::tmem_st32(s_at + hf * 32, pk);
+          tc::wait_st();
+          tc::fence_before();
+          tc::bar_arrive(&sh.phalf[group][hf]);
+        }
+        row.l += l2.x + l2.y;
+      } else {
+        tc::fence_before();
+        tc::bar_arrive(&sh.phalf[group][0]);
+        tc::bar_arrive(&sh.phalf[group][1]);
+      }
+    }
+    const bool some = tiles > s.t0;
+    if (some) {
+      if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
+      tc::fence_after();
+    }
+    // O is read before this group's next weights are handed over, and with them the next segment's first product
+    if (work) finish_rows<DP, BF16>(p, sh, s, r, live, row, o_at, some);
+  }
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map) {
+  using S = Smem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kBlock, *v_smem = k_smem + S::kK * S::kBlock;
+  Shared& sh = *(Shared*)(smem + S::kTiles);
+  if (tc::smem_addr(smem) & 1023) {  // the swizzle goes by address; dynamic shared memory alone starts on 1024
+    if (threadIdx.x == 0) {
+      set_status(p.status, DT_DEV_INTERNAL);
+      p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};
+    }
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 9) tc::tmem_alloc<512>(&sh.tmem);
+  if (tid == 0) {
+    for (int i = 0; i < kMostStages; ++i) {
+      tc::bar_init(&sh.kfull[i], 1);
+      tc::bar_init(&sh.kempty[i], 1);
+      tc::bar_init(&sh.vfull[i], 1);
+      tc::bar_init(&sh.vempty[i], 2);  // the products' end and the fixing warp
+      tc::bar_init(&sh.vfix[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      tc::bar_init(&sh.sfull[g], 1);
+      tc::bar_init(&sh.phalf[g][0], kTile);
+      tc::bar_init(&sh.phalf[g][1], kTile);
+      tc::bar_init(&sh.odone[g], 1);
+      tc::bar_init(&sh.qfull[g], 1);
+      tc::bar_init(&sh.qempty[g], 1);
+    }
+    tc::bar_init(&sh.drained, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      tc::bar_init(&sh.segfull[i], 1);
+      tc::bar_init(&sh.segempty[i], kSegReaders);
+    }
+    tc::bar_init_fence();
+    sh.stop = p.test_stop;
+    sh.odd_values = 0;
+    tc::tma_prefetch_map(&q_map);
+    tc::tma_prefetch_map(&k_map);
+    tc::tma_prefetch_map(&v_map);
+    tc::tma_prefetch_map(&kn_map);
+    tc::tma_prefetch_map(&vn_map);
+  }
+  pdl_begin();
+  make_plan(p, sh);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp < 8) {
+    softmax_group<DP, BF16>(p, sh, warp >> 2);
+  } else if (warp == 8) {
+    load_tiles<DP, true>(p, sh, &k_map, &kn_map, &q_map, tc::smem_addr(k_smem), tc::smem_addr(q_smem), lane);
+  } else if (warp == 9) {
+    issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), lane);
+  } else if (warp == 10) {
+    fix_values<DP, BF16>(p, sh, v_smem, lane);
+  } else {
+    load_tiles<DP, false>(p, sh, &v_map, &vn_map, nullptr, tc::smem_addr(v_smem), 0, lane);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) {
+    if (sh.stop) {  // products in flight end before their memory goes
+      if (tc::elect()) {  // the thread that issued them
+        set_status(p.status, DT_DEV_TIMEOUT);
+        p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};  // what it has left of a cut item is not joined
+        tc::mma_commit(&sh.drained);
+        tc::bar_drain(&sh.drained, 0);
+      }
+      __syncwarp();
+    }
+    tc::tmem_free<512>(sh.tmem);
+  }
+}
+
+// ------------------------------------------------------------------------------- join -----------
+constexpr int kJoinWarps = 4;
+constexpr int kJoinRows = 4 * kJoinWarps;  // rows of a CTA: eight lanes a row, each up to 16 elements of it
+// CTA (c, y): rows [y kJoinRows, ...) of the item that is cut and begins in CTA c of the kernel before.
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PromptParams p) {
+  pdl_begin();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, e = lane & 7;
+  const Cut cut = p.cuts[c0];
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5) * 4 + (lane >> 3);
+  if (r >= cut.rows) return;
+  auto slot = [&](int k) { return ((int64_t)2 * (c0 + k) + (k == 0 ? 1 : 0)) * kItemRows + r; };
+  float m = -INFINITY;
+  for (int k = 0; k < cut.parts; ++k) m = fmaxf(m, p.ml[slot(k)].x);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4 o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+  for (int k = 0; k < cut.parts; ++k) {
+    const float2 x = p.ml[slot(k)];
+    if (x.x == -INFINITY && x.y == 0.0f) continue;  // no tile of the row's group: its result was not written
+    const float w = exp2f(x.x - ref);
+    l += x.y * w;
+    const float* src = p.o + slot(k) * p.a.D + e * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j * 32 + e * 4 < p.a.D) {
+        const float4 v = *(const float4*)(src + j * 32);
+        o[j].x = fmaf(v.x, w, o[j].x);
+        o[j].y = fmaf(v.y, w, o[j].y);
+        o[j].z = fmaf(v.z, w, o[j].z);
+        o[j].w = fmaf(v.w, w, o[j].w);
+      }
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+  const int i = position_of(p, r);
+  uint16_t* out = (uint16_t*)p.a.out + (cut.row + i) * p.a.o_row + ((int64_t)cut.h * p.G + r - i * p.G) * p.a.o_head + e * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j * 32 + e * 4 < p.a.D)
+      *(uint2*)(out + j * 32) = make_uint2(pack16<BF16>(o[j].x * inv, o[j].y * inv), pack16<BF16>(o[j].z * inv, o[j].w * inv));
+}
+
+// ------------------------------------------------------------------------------- host -----------
+// What follows from the heads and the page.
+void shape_params(PromptParams& p) {
+  p.G = p.a.H_q / p.a.H_kv;
+  p.pos = kTile / p.G;
+  p.rows2 = 2 * p.pos * p.G;
+  p.w = 2 * p.pos;
+  p.g_magic = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
+  while ((1 << p.page_shift) < p.a.page) ++p.page_shift;
+  p.period = kTile;
+  p.step = p.w;
+  while (p.period > 1 && p.step % 2 == 0) {
+    p.period /= 2;
+    p.step /= 2;
+  }
+  while ((1 << p.period_shift) < p.period) ++p.period_shift;
+  for (int r = 1, sum = 0; r <= p.period; ++r) {
+    sum += (r * p.step + p.period - 1) / p.period;
+    if (r < p.period) p.part[r] = (uint16_t)sum;
+    p.part_all = sum;
+  }
+  p.min_per = 3;
+}
+
+struct Layout {
+  int64_t ml, o, total;
+};
+Layout layout_of(const dt_handle* h, int D) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  Layout L;
+  L.ml = up((int64_t)sizeof(Cut) * h->num_sms);
+  L.o = up(L.ml + 8ll * 2 * h->num_sms * kItemRows);
+  L.total = up(L.o + 4ll * 2 * h->num_sms * kItemRows * D);
+  return L;
+}
+
+template <int DP, bool BF16>
+cudaError_t launch_t(dt_handle* h, const PromptParams& p, const CUtensorMap* m, cudaStream_t s) {
+  launch_k(prompt_kernel<DP, BF16>, dim3(h->num_sms), dim3(kPromptThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4]);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  launch_k(join_kernel<BF16>, dim3(h->num_sms, (p.rows2 + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinWarps), 0, s, p);
+  return cudaGetLastError();
+}
+
+template <int DP, bool BF16>
+cudaError_t init_t() {
+  return cudaFuncSetAttribute(prompt_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<DP>);
+}
+
+}  // namespace
+
+cudaError_t init_prompt_attributes() {
+  cudaError_t e = init_t<64, true>();
+  if (e == cudaSuccess) e = init_t<64, false>();
+  if (e == cudaSuccess) e = init_t<128, true>();
+  if (e == cudaSuccess) e = init_t<128, false>();
+  return e;
+}
+
+bool prompt_line_fits(const dt_handle* h, const dt_prompt_args* a) {
+  const int w = 2 * (kTile / (a->H_q / a->H_kv));
+  const double tiles = (double)(a->seq_len ? (double)a->max_blocks * a->page / kTile : 0.0) + (double)a->rows / kTile + 2;
+  return (double)a->H_kv * ((double)a->rows / w + a->B) * (kItemUnits + 3 * tiles) < 2.0e9 * h->num_sms;
+}
+
+int64_t prompt_workspace_bytes(const dt_handle* h, int D) { return layout_of(h, D).total; }
+
+cudaError_t launch_prompt(dt_handle* h, const dt_prompt_args* a, cudaStream_t s) {
+  PromptParams p{};
+  p.a = *a;
+  const bool cached = a->seq_len != nullptr;
+  if (!cached) p.a.page = kTile;
+  shape_params(p);
+  p.c = a->scale * kLog2e;
+  const Layout L = layout_of(h, a->D);
+  char* ws = (char*)a->workspace;
+  p.cuts = (Cut*)ws;
+  p.ml = (float2*)(ws + L.ml);
+  p.o = (float*)(ws + L.o);
+  p.status = h->ws.status;
+  p.test_stop = h->cfg.flags & DT_FLAG_TEST_TIMEOUT ? 1 : 0;
+  CUtensorMap m[5];
+  const int64_t nd[3] = {a->D, a->H_kv, a->rows};
+  const int64_t kn[3] = {1, a->kn_head, a->kn_row}, vn[3] = {1, a->vn_head, a->vn_row};
+  const int nb[3] = {64, 1, kTile};
+  const int64_t qd[3] = {a->D, a->H_q, a->rows}, qs[3] = {1, a->q_head, a->q_row};
+  const int qb[3] = {64, p.G, p.pos};
+  bool ok = encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) && encode(&m[3], a->dtype, a->k_new, 3, nd, kn, nb) &&
+            encode(&m[4], a->dtype, a->v_new, 3, nd, vn, nb);
+  if (cached) {
+    const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
+    const int64_t ks[4] = {1, a->k_head, a->k_tok, a->k_block}, vs[4] = {1, a->v_head, a->v_tok, a->v_block};
+    const int pb[4] = {64, 1, std::min<int>(a->page, kTile), 1};
+    ok = ok && encode(&m[1], a->dtype, a->k_pages, 4, pd, ks, pb) && encode(&m[2], a->dtype, a->v_pages, 4, pd, vs, pb);
+  } else {  // never read
+    m[1] = m[3];
+    m[2] = m[4];
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if (a->D <= 64) return a->dtype == DT_BF16 ? launch_t<64, true>(h, p, m, s) : launch_t<64, false>(h, p, m, s);
+  return a->dtype == DT_BF16 ? launch_t<128, true>(h, p, m, s) : launch_t<128, false>(h, p, m, s);
+}
+
+}  // namespace dt

@@ -50,7 +50,7 @@ extern "C" {
 #endif
 
 enum { DT_OK = 0, DT_ERR_ARG = -1, DT_ERR_CUDA = -2, DT_ERR_DEVICE = -3, DT_ERR_DEVICE_TIMEOUT = -4 };
-enum { DT_BF16 = 0, DT_F32 = 1, DT_F16 = 2 }; /* DT_F16: dt_tree_attention only */
+enum { DT_BF16 = 0, DT_F32 = 1, DT_F16 = 2 }; /* DT_F16: dt_tree_attention and dt_prompt_attention only */
 enum { DT_GREEDY = 0, DT_SAMPLE = 1 };
 /* OR-ed into the verify mode: padding-free target rows. Request b's used rows are packed after those
  * of requests 0..b-1: row (b, i) is row row_off[b] + i of the logits buffer, with
@@ -515,6 +515,40 @@ typedef struct {
 int dt_tree_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
 int dt_tree_attention_workspace(dt_handle* h, int32_t B, int32_t P, int32_t H_q, int32_t H_kv, int32_t D,
                                 int32_t shared, int64_t* bytes);
+
+/* Causal attention over prompts: new position i of request b (row row_off[b] + i, i < row_off[b + 1] - row_off[b]) attends
+ * to the request's seq_len[b] cached tokens (pages, through block_table) and to its new positions j <= i:
+ * out = softmax(scale * q k^T) v for query head x with key head x / (H_q / H_kv). A whole prompt, a chunk of a long one behind
+ * what earlier chunks left in the pages, and single tokens may stand in one batch; requests without rows are left out. The
+ * pages are read only: the rows move there by dt_commit_kv_paged, before or after this call.
+ * seq_len, block_table, k_pages and v_pages all NULL: nothing is cached. Rows of no request are left as they were, and K and V
+ * of tokens past seq_len, of rows of other requests and of later positions may hold anything (NaN and infinities too). Offsets
+ * that decrease or pass `rows`, a length below 0 or past the table, or a block outside the pages set DT_DEV_BAD_PAGE. out
+ * overlaps none of the inputs. Types, strides, alignment and head sizes as in dt_tree_attention; so are the rounding and what
+ * follows DT_DEV_TIMEOUT. */
+typedef struct {
+  int32_t B, H_q, H_kv, D, dtype;
+  float scale;
+  int64_t rows;                 /* rows of q, out, k_new, v_new                     */
+  const void* q;
+  int64_t q_row, q_head;
+  void* out;
+  int64_t o_row, o_head;
+  const void *k_new, *v_new;
+  int64_t kn_row, kn_head, vn_row, vn_head;
+  const int32_t* row_off;       /* [B+1] */
+  const void *k_pages, *v_pages;
+  int64_t k_block, k_tok, k_head, v_block, v_tok, v_head;
+  int32_t n_blocks, page;
+  const int32_t* block_table;   /* [B][max_blocks]; entries of tokens past seq_len are not read */
+  int32_t max_blocks;
+  const int32_t* seq_len;       /* [B] */
+  void* workspace;              /* dt_prompt_attention_workspace bytes, 256-byte aligned, no initial value; used
+                                   until the call has run (calls that may overlap need a workspace each) */
+  int64_t workspace_bytes;
+} dt_prompt_args;
+int dt_prompt_attention(dt_handle* h, const dt_prompt_args* a, cudaStream_t s);
+int dt_prompt_attention_workspace(dt_handle* h, int32_t B, int32_t H_q, int32_t H_kv, int32_t D, int64_t* bytes);
 
 /* Per-request token history for dt_logits_process: counts[b][v] = generated occurrences of v, plus
  * DT_SEEN_PROMPT when v is in the prompt. A new request's row is cleared by the caller. */
