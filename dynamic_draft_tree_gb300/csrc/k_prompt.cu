@@ -12,8 +12,8 @@
 // unnormalised result in fp32, joined in the order of the line by join_kernel. Every CTA derives the cuts from the lengths
 // on the device, so a captured call follows them.
 //
-// A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads Q rows and K tiles, warp 11 V tiles (TMA),
-// warp 9 issues the matrix instructions, warp 10 walks along the line and clears value rows. Every wait is bounded
+// A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads tiles (TMA), warps 9 and
+// 11 issue a group's matrix instructions each, warp 10 walks along the line and clears value rows. Every wait is bounded
 // (DT_DEV_TIMEOUT). S = Q K^T of a group's next tile is issued right behind O += P V of its last one, over the ends of
 // segments too: Q has a buffer a group that is loaded again when the group's last S of a segment is done, and O leaves
 // while the other group's products run, so the pipeline does not run empty between items. S (fp32), P (16-bit, over S) and O
@@ -225,20 +225,20 @@ template <int DP>
 struct Smem {
   static constexpr int kHalf = kTile * 128;         // bytes of 64 elements of 128 rows
   static constexpr int kBlock = (DP / 64) * kHalf;  // a tile of Q, K or V
-  // tiles of K and of V in flight: a V tile is held longer, from its load until the weights have come
-  static constexpr int kK = DP == 128 ? 2 : 5, kV = DP == 128 ? 3 : 6;
-  static constexpr int kTiles = (2 + kK + kV) * kBlock;
+  static constexpr int kK = DP == 128 ? 2 : 4, kV = DP == 128 ? 2 : 6;  // tiles of K and of V in flight
+  static constexpr int kOut = 8 * 32 * 128;         // where results turn from a row a thread to rows side by side
+  static constexpr int kTiles = (2 + kK + kV) * kBlock + kOut;
 };
 constexpr int kMostStages = 6;
 constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reader, at most
 
 struct Shared {
   uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
-  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], drained;
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], turn[2], drained[2];
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   Plan plan;
-  int64_t sums[12];
+  int64_t sums[kPromptThreads / 32];
   uint32_t tmem;
   int stop, odd_values, cut;
 };
@@ -261,7 +261,7 @@ struct Segments {
     return s.t1 > s.t0;
   }
 };
-constexpr int kSegReaders = 11;  // eight softmax warps, two loading warps, the issuing warp
+constexpr int kSegReaders = 11;  // eight softmax warps, the loading warp, two issuing warps
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -330,24 +330,40 @@ __device__ __forceinline__ void ring(uint32_t n, int& stage, uint32_t& parity) {
   parity = (n / N) & 1;
 }
 
-// One warp loads the K (or V) tiles of the CTA's line in order; K's warp also a segment's rows of Q, behind the segment's
-// first K tile, whose place is free earlier.
-template <int DP, bool IS_K>
-__device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap* pages, const CUtensorMap* new_map,
-                           const CUtensorMap* q_map, uint32_t smem, uint32_t q_smem, int lane) {
+// One warp loads the tiles of the CTA's line in order, K and then V of each; a segment's rows of Q stand behind its first K
+// tile, whose place is free earlier.
+template <int DP>
+__device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap* k_pages, const CUtensorMap* v_pages,
+                           const CUtensorMap* k_map, const CUtensorMap* v_map, const CUtensorMap* q_map, uint32_t q_smem,
+                           uint32_t k_smem, uint32_t v_smem, int lane) {
   using S = Smem<DP>;
-  uint64_t* full = IS_K ? sh.kfull : sh.vfull;
-  uint64_t* empty = IS_K ? sh.kempty : sh.vempty;
-  constexpr int kHalves = DP / 64, kStages = IS_K ? S::kK : S::kV;
+  constexpr int kHalves = DP / 64;
   const int shift = p.page_shift, page = p.a.page;
   const int box = min(page, kTile);  // tokens of a page box
   const int box_shift = min(shift, 7);
   Segments segs;
   Segment s;
-  uint32_t n = 0;
+  uint32_t n = 0, nv = 0;     // K and V tiles so far
   uint32_t nq0 = 0, nq1 = 0;  // loads of each group's Q so far
   bool ok = true;
   const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
+  // tile t to `at`; id: block of this lane's box
+  auto load = [&](int t, int id, const CUtensorMap* pages, const CUtensorMap* map, uint32_t at, uint64_t* full) {
+    if (t < s.ct) {
+      const int boxes = (min(kTile, s.len - t * kTile) + box - 1) >> box_shift;
+      if (lane == 0) tc::bar_expect(full, kHalves * 128 * boxes * box);
+      __syncwarp();
+      if (part < boxes) {
+        const int tok = t * kTile + (part << box_shift);
+        tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id, full);
+      }
+    } else {  // new positions; rows behind the request's last one are masked
+      if (lane == 0) tc::bar_expect(full, S::kBlock);
+      __syncwarp();
+      if (lane < kHalves)
+        tc::tma_load_3d(at + lane * S::kHalf, map, lane * 64, s.h, (int)s.base + (t - s.ct) * kTile, full);
+    }
+  };
   while (ok && segs.next(sh, s, lane == 0)) {
     const int32_t* table = p.a.block_table + (int64_t)s.b * p.a.max_blocks;
     // block id of this lane's box in tile t (-1: none)
@@ -362,31 +378,16 @@ __device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap*
       return id;
     };
     int id = block_at(s.t0);
-    for (int t = s.t0; t < s.t1; ++t, ++n) {
+    for (int t = s.t0; t < s.t1; ++t) {
       int stage;
       uint32_t parity;
-      ring<kStages>(n, stage, parity);
+      ring<S::kK>(n, stage, parity);
       const int next_id = t + 1 < s.t1 ? block_at(t + 1) : -1;
-      ok = tc::bar_wait_warp(&empty[stage], parity ^ 1, &sh.stop);
+      ok = tc::bar_wait_warp(&sh.kempty[stage], parity ^ 1, &sh.stop);
       if (!ok) break;
-      const uint32_t at = smem + stage * S::kBlock;
-      if (t < s.ct) {
-        const int boxes = (min(kTile, s.len - t * kTile) + box - 1) >> box_shift;
-        if (lane == 0) tc::bar_expect(&full[stage], kHalves * 128 * boxes * box);
-        __syncwarp();
-        if (part < boxes) {
-          const int tok = t * kTile + (part << box_shift);
-          tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id,
-                          &full[stage]);
-        }
-      } else {  // new positions; rows behind the request's last one are masked
-        if (lane == 0) tc::bar_expect(&full[stage], S::kBlock);
-        __syncwarp();
-        if (lane < kHalves)
-          tc::tma_load_3d(at + lane * S::kHalf, new_map, lane * 64, s.h, (int)s.base + (t - s.ct) * kTile, &full[stage]);
-      }
-      id = next_id;
-      if (IS_K && t == s.t0) {
+      load(t, id, k_pages, k_map, k_smem + stage * S::kBlock, &sh.kfull[stage]);
+      ++n;
+      if (t == s.t0) {
         // Whole positions of G heads, once the group's last S of the segment before is done. Rows past the item's belong
         // to other positions or lie past the buffer (zeros); nobody reads theirs.
 #pragma unroll
@@ -402,138 +403,153 @@ __device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap*
             tc::tma_load_3d(q_smem + g * S::kBlock + lane * S::kHalf, q_map, lane * 64, s.h * p.G, (int)s.base + s.i0 + g * p.pos,
                             &sh.qfull[g]);
         }
-        if (!ok) {
-          ++n;
-          break;
-        }
+        if (!ok) break;
       }
+      ring<S::kV>(nv, stage, parity);
+      ok = tc::bar_wait_warp(&sh.vempty[stage], parity ^ 1, &sh.stop);
+      if (!ok) break;
+      load(t, id, v_pages, v_map, v_smem + stage * S::kBlock, &sh.vfull[stage]);
+      ++nv;
+      id = next_id;
     }
   }
   // No load may land once the CTA is gone, and any wait, here or of a reader, may be the one that gave up: the last tiles
   // are waited for whatever ended the loop (in a call that runs through, the products wait for them too).
-  for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
+  for (uint32_t k = n > S::kK ? n - S::kK : 0; k < n; ++k) {
     int stage;
     uint32_t parity;
-    ring<kStages>(k, stage, parity);
-    tc::bar_drain(&full[stage], parity);
+    ring<S::kK>(k, stage, parity);
+    tc::bar_drain(&sh.kfull[stage], parity);
   }
-  if (IS_K) {
-    if (nq0) tc::bar_drain(&sh.qfull[0], (nq0 - 1) & 1);
-    if (nq1) tc::bar_drain(&sh.qfull[1], (nq1 - 1) & 1);
+  for (uint32_t k = nv > S::kV ? nv - S::kV : 0; k < nv; ++k) {
+    int stage;
+    uint32_t parity;
+    ring<S::kV>(k, stage, parity);
+    tc::bar_drain(&sh.vfull[stage], parity);
   }
+  if (nq0) tc::bar_drain(&sh.qfull[0], (nq0 - 1) & 1);
+  if (nq1) tc::bar_drain(&sh.qfull[1], (nq1 - 1) & 1);
 }
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
-// One warp issues the matrix instructions of the CTA's line, all lanes on one path and one thread elected for the
-// instructions themselves, so that descriptors stay in uniform registers. A step is a tile n of the line: for each group
-// O += P V of the tile before (if the group had it), then S of this one (if it has it).
+// One warp issues the matrix instructions of a group along the CTA's line, all lanes on one path and one thread elected for
+// the instructions themselves, so that descriptors stay in uniform registers. A step is a tile n of the line: O += P V of the
+// tile before (if the group had it), then S of this one (if it has it). The two groups' warps take turns, so that one group's
+// softmax runs beside the other's products, and each does its waiting while the other one issues.
 template <int DP, bool BF16>
-__device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int lane) {
+__device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem, int g, int lane) {
   using S = Smem<DP>;
-  constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false);
+  constexpr uint32_t kDescS = tc::instr_desc(BF16, kTile, kTile, false), kDescHalf = tc::instr_desc(BF16, kTile, kTile / 2, false);
   constexpr uint32_t kDescO = tc::instr_desc(BF16, kTile, DP, true);
   const int steps = (p.a.D + 15) / 16;  // the padding elements of a row are zero
   const uint32_t tm = uniform(sh.tmem);
   // shared memory lies below 2^18 bytes, so offsets add up inside a descriptor's address field
-  const uint64_t q_desc = tc::smem_desc(uniform(q_smem), 16, 1024), k_desc = tc::smem_desc(uniform(k_smem), 16, 1024),
+  const uint64_t q_desc = tc::smem_desc(uniform(q_smem + g * S::kBlock), 16, 1024), k_desc = tc::smem_desc(uniform(k_smem), 16, 1024),
                  v_desc = tc::smem_desc(uniform(v_smem), S::kHalf, 1024);
+  const uint32_t s_at = tm + g * kTile, o_at = tm + 2 * kTile + g * DP;
   const bool elected = tc::elect();
   Segments segs;
   Segment s;
-  uint32_t n = 0;             // tiles so far
-  uint32_t np0 = 0, np1 = 0;  // products with V of each group so far (phase of phalf)
-  uint32_t nq0 = 0, nq1 = 0;  // segments of each group so far (phase of qfull)
-  uint32_t fix = 0;           // parity of every stage's vfix
-  // what the groups still owe of the tile before: bit 0 anything, bit 1 it begins the accumulator, bit 2 it ends a segment
-  int owe0 = 0, owe1 = 0;
-  int valid = 0;              // of the tile before
+  uint32_t n = 0;      // tiles so far
+  uint32_t np = 0;     // products with V so far (phase of phalf)
+  uint32_t nq = 0;     // segments of the group so far (phase of qfull)
+  uint32_t turns = 0;  // this warp's turns so far
+  uint32_t fix = 0;    // parity of every stage's vfix
+  int owe = 0;         // of the tile before: bit 0 a product with V, bit 1 it begins the accumulator, bit 2 it ends a segment
+  int valid = 0;       // of the tile before
   bool fixed = false;
-  // O += P V of the tile before for group g; `first`: the tile has not been waited for yet
-  auto add_values = [&](int g, int owe, bool first) {
-    int stage;
+  int v_stage = 0;
+  auto take_turn = [&] {
+    const uint32_t k = turns++;
+    return tc::bar_wait_warp(&sh.turn[g], (k & 1) ^ (g ? 0 : 1), &sh.stop);
+  };
+  auto pass_turn = [&] {
+    if (elected) tc::bar_arrive(&sh.turn[g ^ 1]);
+  };
+  // The values of the tile before are there.
+  auto wait_values = [&] {
     uint32_t parity;
-    ring<S::kV>(n - 1, stage, parity);
-    if (first) {
-      if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return false;
-      if (fixed) {
-        if (!tc::bar_wait_warp(&sh.vfix[stage], fix >> stage & 1, &sh.stop)) return false;
-        fix ^= 1u << stage;
-      }
+    ring<S::kV>(n - 1, v_stage, parity);
+    if (!tc::bar_wait_warp(&sh.vfull[v_stage], parity, &sh.stop)) return false;
+    if (fixed) {
+      if (!tc::bar_wait_warp(&sh.vfix[v_stage], fix >> v_stage & 1, &sh.stop)) return false;
+      fix ^= 1u << v_stage;
     }
-    const uint64_t va = v_desc + (uint32_t)(stage * (S::kBlock >> 4));
-    const uint32_t o = tm + 2 * kTile + g * DP, pr = tm + g * kTile;
-    const uint32_t np = g ? np1++ : np0++;
+    return true;
+  };
+  // O += P V of the tile before, which is then let go. What else a step waits for has been waited for before its weights are
+  // there: in another order (K and the turn behind the weights) a tile of two groups took 2760 clocks instead of 2300.
+  auto add_values = [&]() {
+    if (!owe) {
+      if (elected) tc::bar_arrive(&sh.vempty[v_stage]);
+      return true;
+    }
+    const uint64_t va = v_desc + (uint32_t)(v_stage * (S::kBlock >> 4));
     // the first half's products run while the group works on the second half's weights
     if (!tc::bar_wait_warp(&sh.phalf[g][0], np & 1, &sh.stop)) return false;
     tc::fence_after();
     if (elected) {
-      tc::mma_ts(o, pr, va, kDescO, !(owe & 2));
+      tc::mma_ts(o_at, s_at, va, kDescO, !(owe & 2));
 #pragma unroll
       for (int x = 1; x < kTile / 32; ++x)
-        if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+        if (x * 16 < valid) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
     }
-    if (!tc::bar_wait_warp(&sh.phalf[g][1], np & 1, &sh.stop)) return false;
+    if (!tc::bar_wait_warp(&sh.phalf[g][1], np++ & 1, &sh.stop)) return false;
     tc::fence_after();
     if (elected) {
 #pragma unroll
       for (int x = kTile / 32; x < kTile / 16; ++x)
-        if (x * 16 < valid) tc::mma_ts(o, pr + x * 8, va + x * 128, kDescO, true);
+        if (x * 16 < valid) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
       if (owe & 4) tc::mma_commit(&sh.odone[g]);  // else S's commit says so too
+      tc::mma_commit(&sh.vempty[v_stage]);
     }
     return true;
   };
-  auto release_values = [&] {
-    if (n > 0 && elected) tc::mma_commit(&sh.vempty[(n - 1) % S::kV]);
-  };
   while (segs.next(sh, s, lane == 0)) {
     const int t0 = uniform(s.t0), t1 = uniform(s.t1), ct = uniform(s.ct), len = uniform(s.len), iend = uniform(s.iend),
-              i0 = uniform(s.i0), tiles0 = uniform(s.tiles0), tiles1 = uniform(s.tiles1);
+              i0 = uniform(s.i0), tiles = min(t1, uniform(g ? s.tiles1 : s.tiles0));
     for (int t = t0; t < t1; ++t) {
       int stage;
       uint32_t parity;
       ring<S::kK>(n, stage, parity);
-      bool first_k = true;
-      int owe_next0 = 0, owe_next1 = 0;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int owe = g ? owe1 : owe0;
-        if (owe && !add_values(g, owe, g == 0 || !owe0)) return;
-        const int tiles = g ? tiles1 : tiles0;
-        if (t < tiles) {
-          uint32_t& nq = g ? nq1 : nq0;
-          if (t == t0 && !tc::bar_wait_warp(&sh.qfull[g], nq++ & 1, &sh.stop)) return;
-          if (first_k && !tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
-          first_k = false;
-          tc::fence_after();
-          const uint64_t qa = q_desc + (uint32_t)(g * (S::kBlock >> 4)), ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
-          const uint32_t d = tm + g * kTile;
-          const bool last = t + 1 >= min(t1, tiles);
-          if (elected) {
-            tc::mma_ss(d, qa, ka, kDescS, false);
-#pragma unroll
-            for (int x = 1; x < DP / 16; ++x) {
-              const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
-              if (x < steps) tc::mma_ss(d, qa + off, ka + off, kDescS, true);
-            }
-            tc::mma_commit(&sh.sfull[g]);
-            if (last) tc::mma_commit(&sh.qempty[g]);
-          }
-          (g ? owe_next1 : owe_next0) = 1 | (t == t0 ? 2 : 0) | (last ? 4 : 0);
-        }
+      if (n > 0 && !wait_values()) return;
+      if (t == t0 && n > 0) {  // the last products of a segment do not wait for the next one's Q
+        if (!take_turn() || !add_values()) return;
+        pass_turn();
       }
-      release_values();
-      if (elected) tc::mma_commit(&sh.kempty[stage]);
-      owe0 = owe_next0;
-      owe1 = owe_next1;
+      if (t == t0 && t < tiles && !tc::bar_wait_warp(&sh.qfull[g], nq++ & 1, &sh.stop)) return;
+      // waited for and let go by a group without this tile too, so that it does not run ahead of the ring
+      if (!tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
+      if (!take_turn()) return;
+      if (t > t0 && !add_values()) return;
+      owe = 0;
+      if (t < tiles) {
+        tc::fence_after();
+        const uint64_t ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
+        owe = 1 | (t == t0 ? 2 : 0) | (t + 1 == tiles ? 4 : 0);
+        const uint32_t desc = tile_valid(t, ct, len, iend) > kTile / 2 ? kDescS : kDescHalf;
+        if (elected) {
+          tc::mma_ss(s_at, q_desc, ka, desc, false);
+#pragma unroll
+          for (int x = 1; x < DP / 16; ++x) {
+            const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
+            if (x < steps) tc::mma_ss(s_at, q_desc + off, ka + off, desc, true);
+          }
+          tc::mma_commit(&sh.sfull[g]);
+          if (owe & 4) tc::mma_commit(&sh.qempty[g]);
+          tc::mma_commit(&sh.kempty[stage]);
+        }
+      } else if (elected) {
+        tc::bar_arrive(&sh.kempty[stage]);
+      }
+      pass_turn();
       valid = tile_valid(t, ct, len, iend);
       fixed = tile_fixed(t, ct, valid, i0);
       ++n;
     }
   }
-  if (owe0 && !add_values(0, owe0, true)) return;
-  if (owe1 && !add_values(1, owe1, !owe0)) return;
-  release_values();
+  if (n > 0 && wait_values() && take_turn() && add_values()) pass_turn();
 }
 
 // One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
@@ -542,7 +558,7 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
 template <int DP, bool BF16>
 __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, int lane) {
   using S = Smem<DP>;
-  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u, kExp2 = kExp << 16 | kExp, kUnit2 = BF16 ? 0x00800080u : 0x04000400u;
   Walk w;
   w.start(p, sh.plan);
   Segment s;
@@ -588,28 +604,30 @@ __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, i
       uint8_t* at = v_smem + stage * S::kBlock;
       const int upto = (valid + 15) / 16 * 16;
       const int some = t < s.ct ? valid : max(0, s.i0 + 1 - (t - s.ct) * kTile);  // the first that not all rows attend to
-      bool odd = false;
+      // whether there is a NaN or an infinity, whose exponent's carry reaches the sign's place, and only then where
+      uint32_t carry = 0;
       for (int hf = 0; hf < DP / 64; ++hf) {
         uint8_t* rows = at + hf * S::kHalf;
         for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(rows + c * 16) = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll 8
         for (int c = some * 8 + lane; c < valid * 8; c += 32) {
-          uint4 q = *(uint4*)(rows + c * 16);
-          uint32_t* e = &q.x;
-          bool mine = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if ((e[k] & kExp) == kExp) {
-              e[k] &= 0xFFFF0000u;
-              mine = true;
-            }
-            if ((e[k] >> 16 & kExp) == kExp) {
-              e[k] &= 0xFFFFu;
-              mine = true;
-            }
+          const uint4 q = *(const uint4*)(rows + c * 16);
+          carry |= (q.x & kExp2) + kUnit2;
+          carry |= (q.y & kExp2) + kUnit2;
+          carry |= (q.z & kExp2) + kUnit2;
+          carry |= (q.w & kExp2) + kUnit2;
+        }
+      }
+      const bool odd = __any_sync(0xFFFFFFFFu, carry & 0x80008000u);
+      if (odd) {
+        for (int hf = 0; hf < DP / 64; ++hf) {
+          uint32_t* words = (uint32_t*)(at + hf * S::kHalf);
+          for (int c = some * 32 + lane; c < valid * 32; c += 32) {
+            uint32_t e = words[c];
+            if ((e & kExp) == kExp) e &= 0xFFFF0000u;
+            if ((e >> 16 & kExp) == kExp) e &= 0xFFFFu;
+            words[c] = e;
           }
-          if (mine) *(uint4*)(rows + c * 16) = q;
-          odd |= mine;
         }
       }
       if (odd) *(volatile int*)&sh.odd_values = 1;
@@ -627,24 +645,6 @@ __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, i
 struct Row {
   float m, l;  // reference maximum (log2 units), sum of weights
 };
-
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
-
-// Scores of the columns from `n` on become -inf in tensor memory, whatever they were (few tiles of an item need it: a
-// short loop of its own keeps the common path short).
-__device__ __noinline__ void mask_scores(uint32_t s_at, int n) {
-#pragma unroll 1
-  for (int c = 0; c < kTile; c += 16) {
-    if (__all_sync(0xFFFFFFFFu, n >= c + 16)) continue;
-    uint32_t raw[16];
-    tc::tmem_ld16(s_at + c, raw);
-#pragma unroll
-    for (int x = 0; x < 16; ++x)
-      if (c + x >= n) raw[x] = 0xFF800000u;
-    tc::tmem_st16(s_at + c, raw);
-  }
-  tc::wait_st();
-}
 
 // Values that are no numbers at positions j0 .. j1 - 1, which this row attends to: weight times value, from global memory.
 template <bool BF16>
@@ -669,49 +669,87 @@ __device__ __noinline__ void add_odd_row(const PromptParams& p, int h, int64_t b
 
 template <bool BF16>
 __device__ __forceinline__ void add_odd_values(const PromptParams& p, const Segment& s, int r, float m, float scale, int d0,
-                                               float (&o)[32]) {
+                                               uint32_t* o) {
+  if (d0 >= p.a.D) return;
   float x[32];  // its own array: one whose address is taken does not stay in registers
 #pragma unroll
-  for (int k = 0; k < 32; ++k) x[k] = o[k];
+  for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]);
   const int i = s.i0 + r / p.G;
   add_odd_row<BF16>(p, s.h, s.base, max(s.i0 + 1, (max(s.t0, s.ct) - s.ct) * kTile), min(i + 1, (s.t1 - s.ct) * kTile), i,
                     r % p.G, m, scale, d0, x);
 #pragma unroll
-  for (int k = 0; k < 32; ++k) o[k] = x[k];
+  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(x[k]);
 }
 
-// A group's rows of a segment leave tensor memory, every thread its own: 32 elements a turn.
-template <int DP, bool BF16>
-__device__ __forceinline__ void finish_rows(const PromptParams& p, Shared& sh, const Segment& s, int r, bool live, Row row, uint32_t o_at,
-                                            bool some) {
-  const bool whole = s.t0 == 0 && s.t1 == s.tt;
-  const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
-  const float inv = !whole ? 1.0f : row.l > 0.0f ? 1.0f / row.l : row.l == 0.0f ? 0.0f : row.l;  // NaN stays
-  const float ref = row.m == -INFINITY ? 0.0f : row.m;
-  const int i = position_of(p, r);
-  uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0 + i) * p.a.o_row + ((int64_t)s.h * p.G + r - i * p.G) * p.a.o_head;
-  const int64_t at = (int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r;
-  float* part = p.o + at * p.a.D;
-  if (!whole && live) p.ml[at] = make_float2(row.m, row.l);
-  if (!some) return;  // no tile of this segment is the group's: m = -inf, l = 0 say so
+// A group's rows of a segment leave tensor memory; all lanes of the warp. 128 bytes of a row a turn, through 4 KB of shared
+// memory of the warp's own, so that eight lanes store a row side by side: a store of 32 rows, 16 bytes each, takes 32 turns in
+// L1, and an item's end took 6500 clocks with those (4500 with blocks turned by shuffles).
+// An item in one piece: the quotient, rounded.
+template <bool BF16>
+__device__ __forceinline__ void write_rows(const PromptParams& p, const Segment& s, int r, bool odd, Row row, int end, uint32_t o_at,
+                                           uint8_t* stage) {
+  const int lane = threadIdx.x & 31, eighth = lane & 7, r0 = r - lane;
+  const float inv = row.l > 0.0f ? 1.0f / row.l : row.l == 0.0f ? 0.0f : row.l;  // NaN stays
+  uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0) * p.a.o_row + (int64_t)s.h * p.G * p.a.o_head + eighth * 8;
+  uint16_t* at[8];  // rows (lane >> 3) + 4 u
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int rr = r0 + u * 4 + (lane >> 3), i = position_of(p, rr);
+    at[u] = out + i * p.a.o_row + (rr - i * p.G) * p.a.o_head;
+  }
+  uint8_t *mine = stage + lane * 128, *theirs = stage + (lane >> 3) * 128;
+#pragma unroll 1
+  for (int d0 = 0; d0 < p.a.D; d0 += 64) {
+    uint32_t raw[64];
+    tc::tmem_ld64(o_at + d0, raw);
+#pragma unroll
+    for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
+    if (odd && lane < end) {
+      add_odd_values<BF16>(p, s, r, row.m == -INFINITY ? 0.0f : row.m, inv, d0, raw);
+      add_odd_values<BF16>(p, s, r, row.m == -INFINITY ? 0.0f : row.m, inv, d0 + 32, raw + 32);
+    }
+#pragma unroll
+    for (int k = 0; k < 64; k += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w[x] = pack16<BF16>(__uint_as_float(raw[k + 2 * x]), __uint_as_float(raw[k + 2 * x + 1]));
+      *(uint4*)(mine + (((k / 8) ^ eighth) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    uint4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = *(const uint4*)(theirs + u * 512 + ((eighth ^ ((u * 4 + (lane >> 3)) & 7)) << 4));
+    if (d0 + eighth * 8 < p.a.D) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (u * 4 + (lane >> 3) < end) *(uint4*)(at[u] + d0) = v[u];
+    }
+    __syncwarp();
+  }
+}
+
+// A part of one: as it is, in fp32, to be joined.
+template <bool BF16>
+__device__ __noinline__ void leave_rows(const PromptParams& p, const Segment& s, int r, bool odd, float m, int end, uint32_t o_at,
+                                        uint8_t* stage) {
+  const int lane = threadIdx.x & 31, eighth = lane & 7, r0 = r - lane;
+  float* part = p.o + ((int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r0 + (lane >> 3)) * p.a.D + eighth * 4;
+  uint8_t *mine = stage + lane * 128, *theirs = stage + (lane >> 3) * 128;
 #pragma unroll 1
   for (int d0 = 0; d0 < p.a.D; d0 += 32) {
     uint32_t raw[32];
-    float o[32];
     tc::tmem_ld32(o_at + d0, raw);
+    if (odd && lane < end) add_odd_values<BF16>(p, s, r, m == -INFINITY ? 0.0f : m, 1.0f, d0, raw);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(raw[k]) * inv;
-    if (odd && live) add_odd_values<BF16>(p, s, r, ref, inv, d0, o);
-    if (live && whole) {
+    for (int k = 0; k < 32; k += 4) *(uint4*)(mine + (((k / 4) ^ eighth) << 4)) = make_uint4(raw[k], raw[k + 1], raw[k + 2], raw[k + 3]);
+    __syncwarp();
+    uint4 v[8];
 #pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        if (d0 + k < p.a.D)
-          *(uint4*)(out + d0 + k) = make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]),
-                                               pack16<BF16>(o[k + 4], o[k + 5]), pack16<BF16>(o[k + 6], o[k + 7]));
-    } else if (live) {
+    for (int u = 0; u < 8; ++u) v[u] = *(const uint4*)(theirs + u * 512 + ((eighth ^ ((u * 4 + (lane >> 3)) & 7)) << 4));
+    if (d0 + eighth * 4 < p.a.D) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 4)
-        if (d0 + k < p.a.D) *(float4*)(part + d0 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      for (int u = 0; u < 8; ++u)
+        if (u * 4 + (lane >> 3) < end) *(uint4*)(part + u * 4 * p.a.D + d0) = v[u];
     }
     __syncwarp();
   }
@@ -719,11 +757,12 @@ __device__ __forceinline__ void finish_rows(const PromptParams& p, Shared& sh, c
 
 // A group of 128 threads turns every S of its tiles into weights.
 template <int DP, bool BF16>
-__device__ void softmax_group(const PromptParams& p, Shared& sh, int group) {
+__device__ void softmax_group(const PromptParams& p, Shared& sh, uint8_t* out_smem, int group) {
   const int wl = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
   const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
   const int half = p.rows2 >> 1, r = group * half + wl;  // this thread's row of an item
+  uint8_t* stage = out_smem + (threadIdx.x >> 5) * 32 * 128;
   Segments segs;
   Segment s;
   uint32_t ns = 0, no = 0;  // phases of sfull and odone of this group
@@ -741,17 +780,18 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, int group) {
       // the tile before this one has been added up too: S of this one was issued behind it
       tc::fence_after();
       if (work) {
-        if (__any_sync(0xFFFFFFFFu, see < kTile)) mask_scores(s_at, see);
-        uint32_t raw[64];
+        uint32_t raw[kTile];  // the row's scores, read once
+        tc::tmem_ld128(s_at, raw);
+        if (__any_sync(0xFFFFFFFFu, see < kTile)) {
+#pragma unroll
+          for (int x = 0; x < kTile; ++x)
+            if (x >= see) raw[x] = 0xFF800000u;  // whatever it was
+        }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          tc::tmem_ld64(s_at + hf * 64, raw);
 #pragma unroll
-          for (int x = 0; x < 64; x += 8) {
+        for (int x = 0; x < kTile; x += 8) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
-          }
+          for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
         }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
         if (t == s.t0) {
@@ -766,37 +806,41 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, int group) {
               row.l *= fac;
             }
 #pragma unroll 1
-            for (int d0 = 0; d0 < DP; d0 += 32) {
-              tc::tmem_ld32(o_at + d0, raw);
+            for (int d0 = 0; d0 < DP; d0 += 16) {
+              uint32_t acc[16];
+              tc::tmem_ld16(o_at + d0, acc);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) raw[x] = __float_as_uint(__uint_as_float(raw[x]) * fac);
-              tc::tmem_st32(o_at + d0, raw);
+              for (int x = 0; x < 16; ++x) acc[x] = __float_as_uint(__uint_as_float(acc[x]) * fac);
+              tc::tmem_st16(o_at + d0, acc);
             }
             tc::wait_st();
           }
         }
         const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
         const float2 c2 = make_float2(p.c, p.c), off2 = make_float2(off, off);
-        float2 l2 = make_float2(0.0f, 0.0f);
-        // P's 64 columns lie over S's first half: the second half of S is read before P reaches it
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          tc::tmem_ld64(s_at + hf * 64, raw);
-          uint32_t pk[32];
+        float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        // P's 64 columns lie over S's first half
 #pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[x]), __uint_as_float(raw[x + 1])), c2, off2);
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            l2 = __fadd2_rn(l2, e);
-            pk[x >> 1] = pack16<BF16>(e.x, e.y);
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int q = 0; q < 2 && hf * 64 < valid; ++q) {  // columns past the tile's end are in no product
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const int at = hf * 64 + q * 32 + x;
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[at]), __uint_as_float(raw[at + 1])), c2, off2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              l2[x >> 1 & 1] = __fadd2_rn(l2[x >> 1 & 1], e);
+              pk[x >> 1] = pack16<BF16>(e.x, e.y);
+            }
+            tc::tmem_st16(s_at + hf * 32 + q * 16, pk);
           }
-          tc::tmem_st32(s_at + hf * 32, pk);
           tc::wait_st();
           tc::fence_before();
           tc::bar_arrive(&sh.phalf[group][hf]);
         }
-        row.l += l2.x + l2.y;
+        row.l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       } else {
         tc::fence_before();
         tc::bar_arrive(&sh.phalf[group][0]);
@@ -809,7 +853,16 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, int group) {
       tc::fence_after();
     }
     // O is read before this group's next weights are handed over, and with them the next segment's first product
-    if (work) finish_rows<DP, BF16>(p, sh, s, r, live, row, o_at, some);
+    if (!work) continue;
+    const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
+    const int end = min(32, min(half, s.rows - group * half) - (wl & 96));  // the warp's rows in use
+    if (s.t1 - s.t0 == s.tt) {
+      write_rows<BF16>(p, s, r, odd, row, end, o_at, stage);
+    } else {
+      if (live) p.ml[(int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r] = make_float2(row.m, row.l);
+      // without a tile of this segment the group has no result: m = -inf, l = 0 say so
+      if (some) leave_rows<BF16>(p, s, r, odd, row.m, end, o_at, stage);
+    }
   }
 }
 
@@ -834,9 +887,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMostStages; ++i) {
       tc::bar_init(&sh.kfull[i], 1);
-      tc::bar_init(&sh.kempty[i], 1);
+      tc::bar_init(&sh.kempty[i], 2);
       tc::bar_init(&sh.vfull[i], 1);
-      tc::bar_init(&sh.vempty[i], 2);  // the products' end and the fixing warp
+      tc::bar_init(&sh.vempty[i], 3);  // the end of both groups' products and the fixing warp
       tc::bar_init(&sh.vfix[i], 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -846,8 +899,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::bar_init(&sh.odone[g], 1);
       tc::bar_init(&sh.qfull[g], 1);
       tc::bar_init(&sh.qempty[g], 1);
+      tc::bar_init(&sh.turn[g], 1);
+      tc::bar_init(&sh.drained[g], 1);
     }
-    tc::bar_init(&sh.drained, 1);
     for (int i = 0; i < kSegs; ++i) {
       tc::bar_init(&sh.segfull[i], 1);
       tc::bar_init(&sh.segempty[i], kSegReaders);
@@ -866,32 +920,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  // 384 x 168 registers at launch = 256 x 208 + 128 x 88: a softmax thread holds its row's 128 scores
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
-    softmax_group<DP, BF16>(p, sh, warp >> 2);
+    softmax_group<DP, BF16>(p, sh, v_smem + S::kV * S::kBlock, warp >> 2);
   } else if (warp == 8) {
-    load_tiles<DP, true>(p, sh, &k_map, &kn_map, &q_map, tc::smem_addr(k_smem), tc::smem_addr(q_smem), lane);
-  } else if (warp == 9) {
-    issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), lane);
+    load_tiles<DP>(p, sh, &k_map, &v_map, &kn_map, &vn_map, &q_map, tc::smem_addr(q_smem), tc::smem_addr(k_smem),
+                   tc::smem_addr(v_smem), lane);
   } else if (warp == 10) {
     fix_values<DP, BF16>(p, sh, v_smem, lane);
   } else {
-    load_tiles<DP, false>(p, sh, &v_map, &vn_map, nullptr, tc::smem_addr(v_smem), 0, lane);
+    issue_mma<DP, BF16>(p, sh, tc::smem_addr(q_smem), tc::smem_addr(k_smem), tc::smem_addr(v_smem), warp == 11, lane);
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 9) {
-    if (sh.stop) {  // products in flight end before their memory goes
-      if (tc::elect()) {  // the thread that issued them
-        set_status(p.status, DT_DEV_TIMEOUT);
-        p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};  // what it has left of a cut item is not joined
-        tc::mma_commit(&sh.drained);
-        tc::bar_drain(&sh.drained, 0);
-      }
-      __syncwarp();
+  if (sh.stop) {  // products in flight end before their memory goes, waited for by the threads that issued them
+    if ((warp == 9 || warp == 11) && tc::elect()) {
+      tc::mma_commit(&sh.drained[warp == 11]);
+      tc::bar_drain(&sh.drained[warp == 11], 0);
     }
-    tc::tmem_free<512>(sh.tmem);
+    __syncthreads();
+    if (tid == 0) {
+      set_status(p.status, DT_DEV_TIMEOUT);
+      p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};  // what it has left of a cut item is not joined
+    }
   }
+  if (warp == 9) tc::tmem_free<512>(sh.tmem);
 }
 
 // ------------------------------------------------------------------------------- join -----------
