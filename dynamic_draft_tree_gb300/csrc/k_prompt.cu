@@ -132,14 +132,14 @@ struct Segment {
   int ct, len;          // tiles of cached tokens, cached tokens
   int i0, iend;         // the item's positions
   int rows;             // rows of the item
-  int c0, parts;        // first CTA of the item and how many have tiles of it
+  int64_t next_u;       // unit where tile t1 begins
   int64_t base;         // row of position 0
 };
 
 // One lane walks along the CTA's run.
 struct Walk {
   int64_t x;
-  int64_t z;            // units from x to the current item's first
+  int z;                // units from the current item's first to x
   int b, h, i;          // the current item
   Request r;
   Extent e;
@@ -160,7 +160,7 @@ struct Walk {
       else hi = mid - 1;
     }
     i = lo;
-    z = at - units_before(p, e.ct, i);
+    z = (int)(at - units_before(p, e.ct, i));
   }
   // The next segment that has tiles (a run may end or begin inside an item's first units).
   __device__ __forceinline__ void next(const PromptParams& p, const Plan& pl, Segment& s) {
@@ -180,11 +180,10 @@ struct Walk {
       const bool dual = s.iend - s.i0 > p.pos;
       s.tiles1 = dual ? s.tt : 0;
       const int tw = dual ? 3 : 2;
-      const int64_t units = kItemUnits + (int64_t)tw * s.tt, end = min(units, z + pl.x1 - x), u0 = x - z + kItemUnits;
-      s.c0 = (int)(u0 / pl.per);
-      s.parts = (int)((u0 + (int64_t)(s.tt - 1) * tw) / pl.per) - s.c0 + 1;
-      s.t0 = (int)((max((int64_t)0, z - kItemUnits) + tw - 1) / tw);
-      s.t1 = (int)((max((int64_t)0, end - kItemUnits) + tw - 1) / tw);
+      const int units = kItemUnits + tw * s.tt, end = (int)min((int64_t)units, z + pl.x1 - x);
+      s.t0 = (max(0, z - kItemUnits) + tw - 1) / tw;
+      s.t1 = (max(0, end - kItemUnits) + tw - 1) / tw;
+      s.next_u = x - z + kItemUnits + (int64_t)s.t1 * tw;
       x += end - z;
       z = end;
       if (end == units) {
@@ -211,6 +210,15 @@ struct Walk {
   }
 };
 
+// CTAs with tiles of an item that is cut behind this, its first segment: the last tile begins this many units behind the
+// CTA's run.
+__device__ __forceinline__ int parts_of(const Plan& pl, const Segment& s) {
+  const int tw = s.tiles1 ? 3 : 2;
+  // the first tile that is not this CTA's begins in front of unit x1 + tw
+  const int over = (int)(s.next_u - pl.x1) + (s.tt - 1 - s.t1) * tw;
+  return 2 + over / pl.per;
+}
+
 // Columns of tile t that are in use: cached tokens, or new positions up to the item's last one.
 __device__ __forceinline__ int tile_valid(int t, int ct, int len, int iend) {
   return min(kTile, t < ct ? len - t * kTile : iend - (t - ct) * kTile);
@@ -234,7 +242,7 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
-  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], turn[2], drained[2];
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], ofull[2], ofree[2], turn[2], drained[2];
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   Plan plan;
@@ -247,6 +255,25 @@ template <int DP>
 constexpr int kSmemBytes = Smem<DP>::kTiles + (int)sizeof(Shared);
 static_assert(kSmemBytes<128> <= 232448 && kSmemBytes<64> <= 232448, "227 KB a CTA");
 
+// The whole warp waits and leaves with one answer: as tc::bar_wait_warp, in fewer instructions. What the CTA's roles run must
+// stay in the SM's instruction cache: with softmax code for 128 columns at once and three copies of the products' code one
+// fetch in seven missed it, and the cache behind it, which several SMs share, was busy for 75 % of the time.
+constexpr uint32_t kWaitTicks = 2000000000u;  // about a second
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& sh) {
+  const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+  do {
+    if (__all_sync(0xFFFFFFFFu, tc::bar_try(bar, parity))) return true;
+    if ((uint32_t)clock() - t0 > kWaitTicks) *(volatile int*)&sh.stop = 1;
+  } while (!*(volatile int*)&sh.stop);
+  return false;
+}
+
+// The same with the first look in front, for the waits that the pipeline hangs on.
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, Shared& sh) {
+  return __all_sync(0xFFFFFFFFu, tc::bar_try(bar, parity)) || wait(bar, parity, sh);
+}
+
 // The other warps read the segments that warp 10 puts down, in order. `lead`: the lane that gives the place back.
 struct Segments {
   uint32_t n = 0;
@@ -254,11 +281,22 @@ struct Segments {
     const int at = (int)(n % kSegs);
     const uint32_t parity = n / kSegs & 1;
     ++n;
-    if (!tc::bar_wait_warp(&sh.segfull[at], parity, &sh.stop)) return false;
+    if (!wait(&sh.segfull[at], parity, sh)) return false;
     s = sh.seg[at];
     __syncwarp();
     if (lead) tc::bar_arrive(&sh.segempty[at]);
     return s.t1 > s.t0;
+  }
+  // The same in two halves, for a reader that has no registers for all of it: where the segment is, and that it is done with.
+  __device__ __forceinline__ bool begin(Shared& sh) {
+    if (!wait(&sh.segfull[n % kSegs], n / kSegs & 1, sh)) return false;
+    return sh.seg[n % kSegs].t1 > sh.seg[n % kSegs].t0;
+  }
+  __device__ __forceinline__ const Segment& here(Shared& sh) const { return sh.seg[n % kSegs]; }
+  __device__ __forceinline__ void end(Shared& sh) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::bar_arrive(&sh.segempty[n % kSegs]);
+    ++n;
   }
 };
 constexpr int kSegReaders = 11;  // eight softmax warps, the loading warp, two issuing warps
@@ -347,23 +385,6 @@ __device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap*
   uint32_t nq0 = 0, nq1 = 0;  // loads of each group's Q so far
   bool ok = true;
   const int half = lane & (kHalves - 1), part = lane / kHalves;  // this lane's box of a tile
-  // tile t to `at`; id: block of this lane's box
-  auto load = [&](int t, int id, const CUtensorMap* pages, const CUtensorMap* map, uint32_t at, uint64_t* full) {
-    if (t < s.ct) {
-      const int boxes = (min(kTile, s.len - t * kTile) + box - 1) >> box_shift;
-      if (lane == 0) tc::bar_expect(full, kHalves * 128 * boxes * box);
-      __syncwarp();
-      if (part < boxes) {
-        const int tok = t * kTile + (part << box_shift);
-        tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, pages, half * 64, s.h, tok & (page - 1), id, full);
-      }
-    } else {  // new positions; rows behind the request's last one are masked
-      if (lane == 0) tc::bar_expect(full, S::kBlock);
-      __syncwarp();
-      if (lane < kHalves)
-        tc::tma_load_3d(at + lane * S::kHalf, map, lane * 64, s.h, (int)s.base + (t - s.ct) * kTile, full);
-    }
-  };
   while (ok && segs.next(sh, s, lane == 0)) {
     const int32_t* table = p.a.block_table + (int64_t)s.b * p.a.max_blocks;
     // block id of this lane's box in tile t (-1: none)
@@ -378,25 +399,45 @@ __device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap*
       return id;
     };
     int id = block_at(s.t0);
-    for (int t = s.t0; t < s.t1; ++t) {
-      int stage;
-      uint32_t parity;
-      ring<S::kK>(n, stage, parity);
+    for (int t = s.t0; ok && t < s.t1; ++t) {
       const int next_id = t + 1 < s.t1 ? block_at(t + 1) : -1;
-      ok = tc::bar_wait_warp(&sh.kempty[stage], parity ^ 1, &sh.stop);
-      if (!ok) break;
-      load(t, id, k_pages, k_map, k_smem + stage * S::kBlock, &sh.kfull[stage]);
-      ++n;
-      if (t == s.t0) {
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        int stage;
+        uint32_t parity;
+        if (kv) ring<S::kV>(nv, stage, parity);
+        else ring<S::kK>(n, stage, parity);
+        ok = wait(&(kv ? sh.vempty : sh.kempty)[stage], parity ^ 1, sh);
+        if (!ok) break;
+        uint64_t* full = &(kv ? sh.vfull : sh.kfull)[stage];
+        const uint32_t at = (kv ? v_smem : k_smem) + stage * S::kBlock;
+        if (t < s.ct) {
+          const int boxes = (min(kTile, s.len - t * kTile) + box - 1) >> box_shift;
+          if (lane == 0) tc::bar_expect(full, kHalves * 128 * boxes * box);
+          __syncwarp();
+          if (part < boxes) {
+            const int tok = t * kTile + (part << box_shift);
+            tc::tma_load_4d(at + half * S::kHalf + (part << box_shift) * 128, kv ? v_pages : k_pages, half * 64, s.h,
+                            tok & (page - 1), id, full);
+          }
+        } else {  // new positions; rows behind the request's last one are masked
+          if (lane == 0) tc::bar_expect(full, S::kBlock);
+          __syncwarp();
+          if (lane < kHalves)
+            tc::tma_load_3d(at + lane * S::kHalf, kv ? v_map : k_map, lane * 64, s.h, (int)s.base + (t - s.ct) * kTile, full);
+        }
+        if (kv) ++nv;
+        else ++n;
+        if (kv || t > s.t0) continue;
         // Whole positions of G heads, once the group's last S of the segment before is done. Rows past the item's belong
         // to other positions or lie past the buffer (zeros); nobody reads theirs.
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 2; ++g) {
-          if (s.t0 >= (g ? s.tiles1 : s.tiles0)) continue;
-          uint32_t& nq = g ? nq1 : nq0;
-          ok = tc::bar_wait_warp(&sh.qempty[g], (nq & 1) ^ 1, &sh.stop);
+          if (t >= (g ? s.tiles1 : s.tiles0)) continue;
+          ok = wait(&sh.qempty[g], ((g ? nq1 : nq0) & 1) ^ 1, sh);
           if (!ok) break;
-          ++nq;
+          if (g) ++nq1;
+          else ++nq0;
           if (lane == 0) tc::bar_expect(&sh.qfull[g], kHalves * p.pos * p.G * 128);
           __syncwarp();
           if (lane < kHalves)
@@ -405,11 +446,6 @@ __device__ void load_tiles(const PromptParams& p, Shared& sh, const CUtensorMap*
         }
         if (!ok) break;
       }
-      ring<S::kV>(nv, stage, parity);
-      ok = tc::bar_wait_warp(&sh.vempty[stage], parity ^ 1, &sh.stop);
-      if (!ok) break;
-      load(t, id, v_pages, v_map, v_smem + stage * S::kBlock, &sh.vfull[stage]);
-      ++nv;
       id = next_id;
     }
   }
@@ -457,99 +493,101 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
   uint32_t turns = 0;  // this warp's turns so far
   uint32_t fix = 0;    // parity of every stage's vfix
   int owe = 0;         // of the tile before: bit 0 a product with V, bit 1 it begins the accumulator, bit 2 it ends a segment
-  int valid = 0;       // of the tile before
+  int steps_v = 0;     // 16 tokens each, of the tile before
   bool fixed = false;
   int v_stage = 0;
+  int t = 0, t1 = 0, ct = 0, len = 0, iend = 0, i0 = 0, tiles = 0;
   auto take_turn = [&] {
     const uint32_t k = turns++;
-    return tc::bar_wait_warp(&sh.turn[g], (k & 1) ^ (g ? 0 : 1), &sh.stop);
+    return wait_soon(&sh.turn[g], (k & 1) ^ (g ? 0 : 1), sh);
   };
   auto pass_turn = [&] {
     if (elected) tc::bar_arrive(&sh.turn[g ^ 1]);
   };
-  // The values of the tile before are there.
-  auto wait_values = [&] {
+#pragma unroll 1
+  while (true) {
+    int stage;
     uint32_t parity;
-    ring<S::kV>(n - 1, v_stage, parity);
-    if (!tc::bar_wait_warp(&sh.vfull[v_stage], parity, &sh.stop)) return false;
-    if (fixed) {
-      if (!tc::bar_wait_warp(&sh.vfix[v_stage], fix >> v_stage & 1, &sh.stop)) return false;
-      fix ^= 1u << v_stage;
-    }
-    return true;
-  };
-  // O += P V of the tile before, which is then let go. What else a step waits for has been waited for before its weights are
-  // there: in another order (K and the turn behind the weights) a tile of two groups took 2760 clocks instead of 2300.
-  auto add_values = [&]() {
-    if (!owe) {
-      if (elected) tc::bar_arrive(&sh.vempty[v_stage]);
-      return true;
-    }
-    const uint64_t va = v_desc + (uint32_t)(v_stage * (S::kBlock >> 4));
-    // the first half's products run while the group works on the second half's weights
-    if (!tc::bar_wait_warp(&sh.phalf[g][0], np & 1, &sh.stop)) return false;
-    tc::fence_after();
-    if (elected) {
-      tc::mma_ts(o_at, s_at, va, kDescO, !(owe & 2));
-#pragma unroll
-      for (int x = 1; x < kTile / 32; ++x)
-        if (x * 16 < valid) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
-    }
-    if (!tc::bar_wait_warp(&sh.phalf[g][1], np++ & 1, &sh.stop)) return false;
-    tc::fence_after();
-    if (elected) {
-#pragma unroll
-      for (int x = kTile / 32; x < kTile / 16; ++x)
-        if (x * 16 < valid) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
-      if (owe & 4) tc::mma_commit(&sh.odone[g]);  // else S's commit says so too
-      tc::mma_commit(&sh.vempty[v_stage]);
-    }
-    return true;
-  };
-  while (segs.next(sh, s, lane == 0)) {
-    const int t0 = uniform(s.t0), t1 = uniform(s.t1), ct = uniform(s.ct), len = uniform(s.len), iend = uniform(s.iend),
-              i0 = uniform(s.i0), tiles = min(t1, uniform(g ? s.tiles1 : s.tiles0));
-    for (int t = t0; t < t1; ++t) {
-      int stage;
-      uint32_t parity;
-      ring<S::kK>(n, stage, parity);
-      if (n > 0 && !wait_values()) return;
-      if (t == t0 && n > 0) {  // the last products of a segment do not wait for the next one's Q
-        if (!take_turn() || !add_values()) return;
-        pass_turn();
+    ring<S::kK>(n, stage, parity);
+    bool fresh = t == t1;  // the next tile is another segment's: the products behind this one's do not wait for its Q and K
+    // What a step waits for has been waited for before its weights are there: K and the turn behind the weights made a tile of
+    // two groups 2760 clocks long instead of 2580.
+    if (n > 0) {
+      uint32_t v_parity;
+      ring<S::kV>(n - 1, v_stage, v_parity);
+      if (!wait_soon(&sh.vfull[v_stage], v_parity, sh)) return;
+      if (fixed) {
+        if (!wait(&sh.vfix[v_stage], fix >> v_stage & 1, sh)) return;
+        fix ^= 1u << v_stage;
       }
-      if (t == t0 && t < tiles && !tc::bar_wait_warp(&sh.qfull[g], nq++ & 1, &sh.stop)) return;
-      // waited for and let go by a group without this tile too, so that it does not run ahead of the ring
-      if (!tc::bar_wait_warp(&sh.kfull[stage], parity, &sh.stop)) return;
-      if (!take_turn()) return;
-      if (t > t0 && !add_values()) return;
-      owe = 0;
-      if (t < tiles) {
-        tc::fence_after();
-        const uint64_t ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
-        owe = 1 | (t == t0 ? 2 : 0) | (t + 1 == tiles ? 4 : 0);
-        const uint32_t desc = tile_valid(t, ct, len, iend) > kTile / 2 ? kDescS : kDescHalf;
-        if (elected) {
-          tc::mma_ss(s_at, q_desc, ka, desc, false);
+    }
+    // waited for and let go by a group without this tile too, so that it does not run ahead of the ring
+    if (!fresh && !wait_soon(&sh.kfull[stage], parity, sh)) return;
+    if (!take_turn()) return;
+    if (owe) {  // O += P V of the tile before, which is then let go
+      const uint64_t va = v_desc + (uint32_t)(v_stage * (S::kBlock >> 4));
+      // the first half's products run while the group works on the second half's weights
+      if (!wait_soon(&sh.phalf[g][0], np & 1, sh)) return;
+      tc::fence_after();
+      if (elected) {
+        tc::mma_ts(o_at, s_at, va, kDescO, !(owe & 2));
 #pragma unroll
-          for (int x = 1; x < DP / 16; ++x) {
-            const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
-            if (x < steps) tc::mma_ss(s_at, q_desc + off, ka + off, desc, true);
-          }
-          tc::mma_commit(&sh.sfull[g]);
-          if (owe & 4) tc::mma_commit(&sh.qempty[g]);
-          tc::mma_commit(&sh.kempty[stage]);
-        }
-      } else if (elected) {
-        tc::bar_arrive(&sh.kempty[stage]);
+        for (int x = 1; x < kTile / 32; ++x)
+          if (x < steps_v) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
       }
+      if (!wait_soon(&sh.phalf[g][1], np++ & 1, sh)) return;
+      tc::fence_after();
+      if (elected) {
+#pragma unroll
+        for (int x = kTile / 32; x < kTile / 16; ++x)
+          if (x < steps_v) tc::mma_ts(o_at, s_at + x * 8, va + x * 128, kDescO, true);
+        if (owe & 4) tc::mma_commit(&sh.odone[g]);  // else S's commit says so too
+        tc::mma_commit(&sh.vempty[v_stage]);
+      }
+    } else if (n > 0 && elected) {
+      tc::bar_arrive(&sh.vempty[v_stage]);
+    }
+    if (fresh) {
       pass_turn();
-      valid = tile_valid(t, ct, len, iend);
-      fixed = tile_fixed(t, ct, valid, i0);
-      ++n;
+      if (!segs.next(sh, s, lane == 0)) return;
+      t = uniform(s.t0);
+      t1 = uniform(s.t1);
+      ct = uniform(s.ct);
+      len = uniform(s.len);
+      iend = uniform(s.iend);
+      i0 = uniform(s.i0);
+      tiles = min(t1, uniform(g ? s.tiles1 : s.tiles0));
+      if (t < tiles && !wait(&sh.qfull[g], nq++ & 1, sh)) return;
+      if (!wait_soon(&sh.kfull[stage], parity, sh)) return;
+      if (!take_turn()) return;
     }
+    owe = 0;
+    const int valid = tile_valid(t, ct, len, iend);
+    steps_v = (valid + 15) / 16;
+    fixed = tile_fixed(t, ct, valid, i0);
+    if (t < tiles) {
+      tc::fence_after();
+      const uint64_t ka = k_desc + (uint32_t)(stage * (S::kBlock >> 4));
+      owe = 1 | (fresh ? 2 : 0) | (t + 1 == tiles ? 4 : 0);
+      const uint32_t desc = valid > kTile / 2 ? kDescS : kDescHalf;
+      if (elected) {
+        tc::mma_ss(s_at, q_desc, ka, desc, false);
+#pragma unroll
+        for (int x = 1; x < DP / 16; ++x) {
+          const uint32_t off = ((x >> 2) * S::kHalf + (x & 3) * 32) >> 4;
+          if (x < steps) tc::mma_ss(s_at, q_desc + off, ka + off, desc, true);
+        }
+        tc::mma_commit(&sh.sfull[g]);
+        if (owe & 4) tc::mma_commit(&sh.qempty[g]);
+        tc::mma_commit(&sh.kempty[stage]);
+      }
+    } else if (elected) {
+      tc::bar_arrive(&sh.kempty[stage]);
+    }
+    pass_turn();
+    ++t;
+    ++n;
   }
-  if (n > 0 && wait_values() && take_turn() && add_values()) pass_turn();
 }
 
 // One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
@@ -569,12 +607,12 @@ __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, i
     const int at = (int)(put % kSegs);
     const uint32_t parity = put / kSegs & 1;
     ++put;
-    if (!tc::bar_wait_warp(&sh.segempty[at], parity ^ 1, &sh.stop)) return false;
+    if (!wait(&sh.segempty[at], parity ^ 1, sh)) return false;
     if (lane == 0) {
       w.next(p, sh.plan, sh.seg[at]);
       const Segment& q = sh.seg[at];
-      if (q.t0 == 0 && q.t1 > 0 && q.t1 < q.tt) {
-        p.cuts[blockIdx.x] = Cut{q.parts, q.rows, q.h, 0, q.base + q.i0};
+      if (q.t0 == 0 && q.t1 > 0 && q.t1 < q.tt) {  // it begins here and goes on in the next CTAs
+        p.cuts[blockIdx.x] = Cut{parts_of(sh.plan, q), q.rows, q.h, 0, q.base + q.i0};
         sh.cut = 1;
       }
       if (q.t1 == q.t0 && !sh.cut) p.cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0};
@@ -596,7 +634,7 @@ __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, i
       uint32_t parity;
       ring<S::kV>(n, stage, parity);
       // every tile is waited for and let go here too, so that the ring never runs ahead of this warp
-      if (!tc::bar_wait_warp(&sh.vfull[stage], parity, &sh.stop)) return;
+      if (!wait(&sh.vfull[stage], parity, sh)) return;
       if (!tile_fixed(t, s.ct, valid, s.i0)) {
         if (lane == 0) tc::bar_arrive(&sh.vempty[stage]);
         continue;
@@ -646,92 +684,118 @@ struct Row {
   float m, l;  // reference maximum (log2 units), sum of weights
 };
 
-// Values that are no numbers at positions j0 .. j1 - 1, which this row attends to: weight times value, from global memory.
+// Scores of the columns from `n` to `upto` become -inf in tensor memory, whatever they were: few tiles of an item need it.
+__device__ __noinline__ void mask_scores(uint32_t s_at, int n, int upto) {
+#pragma unroll 1
+  for (int c = 0; c < upto; c += 32) {
+    if (__all_sync(0xFFFFFFFFu, n >= c + 32)) continue;
+    uint32_t raw[32];
+    tc::tmem_ld32(s_at + c, raw);
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (c + x >= n) raw[x] = 0xFF800000u;
+    tc::tmem_st32(s_at + c, raw);
+  }
+  tc::wait_st();
+}
+
+// Values that are no numbers, which were cleared: a row that attends to one (positions j0 .. j1 - 1) shows it, whatever its
+// weight, which is positive. Added to the row where it lies: in the result, or in the part that is to be joined.
 template <bool BF16>
-__device__ __noinline__ void add_odd_row(const PromptParams& p, int h, int64_t base, int j0, int j1, int i, int g, float m,
-                                         float scale, int d0, float* o) {
-  const uint16_t* q = (const uint16_t*)p.a.q + (base + i) * p.a.q_row + ((int64_t)h * p.G + g) * p.a.q_head;
+__device__ __noinline__ void add_odd_values(const PromptParams& p, int h, int64_t base, int j0, int j1, uint16_t* out, float* part) {
   for (int j = j0; j < j1; ++j) {
     const uint16_t* v = (const uint16_t*)p.a.v_new + (base + j) * p.a.vn_row + h * p.a.vn_head;
-    const uint16_t* k = (const uint16_t*)p.a.k_new + (base + j) * p.a.kn_row + h * p.a.kn_head;
-    bool odd = false;
-    for (int d = d0; d < min(d0 + 32, p.a.D); ++d) odd |= !isfinite(unpack16<BF16>(v[d]));
-    if (!odd) continue;
-    float dot = 0.0f;
-    for (int d = 0; d < p.a.D; ++d) dot += unpack16<BF16>(q[d]) * unpack16<BF16>(k[d]);
-    const float wgt = exp2f(dot * p.c - m + kShift);
-    for (int d = 0; d < min(32, p.a.D - d0); ++d) {
-      const float x = unpack16<BF16>(v[d0 + d]);
-      if (!isfinite(x)) o[d] += wgt * x * scale;
+    for (int d = 0; d < p.a.D; ++d) {
+      const float x = unpack16<BF16>(v[d]);
+      if (isfinite(x)) continue;
+      if (out) out[d] = (uint16_t)pack16<BF16>(unpack16<BF16>(out[d]) + x, 0.0f);
+      else part[d] += x;
     }
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void add_odd_values(const PromptParams& p, const Segment& s, int r, float m, float scale, int d0,
-                                               uint32_t* o) {
-  if (d0 >= p.a.D) return;
-  float x[32];  // its own array: one whose address is taken does not stay in registers
-#pragma unroll
-  for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]);
-  const int i = s.i0 + r / p.G;
-  add_odd_row<BF16>(p, s.h, s.base, max(s.i0 + 1, (max(s.t0, s.ct) - s.ct) * kTile), min(i + 1, (s.t1 - s.ct) * kTile), i,
-                    r % p.G, m, scale, d0, x);
-#pragma unroll
-  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(x[k]);
-}
-
-// A group's rows of a segment leave tensor memory; all lanes of the warp. 128 bytes of a row a turn, through 4 KB of shared
-// memory of the warp's own, so that eight lanes store a row side by side: a store of 32 rows, 16 bytes each, takes 32 turns in
-// L1, and an item's end took 6500 clocks with those (4500 with blocks turned by shuffles).
-// An item in one piece: the quotient, rounded.
-template <bool BF16>
-__device__ __forceinline__ void write_rows(const PromptParams& p, const Segment& s, int r, bool odd, Row row, int end, uint32_t o_at,
-                                           uint8_t* stage) {
-  const int lane = threadIdx.x & 31, eighth = lane & 7, r0 = r - lane;
-  const float inv = row.l > 0.0f ? 1.0f / row.l : row.l == 0.0f ? 0.0f : row.l;  // NaN stays
-  uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0) * p.a.o_row + (int64_t)s.h * p.G * p.a.o_head + eighth * 8;
-  uint16_t* at[8];  // rows (lane >> 3) + 4 u
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int rr = r0 + u * 4 + (lane >> 3), i = position_of(p, rr);
-    at[u] = out + i * p.a.o_row + (rr - i * p.G) * p.a.o_head;
+// 16 KB of shared memory through which a group's results leave, in turns of which all warps of the group take part: free(),
+// writing, done().
+struct Stage {
+  uint8_t* at;
+  uint32_t turns = 0;  // begun so far
+  // The last turn is over in every warp and its store has read what it took. (Without the first, a warp could miss a phase.)
+  __device__ __forceinline__ bool free(Shared& sh, int group) {
+    if ((threadIdx.x & 127) < 32) {
+      if (turns > 0 && !wait(&sh.ofull[group], (turns - 1) & 1, sh)) return false;
+      if ((threadIdx.x & 31) == 0) {
+        tc::tma_stores_read();
+        tc::bar_arrive(&sh.ofree[group]);
+      }
+      __syncwarp();
+    }
+    return wait(&sh.ofree[group], turns++ & 1, sh);
   }
-  uint8_t *mine = stage + lane * 128, *theirs = stage + (lane >> 3) * 128;
+  __device__ __forceinline__ void done(Shared& sh, int group) {
+    tc::fence_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::bar_arrive(&sh.ofull[group]);
+  }
+  // Behind done(): the first warp stores the box.
+  __device__ __forceinline__ bool store(Shared& sh, int group, const CUtensorMap* map, int x, int y, int z) {
+    if ((threadIdx.x & 127) >= 32) return true;
+    if (!wait(&sh.ofull[group], (turns - 1) & 1, sh)) return false;
+    if ((threadIdx.x & 31) == 0) tc::tma_store_3d(map, tc::smem_addr(at), x, y, z);
+    __syncwarp();
+    return true;
+  }
+};
+
+// A group's rows of a segment leave tensor memory, 128 bytes of a row a turn, through 16 KB of shared memory of the group's own.
+// An item in one piece: the quotient, rounded. Rows of a full group are stored by TMA, others by the threads, eight of them a
+// row. The way of 32 KB out of an SM takes 1000 clocks, for both groups together twice that, and stores by threads wait for it:
+// 4000 clocks an item with them (6500 with a row a thread).
+template <bool BF16>
+__device__ __forceinline__ bool write_rows(const PromptParams& p, Shared& sh, const Segment& s, int group, int wl, bool odd, float l,
+                                           int end, uint32_t o_at, Stage& stage, const CUtensorMap* out_map) {
+  const int lane = threadIdx.x & 31, eighth = lane & 7, half = p.rows2 >> 1, r = group * half + wl;
+  const bool full = s.rows - group * half >= half && !odd;
+  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays
+  uint8_t *mine = stage.at + wl * 128, *warps = stage.at + (wl & 96) * 128;
 #pragma unroll 1
   for (int d0 = 0; d0 < p.a.D; d0 += 64) {
     uint32_t raw[64];
-    tc::tmem_ld64(o_at + d0, raw);
+    if (end > 0) {
+      tc::tmem_ld64(o_at + d0, raw);
 #pragma unroll
-    for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
-    if (odd && lane < end) {
-      add_odd_values<BF16>(p, s, r, row.m == -INFINITY ? 0.0f : row.m, inv, d0, raw);
-      add_odd_values<BF16>(p, s, r, row.m == -INFINITY ? 0.0f : row.m, inv, d0 + 32, raw + 32);
+      for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
     }
+    if (!stage.free(sh, group)) return false;
+    if (end > 0) {
 #pragma unroll
-    for (int k = 0; k < 64; k += 8) {
-      uint32_t w[4];
+      for (int k = 0; k < 64; k += 8) {
+        uint32_t w[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) w[x] = pack16<BF16>(__uint_as_float(raw[k + 2 * x]), __uint_as_float(raw[k + 2 * x + 1]));
-      *(uint4*)(mine + (((k / 8) ^ eighth) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int x = 0; x < 4; ++x) w[x] = pack16<BF16>(__uint_as_float(raw[k + 2 * x]), __uint_as_float(raw[k + 2 * x + 1]));
+        *(uint4*)(mine + (((k / 8) ^ eighth) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    __syncwarp();
-    uint4 v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = *(const uint4*)(theirs + u * 512 + ((eighth ^ ((u * 4 + (lane >> 3)) & 7)) << 4));
-    if (d0 + eighth * 8 < p.a.D) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (u * 4 + (lane >> 3) < end) *(uint4*)(at[u] + d0) = v[u];
+    if (full) {
+      stage.done(sh, group);
+      if (!stage.store(sh, group, out_map, d0, s.h * p.G, (int)s.base + s.i0 + group * p.pos)) return false;
+    } else {
+      __syncwarp();
+      uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0) * p.a.o_row + (int64_t)s.h * p.G * p.a.o_head + eighth * 8 + d0;
+#pragma unroll 1
+      for (int x = lane >> 3; x < end; x += 4) {
+        const int f = r - lane + x, i = position_of(p, f);
+        if (d0 + eighth * 8 < p.a.D)
+          *(uint4*)(out + i * p.a.o_row + (f - i * p.G) * p.a.o_head) = *(const uint4*)(warps + x * 128 + ((eighth ^ (x & 7)) << 4));
+      }
+      stage.done(sh, group);
     }
-    __syncwarp();
   }
+  return true;
 }
 
 // A part of one: as it is, in fp32, to be joined.
 template <bool BF16>
-__device__ __noinline__ void leave_rows(const PromptParams& p, const Segment& s, int r, bool odd, float m, int end, uint32_t o_at,
-                                        uint8_t* stage) {
+__device__ __noinline__ void leave_rows(const PromptParams& p, const Segment& s, int r, int end, uint32_t o_at, uint8_t* stage) {
   const int lane = threadIdx.x & 31, eighth = lane & 7, r0 = r - lane;
   float* part = p.o + ((int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r0 + (lane >> 3)) * p.a.D + eighth * 4;
   uint8_t *mine = stage + lane * 128, *theirs = stage + (lane >> 3) * 128;
@@ -739,7 +803,6 @@ __device__ __noinline__ void leave_rows(const PromptParams& p, const Segment& s,
   for (int d0 = 0; d0 < p.a.D; d0 += 32) {
     uint32_t raw[32];
     tc::tmem_ld32(o_at + d0, raw);
-    if (odd && lane < end) add_odd_values<BF16>(p, s, r, m == -INFINITY ? 0.0f : m, 1.0f, d0, raw);
 #pragma unroll
     for (int k = 0; k < 32; k += 4) *(uint4*)(mine + (((k / 4) ^ eighth) << 4)) = make_uint4(raw[k], raw[k + 1], raw[k + 2], raw[k + 3]);
     __syncwarp();
@@ -757,44 +820,44 @@ __device__ __noinline__ void leave_rows(const PromptParams& p, const Segment& s,
 
 // A group of 128 threads turns every S of its tiles into weights.
 template <int DP, bool BF16>
-__device__ void softmax_group(const PromptParams& p, Shared& sh, uint8_t* out_smem, int group) {
+__device__ void softmax_group(const PromptParams& p, Shared& sh, const CUtensorMap* out_map, uint8_t* out_smem, int group) {
   const int wl = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
   const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
   const int half = p.rows2 >> 1, r = group * half + wl;  // this thread's row of an item
-  uint8_t* stage = out_smem + (threadIdx.x >> 5) * 32 * 128;
+  Stage stage{out_smem + group * kTile * 128};
   Segments segs;
-  Segment s;
   uint32_t ns = 0, no = 0;  // phases of sfull and odone of this group
-  while (segs.next(sh, s, (threadIdx.x & 31) == 0)) {
-    const bool live = wl < half && r < s.rows;
-    const int i = live ? s.i0 + position_of(p, r) : -1;  // this thread's position
-    const int tiles = min(s.t1, group ? s.tiles1 : s.tiles0);
+  while (segs.begin(sh)) {
+    const int t0 = segs.here(sh).t0, ct = segs.here(sh).ct, len = segs.here(sh).len, iend = segs.here(sh).iend;
+    const bool live = wl < half && r < segs.here(sh).rows;
+    const int i = live ? segs.here(sh).i0 + position_of(p, r) : -1;  // this thread's position
+    const int tiles = min(segs.here(sh).t1, group ? segs.here(sh).tiles1 : segs.here(sh).tiles0);
     Row row{-INFINITY, 0.0f};
     const bool work = __any_sync(0xFFFFFFFFu, live);
-    for (int t = s.t0; t < tiles; ++t) {
-      const int valid = tile_valid(t, s.ct, s.len, s.iend);
+    for (int t = t0; t < tiles; ++t) {
+      const int valid = tile_valid(t, ct, len, iend);
       // columns that this row attends to: all, or up to its own position
-      const int see = !live ? kTile : t < s.ct ? valid : min(valid, i + 1 - (t - s.ct) * kTile);
-      if (!tc::bar_wait_warp(&sh.sfull[group], ns++ & 1, &sh.stop)) return;
+      const int see = !live ? kTile : t < ct ? valid : min(valid, i + 1 - (t - ct) * kTile);
+      if (!wait_soon(&sh.sfull[group], ns++ & 1, sh)) return;
       // the tile before this one has been added up too: S of this one was issued behind it
       tc::fence_after();
       if (work) {
-        uint32_t raw[kTile];  // the row's scores, read once
-        tc::tmem_ld128(s_at, raw);
-        if (__any_sync(0xFFFFFFFFu, see < kTile)) {
-#pragma unroll
-          for (int x = 0; x < kTile; ++x)
-            if (x >= see) raw[x] = 0xFF800000u;  // whatever it was
-        }
+        const int upto = valid > 64 ? kTile : 64;  // columns past the tile's end are in no product
+        if (__any_sync(0xFFFFFFFFu, see < upto)) mask_scores(s_at, see, upto);
+        uint32_t raw[64];
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < upto; c += 64) {
+          tc::tmem_ld64(s_at + c, raw);
 #pragma unroll
-        for (int x = 0; x < kTile; x += 8) {
+          for (int x = 0; x < 64; x += 8) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
+            for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
+          }
         }
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
-        if (t == s.t0) {
+        if (t == t0) {
           row.m = top;
         } else {
           const bool up = top > row.m + kLazy;
@@ -819,24 +882,23 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, uint8_t* out_sm
         const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
         const float2 c2 = make_float2(p.c, p.c), off2 = make_float2(off, off);
         float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        // P's 64 columns lie over S's first half
-#pragma unroll
+        // P's 64 columns lie over S's first half: the second half of S is read before P reaches it
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
+          if (hf * 64 < upto) {
+            tc::tmem_ld64(s_at + hf * 64, raw);
+            uint32_t pk[32];
 #pragma unroll
-          for (int q = 0; q < 2 && hf * 64 < valid; ++q) {  // columns past the tile's end are in no product
-            uint32_t pk[16];
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const int at = hf * 64 + q * 32 + x;
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[at]), __uint_as_float(raw[at + 1])), c2, off2);
+            for (int x = 0; x < 64; x += 2) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(raw[x]), __uint_as_float(raw[x + 1])), c2, off2);
               e.x = ex2(e.x);
               e.y = ex2(e.y);
               l2[x >> 1 & 1] = __fadd2_rn(l2[x >> 1 & 1], e);
               pk[x >> 1] = pack16<BF16>(e.x, e.y);
             }
-            tc::tmem_st16(s_at + hf * 32 + q * 16, pk);
+            tc::tmem_st32(s_at + hf * 32, pk);
+            tc::wait_st();
           }
-          tc::wait_st();
           tc::fence_before();
           tc::bar_arrive(&sh.phalf[group][hf]);
         }
@@ -847,21 +909,36 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, uint8_t* out_sm
         tc::bar_arrive(&sh.phalf[group][1]);
       }
     }
-    const bool some = tiles > s.t0;
+    const bool some = tiles > t0;
     if (some) {
-      if (!tc::bar_wait_warp(&sh.odone[group], no++ & 1, &sh.stop)) return;
+      if (!wait(&sh.odone[group], no++ & 1, sh)) break;
       tc::fence_after();
     }
     // O is read before this group's next weights are handed over, and with them the next segment's first product
-    if (!work) continue;
+    const Segment s = segs.here(sh);
+    segs.end(sh);
     const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
-    const int end = min(32, min(half, s.rows - group * half) - (wl & 96));  // the warp's rows in use
+    const int end = max(0, min(32, min(half, s.rows - group * half) - (wl & 96)));  // the warp's rows in use
     if (s.t1 - s.t0 == s.tt) {
-      write_rows<BF16>(p, s, r, odd, row, end, o_at, stage);
+      if (some && !write_rows<BF16>(p, sh, s, group, wl, odd, row.l, end, o_at, stage, out_map)) return;
     } else {
       if (live) p.ml[(int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r] = make_float2(row.m, row.l);
       // without a tile of this segment the group has no result: m = -inf, l = 0 say so
-      if (some) leave_rows<BF16>(p, s, r, odd, row.m, end, o_at, stage);
+      if (some) {
+        if (!stage.free(sh, group)) return;
+        if (end > 0) leave_rows<BF16>(p, s, r, end, o_at, stage.at + (wl & 96) * 128);
+        stage.done(sh, group);
+      }
+    }
+    if (odd && some) {
+      __syncwarp();  // the warp's rows have been written, by other lanes
+      const int pos = position_of(p, r);
+      if (live)
+        add_odd_values<BF16>(p, s.h, s.base, max(s.i0 + 1, (max(s.t0, s.ct) - s.ct) * kTile), min(i + 1, (s.t1 - s.ct) * kTile),
+                             s.t1 - s.t0 < s.tt ? nullptr
+                                                : (uint16_t*)p.a.out + (s.base + i) * p.a.o_row + ((int64_t)s.h * p.G + r - pos * p.G) * p.a.o_head,
+                             p.o + ((int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r) * p.a.D);
+      __syncwarp();
     }
   }
 }
@@ -870,7 +947,8 @@ template <int DP, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                  const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map) {
+                  const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap vn_map,
+                  const __grid_constant__ CUtensorMap out_map) {
   using S = Smem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *q_smem = smem, *k_smem = smem + 2 * S::kBlock, *v_smem = k_smem + S::kK * S::kBlock;
@@ -899,6 +977,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::bar_init(&sh.odone[g], 1);
       tc::bar_init(&sh.qfull[g], 1);
       tc::bar_init(&sh.qempty[g], 1);
+      tc::bar_init(&sh.ofull[g], 4);
+      tc::bar_init(&sh.ofree[g], 1);
       tc::bar_init(&sh.turn[g], 1);
       tc::bar_init(&sh.drained[g], 1);
     }
@@ -914,6 +994,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     tc::tma_prefetch_map(&v_map);
     tc::tma_prefetch_map(&kn_map);
     tc::tma_prefetch_map(&vn_map);
+    tc::tma_prefetch_map(&out_map);
   }
   pdl_begin();
   make_plan(p, sh);
@@ -924,7 +1005,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
-    softmax_group<DP, BF16>(p, sh, v_smem + S::kV * S::kBlock, warp >> 2);
+    softmax_group<DP, BF16>(p, sh, &out_map, v_smem + S::kV * S::kBlock, warp >> 2);
+    if ((tid & 127) == 0) tc::tma_stores_done();  // whichever way it left
   } else if (warp == 8) {
     load_tiles<DP>(p, sh, &k_map, &v_map, &kn_map, &vn_map, &q_map, tc::smem_addr(q_smem), tc::smem_addr(k_smem),
                    tc::smem_addr(v_smem), lane);
@@ -1034,7 +1116,7 @@ Layout layout_of(const dt_handle* h, int D) {
 
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const PromptParams& p, const CUtensorMap* m, cudaStream_t s) {
-  launch_k(prompt_kernel<DP, BF16>, dim3(h->num_sms), dim3(kPromptThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4]);
+  launch_k(prompt_kernel<DP, BF16>, dim3(h->num_sms), dim3(kPromptThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4], m[5]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   launch_k(join_kernel<BF16>, dim3(h->num_sms, (p.rows2 + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinWarps), 0, s, p);
@@ -1078,13 +1160,14 @@ cudaError_t launch_prompt(dt_handle* h, const dt_prompt_args* a, cudaStream_t s)
   p.o = (float*)(ws + L.o);
   p.status = h->ws.status;
   p.test_stop = h->cfg.flags & DT_FLAG_TEST_TIMEOUT ? 1 : 0;
-  CUtensorMap m[5];
+  CUtensorMap m[6];
   const int64_t nd[3] = {a->D, a->H_kv, a->rows};
   const int64_t kn[3] = {1, a->kn_head, a->kn_row}, vn[3] = {1, a->vn_head, a->vn_row};
   const int nb[3] = {64, 1, kTile};
   const int64_t qd[3] = {a->D, a->H_q, a->rows}, qs[3] = {1, a->q_head, a->q_row};
   const int qb[3] = {64, p.G, p.pos};
-  bool ok = encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) && encode(&m[3], a->dtype, a->k_new, 3, nd, kn, nb) &&
+  const int64_t os[3] = {1, a->o_head, a->o_row};
+  bool ok = encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) && encode(&m[5], a->dtype, a->out, 3, qd, os, qb) && encode(&m[3], a->dtype, a->k_new, 3, nd, kn, nb) &&
             encode(&m[4], a->dtype, a->v_new, 3, nd, vn, nb);
   if (cached) {
     const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
