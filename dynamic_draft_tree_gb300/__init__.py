@@ -15,7 +15,7 @@ from ._lib import (lib, check, DtError, DtConfig, DtTreeView, DtPruneParams, DtP
                    DT_ERR_DEVICE_TIMEOUT, DT_BF16, DT_F32, DT_GREEDY, DT_SAMPLE, DT_VERIFY_PACKED,
                    DT_POLICY_CAST_WIDTH_DEPTH, DT_POLICY_CAST_VERIFY, DT_POLICY_GRAFT_CHECKPOINT, DT_POLICY_NONE,
                    DT_DEV_BAD_LOGITS, DT_DEV_BAD_TOKEN, DT_DEV_BAD_TREE, DT_DEV_TIMEOUT, DT_DEV_INTERNAL, DT_DEV_KV_FULL,
-                   DT_DEV_BAD_PAGE, DT_SEEN_PROMPT, DT_F16, DtBlockPool, DtKvRows, DtAttnArgs, DtLogitsParams, DtPromptArgs,
+                   DT_DEV_BAD_PAGE, DT_SEEN_PROMPT, DT_F16, DtBlockPool, DtKvRows, DtAttnArgs, DtLogitsParams, DtPromptArgs, DtLogprobArgs, DtKvPages,
                    DT_FLAG_TEST_TIMEOUT, DT_FLAG_TEST_ARRIVED, DT_ANCHOR_ROOT, DT_ANCHOR_TAIL, LIB_PATH)
 
 
@@ -278,7 +278,7 @@ def _packer(struct_type):
 
 
 _pack_kv_rows, _pack_attn, _pack_logits = _packer(DtKvRows), _packer(DtAttnArgs), _packer(DtLogitsParams)
-_pack_prompt = _packer(DtPromptArgs)
+_pack_prompt, _pack_logprobs, _pack_kv_pages = _packer(DtPromptArgs), _packer(DtLogprobArgs), _packer(DtKvPages)
 
 
 def _refuse(t, dtype, dev, name, n):
@@ -374,6 +374,38 @@ def dt_kv_release(h, pool, keep_len, stream=None):
         raise ValueError("the pool holds fewer requests than keep_len, or is on another device")
     rc = lib.dt_kv_release(h.h, B, pool.ref, _dev(keep_len, _I32, dev, "keep_len"),
                            _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
+
+
+def dt_kv_fork(h, pool, refs, cache, src, dst, seq_len, length=None, shared_len=0, stream=None):
+    """Requests dst continue requests src (int32, one entry a fork) behind their first ``length`` tokens (default seq_len, which is
+    updated): whole pages shared, the last one's tokens copied in cache [planes][blocks][page][H][D], any strides but the
+    last dimension's. refs [n_blocks] int32: owners of a block beyond its first, zero at the start."""
+    n, dev, cs, sc = src.numel(), _device(), cache.shape, cache.stride()
+    if pool.device != dev:
+        raise ValueError("the pool is on another device")
+    if len(cs) != 5 or cs[1] != pool.n_blocks or cs[2] != pool.page:
+        raise ValueError("cache must be [planes][blocks][page][H][D] with the pool's blocks and page")
+    if cache.get_device() != dev or sc[4] != 1:
+        _strided(cache, cache.dtype, dev, sc, "cache")
+    e = cache.element_size()
+    kv = _pack_kv_pages(cache.data_ptr(), sc[0] * e, sc[1] * e, sc[2] * e, sc[3] * e, cs[0], cs[3], cs[4] * e)
+    rc = lib.dt_kv_fork(h.h, pool.B, pool.ref, _dev(refs, _I32, dev, "refs", pool.n_blocks), kv, n, _dev(src, _I32, dev, "src"),
+                        _dev(dst, _I32, dev, "dst", n), 0 if length is None else _dev(length, _I32, dev, "length", n),
+                        _dev(seq_len, _I32, dev, "seq_len", pool.B), shared_len,
+                        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
+
+
+def dt_kv_release_shared(h, pool, refs, keep_len, stream=None):
+    """Gives back every request's blocks past keep_len tokens (0: all of them) in a pool with forks."""
+    B, dev = keep_len.numel(), _device()
+    if B > pool.B or pool.device != dev:
+        raise ValueError("the pool holds fewer requests than keep_len, or is on another device")
+    rc = lib.dt_kv_release_shared(h.h, B, pool.ref, _dev(refs, _I32, dev, "refs", pool.n_blocks),
+                                  _dev(keep_len, _I32, dev, "keep_len"), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 
@@ -639,6 +671,70 @@ def dt_logits_process(h, logits, out, n_pos, tokens=None, mask=None, row_off=Non
                      0 if allow is None else _dev(allow, _I32, dev, "allow"), words)
     rc = lib.dt_logits_process(h.h, B, logits.data_ptr(), ls_[at], out.data_ptr(), os_[at], p,
                                _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc)
+
+
+def dt_token_logprobs_workspace(h, entries, K=0):
+    """A workspace tensor for dt_token_logprobs calls of at most so many entries and alternatives (one call at a time)."""
+    n = ctypes.c_int64(0)
+    check(lib.dt_token_logprobs_workspace(h.h, entries, K, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=_U8, device="cuda")
+
+
+def dt_token_logprobs(h, logits, n_new, logp, workspace, tokens=None, last=None, shift=1, n_extra=0, path=None, row_off=None,
+                      entropy=None, rank=None, top_ids=None, top_logp=None, P=None, stream=None):
+    """Log probabilities of tokens under rows of logits: logits [B][P][V], or packed [rows][V] with row_off [B+1] (rows may be
+    further apart than V). Outputs (float32, rank and top_ids int32, any of them None) [B][P], or [rows] packed, or with
+    path [B][D_path] one entry a path position; top_ids and top_logp have a last dimension of K alternatives. tokens: laid
+    out as the outputs, with path [B][P] (P: positions a request); last [B]: the token behind a request's last entry."""
+    cfg = h.cfg
+    dtype = torch.bfloat16 if cfg.dtype == DT_BF16 else _F32
+    B, V, dev = n_new.numel(), cfg.V, _device()
+    ls, ls_ = logits.shape, logits.stride()
+    if len(ls) != (3 if row_off is None else 2) or ls[-1] != V:
+        raise ValueError("logits need [B][P][V] ([rows][V] packed)")
+    at = -2  # dimension of the rows
+    if row_off is None:
+        P, rows = ls[1], ls[0] * ls[1]
+        if ls[0] < B:
+            raise ValueError("logits holds fewer requests than n_new")
+        if ls[0] > 1:
+            if P == 1:  # the requests are the rows (a dimension of one has any stride)
+                at = 0
+            elif ls_[0] != P * ls_[1]:
+                raise ValueError("padded rows must be P rows apart")
+    else:
+        rows = ls[0]
+        if P is None:
+            P = tokens.shape[1] if path is not None and tokens is not None and tokens.dim() == 2 else max(1, rows)
+    dp = 0
+    if path is not None:
+        if path.dim() != 2 or path.shape[0] < B:
+            raise ValueError("path must be [B][D_path]")
+        dp = path.shape[1]
+    if tokens is not None and (path is not None or row_off is None) and \
+            (tokens.dim() != 2 or tokens.shape[0] < B or tokens.shape[1] != P):
+        raise ValueError("tokens must be [B][P]")
+    n_out = B * dp if path is not None else rows if row_off is not None else B * P
+    K = 0
+    if top_ids is not None or top_logp is not None:
+        if top_ids is None or top_logp is None or top_ids.shape != top_logp.shape:
+            raise ValueError("top_ids and top_logp come together, of one shape")
+        K = top_ids.shape[-1]
+    if not (logits.dtype is dtype and logits.get_device() == dev and ls_[-1] == 1):
+        _strided(logits, dtype, dev, ls_, "logits")
+    a = _pack_logprobs(B, P, rows, 0 if row_off is None else _dev(row_off, _I32, dev, "row_off", B + 1),
+                       0 if path is None else _dev(path, _I32, dev, "path"), dp, _dev(n_new, _I32, dev, "n_new"), n_extra, shift,
+                       0 if tokens is None else _dev(tokens, _I32, dev, "tokens"), 0 if tokens is None else tokens.numel(),
+                       0 if last is None else _dev(last, _I32, dev, "last", B), n_out,
+                       0 if logp is None else _dev(logp, _F32, dev, "logp", n_out),
+                       0 if entropy is None else _dev(entropy, _F32, dev, "entropy", n_out),
+                       0 if rank is None else _dev(rank, _I32, dev, "rank", n_out), K,
+                       0 if K == 0 else _dev(top_ids, _I32, dev, "top_ids", n_out * K),
+                       0 if K == 0 else _dev(top_logp, _F32, dev, "top_logp", n_out * K), _dev(workspace, _U8, dev, "workspace"),
+                       workspace.numel())
+    rc = lib.dt_token_logprobs(h.h, logits.data_ptr(), ls_[at], a, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 

@@ -29,7 +29,8 @@ EXPORTS = ["dt_last_error_string", "dt_create", "dt_destroy", "dt_get_tree", "dt
            "dt_commit_kv", "dt_block_expand", "dt_expand_layer_sampled", "dt_verify_sampled",
            "dt_kv_reserve", "dt_kv_release", "dt_commit_kv_paged", "dt_tree_attention",
            "dt_tree_attention_workspace", "dt_count_tokens", "dt_logits_process", "dt_prompt_attention",
-           "dt_prompt_attention_workspace"]
+           "dt_prompt_attention_workspace", "dt_token_logprobs", "dt_token_logprobs_workspace",
+           "dt_kv_fork", "dt_kv_release_shared"]
 
 c_i32p = ctypes.c_void_p
 vp = ctypes.c_void_p
@@ -86,6 +87,12 @@ class DtKvRows(ctypes.Structure):
                 ("head_bytes", ctypes.c_int64), ("page", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("committed", vp)]
 
 
+class DtKvPages(ctypes.Structure):
+    _fields_ = [("cache", vp), ("cache_plane", ctypes.c_int64), ("cache_block", ctypes.c_int64),
+                ("cache_tok", ctypes.c_int64), ("cache_head", ctypes.c_int64), ("planes", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_bytes", ctypes.c_int64)]
+
+
 class DtAttnArgs(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("P", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
@@ -113,6 +120,14 @@ class DtPromptArgs(ctypes.Structure):
                 ("v_head", ctypes.c_int64), ("n_blocks", ctypes.c_int32), ("page", ctypes.c_int32),
                 ("block_table", vp), ("max_blocks", ctypes.c_int32), ("seq_len", vp), ("workspace", vp),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class DtLogprobArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("P", ctypes.c_int32), ("rows", ctypes.c_int64), ("row_off", vp), ("path", vp),
+                ("D_path", ctypes.c_int32), ("n_new", vp), ("n_extra", ctypes.c_int32), ("shift", ctypes.c_int32),
+                ("tokens", vp), ("n_tokens", ctypes.c_int64), ("last", vp), ("n_out", ctypes.c_int64), ("logp", vp),
+                ("entropy", vp), ("rank", vp), ("K", ctypes.c_int32), ("top_ids", vp), ("top_logp", vp),
+                ("workspace", vp), ("workspace_bytes", ctypes.c_int64)]
 
 
 class DtLogitsParams(ctypes.Structure):
@@ -171,6 +186,10 @@ def _load():
         "dt_tree_attention_workspace": ([vp] + [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int64)], I),
         "dt_prompt_attention": ([vp, vp, vp], I),
         "dt_prompt_attention_workspace": ([vp] + [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_int64)], I),
+        "dt_token_logprobs": ([vp, vp, ctypes.c_int64, vp, vp], I),
+        "dt_token_logprobs_workspace": ([vp, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)], I),
+        "dt_kv_fork": ([vp, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, ctypes.c_int32, vp], I),
+        "dt_kv_release_shared": ([vp, ctypes.c_int32, vp, vp, vp, vp], I),
         "dt_count_tokens": ([vp, ctypes.c_int32, vp, vp, ctypes.c_int64, ctypes.c_int32, vp, vp, ctypes.c_int32, vp, ctypes.c_int32,
                              ctypes.c_int32, vp], I),
         "dt_logits_process": ([vp, ctypes.c_int32, vp, ctypes.c_int64, vp, ctypes.c_int64,

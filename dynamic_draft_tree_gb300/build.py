@@ -18,8 +18,8 @@ ARCH = "103a"
 
 SOURCES = ["dt_api.cu", "k_tree.cu", "k_select.cu", "k_meta.cu", "k_verify.cu", "k_graft.cu",
            "k_rowtopk_static.cu", "k_kv.cu", "k_block.cu", "k_sampled.cu", "k_paged.cu", "k_attn.cu", "k_logits.cu",
-           "k_prompt.cu"]
-HEADERS = ["dt_internal.cuh", "rowscan.cuh", "rowstream.cuh", "cast_block.cuh", "tc.cuh", "tma_map.cuh"]
+           "k_prompt.cu", "k_logprobs.cu", "k_fork.cu"]
+HEADERS = ["dt_internal.cuh", "rowscan.cuh", "rowstream.cuh", "cast_block.cuh", "tc.cuh", "tma_map.cuh", "pages.cuh"]
 
 
 def nvcc_flags(verbose_ptxas=False):

@@ -124,6 +124,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   const size_t o_status = cv.take<int32_t>(1);
   const size_t o_ticket = cv.take<unsigned>(1);
   const size_t o_atick = cv.take<unsigned>(h->num_sms);
+  const size_t o_pstate = cv.take<int32_t>(c.B_max);
   const size_t total = cv.off;
 
   void* base = nullptr;
@@ -173,6 +174,7 @@ int dt_create(const dt_config* cfg, dt_handle** out) {
   w.status = reinterpret_cast<int32_t*>(bp + o_status);
   w.ticket = reinterpret_cast<unsigned*>(bp + o_ticket);
   w.attn_tickets = reinterpret_cast<unsigned*>(bp + o_atick);
+  w.page_state = reinterpret_cast<int32_t*>(bp + o_pstate);
   if (c.flags & DT_FLAG_TEST_ARRIVED) {
     const std::vector<unsigned> one(h->num_sms, 1u);
     e = cudaMemcpy(w.attn_tickets, one.data(), sizeof(unsigned) * one.size(), cudaMemcpyHostToDevice);
@@ -617,6 +619,43 @@ int dt_kv_release(dt_handle* h, int32_t B, const dt_block_pool* pool, const int3
   return DT_OK;
 }
 
+int dt_kv_fork(dt_handle* h, int32_t B, const dt_block_pool* pool, int32_t* refs, const dt_kv_pages* kv, int32_t n,
+               const int32_t* src, const int32_t* dst, const int32_t* length, int32_t* seq_len, int32_t shared_len,
+               cudaStream_t s) {
+  int rc = check_batch(h, "dt_kv_fork", B);
+  if (rc == DT_OK) rc = check_pool("dt_kv_fork", pool);
+  if (rc != DT_OK) return rc;
+  if (!refs || !kv || !kv->cache || !src || !dst || !seq_len) return fail(DT_ERR_ARG, "dt_kv_fork: null argument");
+  if (n < 1 || n > h->cfg.B_max) return fail(DT_ERR_ARG, "dt_kv_fork: n must be in [1, B_max]");
+  if (pool->n_blocks >= 1 << 30) return fail(DT_ERR_ARG, "dt_kv_fork: n_blocks must be below 2^30");
+  if (shared_len < 0 || shared_len % pool->page || shared_len / pool->page > pool->max_blocks)
+    return fail(DT_ERR_ARG, "dt_kv_fork: shared_len must be a multiple of page within max_blocks");
+  if (kv->planes < 1 || kv->planes > 65535) return fail(DT_ERR_ARG, "dt_kv_fork: planes must be in [1, 65535]");
+  if (kv->heads < 1 || kv->head_bytes < 16 || kv->heads > (int64_t)(1 << 20) / kv->head_bytes)
+    return fail(DT_ERR_ARG, "dt_kv_fork: heads >= 1, head_bytes >= 16, a plane's row at most 1 MB");
+  if (!aligned(kv->cache, 16) || kv->cache_plane % 16 || kv->cache_block % 16 || kv->cache_tok % 16 || kv->cache_head % 16 ||
+      kv->head_bytes % 16)
+    return fail(DT_ERR_ARG, "dt_kv_fork: pointers, strides and head_bytes must be multiples of 16 bytes");
+  if (!aligned(refs, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(length, 4) || !aligned(seq_len, 4))
+    return fail(DT_ERR_ARG, "dt_kv_fork: int32 arrays must be 4-byte aligned");
+  cudaError_t e = dt::launch_kv_fork(h, B, pool, refs, kv, n, src, dst, length, seq_len, shared_len, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_kv_fork");
+  return DT_OK;
+}
+
+int dt_kv_release_shared(dt_handle* h, int32_t B, const dt_block_pool* pool, int32_t* refs, const int32_t* keep_len,
+                         cudaStream_t s) {
+  int rc = check_batch(h, "dt_kv_release_shared", B);
+  if (rc == DT_OK) rc = check_pool("dt_kv_release_shared", pool);
+  if (rc != DT_OK) return rc;
+  if (!refs || !keep_len) return fail(DT_ERR_ARG, "dt_kv_release_shared: null argument");
+  if (pool->n_blocks >= 1 << 30) return fail(DT_ERR_ARG, "dt_kv_release_shared: n_blocks must be below 2^30");
+  if (!aligned(refs, 4) || !aligned(keep_len, 4)) return fail(DT_ERR_ARG, "dt_kv_release_shared: int32 arrays must be 4-byte aligned");
+  cudaError_t e = dt::launch_kv_release_shared(h, B, pool, refs, keep_len, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_kv_release_shared");
+  return DT_OK;
+}
+
 int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P, const int32_t* row_off,
                        const int32_t* path, int32_t D_path, const int32_t* n_new, int32_t n_extra,
                        const int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
@@ -785,6 +824,45 @@ int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, v
     return fail(DT_ERR_ARG, "dt_logits_process: arrays must be 4-byte aligned");
   cudaError_t e = dt::launch_logits(h, B, logits, ld, out, ld_out, p, s);
   if (e != cudaSuccess) return cuda_fail(e, "dt_logits_process");
+  return DT_OK;
+}
+
+int dt_token_logprobs_workspace(dt_handle* h, int64_t entries, int32_t K, int64_t* bytes) {
+  if (!h || !bytes) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: null argument");
+  if (K < 0 || K > dt::kMaxK || K > h->cfg.V) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: K must be in [0, min(32, V)]");
+  if (entries < 1 || entries > 0x7FFFFFFF) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: entries must be in [1, 2^31)");
+  *bytes = dt::logprob_workspace_bytes(h, entries, K);
+  return DT_OK;
+}
+
+int dt_token_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s) {
+  if (!h || !a) return fail(DT_ERR_ARG, "dt_token_logprobs: null argument");
+  const int rc = check_batch(h, "dt_token_logprobs", a->B);
+  if (rc != DT_OK) return rc;
+  if (!logits || !a->n_new || !a->workspace) return fail(DT_ERR_ARG, "dt_token_logprobs: null argument");
+  if (ld < h->cfg.V) return fail(DT_ERR_ARG, "dt_token_logprobs: ld < V");
+  if (a->P < 1 || (a->path && a->D_path < 1) || a->n_extra < 0 || (a->shift != 0 && a->shift != 1))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: P, D_path >= 1, n_extra >= 0, shift 0 or 1");
+  if (a->rows < 1 || a->rows > 0x7FFFFFFF || (!a->row_off && a->rows < (int64_t)a->B * a->P))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: rows must hold B * P rows and fit 31 bits");
+  const int64_t entries = a->path ? (int64_t)a->B * a->D_path : a->row_off ? a->rows : (int64_t)a->B * a->P;
+  if (a->n_out < entries) return fail(DT_ERR_ARG, "dt_token_logprobs: outputs hold fewer entries than the call has");
+  if (a->tokens && a->n_tokens < (a->row_off && !a->path ? 1 : (int64_t)a->B * a->P))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: tokens holds fewer than B * P entries");
+  if ((a->logp || a->rank) && !a->tokens && !a->last) return fail(DT_ERR_ARG, "dt_token_logprobs: logp and rank need tokens or last");
+  if (a->K < 0 || a->K > dt::kMaxK || a->K > h->cfg.V || (a->K > 0 && (!a->top_ids || !a->top_logp)))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: K must be in [0, min(32, V)], with top_ids and top_logp");
+  if (!aligned(logits, h->cfg.dtype == DT_BF16 ? 2 : 4)) return fail(DT_ERR_ARG, "dt_token_logprobs: logits not aligned to their element size");
+  if (!aligned(a->row_off, 4) || !aligned(a->path, 4) || !aligned(a->n_new, 4) || !aligned(a->tokens, 4) || !aligned(a->last, 4) ||
+      !aligned(a->logp, 4) || !aligned(a->entropy, 4) || !aligned(a->rank, 4) || !aligned(a->top_ids, 4) || !aligned(a->top_logp, 4))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: arrays must be 4-byte aligned");
+  if (!aligned(a->workspace, 256) || a->workspace_bytes < dt::logprob_workspace_bytes(h, entries, a->K))
+    return fail(DT_ERR_ARG, "dt_token_logprobs: workspace too small (dt_token_logprobs_workspace) or not 256-byte aligned");
+  if (dt::logprob_ctas(h, entries) > 0x7FFFFFFF) return fail(DT_ERR_ARG, "dt_token_logprobs: entries * V too large");
+  dt_logprob_args b = *a;
+  b.n_out = entries;
+  cudaError_t e = dt::launch_logprobs(h, logits, ld, &b, s);
+  if (e != cudaSuccess) return cuda_fail(e, "dt_token_logprobs");
   return DT_OK;
 }
 

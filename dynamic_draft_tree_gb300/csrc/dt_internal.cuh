@@ -93,6 +93,7 @@ struct Workspace {
   int32_t* bonus_counter;         // [B_max]
   int32_t* status;
   unsigned* ticket;      // arrivals of a page call's CTAs; zero between calls
+  int32_t* page_state;   // [B_max] between the launches of dt_kv_fork and of dt_kv_release_shared
   unsigned* attn_tickets;  // [num_sms] arrivals at split items of dt_tree_attention; zero between calls
 };
 
@@ -189,6 +190,11 @@ cudaError_t launch_commit_kv_paged(dt_handle* h, int B, const dt_kv_rows* kv, in
                                    const int32_t* path, int D_path, const int32_t* n_new, int n_extra,
                                    const int64_t* slots, int64_t n_slots, int S, const int32_t* slot_off,
                                    const int32_t* seq_len, int32_t* len_out, cudaStream_t s);
+cudaError_t launch_kv_fork(dt_handle* h, int B, const dt_block_pool* pool, int32_t* refs, const dt_kv_pages* kv, int n,
+                           const int32_t* src, const int32_t* dst, const int32_t* length, int32_t* seq_len, int shared_len,
+                           cudaStream_t s);
+cudaError_t launch_kv_release_shared(dt_handle* h, int B, const dt_block_pool* pool, int32_t* refs, const int32_t* keep_len,
+                                     cudaStream_t s);
 cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s);
 bool attn_line_fits(const dt_attn_args* a);  // places on the kernel's line of work are 32-bit
 int64_t attn_workspace_bytes(const dt_handle* h, int B, int P, int H_q, int H_kv, int D, int shared);
@@ -200,6 +206,9 @@ cudaError_t launch_logits(dt_handle* h, int B, const void* logits, int64_t ld, v
 cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int32_t* tokens, int64_t n_tokens, int P,
                                 const int32_t* row_off, const int32_t* path, int D_path, const int32_t* n_new,
                                 int n_extra, int prompt, cudaStream_t s);
+cudaError_t launch_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s);
+int64_t logprob_workspace_bytes(const dt_handle* h, int64_t entries, int K);
+int64_t logprob_ctas(const dt_handle* h, int64_t entries);
 cudaError_t launch_row_topk_static(const void* logits, int64_t ld, int rows, int V, int K, int dtype, float* logp,
                                    int32_t* ids, int32_t* status, cudaStream_t s);
 

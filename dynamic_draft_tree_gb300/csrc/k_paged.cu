@@ -10,16 +10,12 @@
 #include <algorithm>
 
 #include "dt_internal.cuh"
+#include "pages.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kPageThreads = 256;
 constexpr int kSlotsPerCta = 512;  // slots of one request that a CTA writes at a time: two independent chains a thread
-// Up to this many CTAs the last one changes the counts; more of them queue up at the ticket, and a second launch is
-// faster. Reserve + release, 64 requests of up to 8000 slots: 13.0 us with two launches each, 15.0 with the ticket;
-// 8 requests of 9 slots: 8.2 and 8.3 us on the device, but two launches take 3 us more on the host.
-constexpr int kTicketCtas = 64;
 
 
 struct ReserveArgs {
@@ -67,32 +63,6 @@ __device__ __forceinline__ Ask ask_of(const ReserveArgs& a, int b) {
   r.need = r.status ? 0 : (int32_t)max((int64_t)0, r.want - r.owned);
   return r;
 }
-
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* smem) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += (int64_t)shfl_xor_u64((uint64_t)v, m);
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t t = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += smem[w];
-  __syncthreads();
-  return t;
-}
-
-// True in every thread of the CTA that comes last: what the others read and wrote before is done.
-__device__ __forceinline__ bool comes_last(unsigned* ticket, unsigned ctas) {
-  __shared__ int last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicInc(ticket, ctas - 1) == ctas - 1;
-    __threadfence();
-  }
-  __syncthreads();
-  return last;
-}
-
-__device__ __forceinline__ int free_blocks(const dt_block_pool& p) { return min(max(p.free_count[0], 0), p.n_blocks); }
 
 // One CTA: owned counts of the requests that were served, and the free count.
 __device__ void reserve_counts(const ReserveArgs& a, int nfree) {
@@ -351,12 +321,6 @@ __global__ void __launch_bounds__(kPageThreads) commit_paged_kernel(PagedCommitA
     if (t0 != begin) __syncthreads();  // the addresses of the last turn have been used
     commit_rows(a, b, plane, first, (int)t0, (int)min((int64_t)a.tok_per_cta, n - t0), src_s, dst_s);
   }
-}
-
-int shift_of(int page) {
-  int s = 0;
-  while ((1 << s) < page) ++s;
-  return s;
 }
 
 }  // namespace

@@ -471,6 +471,41 @@ int dt_commit_kv_paged(dt_handle* h, int32_t B, const dt_kv_rows* kv, int32_t P,
                        const int64_t* slots, int64_t n_slots, int32_t S, const int32_t* slot_off,
                        const int32_t* seq_len, int32_t* len_out, cudaStream_t s);
 
+/* ---- Requests that continue others ------------------------------------------------------------------------------
+ * refs: device [n_blocks], caller-owned, zero for a new pool: owners of a block beyond its first. Reservations and commits
+ * need no counts; a pool with forks gives blocks back by dt_kv_release_shared, never by dt_kv_release. */
+/* The pages' memory: as dt_kv_rows, without the rows. */
+typedef struct {
+  void* cache;
+  int64_t cache_plane, cache_block, cache_tok, cache_head;
+  int32_t planes, heads;
+  int64_t head_bytes;
+} dt_kv_pages;
+
+/* Request dst[f] (a place that owns nothing) continues request src[f] behind its first length[f] tokens (length NULL:
+ * seq_len[src[f]], all of them), f < n: samples of one prompt, branches of a beam. It owns the whole pages with src[f] from
+ * then on (refs), and a page of its own that the other tokens (length mod page) of all planes are copied to; seq_len[dst[f]]
+ * becomes the length. src[f] goes on as it was, in its own last page.
+ * Blocks are taken from the end of the free list, forks in ascending order; one whose block, together with those that the forks
+ * before it need, is more than the list holds does nothing and sets DT_DEV_KV_FULL, as all further ones that need one do. A
+ * place outside [0, B), a destination that owns pages, that an earlier fork names too or that is any fork's source, or a length below
+ * shared_len or past what the source has, sets DT_DEV_BAD_PAGE and does nothing.
+ * shared_len: the first shared_len tokens are a prefix that every place owns (PagedCache.prefix; a multiple of page): dst owns
+ * exactly its blocks before, and they are counted nowhere.
+ * n <= B_max; strides, pointers and head_bytes multiples of 16, a plane's row at most 1 MB. */
+int dt_kv_fork(dt_handle* h, int32_t B, const dt_block_pool* pool, int32_t* refs, const dt_kv_pages* kv, int32_t n,
+               const int32_t* src, const int32_t* dst, const int32_t* length, int32_t* seq_len, int32_t shared_len,
+               cudaStream_t s);
+
+/* dt_kv_release for a pool with forks: every request gives back its blocks past the first ceil(keep_len[b] / page). A block that
+ * others own is theirs; one that all of its owners give back in this or earlier calls goes to the free list, at the place of the last
+ * of this call's givers in request order (the order of dt_kv_release, so that the forks and reservations that took blocks last are undone
+ * exactly). A keep_len inside a page that others go on owning sets DT_DEV_BAD_PAGE: the blocks behind it are given back, but the request
+ * must not append there (fork it at that length instead). The owners of a block have it at the same place of
+ * their tables, as forks and prefixes leave it. */
+int dt_kv_release_shared(dt_handle* h, int32_t B, const dt_block_pool* pool, int32_t* refs, const int32_t* keep_len,
+                         cudaStream_t s);
+
 /* Attention of the verify tree (EAGLE-2 page, the reranking step's ancestor-only mask): query position i of
  * request b attends to the request's seq_len[b] cached tokens (pages, through block_table) and to the tree
  * positions j < n_pos[b] with mask[b][i][j] != 0 (mask NULL: j <= i, a chain, so that P = 1 is a plain
@@ -593,6 +628,45 @@ typedef struct {
 } dt_logits_params;
 int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, void* out, int64_t ld_out,
                       const dt_logits_params* p, cudaStream_t s);
+
+/* Log probabilities under rows of logits (of the handle's type; the target's rows after dt_verify, or a prompt's): for
+ * entry j < n = n_new[b] + n_extra of request b, the row of its position (path ? path[b*D_path + j] : j) at element
+ * ((row_off ? row_off[b] : b*P) + position) * ld, and the token of entry j + shift, last[b] behind the last one:
+ *   path:   tokens[b*P + path[b*D_path + j + shift]], outputs [B][D_path] (a round: tokens = dt_tree_meta.tokens, path =
+ *           accept_path, n_new = accept_len, n_extra = 1, shift = 1, last = bonus give the answered tokens' log probabilities);
+ *   no path, row_off:  tokens[row_off[b] + j + shift], outputs at row_off[b] + j (prompts: shift = 1, last = the first answered
+ *           token; shift = 0: labels);
+ *   neither: tokens[b*P + j + shift], outputs [B][P].
+ * With m = max x, S = sum exp(x - m): logp = x_t - m - log S, entropy = log S + sum exp(x - m) (m - x) / S, rank = tokens with a
+ * larger logit, or an equal one and a lower id, top_ids and top_logp = the K largest logits' tokens (ties: lower id; logits of
+ * -inf are none: id -1, -inf). Any of logp, entropy, rank, last and (K = 0) top_ids and top_logp may be NULL, tokens too. Where no
+ * token is given (-1, or last NULL behind the last one) logp is NaN and rank -1; other ids outside [0, V) set
+ * DT_DEV_BAD_TOKEN and count as none. A row with NaN or +inf, or without a finite logit, sets DT_DEV_BAD_LOGITS: NaN, -1 and no
+ * alternatives. n past D_path, P or the request's rows, or a position outside [0, P) or the rows, sets DT_DEV_BAD_TREE and
+ * is left out. Outputs of no entry are left as they were. */
+typedef struct {
+  int32_t B, P;
+  int64_t rows;              /* rows of logits                                          */
+  const int32_t* row_off;    /* [B+1] or NULL                                           */
+  const int32_t* path;       /* [B][D_path] or NULL                                     */
+  int32_t D_path;
+  const int32_t* n_new;      /* [B]                                                     */
+  int32_t n_extra, shift;    /* shift: 0 or 1                                           */
+  const int32_t* tokens;
+  int64_t n_tokens;          /* entries of tokens                                       */
+  const int32_t* last;       /* [B] or NULL                                             */
+  int64_t n_out;             /* entries of the outputs: B*D_path, rows or B*P at least  */
+  float *logp, *entropy;
+  int32_t* rank;
+  int32_t K;                 /* 0..32, <= V                                             */
+  int32_t* top_ids;          /* [n_out][K]                                              */
+  float* top_logp;           /* [n_out][K]                                              */
+  void* workspace;           /* dt_token_logprobs_workspace bytes, 256-byte aligned, no initial value; used until the
+                                call has run (calls that may overlap need a workspace each) */
+  int64_t workspace_bytes;
+} dt_logprob_args;
+int dt_token_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s);
+int dt_token_logprobs_workspace(dt_handle* h, int64_t entries, int32_t K, int64_t* bytes);
 
 /* Standalone row log-softmax top-K that allocates nothing. This entry point has no counterpart in
  * the method's pages: it is the expansion's row pass (EAGLE-2 §扩展阶段: the children of a node
