@@ -100,7 +100,8 @@ class RoundRunner:
         self.prune_out = make_prune_out(width=self.width, stop=self.stop)
         self.verify_out = make_prune_out(m=self.m_dev)
 
-    def run(self, roots, draft_rows, target_rows, seed=0, rnd=0, M=None, n0=0, timing=None, kv=None, tokens=None):
+    def run(self, roots, draft_rows, target_rows, seed=0, rnd=0, M=None, n0=0, timing=None, kv=None, tokens=None,
+            logprobs=None):
         """Launch one round; returns nothing (outputs live in this object's tensors).
 
         ``timing`` (optional): an object with ``start(kind)`` and ``stop(kind)``; the composite
@@ -111,6 +112,8 @@ class RoundRunner:
         ``tokens`` (optional, paged.TokenState): the target rows get its penalties, biases and grammar words in
         place before they are verified, and the accepted tokens are counted afterwards (with ``kv``, those of
         requests whose rows found pages: one that did not, DT_DEV_KV_FULL, keeps its length and its history).
+        ``logprobs`` (optional, paged.TokenLogprobs): log probabilities of the accepted tokens and the bonus token under the
+        rows that were verified.
         ``kv`` (optional, paged.PagedCache, packed like the rows): the accepted positions' rows of kv.tmp, which
         ``target_rows`` fills, move into the pages after the verify. The tree's root stands behind the cached
         tokens: meta.position_ids are kv.seq_len + depth (without kv, self.pos_offset + depth).
@@ -222,6 +225,8 @@ class RoundRunner:
                       self.top8)
         if pol == "graft":
             dt_adj_update(h, M, self.meta, self.top8)
+        if logprobs is not None:
+            logprobs.round(logits, self.accept_len, self.accept_path, self.bonus, self.meta, self.packed)
         if kv is not None:
             kv.commit(self.accept_len, self.accept_path, self.meta)
         if tokens is not None:
