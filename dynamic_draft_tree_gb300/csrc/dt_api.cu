@@ -858,7 +858,7 @@ int dt_token_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_log
     return fail(DT_ERR_ARG, "dt_token_logprobs: arrays must be 4-byte aligned");
   if (!aligned(a->workspace, 256) || a->workspace_bytes < dt::logprob_workspace_bytes(h, entries, a->K))
     return fail(DT_ERR_ARG, "dt_token_logprobs: workspace too small (dt_token_logprobs_workspace) or not 256-byte aligned");
-  if (dt::logprob_ctas(h, entries) > 0x7FFFFFFF) return fail(DT_ERR_ARG, "dt_token_logprobs: entries * V too large");
+  if (dt::logprob_pieces(h, entries) > 0x7FFFFFFF) return fail(DT_ERR_ARG, "dt_token_logprobs: entries * V too large");
   dt_logprob_args b = *a;
   b.n_out = entries;
   cudaError_t e = dt::launch_logprobs(h, logits, ld, &b, s);

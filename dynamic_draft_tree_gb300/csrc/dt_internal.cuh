@@ -208,7 +208,7 @@ cudaError_t launch_count_tokens(dt_handle* h, int B, int32_t* counts, const int3
                                 int n_extra, int prompt, cudaStream_t s);
 cudaError_t launch_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s);
 int64_t logprob_workspace_bytes(const dt_handle* h, int64_t entries, int K);
-int64_t logprob_ctas(const dt_handle* h, int64_t entries);
+int64_t logprob_pieces(const dt_handle* h, int64_t entries);
 cudaError_t launch_row_topk_static(const void* logits, int64_t ld, int rows, int V, int K, int dtype, float* logp,
                                    int32_t* ids, int32_t* status, cudaStream_t s);
 

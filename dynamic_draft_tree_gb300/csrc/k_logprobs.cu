@@ -3,12 +3,16 @@
 // With m = max x, S = sum exp(x - m):  log p(t) = x_t - m - log S,  H = log S + (1 / S) sum exp(x - m) (m - x),
 // rank = tokens with a larger logit, or an equal one and a lower id.
 //
-// Every row is read once, in pieces of 8192 tokens that a CTA holds in registers: a maximum a warp, then sums relative to it
-// (sums of 32 terms a thread, then trees), and the count in front of the token. The K largest of a piece need no order over
-// it: the K-th largest of the maxima of 64 groups of four threads is no larger than the K-th largest token, so that a handful of tokens
-// reach it (about 24 for K = 20), which are ranked by counting. Pieces' results (24 to 280 bytes for 16 or 32 KB read) are put together by a
-// warp an entry in a second launch, in a fixed order.
-// Bound by DRAM in large calls.
+// Every row is read once. A warp takes a piece of a row, 1024 tokens at a time (32 a lane, the next 1024 on their way), and
+// shares nothing with other warps: sums a lane, relative to a reference that moves when a lane passes it by 2^8, the count in front
+// of the token, and the largest logit of every step. Pieces' sums are put together in a fixed order, a warp an entry. The K
+// alternatives are read again: the K-th largest of a row's steps' maxima is no larger than the K-th largest token, so that
+// only the steps that reach it are looked at (K of 126 for 128256 tokens, but for ties), a CTA an entry.
+// With lists of the K largest that every warp kept as it went, one alternative made 2048 rows of 128256 bf16 three times as long
+// (102 and 301 us), and CTAs of 256 threads that met four times in 8192 tokens were no faster (302 us with ranks).
+#include <cuda_bf16.h>
+#include <string.h>
+
 #include <algorithm>
 
 #include "dt_internal.cuh"
@@ -16,46 +20,42 @@
 namespace dt {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpPer = 32;                        // tokens of a thread
-constexpr int kLpPiece = kLpThreads * kLpPer;     // tokens of a CTA
-constexpr int kLpGroups = kLpThreads / 4;
-constexpr int kLpCand = 512;                      // candidates that are ranked by counting; more are taken one by one
-static_assert(kLpGroups >= kMaxK, "as many groups as alternatives");
+constexpr int kLpWarps = 4;
+constexpr int kLpThreads = 32 * kLpWarps;
+constexpr int kLpPer = 32;            // tokens of a lane at a time
+constexpr int kLpStep = 32 * kLpPer;  // tokens of a warp at a time
+constexpr int kLpMost = 8;            // steps of a piece, at most
+constexpr float kLpLazy = 8.0f;       // the reference moves when a lane passes it by 2^kLpLazy
+template <typename T>
+constexpr int kLpCtas = sizeof(T) == 2 ? 7 : 5;  // CTAs of an SM
 
 struct LpArgs {
   dt_logprob_args a;
   const void* logits;
   int64_t ld;
-  int32_t V, S, per;  // pieces of a row; entries of a request (path, padded)
+  int32_t V, per;     // entries of a request (path, padded)
+  uint32_t S, steps;  // pieces of a row, steps of a piece
   int64_t entries;
+  uint32_t all;       // pieces of all entries
+  int2* what;         // [entries] (row, token); row -1: none, token -1: none
   float4* sums;       // [entries][S] (m, s, t, count): t = sum e d, d = log2 e
-  uint64_t* keys;     // [entries][S][K], descending
+  float* tops;        // [entries][S * steps] largest logit of a step
   int32_t* status;
 };
 
-struct Entry {
-  bool used;
-  int64_t row;
-  int32_t token;  // -1: none
-};
-
-// What entry e is. Its request's counts are checked, and its positions; `report`: by whom.
-__device__ Entry entry_of(const LpArgs& p, int64_t e, bool report) {
+// What entry e is, after checks of its request's counts and its positions.
+__device__ __forceinline__ int2 entry_of(const LpArgs& p, int64_t e) {
   const dt_logprob_args& a = p.a;
-  Entry r{false, 0, -1};
+  const int2 none = make_int2(-1, -1);
   int b, j;
   const bool packed = !a.path && a.row_off;
-  if (packed) {  // the request whose rows hold e: 32 looks at once
-    const int lane = threadIdx.x & 31;
+  if (packed) {  // the request whose rows hold e
     int lo = 0, hi = a.B;  // row_off[lo] <= e < row_off[hi], if it is anybody's
-    if (e < a.row_off[0] || e >= a.row_off[a.B]) return r;
+    if (e < a.row_off[0] || e >= a.row_off[a.B]) return none;
     while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = min(hi, lo + (lane + 1) * step);
-      const uint32_t le = __ballot_sync(0xFFFFFFFFu, at < hi && a.row_off[at] <= e);
-      const int k = __popc(le);
-      hi = min(hi, lo + (k + 1) * step);
-      lo += k * step;
+      const int mid = (lo + hi) >> 1;
+      if (a.row_off[mid] <= e) lo = mid;
+      else hi = mid;
     }
     b = lo;
     j = (int)(e - a.row_off[b]);
@@ -67,45 +67,46 @@ __device__ Entry entry_of(const LpArgs& p, int64_t e, bool report) {
   const int64_t first = a.row_off ? (int64_t)a.row_off[b] : (int64_t)b * a.P;
   const int64_t room = packed ? (int64_t)a.row_off[b + 1] - first : p.per;
   if (n < 0 || n > room) {
-    if (report && j == 0) set_status(p.status, DT_DEV_BAD_TREE);
-    return r;
+    if (j == 0) set_status(p.status, DT_DEV_BAD_TREE);
+    return none;
   }
-  if (j >= n) return r;
-  int64_t pos = j;
+  if (j >= n) return none;
+  const int64_t k = (int64_t)j + a.shift;
+  int pos = j, next = -1;
   if (a.path) {
     pos = a.path[(int64_t)b * a.D_path + j];
+    if (k < n) next = a.path[(int64_t)b * a.D_path + k];
     if (pos < 0 || pos >= a.P) {
-      if (report) set_status(p.status, DT_DEV_BAD_TREE);
-      return r;
+      set_status(p.status, DT_DEV_BAD_TREE);
+      return none;
     }
   }
-  r.row = first + pos;
-  if (r.row < 0 || r.row >= a.rows) {
-    if (report) set_status(p.status, DT_DEV_BAD_TREE);
-    return r;
+  const int64_t row = first + pos;
+  if (row < 0 || row >= a.rows) {
+    set_status(p.status, DT_DEV_BAD_TREE);
+    return none;
   }
-  r.used = true;
-  if (a.tokens) {
-    const int64_t k = (int64_t)j + a.shift;
-    int64_t at = -1;
-    if (k < n) {
-      if (!a.path) at = first + k;
-      else {
-        const int next = a.path[(int64_t)b * a.D_path + k];
-        if (next >= 0 && next < a.P) at = (int64_t)b * a.P + next;
-        else if (report) set_status(p.status, DT_DEV_BAD_TREE);
-      }
-      if (at >= 0 && at < a.n_tokens) r.token = a.tokens[at];
-      else if (at >= 0 && report) set_status(p.status, DT_DEV_BAD_TREE);
-    } else if (a.last) {
-      r.token = a.last[b];
-    }
-    if (r.token < -1 || r.token >= p.V) {
-      if (report) set_status(p.status, DT_DEV_BAD_TOKEN);
-      r.token = -1;
-    }
+  int token = -1;
+  if (k >= n) {
+    if (a.last) token = a.last[b];
+  } else if (a.tokens) {
+    const int64_t at = !a.path ? first + k : next >= 0 && next < a.P ? (int64_t)b * a.P + next : -1;
+    if (at >= 0 && at < a.n_tokens) token = a.tokens[at];
+    else set_status(p.status, DT_DEV_BAD_TREE);
   }
-  return r;
+  if (token < -1 || token >= p.V) {
+    set_status(p.status, DT_DEV_BAD_TOKEN);
+    token = -1;
+  }
+  return make_int2((int)row, token);
+}
+
+// The entries' rows and tokens first: with the search for them in front of every piece, a piece's CTA waited for five loads
+// one after the other before its row's (2287 rows of 128256 bf16: 439 us).
+__global__ void __launch_bounds__(kLpThreads) logprob_entries_kernel(const __grid_constant__ LpArgs p) {
+  pdl_begin();
+  const int64_t e = (int64_t)blockIdx.x * kLpThreads + threadIdx.x;
+  if (e < p.entries) p.what[e] = entry_of(p, e);
 }
 
 template <typename T>
@@ -114,7 +115,7 @@ __device__ __forceinline__ float logit_at(const void* logits, int64_t at) {
   return __uint_as_float((uint32_t)((const uint16_t*)logits)[at] << 16);
 }
 
-// A thread's tokens: kVecs 16-byte vectors, kLpThreads apart.
+// A lane's tokens of a step: kVecs 16-byte vectors, 32 apart.
 template <typename T>
 struct Held {
   static constexpr int E = 16 / (int)sizeof(T), kVecs = kLpPer / E;
@@ -123,14 +124,14 @@ struct Held {
     if (sizeof(T) == 4) return __uint_as_float(w[i]);
     return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
   }
-  // v0: token of the piece's first place (negative in front of a row that does not start on 16 bytes). Vectors that lie in
+  // v0: token of the step's first place (negative in front of a row that does not start on 16 bytes). Vectors that lie in
   // the row are read whole, others token by token; places without a token get -inf.
-  __device__ __forceinline__ void load(const T* row, int64_t v0, int V) {
+  __device__ __forceinline__ void load(const T* row, int v0, int V) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const int64_t v = v0 + ((int64_t)u * kLpThreads + threadIdx.x) * E;
+      const int v = token(v0, u * E);
       uint4 q;
-      if (v >= 0 && v + E <= V) {
+      if (v >= 0 && v <= V - E) {
         q = __ldcs((const uint4*)(row + v));
       } else {
         uint32_t* x = &q.x;
@@ -151,181 +152,163 @@ struct Held {
       w[4 * u + 3] = q.w;
     }
   }
-  __device__ __forceinline__ static int64_t token(int64_t v0, int i) {  // of place i
-    return v0 + ((int64_t)(i / E) * kLpThreads + threadIdx.x) * E + i % E;
+  __device__ __forceinline__ static int token(int v0, int i) {  // of place i
+    return v0 + (i / E * 32 + (int)(threadIdx.x & 31)) * E + i % E;
   }
-};
-
-struct LpShared {
-  float m[kLpThreads / 32], s[kLpThreads / 32], t[kLpThreads / 32];
-  int cnt[kLpThreads / 32];
-  float group[kLpGroups];
-  float tau;
-  int n_cand;
-  uint64_t cand[kLpCand];
-  uint64_t best[kLpThreads / 32];
+  __device__ __forceinline__ float top() const {  // the largest; NaN is left out
+    if constexpr (sizeof(T) == 4) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kLpPer; i += 2) m = fmaxf(fmaxf(m, get(i)), get(i + 1));
+      return m;
+    } else {
+      uint32_t m = w[0];
+#pragma unroll
+      for (int i = 1; i < kLpPer / 2; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+      return fmaxf(fmaxf(-INFINITY, bf16_lo(m)), bf16_hi(m));
+    }
+  }
+  // Two tokens' logits, no smaller than about -1e37: a weight of zero times its distance is then zero, not NaN (NaN stays).
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      float2 r;
+      asm("max.NaN.f32 %0, %1, 0fFCF0BDC2;" : "=f"(r.x) : "f"(get(i)));
+      asm("max.NaN.f32 %0, %1, 0fFCF0BDC2;" : "=f"(r.y) : "f"(get(i + 1)));
+      return r;
+    } else {
+      uint32_t q;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(w[i >> 1]), "r"(0xFCF1FCF1u));
+      return make_float2(bf16_lo(q), bf16_hi(q));
+    }
+  }
+  // How many stand in front of a token with logit xt: larger ones, and equal ones with a lower id.
+  __device__ __forceinline__ int before(float xt, int token_, int v0) const {
+    const uint32_t x2 = (__float_as_uint(xt) >> 16) * 0x10001u;
+    uint32_t sum = 0;  // bf16: a pair of bf16, up to 16 each, exact
+    int cnt = 0;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int v = token(v0, u * E);
+      if (v + E <= token_) {
+        count<true>(u, xt, x2, cnt, sum);
+      } else {
+        count<false>(u, xt, x2, cnt, sum);
+        if (v <= token_) {  // the token's own vector
+#pragma unroll
+          for (int k = 0; k < E; ++k) cnt += get(u * E + k) == xt && v + k < token_ && v + k >= 0;
+        }
+      }
+    }
+    if (sizeof(T) == 2) cnt += (int)bf16_lo(sum) + (int)bf16_hi(sum);
+    // places in front of the row hold -inf
+    const int v = token(v0, 0);
+    if (v < 0 && xt == -INFINITY && v + E <= token_) cnt -= min(E, -v);
+    return cnt;
+  }
+  template <bool EQ>
+  __device__ __forceinline__ void count(int u, float xt, uint32_t x2, int& cnt, uint32_t& sum) const {
+#pragma unroll
+    for (int k = 0; k < E; k += 4 / (int)sizeof(T)) {
+      if constexpr (sizeof(T) == 4) {
+        const float y = get(u * E + k);
+        cnt += EQ ? y >= xt : y > xt;
+      } else {
+        __nv_bfloat162 x, y, n;
+        memcpy(&x, &w[(u * E + k) / 2], 4);
+        memcpy(&y, &x2, 4);
+        memcpy(&n, &sum, 4);
+        n = __hadd2(n, EQ ? __hge2(x, y) : __hgt2(x, y));
+        memcpy(&sum, &n, 4);
+      }
+    }
+  }
 };
 
 template <typename T, bool RANK, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) logprob_pieces_kernel(const __grid_constant__ LpArgs p) {
-  __shared__ LpShared sh;
+__global__ void __launch_bounds__(kLpThreads, kLpCtas<T>) logprob_pieces_kernel(const __grid_constant__ LpArgs p) {
   using H = Held<T>;
   pdl_begin();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t e = blockIdx.x / p.S;
-  const int piece = (int)(blockIdx.x - e * p.S);
-  const Entry en = entry_of(p, e, piece == 0 && tid == 0);
-  if (!en.used) return;
-  const T* row = (const T*)p.logits + en.row * p.ld;
-  const int64_t v0 = (int64_t)piece * kLpPiece - (int64_t)((uintptr_t)row % 16 / sizeof(T));
-  H x;
-  x.load(row, v0, p.V);
-  const float xt = RANK && en.token >= 0 ? logit_at<T>(row, en.token) : INFINITY;
-  // maxima: this thread's, its group's, its warp's
-  float mt = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kLpPer; i += 2) mt = fmaxf(fmaxf(mt, x.get(i)), x.get(i + 1));
-  const float mw = ord2f(__reduce_max_sync(0xFFFFFFFFu, f2ord(mt)));
-  if (TOP) {
-    float mg = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
-    mg = fmaxf(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, 2));
-    if ((tid & 3) == 0) sh.group[tid >> 2] = mg;
-    if (tid == 0) sh.n_cand = 0;
-  }
-  // sums relative to the warp's maximum; a weight of zero adds nothing to t, whatever its distance
-  const float off = mw == -INFINITY ? 0.0f : -mw * kLog2e;
-  const float2 c2 = make_float2(kLog2e, kLog2e), off2 = make_float2(off, off);
-  float2 s2 = make_float2(0.0f, 0.0f), t2 = make_float2(0.0f, 0.0f);
-  int cnt = 0;
-#pragma unroll
-  for (int i = 0; i < kLpPer; i += 2) {
-    const float2 d = __ffma2_rn(make_float2(x.get(i), x.get(i + 1)), c2, off2);
-    const float2 w = make_float2(ex2(d.x), ex2(d.y));
-    s2 = __fadd2_rn(s2, w);
-    t2 = __ffma2_rn(w, make_float2(fmaxf(d.x, -200.0f), fmaxf(d.y, -200.0f)), t2);
-  }
-  if (RANK) {
-#pragma unroll
-    for (int u = 0; u < H::kVecs; ++u) {
-      const int64_t v = H::token(v0, u * H::E);
-#pragma unroll
-      for (int k = 0; k < H::E; ++k) {
-        const float y = x.get(u * H::E + k);
-        cnt += y > xt || (y == xt && v + k < en.token && v + k >= 0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+  for (uint32_t at = blockIdx.x * kLpWarps + warp; at < p.all; at += gridDim.x * kLpWarps) {
+    const uint32_t e = at / p.S;
+    const int2 en = p.what[e];
+    if (en.x < 0) continue;
+    const T* row = (const T*)p.logits + (int64_t)en.x * p.ld;
+    int v0 = (int)(at - e * p.S) * (int)p.steps * kLpStep - (int)((uintptr_t)row % 16 / sizeof(T));
+    const int end = min(p.V, v0 + (int)p.steps * kLpStep);  // the piece's end
+    H x;
+    x.load(row, v0, p.V);
+    const float xt = RANK && en.y >= 0 ? logit_at<T>(row, en.y) : INFINITY;
+    float ref = -INFINITY, off = 0.0f;  // the reference, and minus it in log2 units
+    float2 s2 = make_float2(0.0f, 0.0f), t2 = make_float2(0.0f, 0.0f);
+    int cnt = 0;
+    float* tops = p.tops + (int64_t)at * p.steps;
+#pragma unroll 1
+    while (true) {
+      const int v1 = v0 + kLpStep;
+      H next;
+      if (v1 < end) next.load(row, v1, p.V);  // on its way while this one is worked on
+      const float mt = x.top();
+      if (TOP) {
+        const float top = ord2f(__reduce_max_sync(0xFFFFFFFFu, f2ord(mt)));
+        if (lane == 0) *tops = top;
+        ++tops;
       }
-    }
-  }
-  float s = s2.x + s2.y, t = t2.x + t2.y;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-  }
-  if (RANK) cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-  if (lane == 0) {
-    sh.m[warp] = mw;
-    sh.s[warp] = s;
-    sh.t[warp] = t;
-    sh.cnt[warp] = cnt;
-  }
-  __syncthreads();
-  if (tid == kLpThreads - 32) {  // one thread of a warp without candidates to rank
-    float M = -INFINITY, ss = 0.0f, tt = 0.0f;
-    int c = 0;
-#pragma unroll
-    for (int k = 0; k < kLpThreads / 32; ++k) M = fmaxf(M, sh.m[k]);
-#pragma unroll
-    for (int k = 0; k < kLpThreads / 32; ++k) {
-      const float d = sh.m[k] == -INFINITY ? 0.0f : (sh.m[k] - M) * kLog2e, f = ex2(d);
-      ss += sh.s[k] * f;
-      tt += (sh.t[k] + sh.s[k] * fmaxf(d, -1000.0f)) * f;
-      c += sh.cnt[k];
-    }
-    p.sums[e * p.S + piece] = make_float4(M, ss, tt, __int_as_float(c));
-  }
-  if constexpr (TOP) {
-    const int K = p.a.K;
-    // the K-th largest of the groups' maxima
-    if (tid < kLpGroups) {
-      const float g = sh.group[tid];
-      int before = 0;
-#pragma unroll 8
-      for (int k = 0; k < kLpGroups; ++k) {
-        const float o = sh.group[k];
-        before += o > g || (o == g && k < tid);
-      }
-      if (before == K - 1) sh.tau = g;
-    }
-    __syncthreads();
-    const float tau = sh.tau;
-    if (mt >= tau && mt > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < kLpPer; ++i) {
-        const float y = x.get(i);
-        if (y >= tau && y > -INFINITY) {
-          const int at = atomicAdd(&sh.n_cand, 1);
-          if (at < kLpCand) sh.cand[at] = make_key(y, (uint32_t)H::token(v0, i));
+      if (__any_sync(0xFFFFFFFFu, mt > ref && fmaf(mt, kLog2e, off) > (ref == -INFINITY ? -INFINITY : kLpLazy))) {
+        const float top = ord2f(__reduce_max_sync(0xFFFFFFFFu, f2ord(mt)));
+        if (ref != -INFINITY) {  // the sums so far move to the new reference
+          const float d = (ref - top) * kLog2e, f = ex2(d);
+          t2 = make_float2((t2.x + s2.x * d) * f, (t2.y + s2.y * d) * f);
+          s2 = make_float2(s2.x * f, s2.y * f);
         }
+        ref = top;
+        off = -top * kLog2e;
       }
-    }
-    __syncthreads();
-    uint64_t* out = p.keys + (e * p.S + piece) * K;
-    const int n = sh.n_cand;
-    if (n <= kLpCand) {
-      // the order in which candidates came does not matter: their ranks among each other are unique
-      for (int c = tid; c < n; c += kLpThreads) {
-        const uint64_t key = sh.cand[c];
-        int before = 0;
-        for (int k = 0; k < n; ++k) before += sh.cand[k] > key;
-        if (before < K) out[before] = key;
-      }
-      for (int k = n + tid; k < K; k += kLpThreads) out[k] = 0;
-    } else {  // many equal logits: the largest key below the last one, K times
-      uint64_t last = ~0ull;
-      for (int k = 0; k < K; ++k) {
-        uint64_t best = 0;
-        for (int i = 0; i < kLpPer; ++i) {
-          float y = 0.0f;
+      const float2 c2 = make_float2(kLog2e, kLog2e), off2 = make_float2(off, off);
 #pragma unroll
-          for (int q = 0; q < kLpPer; ++q)
-            if (q == i) y = x.get(q);
-          const uint64_t key = y > -INFINITY ? make_key(y, (uint32_t)H::token(v0, i)) : 0;
-          if (key < last && key > best) best = key;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) best = max(best, shfl_xor_u64(best, d));
-        if (lane == 0) sh.best[warp] = best;
-        __syncthreads();
-        for (int q = 0; q < kLpThreads / 32; ++q) best = max(best, sh.best[q]);
-        __syncthreads();
-        if (tid == 0) out[k] = best;
-        last = best;
+      for (int i = 0; i < kLpPer; i += 2) {
+        const float2 d = __ffma2_rn(x.pair(i), c2, off2);
+        const float2 w = make_float2(ex2(d.x), ex2(d.y));
+        s2 = __fadd2_rn(s2, w);
+        t2 = __ffma2_rn(w, d, t2);
       }
+      if (RANK) cnt += x.before(xt, en.y, v0);
+      if (v1 >= end) break;
+      x = next;
+      v0 = v1;
     }
+    float s = s2.x + s2.y, t = t2.x + t2.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+    }
+    if (RANK) cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+    if (lane == 0) p.sums[at] = make_float4(ref, s, t, __int_as_float(cnt));
   }
 }
 
-constexpr int kFinishWarps = 4;
-// A warp an entry: lanes take its pieces.
+// What a row's pieces add up to.
+struct Total {
+  float M;
+  double logS;
+  bool bad;
+};
+// One warp: lanes take entry e's pieces; writes its log probability, entropy and rank.
 template <typename T>
-__global__ void __launch_bounds__(32 * kFinishWarps) logprob_finish_kernel(const __grid_constant__ LpArgs p) {
-  __shared__ uint64_t top_s[kFinishWarps][kMaxK];
-  pdl_begin();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t e = (int64_t)blockIdx.x * kFinishWarps + warp;
-  if (e >= p.entries) return;
-  const Entry en = entry_of(p, e, false);
-  if (!en.used) return;
+__device__ __forceinline__ Total finish_entry(const LpArgs& p, int64_t e, int2 en) {
+  const int lane = threadIdx.x & 31;
   const dt_logprob_args& a = p.a;
   const float4* part = p.sums + e * p.S;
-  const float xt = en.token >= 0 ? logit_at<T>(p.logits, en.row * p.ld + en.token) : 0.0f;
+  const float xt = en.y >= 0 ? logit_at<T>(p.logits, (int64_t)en.x * p.ld + en.y) : 0.0f;
   float M = -INFINITY;
-  for (int k = lane; k < p.S; k += 32) M = fmaxf(M, part[k].x);
+  for (int k = lane; k < (int)p.S; k += 32) M = fmaxf(M, part[k].x);
   M = ord2f(__reduce_max_sync(0xFFFFFFFFu, f2ord(M)));
   // sums over pieces in 64 bits: the row's largest token alone is 1 of S, and what the others add may be small beside it
   double S = 0.0, T2 = 0.0;
   int cnt = 0;
-  for (int k = lane; k < p.S; k += 32) {
+  for (int k = lane; k < (int)p.S; k += 32) {
     const float4 q = part[k];
     const float d = q.x == -INFINITY ? 0.0f : (q.x - M) * kLog2e, f = exp2f(d);
     S += (double)(q.y * f);
@@ -346,65 +329,214 @@ __global__ void __launch_bounds__(32 * kFinishWarps) logprob_finish_kernel(const
   const double logS = bad ? __longlong_as_double(0x7FF8000000000000ll)
                           : (double)((int)(bits >> 52 & 0x7FF) - 1023) * 0.6931471805599453 + (double)logf((float)mant);
   if (lane == 0) {
-    const bool none = bad || en.token < 0;
+    const bool none = bad || en.y < 0;
     const float nan = __int_as_float(0x7FC00000);
     if (a.logp) a.logp[e] = none ? nan : (float)((double)xt - (double)M - logS);
     if (a.rank) a.rank[e] = none ? -1 : cnt;
     if (a.entropy) a.entropy[e] = bad ? nan : (float)(logS - 0.6931471805599453 * T2 / S);
   }
-  if (a.K == 0) return;
-  // 31 pieces' lists and the one of the pieces before them at a time: every lane shows its list's largest key
-  uint64_t* top = top_s[warp];
-  top[lane] = 0;
-  __syncwarp();
-  for (int k0 = 0; k0 < p.S; k0 += 31) {
-    const bool carry = lane == 31;
-    const bool mine = carry ? k0 > 0 : k0 + lane < p.S;
-    const uint64_t* list = carry ? top : p.keys + (e * p.S + min(k0 + lane, p.S - 1)) * a.K;
-    int at = 0;
-    uint64_t key = mine ? list[0] : 0, kept = 0;
-    for (int k = 0; k < a.K; ++k) {
-      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32));
-      const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
-      const uint64_t best = (uint64_t)hi << 32 | lo;
-      if (lane == k) kept = best;
-      if (best == 0) break;
-      if (key == best) key = ++at < a.K ? list[at] : 0;
+  return Total{M, logS, bad};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) logprob_finish_kernel(const __grid_constant__ LpArgs p) {
+  pdl_begin();
+  const int64_t e = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5);
+  if (e >= p.entries) return;
+  const int2 en = p.what[e];
+  if (en.x >= 0) finish_entry<T>(p, e, en);
+}
+
+constexpr int kTopWarps = 8;
+constexpr int kTopThreads = 32 * kTopWarps;
+constexpr int kTopSteps = 1024;  // steps whose maxima are ranked at once; with more, K times the largest below the last one
+constexpr int kTopCand = 512;    // candidates that are ranked by counting; with more, the same
+struct TopShared {
+  float tops[kTopSteps];
+  uint64_t cand[kTopCand], best[kTopWarps];
+  int n, n_steps;
+  int list[kTopSteps];
+  float tau;
+  Total total;
+};
+
+// The largest over the CTA.
+__device__ __forceinline__ uint64_t cta_max(uint64_t x, uint64_t* best) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = max(x, shfl_xor_u64(x, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) best[threadIdx.x >> 5] = x;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) x = max(x, best[w]);
+  return x;
+}
+
+// A CTA an entry: its sums, and its K alternatives.
+template <typename T>
+__global__ void __launch_bounds__(kTopThreads) logprob_top_kernel(const __grid_constant__ LpArgs p) {
+  __shared__ TopShared sh;
+  pdl_begin();
+  const int64_t e = blockIdx.x;
+  const int2 en = p.what[e];
+  if (en.x < 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = p.a.K;
+  const T* row = (const T*)p.logits + (int64_t)en.x * p.ld;
+  const int first = -(int)((uintptr_t)row % 16 / sizeof(T));  // token of the row's first place
+  const int steps = (p.V - first + kLpStep - 1) / kLpStep;
+  const float* tops = p.tops + e * p.S * p.steps;
+  const bool few = steps <= kTopSteps;
+  if (tid == 0) sh.n = sh.n_steps = 0;
+  float tau = -INFINITY;  // of at most K steps: all of them
+  if (few)
+    for (int k = tid; k < steps; k += kTopThreads) sh.tops[k] = tops[k];
+  if (tid == 0) sh.tau = -INFINITY;
+  __syncthreads();
+  if (warp == kTopWarps - 1) {
+    const Total total = finish_entry<T>(p, e, en);
+    if (lane == 0) sh.total = total;
+  } else if (few && steps > K) {
+    for (int s = tid; s < steps; s += kTopThreads - 32) {
+      const float x = sh.tops[s];
+      int before = 0;
+#pragma unroll 8
+      for (int k = 0; k < steps; ++k) {
+        const float o = sh.tops[k];
+        before += o > x || (o == x && k < s);
+      }
+      if (before == K - 1) sh.tau = x;
     }
-    __syncwarp();
-    top[lane] = kept;
-    __syncwarp();
   }
-  if (lane < a.K) {
-    const uint64_t key = bad ? 0 : top[lane];
-    a.top_ids[e * a.K + lane] = key ? (int32_t)key_id(key) : -1;
-    a.top_logp[e * a.K + lane] = key ? (float)((double)key_value(key) - (double)M - logS) : -INFINITY;
+  __syncthreads();
+  if (sh.total.bad) {
+    for (int k = tid; k < K; k += kTopThreads) {
+      p.a.top_ids[e * K + k] = -1;
+      p.a.top_logp[e * K + k] = -INFINITY;
+    }
+    return;
+  }
+  if (few) {
+    tau = sh.tau;
+  } else {
+    uint64_t last = ~0ull;
+    for (int k = 0; k < K; ++k) {
+      uint64_t best = 0;
+      for (int s = tid; s < steps; s += kTopThreads) {
+        const uint64_t key = make_key(tops[s], (uint32_t)s);
+        if (key < last && key > best) best = key;
+      }
+      last = cta_max(best, sh.best);
+    }
+    tau = key_value(last);
+  }
+  // tokens that reach it, of the steps that do
+  using H = Held<T>;
+  auto add = [&](int s) {
+    H x;
+    const int v0 = first + s * kLpStep;
+    x.load(row, v0, p.V);
+#pragma unroll
+    for (int i = 0; i < kLpPer; ++i) {
+      const float y = x.get(i);
+      if (y >= tau && y > -INFINITY) {
+        const int c = atomicAdd(&sh.n, 1);
+        if (c < kTopCand) sh.cand[c] = make_key(y, (uint32_t)H::token(v0, i));
+      }
+    }
+  };
+  if (few) {
+    for (int s = tid; s < steps; s += kTopThreads)
+      if (sh.tops[s] >= tau) sh.list[atomicAdd(&sh.n_steps, 1)] = s;
+    __syncthreads();
+    for (int k = warp; k < sh.n_steps; k += kTopWarps) add(sh.list[k]);
+  } else {
+    for (int s = warp; s < steps; s += kTopWarps)
+      if (tops[s] >= tau) add(s);
+  }
+  __syncthreads();
+  auto put = [&](int k, uint64_t key) {
+    p.a.top_ids[e * K + k] = key ? (int32_t)key_id(key) : -1;
+    p.a.top_logp[e * K + k] = key ? (float)((double)key_value(key) - (double)sh.total.M - sh.total.logS) : -INFINITY;
+  };
+  const int n = sh.n;
+  if (n <= kTopCand) {
+    // the order in which candidates came does not matter: their ranks among each other are unique
+    for (int c = tid; c < n; c += kTopThreads) {
+      const uint64_t key = sh.cand[c];
+      int before = 0;
+      for (int k = 0; k < n; ++k) before += sh.cand[k] > key;
+      if (before < K) put(before, key);
+    }
+    for (int k = n + tid; k < K; k += kTopThreads) put(k, 0);
+  } else {  // many equal logits: the largest key below the last one, K times
+    uint64_t last = ~0ull;
+    for (int k = 0; k < K; ++k) {
+      uint64_t best = 0;
+      for (int v = tid; v < p.V; v += kTopThreads) {
+        const float y = logit_at<T>(row, v);
+        const uint64_t key = y >= tau && y > -INFINITY ? make_key(y, (uint32_t)v) : 0;
+        if (key < last && key > best) best = key;
+      }
+      last = cta_max(best, sh.best);
+      if (tid == 0) put(k, last);
+    }
   }
 }
 
-int pieces_of(int V, int dtype) { return (int)(((int64_t)V + (dtype == DT_BF16 ? 7 : 3) + kLpPiece - 1) / kLpPiece); }
+// Steps of a piece and pieces of a row: as many pieces as warps are resident, of one to kLpMost steps.
+void split_of(const dt_handle* h, int64_t entries, int& steps, int64_t& S) {
+  const int64_t most = ((int64_t)h->cfg.V + (h->cfg.dtype == DT_BF16 ? 7 : 3) + kLpStep - 1) / kLpStep;
+  const int64_t warps = (int64_t)h->num_sms * kLpWarps * (h->cfg.dtype == DT_BF16 ? kLpCtas<uint16_t> : kLpCtas<float>);
+  steps = (int)std::max<int64_t>(1, std::min<int64_t>(kLpMost, most * entries / warps));
+  S = (most + steps - 1) / steps;
+}
 
 template <typename T>
-cudaError_t launch_t(const LpArgs& p, cudaStream_t s) {
-  const dim3 grid((unsigned)(p.entries * p.S)), block(kLpThreads);
+cudaError_t launch_t(const LpArgs& p, int num_sms, cudaStream_t s) {
+  const dim3 block(kLpThreads);
+  launch_k(logprob_entries_kernel, dim3((unsigned)((p.entries + kLpThreads - 1) / kLpThreads)), block, 0, s, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(std::min<uint32_t>((p.all + kLpWarps - 1) / kLpWarps, (uint32_t)num_sms * kLpCtas<T>));  // as many as are resident
   if (p.a.rank)
     p.a.K ? launch_k(logprob_pieces_kernel<T, true, true>, grid, block, 0, s, p) : launch_k(logprob_pieces_kernel<T, true, false>, grid, block, 0, s, p);
   else
     p.a.K ? launch_k(logprob_pieces_kernel<T, false, true>, grid, block, 0, s, p) : launch_k(logprob_pieces_kernel<T, false, false>, grid, block, 0, s, p);
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  launch_k(logprob_finish_kernel<T>, dim3((unsigned)((p.entries + kFinishWarps - 1) / kFinishWarps)), dim3(32 * kFinishWarps), 0, s, p);
+  if (p.a.K)
+    launch_k(logprob_top_kernel<T>, dim3((unsigned)p.entries), dim3(kTopThreads), 0, s, p);
+  else
+    launch_k(logprob_finish_kernel<T>, dim3((unsigned)((p.entries + kLpWarps - 1) / kLpWarps)), block, 0, s, p);
   return cudaGetLastError();
+}
+
+struct LpLayout {
+  int64_t sums, tops, total;
+};
+LpLayout layout_of(const dt_handle* h, int64_t entries, int K) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  int steps;
+  int64_t S;
+  split_of(h, entries, steps, S);
+  const int64_t n = entries * S;
+  LpLayout L;
+  L.sums = up(8 * entries);
+  L.tops = up(L.sums + 16 * n);
+  L.total = L.tops + (K ? 4 * n * steps : 0);
+  return L;
 }
 
 }  // namespace
 
-int64_t logprob_ctas(const dt_handle* h, int64_t entries) { return entries * pieces_of(h->cfg.V, h->cfg.dtype); }
-
-int64_t logprob_workspace_bytes(const dt_handle* h, int64_t entries, int K) {
-  const int64_t n = entries * pieces_of(h->cfg.V, h->cfg.dtype);
-  return (16 * n + 255) / 256 * 256 + 8 * n * K;
+int64_t logprob_pieces(const dt_handle* h, int64_t entries) {
+  int steps;
+  int64_t S;
+  split_of(h, entries, steps, S);
+  return entries * S;
 }
+
+int64_t logprob_workspace_bytes(const dt_handle* h, int64_t entries, int K) { return layout_of(h, entries, K).total; }
 
 cudaError_t launch_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s) {
   LpArgs p{};
@@ -412,13 +544,20 @@ cudaError_t launch_logprobs(dt_handle* h, const void* logits, int64_t ld, const 
   p.logits = logits;
   p.ld = ld;
   p.V = h->cfg.V;
-  p.S = pieces_of(h->cfg.V, h->cfg.dtype);
   p.per = a->path ? a->D_path : a->P;
   p.entries = a->n_out;
-  p.sums = (float4*)a->workspace;
-  p.keys = (uint64_t*)((char*)a->workspace + (16 * p.entries * p.S + 255) / 256 * 256);
+  int steps;
+  int64_t S;
+  split_of(h, p.entries, steps, S);
+  p.steps = (uint32_t)steps;
+  p.S = (uint32_t)S;
+  p.all = (uint32_t)(p.entries * S);
+  const LpLayout L = layout_of(h, p.entries, a->K);
+  p.what = (int2*)a->workspace;
+  p.sums = (float4*)((char*)a->workspace + L.sums);
+  p.tops = (float*)((char*)a->workspace + L.tops);
   p.status = h->ws.status;
-  return h->cfg.dtype == DT_BF16 ? launch_t<uint16_t>(p, s) : launch_t<float>(p, s);
+  return h->cfg.dtype == DT_BF16 ? launch_t<uint16_t>(p, h->num_sms, s) : launch_t<float>(p, h->num_sms, s);
 }
 
 }  // namespace dt
