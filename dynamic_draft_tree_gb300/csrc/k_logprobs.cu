@@ -27,7 +27,7 @@ constexpr int kLpStep = 32 * kLpPer;  // tokens of a warp at a time
 constexpr int kLpMost = 8;            // steps of a piece, at most
 constexpr float kLpLazy = 8.0f;       // the reference moves when a lane passes it by 2^kLpLazy
 template <typename T>
-constexpr int kLpCtas = sizeof(T) == 2 ? 7 : 5;  // CTAs of an SM
+constexpr int kLpCtas = sizeof(T) == 2 ? 8 : 4;  // CTAs of an SM
 
 struct LpArgs {
   dt_logprob_args a;
@@ -37,6 +37,7 @@ struct LpArgs {
   uint32_t S, steps;  // pieces of a row, steps of a piece
   int64_t entries;
   uint32_t all;       // pieces of all entries
+  bool direct;        // the pieces' warps look their entry up
   int2* what;         // [entries] (row, token); row -1: none, token -1: none
   float4* sums;       // [entries][S] (m, s, t, count): t = sum e d, d = log2 e
   float* tops;        // [entries][S * steps] largest logit of a step
@@ -101,7 +102,7 @@ __device__ __forceinline__ int2 entry_of(const LpArgs& p, int64_t e) {
   return make_int2((int)row, token);
 }
 
-// The entries' rows and tokens first: with the search for them in front of every piece, a piece's CTA waited for five loads
+// The entries' rows and tokens first where a warp takes many pieces: with the search for them in front of every piece, a piece's CTA waited for five loads
 // one after the other before its row's (2287 rows of 128256 bf16: 439 us).
 __global__ void __launch_bounds__(kLpThreads) logprob_entries_kernel(const __grid_constant__ LpArgs p) {
   pdl_begin();
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<T>) logprob_pieces_kernel(
 #pragma unroll 1
   for (uint32_t at = blockIdx.x * kLpWarps + warp; at < p.all; at += gridDim.x * kLpWarps) {
     const uint32_t e = at / p.S;
-    const int2 en = p.what[e];
+    const int2 en = p.direct ? entry_of(p, e) : p.what[e];
+    if (p.direct && at == e * p.S && lane == 0) p.what[e] = en;
     if (en.x < 0) continue;
     const T* row = (const T*)p.logits + (int64_t)en.x * p.ld;
     int v0 = (int)(at - e * p.S) * (int)p.steps * kLpStep - (int)((uintptr_t)row % 16 / sizeof(T));
@@ -494,9 +496,12 @@ void split_of(const dt_handle* h, int64_t entries, int& steps, int64_t& S) {
 template <typename T>
 cudaError_t launch_t(const LpArgs& p, int num_sms, cudaStream_t s) {
   const dim3 block(kLpThreads);
-  launch_k(logprob_entries_kernel, dim3((unsigned)((p.entries + kLpThreads - 1) / kLpThreads)), block, 0, s, p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!p.direct) {
+    launch_k(logprob_entries_kernel, dim3((unsigned)((p.entries + kLpThreads - 1) / kLpThreads)), block, 0, s, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const dim3 grid(std::min<uint32_t>((p.all + kLpWarps - 1) / kLpWarps, (uint32_t)num_sms * kLpCtas<T>));  // as many as are resident
   if (p.a.rank)
     p.a.K ? launch_k(logprob_pieces_kernel<T, true, true>, grid, block, 0, s, p) : launch_k(logprob_pieces_kernel<T, true, false>, grid, block, 0, s, p);
@@ -552,6 +557,8 @@ cudaError_t launch_logprobs(dt_handle* h, const void* logits, int64_t ld, const 
   p.steps = (uint32_t)steps;
   p.S = (uint32_t)S;
   p.all = (uint32_t)(p.entries * S);
+  // one piece a warp: the look-up instead of a launch (a search among many packed requests would be the longer way)
+  p.direct = steps == 1 && (a->path || !a->row_off || a->B <= 16);
   const LpLayout L = layout_of(h, p.entries, a->K);
   p.what = (int2*)a->workspace;
   p.sums = (float4*)((char*)a->workspace + L.sums);
