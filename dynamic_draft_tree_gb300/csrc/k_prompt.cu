@@ -36,10 +36,11 @@ constexpr int kPromptThreads = 384;
 constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes it by 2^kLazy
 constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
                                 // small ones stay normal in fp16 for longer; it cancels in the quotient
-// Units of the line: a tile takes three for two groups of rows and two for one; an item has kItemUnits more in front for
-// its ends. Tile t of an item at unit u starts at u + kItemUnits + t * units of a tile, and belongs to the CTA that unit
-// falls to.
-constexpr int kItemUnits = 3;
+// Units of the line: a tile, for one group of rows (whose chain of softmax and products takes as long) as for two; an item has
+// kItemUnits more in front for its ends. Tile t of an item at unit u is at u + kItemUnits + t, and belongs to the CTA that
+// this falls to. With two thirds of a unit for a tile of one group and one for an item 16 prompts of up to 2000 tokens took
+// 210 us instead of 195, prompts among single tokens (32 requests) 46 instead of 44; with three units for an item 206 and 45.
+constexpr int kItemUnits = 2;
 
 // An item that is cut: left by its first CTA for the join.
 struct Cut {
@@ -57,7 +58,7 @@ struct PromptParams {
   float c;              // scale * log2 e
   int32_t period, step; // w / 128 = step / period in lowest terms, period a power of two
   int32_t period_shift;
-  int32_t min_per;      // least units of a CTA
+  int32_t whole;        // no item is cut: a CTA takes those that begin in its run
   uint16_t part[128];   // part[r] = sum of ceil(k step / period), k = 1 .. r < period
   int32_t part_all;     // the same up to r = period
   Cut* cuts;            // [CTAs]
@@ -100,19 +101,17 @@ __device__ __forceinline__ int64_t new_tiles(const PromptParams& p, int m) {
 
 // Items of a request and key head.
 struct Extent {
-  int items, ct;      // items; tiles of cached tokens
-  int64_t head;       // units of a key head
-  int last_tw;        // units of a tile of the last item
+  int items, ct;  // items; tiles of cached tokens
+  int64_t head;   // units of a key head
 };
 __device__ __forceinline__ int64_t units_before(const PromptParams& p, int ct, int i) {  // of items 0 .. i - 1, not the last
-  return (int64_t)i * kItemUnits + 3 * ((int64_t)i * ct + new_tiles(p, i));
+  return (int64_t)i * (kItemUnits + ct) + new_tiles(p, i);
 }
 __device__ __forceinline__ Extent extent_of(const PromptParams& p, const Request& r) {
   Extent e;
   e.items = (r.n + p.w - 1) / p.w;
   e.ct = (r.len + kTile - 1) / kTile;
-  e.last_tw = r.n - (e.items - 1) * p.w > p.pos ? 3 : 2;
-  e.head = r.n > 0 ? units_before(p, e.ct, e.items - 1) + kItemUnits + (int64_t)e.last_tw * (e.ct + (r.n + kTile - 1) / kTile) : 0;
+  e.head = r.n > 0 ? units_before(p, e.ct, e.items - 1) + kItemUnits + e.ct + (r.n + kTile - 1) / kTile : 0;
   return e;
 }
 
@@ -177,13 +176,11 @@ struct Walk {
       s.rows = (s.iend - s.i0) * p.G;
       s.tiles0 = e.ct + (min(s.iend, s.i0 + p.pos) + kTile - 1) / kTile;
       s.tt = e.ct + (s.iend + kTile - 1) / kTile;
-      const bool dual = s.iend - s.i0 > p.pos;
-      s.tiles1 = dual ? s.tt : 0;
-      const int tw = dual ? 3 : 2;
-      const int units = kItemUnits + tw * s.tt, end = (int)min((int64_t)units, z + pl.x1 - x);
-      s.t0 = (max(0, z - kItemUnits) + tw - 1) / tw;
-      s.t1 = (max(0, end - kItemUnits) + tw - 1) / tw;
-      s.next_u = x - z + kItemUnits + (int64_t)s.t1 * tw;
+      s.tiles1 = s.iend - s.i0 > p.pos ? s.tt : 0;
+      const int units = kItemUnits + s.tt, end = p.whole ? units : (int)min((int64_t)units, z + pl.x1 - x);
+      s.t0 = max(0, z - kItemUnits);
+      s.t1 = p.whole && z > 0 ? s.t0 : max(0, end - kItemUnits);  // (one that begins in the run before)
+      s.next_u = x - z + kItemUnits + s.t1;
       x += end - z;
       z = end;
       if (end == units) {
@@ -210,12 +207,9 @@ struct Walk {
   }
 };
 
-// CTAs with tiles of an item that is cut behind this, its first segment: the last tile begins this many units behind the
-// CTA's run.
+// CTAs with tiles of an item that is cut behind this, its first segment.
 __device__ __forceinline__ int parts_of(const Plan& pl, const Segment& s) {
-  const int tw = s.tiles1 ? 3 : 2;
-  // the first tile that is not this CTA's begins in front of unit x1 + tw
-  const int over = (int)(s.next_u - pl.x1) + (s.tt - 1 - s.t1) * tw;
+  const int over = (int)(s.next_u - pl.x1) + s.tt - 1 - s.t1;  // from the first unit behind the run to the last tile
   return 2 + over / pl.per;
 }
 
@@ -341,8 +335,8 @@ __device__ __forceinline__ void make_plan(const PromptParams& p, Shared& sh) {
     if (w < warp) t_b += o;
     total += o;
   }
-  // at least a tile's units: no CTA between an item's first and last one is without a tile
-  const int64_t per = max((int64_t)p.min_per, (total + (int64_t)gridDim.x - 1) / (int64_t)gridDim.x);
+  // at least one: no CTA between an item's first and last one is without a tile
+  const int64_t per = max((int64_t)1, (total + (int64_t)gridDim.x - 1) / (int64_t)gridDim.x);
   const int64_t x0 = min(total, per * (int64_t)blockIdx.x), x1 = min(total, x0 + per);
   if (tid == 0) {
     sh.plan.x0 = x0;
@@ -1099,7 +1093,6 @@ void shape_params(PromptParams& p) {
     if (r < p.period) p.part[r] = (uint16_t)sum;
     p.part_all = sum;
   }
-  p.min_per = 3;
 }
 
 struct Layout {
@@ -1114,11 +1107,15 @@ Layout layout_of(const dt_handle* h, int D) {
   return L;
 }
 
+// Items of few tiles are not cut: a launch to join them costs more than an uneven share. One prompt, 8 x 4 heads of 128, cut
+// and whole: 93 tokens 13.0 and 9.7 us, 512 17.2 and 14.4, 1024 24.0 and 20.7, 1500 32.0 and 32.1, 2000 42.1 and 50.8.
+constexpr int kWholeTiles = 8;
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const PromptParams& p, const CUtensorMap* m, cudaStream_t s) {
   launch_k(prompt_kernel<DP, BF16>, dim3(h->num_sms), dim3(kPromptThreads), kSmemBytes<DP>, s, p, m[0], m[1], m[2], m[3], m[4], m[5]);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (p.whole) return e;
   launch_k(join_kernel<BF16>, dim3(h->num_sms, (p.rows2 + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinWarps), 0, s, p);
   return cudaGetLastError();
 }
@@ -1141,7 +1138,7 @@ cudaError_t init_prompt_attributes() {
 bool prompt_line_fits(const dt_handle* h, const dt_prompt_args* a) {
   const int w = 2 * (kTile / (a->H_q / a->H_kv));
   const double tiles = (double)(a->seq_len ? (double)a->max_blocks * a->page / kTile : 0.0) + (double)a->rows / kTile + 2;
-  return (double)a->H_kv * ((double)a->rows / w + a->B) * (kItemUnits + 3 * tiles) < 2.0e9 * h->num_sms;
+  return (double)a->H_kv * ((double)a->rows / w + a->B) * (kItemUnits + tiles) < 2.0e9 * h->num_sms;
 }
 
 int64_t prompt_workspace_bytes(const dt_handle* h, int D) { return layout_of(h, D).total; }
@@ -1153,6 +1150,9 @@ cudaError_t launch_prompt(dt_handle* h, const dt_prompt_args* a, cudaStream_t s)
   if (!cached) p.a.page = kTile;
   shape_params(p);
   p.c = a->scale * kLog2e;
+  // tiles of an item, at most
+  const int64_t most = (cached ? ((int64_t)a->max_blocks * a->page + kTile - 1) / kTile : 0) + (a->rows + kTile - 1) / kTile;
+  p.whole = most <= kWholeTiles;
   const Layout L = layout_of(h, a->D);
   char* ws = (char*)a->workspace;
   p.cuts = (Cut*)ws;

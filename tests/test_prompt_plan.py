@@ -48,14 +48,15 @@ static int rnd(int n) {
   seed_ = seed_ * 1664525u + 1013904223u;
   return (int)((seed_ >> 8) % (uint32_t)n);
 }
-static int check(int G, int H_kv, int B, int most_n, int most_len, int ctas) {
+static int check(int G, int H_kv, int B, int most_n, int most_len, int ctas, bool whole = false) {
   std::vector<int32_t> off(B + 1, 0), len(B, 0);
   for (int b = 0; b < B; ++b) {
     const int kind = rnd(4);
     off[b + 1] = off[b] + (kind == 0 ? 0 : kind == 1 ? 1 : rnd(most_n + 1));
     len[b] = rnd(3) ? rnd(most_len + 1) : 0;
   }
-  const PromptParams p = params_for(G, H_kv, B, 16, most_len / 16 + 1, off.data(), len.data());
+  PromptParams p = params_for(G, H_kv, B, 16, most_len / 16 + 1, off.data(), len.data());
+  p.whole = whole;
   int bad = 0;
   int64_t total = 0;
   std::vector<int64_t> before(B + 1, 0);
@@ -67,13 +68,13 @@ static int check(int G, int H_kv, int B, int most_n, int most_len, int ctas) {
     for (int i = 0; i * p.w < r.n; ++i) {
       bad += units_before(p, e.ct, i) != units;
       const int end = std::min(r.n, (i + 1) * p.w), t = e.ct + (end + 127) / 128;
-      units += kItemUnits + (int64_t)(end - i * p.w > p.pos ? 3 : 2) * t;
+      units += kItemUnits + t;
     }
     bad += e.head != units;
     before[b + 1] = before[b] + H_kv * e.head;
   }
   total = before[B];
-  const int64_t per = std::max<int64_t>(p.min_per, (total + ctas - 1) / ctas);
+  const int64_t per = std::max<int64_t>(1, (total + ctas - 1) / ctas);
   std::map<std::tuple<int, int, int>, std::vector<std::array<int, 3>>> got;  // item -> (t0, t1, CTA), in order
   std::map<std::tuple<int, int, int>, Segment> first;
   std::map<std::tuple<int, int, int>, int> parts;
@@ -99,6 +100,7 @@ static int check(int G, int H_kv, int B, int most_n, int most_len, int ctas) {
       got[key].push_back({s.t0, s.t1, c});
       cuts += s.t0 == 0 && s.t1 < s.tt;
       firsts += s.t0 > 0;
+      bad += whole && (s.t0 != 0 || s.t1 != s.tt);
       bad += s.t0 > 0 && k > 0;  // only a CTA's first segment goes on with another CTA's item
       if (s.t0 == 0 && s.t1 < s.tt) parts[key] = parts_of(pl, s);
       bad += s.rows != (s.iend - s.i0) * G || s.rows > kItemRows || s.iend > off[s.b + 1] - off[s.b];
@@ -180,8 +182,8 @@ int main() {
   const int groups[] = {1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 31, 32, 64, 65, 128};
   for (int G : groups) {
     for (int k = 0; k < 30; ++k)
-      bad += dt::check(G, 1 + dt::rnd(5), 1 + dt::rnd(12), 1 + dt::rnd(700), dt::rnd(900), k % 3 ? 152 : 1 + dt::rnd(20));
-    bad += dt::check(G, 2, 400, 3, 300, 152);
+      bad += dt::check(G, 1 + dt::rnd(5), 1 + dt::rnd(12), 1 + dt::rnd(700), dt::rnd(900), k % 3 ? 152 : 1 + dt::rnd(20), k % 5 == 0);
+    bad += dt::check(G, 2, 400, 3, 300, 152) + dt::check(G, 3, 40, 9, 0, 152, true) + dt::check(G, 1, 1, 300, 0, 152, true);
     bad += dt::check(G, 1, 2, 20000, 20000, 152);
   }
   bad += dt::all<64>() + dt::all<128>();
