@@ -71,7 +71,8 @@ enum {
   DT_DEV_TIMEOUT = 8,      /* a bounded wait on an asynchronous copy ran out                   */
   DT_DEV_INTERNAL = 16,    /* an internal iteration bound was hit                              */
   DT_DEV_KV_FULL = 32,     /* dt_commit_kv: a request's rows would pass the cache's capacity;
-                              dt_kv_reserve, dt_commit_kv_paged: no pages for a request's tokens */
+                              dt_kv_reserve, dt_commit_kv_paged: no pages for a request's tokens;
+                              dt_kv_fork: no page for a fork's last tokens */
   DT_DEV_BAD_PAGE = 64     /* a block id, slot, length or row offset outside its pool or buffer  */
 };
 /* dt_config.flags */
@@ -79,8 +80,9 @@ enum { DT_FLAG_TEST_TIMEOUT = 1 }; /* test only: the expansion row scans (dt_exp
                                       calls built on it, dt_block_expand) give their first bounded
                                       copy wait a limit of zero, so it runs out; the verify streaming
                                       pass behaves as if its reads had timed out (reads nothing);
-                                      dt_tree_attention gives up every wait that is not over at
-                                      once, after its copies in flight have landed.
+                                      dt_tree_attention and dt_prompt_attention give up every wait
+                                      that is not over at once, after their copies in flight have
+                                      landed.
                                       Either way empty results and DT_DEV_TIMEOUT, no fault */
 enum { DT_FLAG_TEST_ARRIVED = 2 }; /* test only: dt_create leaves one arrival at every split item of
                                       dt_tree_attention, as a call that gave up may; dt_clear_status
@@ -488,8 +490,8 @@ typedef struct {
  * becomes the length. src[f] goes on as it was, in its own last page.
  * Blocks are taken from the end of the free list, forks in ascending order; one whose block, together with those that the forks
  * before it need, is more than the list holds does nothing and sets DT_DEV_KV_FULL, as all further ones that need one do. A
- * place outside [0, B), a destination that owns pages, that an earlier fork names too or that is any fork's source, or a length below
- * shared_len or past what the source has, sets DT_DEV_BAD_PAGE and does nothing.
+ * place outside [0, B), a destination that owns pages or that an earlier fork names too, a source that is any fork's destination, or
+ * a length below shared_len or past what the source has, sets DT_DEV_BAD_PAGE and does nothing.
  * shared_len: the first shared_len tokens are a prefix that every place owns (PagedCache.prefix; a multiple of page): dst owns
  * exactly its blocks before, and they are counted nowhere.
  * n <= B_max; strides, pointers and head_bytes multiples of 16, a plane's row at most 1 MB. */
@@ -661,8 +663,9 @@ typedef struct {
   int32_t K;                 /* 0..32, <= V                                             */
   int32_t* top_ids;          /* [n_out][K]                                              */
   float* top_logp;           /* [n_out][K]                                              */
-  void* workspace;           /* dt_token_logprobs_workspace bytes, 256-byte aligned, no initial value; used until the
-                                call has run (calls that may overlap need a workspace each) */
+  void* workspace;           /* dt_token_logprobs_workspace bytes (of as many entries and alternatives or more), 256-byte
+                                aligned, no initial value; used until the call has run (calls that may overlap need a
+                                workspace each) */
   int64_t workspace_bytes;
 } dt_logprob_args;
 int dt_token_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_logprob_args* a, cudaStream_t s);
