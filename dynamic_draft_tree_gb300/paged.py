@@ -74,9 +74,11 @@ class PagedCache:
     def attend_prompts(self, layer, q, k, v, row_off, out, scale=None, stream=None):
         """A layer's prompts, or chunks of them, before ``prefill`` appends their rows: q and out [rows][H_q][D], k and v
         [rows][H_kv][D], request b's rows at row_off[b], causal and behind the tokens that are in the pages. Calls of one
-        cache share a workspace: one stream at a time. The first one makes it, so it is not one to capture."""
+        cache share a workspace: one stream at a time. The first one makes it, so that a capture of it is refused."""
         if self.prompt_workspace is None:
             with torch.cuda.stream(stream):  # memory of the stream that the calls run on
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("a cache's first attend_prompts makes its workspace: run one before the capture")
                 self.prompt_workspace = dt_prompt_attention_workspace(self.h, self.B, self.H_q, self.H_kv, self.D)
         dt_prompt_attention(self.h, q, k, v, row_off, out, self.prompt_workspace, k_pages=self.pages[2 * layer],
                             v_pages=self.pages[2 * layer + 1], block_table=self.pool.block_table, seq_len=self.seq_len,
