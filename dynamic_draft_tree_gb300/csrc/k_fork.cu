@@ -253,19 +253,28 @@ __device__ __forceinline__ void give(const SharedReleaseArgs& a, int32_t* entry)
   }
 }
 // After all have given: marks the entry if request b acts for its block (a later request looks through the mark); true if
-// the block goes back to the list. `keep_at(o, has)`: blocks that request o keeps and has.
-template <typename Keep>
-__device__ __forceinline__ bool mark(const SharedReleaseArgs& a, int b, int e, int32_t* entry, Keep keep_at) {
+// the block goes back to the list. keep_s, has_s: blocks that each request keeps and has. LOOK later requests' entries are looked at
+// together: 56 samples of 8 prompts of 2000 tokens, fork and release, 59.0 us with two, 55.6 with four, 53.6 with eight, 65.7 one
+// after the other; 8 samples of one prompt (one CTA) 13.6, 13.7 and 14.2.
+template <int LOOK>
+__device__ __forceinline__ bool mark(const SharedReleaseArgs& a, int b, int e, int32_t* entry, const int32_t* keep_s, const int32_t* has_s) {
   const int id = *entry;
   if (id >= a.pool.n_blocks) return false;
   const int refs = __ldcg(a.refs + id), extra = refs & (kGiver - 1), givers = refs >> 16;
   if (givers > extra + 1) set_status(a.status, DT_DEV_BAD_PAGE);  // given back by more than own it
   if (givers > 1) {
-    for (int o = b + 1; o < a.B; ++o) {
-      int has;
-      const int kept = keep_at(o, has);
-      if (e >= kept && e < has && block_of(*(volatile int32_t*)(a.pool.block_table + (int64_t)o * a.pool.max_blocks + e)) == id)
-        return false;
+    const int32_t* at = a.pool.block_table + e;
+    for (int o0 = b + 1; o0 < a.B; o0 += LOOK) {
+      int32_t x[LOOK];
+#pragma unroll
+      for (int u = 0; u < LOOK; ++u) {
+        const int o = min(o0 + u, a.B - 1);
+        x[u] = e >= keep_s[o] && e < has_s[o] ? __ldcg(at + (int64_t)o * a.pool.max_blocks) : INT32_MAX;
+      }
+      bool later = false;
+#pragma unroll
+      for (int u = 0; u < LOOK; ++u) later |= o0 + u < a.B && block_of(x[u]) == id;
+      if (later) return false;
     }
   }
   *entry = givers > extra ? ~id : id | kSettles;
@@ -309,15 +318,21 @@ __global__ void __launch_bounds__(kPageThreads) release_give_kernel(const __grid
 
 // CTA b: which of them request b acts for.
 __global__ void __launch_bounds__(kPageThreads) release_mark_kernel(const __grid_constant__ SharedReleaseArgs a) {
+  extern __shared__ int32_t kept[];  // [B] blocks that are kept, [B] that there are
   __shared__ int64_t red[kPageThreads / 32];
   pdl_begin();
   const int b = blockIdx.x;
-  int owned;
-  const int keep = keep_blocks(a, b, owned);
+  for (int o = b + threadIdx.x; o < a.B; o += kPageThreads) {
+    int has;
+    kept[o] = keep_blocks(a, o, has);
+    kept[a.B + o] = has;
+  }
+  __syncthreads();
+  const int keep = kept[b], owned = kept[a.B + b];
   int32_t* table = a.pool.block_table + (int64_t)b * a.pool.max_blocks;
   int64_t mine = 0;
   for (int e = keep + threadIdx.x; e < owned; e += kPageThreads)
-    mine += mark(a, b, e, table + e, [&](int o, int& has) { return keep_blocks(a, o, has); });
+    mine += mark<8>(a, b, e, table + e, kept, kept + a.B);
   if (threadIdx.x == 0) check_kept(a, b, keep);
   mine = block_sum(mine, red);
   if (threadIdx.x == 0) a.count[b] = (int32_t)mine;
@@ -390,10 +405,7 @@ __global__ void __launch_bounds__(kSmallThreads) release_small_kernel(const __gr
   __syncthreads();
   int back = 0;
   for (int i = tid; i < all; i += kSmallThreads)
-    if (mine(i, b, e)) back += mark(a, b, e, a.pool.block_table + i, [&](int o, int& has) {
-        has = has_s[o];
-        return keep_s[o];
-      });
+    if (mine(i, b, e)) back += mark<2>(a, b, e, a.pool.block_table + i, keep_s, has_s);
   for (int q = tid; q < a.B; q += kSmallThreads) check_kept(a, q, keep_s[q]);
   back = __reduce_add_sync(0xFFFFFFFFu, back);
   if (lane == 0) atomicAdd(&total_s, back);
@@ -484,7 +496,7 @@ cudaError_t launch_kv_release_shared(dt_handle* h, int B, const dt_block_pool* p
   launch_k(release_give_kernel, grid, block, 0, s, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  launch_k(release_mark_kernel, grid, block, 0, s, a);
+  launch_k(release_mark_kernel, grid, block, 8 * (size_t)B, s, a);  // B <= 4096: 32 KB
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   launch_k(release_return_kernel, grid, block, 0, s, a);
