@@ -58,6 +58,7 @@ struct PromptParams {
   float c;              // scale * log2 e
   int32_t period, step; // w / 128 = step / period in lowest terms, period a power of two
   int32_t period_shift;
+  int32_t warp_box;     // 32 rows of a group are a box of the output: whole positions, or a part of one
   int32_t whole;        // no item is cut: a CTA takes those that begin in its run
   uint16_t part[128];   // part[r] = sum of ceil(k step / period), k = 1 .. r < period
   int32_t part_all;     // the same up to r = period
@@ -236,7 +237,7 @@ constexpr int kSegs = 4;  // segments that warp 10 is ahead of the slowest reade
 
 struct Shared {
   uint64_t kfull[kMostStages], kempty[kMostStages], vfull[kMostStages], vempty[kMostStages], vfix[kMostStages];
-  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], ofull[2], ofree[2], turn[2], drained[2];
+  uint64_t sfull[2], phalf[2][2], odone[2], qfull[2], qempty[2], turn[2], drained[2];
   uint64_t segfull[kSegs], segempty[kSegs];
   Segment seg[kSegs];
   Plan plan;
@@ -708,83 +709,52 @@ __device__ __noinline__ void add_odd_values(const PromptParams& p, int h, int64_
   }
 }
 
-// 16 KB of shared memory through which a group's results leave, in turns of which all warps of the group take part: free(),
-// writing, done().
-struct Stage {
-  uint8_t* at;
-  uint32_t turns = 0;  // begun so far
-  // The last turn is over in every warp and its store has read what it took. (Without the first, a warp could miss a phase.)
-  __device__ __forceinline__ bool free(Shared& sh, int group) {
-    if ((threadIdx.x & 127) < 32) {
-      if (turns > 0 && !wait(&sh.ofull[group], (turns - 1) & 1, sh)) return false;
-      if ((threadIdx.x & 31) == 0) {
-        tc::tma_stores_read();
-        tc::bar_arrive(&sh.ofree[group]);
-      }
-      __syncwarp();
-    }
-    return wait(&sh.ofree[group], turns++ & 1, sh);
-  }
-  __device__ __forceinline__ void done(Shared& sh, int group) {
-    tc::fence_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::bar_arrive(&sh.ofull[group]);
-  }
-  // Behind done(): the first warp stores the box.
-  __device__ __forceinline__ bool store(Shared& sh, int group, const CUtensorMap* map, int x, int y, int z) {
-    if ((threadIdx.x & 127) >= 32) return true;
-    if (!wait(&sh.ofull[group], (turns - 1) & 1, sh)) return false;
-    if ((threadIdx.x & 31) == 0) tc::tma_store_3d(map, tc::smem_addr(at), x, y, z);
-    __syncwarp();
-    return true;
-  }
-};
+// The warp's place in shared memory is free: its last store has read what it took.
+__device__ __forceinline__ void place_free() {
+  if ((threadIdx.x & 31) == 0) tc::tma_stores_read();
+  __syncwarp();
+}
 
-// A group's rows of a segment leave tensor memory, 128 bytes of a row a turn, through 16 KB of shared memory of the group's own.
-// An item in one piece: the quotient, rounded. Rows of a full group are stored by TMA, others by the threads, eight of them a
-// row. The way of 32 KB out of an SM takes 1000 clocks, for both groups together twice that, and stores by threads wait for it:
-// 4000 clocks an item with them (6500 with a row a thread).
+// A group's rows of a segment leave tensor memory, 128 bytes of a row a turn, through 4 KB of shared memory of each warp's own.
+// An item in one piece: the quotient, rounded. A warp whose 32 rows are in use stores them by TMA (where they are whole positions,
+// or whole parts of one); other rows are stored by the threads, eight of them a row.
 template <bool BF16>
-__device__ __forceinline__ bool write_rows(const PromptParams& p, Shared& sh, const Segment& s, int group, int wl, bool odd, float l,
-                                           int end, uint32_t o_at, Stage& stage, const CUtensorMap* out_map) {
-  const int lane = threadIdx.x & 31, eighth = lane & 7, half = p.rows2 >> 1, r = group * half + wl;
-  const bool full = s.rows - group * half >= half && !odd;
+__device__ __forceinline__ void write_rows(const PromptParams& p, const Segment& s, int group, int wl, bool odd, float l, int end,
+                                           uint32_t o_at, uint8_t* place, const CUtensorMap* out_map) {
+  const int lane = threadIdx.x & 31, eighth = lane & 7, half = p.rows2 >> 1, r0 = group * half + (wl & 96);
+  const bool full = end == 32 && p.warp_box && !odd;
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays
-  uint8_t *mine = stage.at + wl * 128, *warps = stage.at + (wl & 96) * 128;
+  const int i0 = position_of(p, r0), h0 = r0 - i0 * p.G;  // the warp's first row
 #pragma unroll 1
   for (int d0 = 0; d0 < p.a.D; d0 += 64) {
     uint32_t raw[64];
-    if (end > 0) {
-      tc::tmem_ld64(o_at + d0, raw);
+    tc::tmem_ld64(o_at + d0, raw);
 #pragma unroll
-      for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
-    }
-    if (!stage.free(sh, group)) return false;
-    if (end > 0) {
+    for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
+    place_free();
 #pragma unroll
-      for (int k = 0; k < 64; k += 8) {
-        uint32_t w[4];
+    for (int k = 0; k < 64; k += 8) {
+      uint32_t w[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] = pack16<BF16>(__uint_as_float(raw[k + 2 * x]), __uint_as_float(raw[k + 2 * x + 1]));
-        *(uint4*)(mine + (((k / 8) ^ eighth) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int x = 0; x < 4; ++x) w[x] = pack16<BF16>(__uint_as_float(raw[k + 2 * x]), __uint_as_float(raw[k + 2 * x + 1]));
+      *(uint4*)(place + lane * 128 + (((k / 8) ^ eighth) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (full) {
-      stage.done(sh, group);
-      if (!stage.store(sh, group, out_map, d0, s.h * p.G, (int)s.base + s.i0 + group * p.pos)) return false;
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::tma_store_3d(out_map, tc::smem_addr(place), d0, s.h * p.G + h0, (int)s.base + s.i0 + i0);
     } else {
       __syncwarp();
       uint16_t* out = (uint16_t*)p.a.out + (s.base + s.i0) * p.a.o_row + (int64_t)s.h * p.G * p.a.o_head + eighth * 8 + d0;
 #pragma unroll 1
       for (int x = lane >> 3; x < end; x += 4) {
-        const int f = r - lane + x, i = position_of(p, f);
+        const int f = r0 + x, i = position_of(p, f);
         if (d0 + eighth * 8 < p.a.D)
-          *(uint4*)(out + i * p.a.o_row + (f - i * p.G) * p.a.o_head) = *(const uint4*)(warps + x * 128 + ((eighth ^ (x & 7)) << 4));
+          *(uint4*)(out + i * p.a.o_row + (f - i * p.G) * p.a.o_head) = *(const uint4*)(place + x * 128 + ((eighth ^ (x & 7)) << 4));
       }
-      stage.done(sh, group);
+      __syncwarp();
     }
   }
-  return true;
 }
 
 // A part of one: as it is, in fp32, to be joined.
@@ -819,7 +789,7 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, const CUtensorM
   const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16, tm = sh.tmem;
   const uint32_t s_at = tm + lanes + group * kTile, o_at = tm + lanes + 2 * kTile + group * DP;
   const int half = p.rows2 >> 1, r = group * half + wl;  // this thread's row of an item
-  Stage stage{out_smem + group * kTile * 128};
+  uint8_t* place = out_smem + (threadIdx.x >> 5) * 4096;  // this warp's
   Segments segs;
   uint32_t ns = 0, no = 0;  // phases of sfull and odone of this group
   while (segs.begin(sh)) {
@@ -914,14 +884,13 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, const CUtensorM
     const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
     const int end = max(0, min(32, min(half, s.rows - group * half) - (wl & 96)));  // the warp's rows in use
     if (s.t1 - s.t0 == s.tt) {
-      if (some && !write_rows<BF16>(p, sh, s, group, wl, odd, row.l, end, o_at, stage, out_map)) return;
+      if (some && end > 0) write_rows<BF16>(p, s, group, wl, odd, row.l, end, o_at, place, out_map);
     } else {
       if (live) p.ml[(int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * kItemRows + r] = make_float2(row.m, row.l);
       // without a tile of this segment the group has no result: m = -inf, l = 0 say so
-      if (some) {
-        if (!stage.free(sh, group)) return;
-        if (end > 0) leave_rows<BF16>(p, s, r, end, o_at, stage.at + (wl & 96) * 128);
-        stage.done(sh, group);
+      if (some && end > 0) {
+        place_free();
+        leave_rows<BF16>(p, s, r, end, o_at, place);
       }
     }
     if (odd && some) {
@@ -971,8 +940,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::bar_init(&sh.odone[g], 1);
       tc::bar_init(&sh.qfull[g], 1);
       tc::bar_init(&sh.qempty[g], 1);
-      tc::bar_init(&sh.ofull[g], 4);
-      tc::bar_init(&sh.ofree[g], 1);
       tc::bar_init(&sh.turn[g], 1);
       tc::bar_init(&sh.drained[g], 1);
     }
@@ -1000,7 +967,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
     softmax_group<DP, BF16>(p, sh, &out_map, v_smem + S::kV * S::kBlock, warp >> 2);
-    if ((tid & 127) == 0) tc::tma_stores_done();  // whichever way it left
+    if (lane == 0) tc::tma_stores_done();  // whichever way it left
   } else if (warp == 8) {
     load_tiles<DP>(p, sh, &k_map, &v_map, &kn_map, &vn_map, &q_map, tc::smem_addr(q_smem), tc::smem_addr(k_smem),
                    tc::smem_addr(v_smem), lane);
@@ -1079,6 +1046,7 @@ void shape_params(PromptParams& p) {
   p.pos = kTile / p.G;
   p.rows2 = 2 * p.pos * p.G;
   p.w = 2 * p.pos;
+  p.warp_box = 32 % p.G == 0 || p.G % 32 == 0;
   p.g_magic = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
   while ((1 << p.page_shift) < p.a.page) ++p.page_shift;
   p.period = kTile;
@@ -1165,9 +1133,9 @@ cudaError_t launch_prompt(dt_handle* h, const dt_prompt_args* a, cudaStream_t s)
   const int64_t kn[3] = {1, a->kn_head, a->kn_row}, vn[3] = {1, a->vn_head, a->vn_row};
   const int nb[3] = {64, 1, kTile};
   const int64_t qd[3] = {a->D, a->H_q, a->rows}, qs[3] = {1, a->q_head, a->q_row};
-  const int qb[3] = {64, p.G, p.pos};
+  const int qb[3] = {64, p.G, p.pos}, ob[3] = {64, std::min(p.G, 32), std::max(32 / p.G, 1)};
   const int64_t os[3] = {1, a->o_head, a->o_row};
-  bool ok = encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) && encode(&m[5], a->dtype, a->out, 3, qd, os, qb) && encode(&m[3], a->dtype, a->k_new, 3, nd, kn, nb) &&
+  bool ok = encode(&m[0], a->dtype, a->q, 3, qd, qs, qb) && encode(&m[5], a->dtype, a->out, 3, qd, os, ob) && encode(&m[3], a->dtype, a->k_new, 3, nd, kn, nb) &&
             encode(&m[4], a->dtype, a->v_new, 3, nd, vn, nb);
   if (cached) {
     const int64_t pd[4] = {a->D, a->H_kv, a->page, a->n_blocks};
