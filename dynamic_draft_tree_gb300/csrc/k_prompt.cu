@@ -15,9 +15,13 @@
 // A CTA: warps 0-3 and 4-7 are two softmax groups (thread = row), warp 8 loads tiles (TMA), warps 9 and
 // 11 issue a group's matrix instructions each, warp 10 walks along the line and clears value rows. Every wait is bounded
 // (DT_DEV_TIMEOUT). S = Q K^T of a group's next tile is issued right behind O += P V of its last one, over the ends of
-// segments too: Q has a buffer a group that is loaded again when the group's last S of a segment is done, and O leaves
-// while the other group's products run, so the pipeline does not run empty between items. S (fp32), P (16-bit, over S) and O
-// live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
+// segments too: Q has a buffer a group that is loaded again when the group's last S of a segment is done. S (fp32), P (16-bit,
+// over S) and O live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
+//
+// Bound by the chain S, softmax, P V of the two groups in turn: a tile of both takes 2810 clocks at D = 128, of which the tensor
+// cores need 2048, and by power where all SMs are at it: one prompt of 16384 tokens, 8 x 4 heads of 128, bf16: 1305 us,
+// 1.69 PFLOP/s, at first and 1400 us, 1.57 PFLOP/s, at 1.84 GHz when it goes on. An item's ends cost about 1.4 tiles more: its
+// masked tile, and the softmax of the next item, which begins when the rows have left.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,10 +41,10 @@ constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes
 constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
                                 // small ones stay normal in fp16 for longer; it cancels in the quotient
 // Units of the line: a tile, for one group of rows (whose chain of softmax and products takes as long) as for two; an item has
-// kItemUnits more in front for its ends. Tile t of an item at unit u is at u + kItemUnits + t, and belongs to the CTA that
-// this falls to. With two thirds of a unit for a tile of one group and one for an item 16 prompts of up to 2000 tokens took
-// 210 us instead of 195, prompts among single tokens (32 requests) 46 instead of 44; with three units for an item 206 and 45.
-constexpr int kItemUnits = 2;
+// kItemUnits more in front for its ends. Tile t of an item at unit u is at u + kItemUnits + t, and belongs to the CTA that this
+// falls to. 16 prompts of up to 2000 tokens, whose CTAs have 8 to 33 items each, take 188 us with one unit for an item, 193 with two
+// and 205 with three; with one and a half tiles 186 beside 185 for one in the same run.
+constexpr int kItemUnits = 1;
 
 // An item that is cut: left by its first CTA for the join.
 struct Cut {
@@ -504,7 +508,7 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
     int stage;
     uint32_t parity;
     ring<S::kK>(n, stage, parity);
-    bool fresh = t == t1;  // the next tile is another segment's: the products behind this one's do not wait for its Q and K
+    const bool fresh = t == t1;  // the next tile is another segment's
     // What a step waits for has been waited for before its weights are there: K and the turn behind the weights made a tile of
     // two groups 2760 clocks long instead of 2580.
     if (n > 0) {
@@ -515,6 +519,17 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
         if (!wait(&sh.vfix[v_stage], fix >> v_stage & 1, sh)) return;
         fix ^= 1u << v_stage;
       }
+    }
+    bool more = true;
+    if (fresh) {
+      more = segs.next(sh, s, lane == 0);
+      t = uniform(s.t0);
+      t1 = uniform(s.t1);
+      ct = uniform(s.ct);
+      len = uniform(s.len);
+      iend = uniform(s.iend);
+      i0 = uniform(s.i0);
+      tiles = min(t1, uniform(g ? s.tiles1 : s.tiles0));
     }
     // waited for and let go by a group without this tile too, so that it does not run ahead of the ring
     if (!fresh && !wait_soon(&sh.kfull[stage], parity, sh)) return;
@@ -542,19 +557,15 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
     } else if (n > 0 && elected) {
       tc::bar_arrive(&sh.vempty[v_stage]);
     }
+    // The turn is kept for another segment's Q and K too, which are mostly there. (Given to the other group in between, S came
+    // behind that group's products: 16 prompts of up to 2000 tokens 193 us instead of 191.)
     if (fresh) {
-      pass_turn();
-      if (!segs.next(sh, s, lane == 0)) return;
-      t = uniform(s.t0);
-      t1 = uniform(s.t1);
-      ct = uniform(s.ct);
-      len = uniform(s.len);
-      iend = uniform(s.iend);
-      i0 = uniform(s.i0);
-      tiles = min(t1, uniform(g ? s.tiles1 : s.tiles0));
+      if (!more) {
+        pass_turn();
+        return;
+      }
       if (t < tiles && !wait(&sh.qfull[g], nq++ & 1, sh)) return;
       if (!wait_soon(&sh.kfull[stage], parity, sh)) return;
-      if (!take_turn()) return;
     }
     owe = 0;
     const int valid = tile_valid(t, ct, len, iend);
@@ -715,8 +726,8 @@ __device__ __forceinline__ void place_free() {
   __syncwarp();
 }
 
-// A group's rows of a segment leave tensor memory, 128 bytes of a row a turn, through 4 KB of shared memory of each warp's own.
-// An item in one piece: the quotient, rounded. A warp whose 32 rows are in use stores them by TMA (where they are whole positions,
+// A group's rows of a segment leave tensor memory, 128 bytes of a row a turn, through 4 KB of shared memory of each warp's own
+// (2500 clocks; 4000 with one store for a group's rows, 6500 with a row a thread). An item in one piece: the quotient, rounded. A warp whose 32 rows are in use stores them by TMA (where they are whole positions,
 // or whole parts of one); other rows are stored by the threads, eight of them a row.
 template <bool BF16>
 __device__ __forceinline__ void write_rows(const PromptParams& p, const Segment& s, int group, int wl, bool odd, float l, int end,
@@ -962,7 +973,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  // 384 x 168 registers at launch = 256 x 208 + 128 x 88: a softmax thread holds its row's 128 scores
+  // 384 x 168 registers at launch = 256 x 208 + 128 x 88: a softmax thread holds 64 scores of its row and their weights
   if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
