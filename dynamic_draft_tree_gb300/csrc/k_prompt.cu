@@ -973,9 +973,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  // 384 x 168 registers at launch = 256 x 208 + 128 x 88: a softmax thread holds 64 scores of its row and their weights
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
     softmax_group<DP, BF16>(p, sh, &out_map, v_smem + S::kV * S::kBlock, warp >> 2);
     if (lane == 0) tc::tma_stores_done();  // whichever way it left
