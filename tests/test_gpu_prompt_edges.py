@@ -47,6 +47,27 @@ def test_offsets_past_31_bits(torch):
     h.close()
 
 
+@pytest.mark.parametrize("G,D,dtype", [(4, 128, "bf16"), (1, 64, "fp16"), (5, 80, "bf16")])
+def test_values_that_are_no_numbers_in_cut_items(torch, G, D, dtype):
+    """Infinities and NaN in the values of a prompt that several CTAs work on, at the borders of tiles and items: they show in the
+    rows that attend to them, in their elements alone."""
+    import dynamic_draft_tree_gb300 as dt
+
+    pr = Problem(torch, n=[2500, 20], H_kv=2, G=G, D=D, lens=[300, 3000], seed=G, dtype=dtype)
+    for k, (at, x) in enumerate(((0, float("inf")), (127, float("nan")), (128, float("-inf")), (1000, float("inf")),
+                                 (1919, float("nan")), (2047, float("-inf")), (2499, float("nan")))):
+        d = (11 * k + 3) % D
+        pr.vn[at, :, d] = x
+        pr.v[0][300 + at, :, d] = x
+    h, ws = pr.handle(dt)
+    pr.call(dt, h, ws)
+    assert dt.dt_get_status(h) == 0
+    got = pr.out.clone()
+    pr.out.fill_(7.0)
+    _check(pr, got)
+    h.close()
+
+
 def test_two_calls_at_once(torch):
     """Two streams, one handle, a workspace each: cut items of both."""
     import dynamic_draft_tree_gb300 as dt
