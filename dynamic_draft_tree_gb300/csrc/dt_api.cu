@@ -827,10 +827,13 @@ int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, v
   return DT_OK;
 }
 
+static constexpr int32_t kLogprobV = 0x7FFF0000;  // places of a row's last piece are counted in 32 bits
+
 int dt_token_logprobs_workspace(dt_handle* h, int64_t entries, int32_t K, int64_t* bytes) {
   if (!h || !bytes) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: null argument");
   if (K < 0 || K > dt::kMaxK || K > h->cfg.V) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: K must be in [0, min(32, V)]");
   if (entries < 1 || entries > 0x7FFFFFFF) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: entries must be in [1, 2^31)");
+  if (h->cfg.V > kLogprobV) return fail(DT_ERR_ARG, "dt_token_logprobs_workspace: V must be at most 2^31 - 2^16");
   *bytes = dt::logprob_workspace_bytes(h, entries, K);
   return DT_OK;
 }
@@ -841,6 +844,7 @@ int dt_token_logprobs(dt_handle* h, const void* logits, int64_t ld, const dt_log
   if (rc != DT_OK) return rc;
   if (!logits || !a->n_new || !a->workspace) return fail(DT_ERR_ARG, "dt_token_logprobs: null argument");
   if (ld < h->cfg.V) return fail(DT_ERR_ARG, "dt_token_logprobs: ld < V");
+  if (h->cfg.V > kLogprobV) return fail(DT_ERR_ARG, "dt_token_logprobs: V must be at most 2^31 - 2^16");
   if (a->P < 1 || (a->path && a->D_path < 1) || a->n_extra < 0 || (a->shift != 0 && a->shift != 1))
     return fail(DT_ERR_ARG, "dt_token_logprobs: P, D_path >= 1, n_extra >= 0, shift 0 or 1");
   if (a->rows < 1 || a->rows > 0x7FFFFFFF || (!a->row_off && a->rows < (int64_t)a->B * a->P))

@@ -645,7 +645,7 @@ int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, v
  * token is given (-1, or last NULL behind the last one) logp is NaN and rank -1; other ids outside [0, V) set
  * DT_DEV_BAD_TOKEN and count as none. A row with NaN or +inf, or without a finite logit, sets DT_DEV_BAD_LOGITS: NaN, -1 and no
  * alternatives. n past D_path, P or the request's rows, or a position outside [0, P) or the rows, sets DT_DEV_BAD_TREE and
- * is left out. Outputs of no entry are left as they were. */
+ * is left out. Outputs of no entry are left as they were. V <= 2^31 - 2^16. */
 typedef struct {
   int32_t B, P;
   int64_t rows;              /* rows of logits                                          */

@@ -222,6 +222,20 @@ def test_requests_outside_the_rows_are_reported(torch, B):
     h.close()
 
 
+def test_vocabularies_past_the_counting_of_places_are_refused(torch):
+    import dynamic_draft_tree_gb300 as dt
+
+    for V, ok in ((2 ** 31 - 2 ** 16, True), (2 ** 31 - 2 ** 16 + 1, False), (2 ** 31 - 1, False)):
+        h = dt.Handle(1, V, 1, 1, 1, 1)
+        if ok:
+            dt.dt_token_logprobs_workspace(h, 1)
+        else:
+            with pytest.raises(dt.DtError) as e:
+                dt.dt_token_logprobs_workspace(h, 1)
+            assert e.value.code == dt.DT_ERR_ARG
+        h.close()
+
+
 def test_offsets_past_31_bits(torch):
     """Rows 2^30 elements apart."""
     import dynamic_draft_tree_gb300 as dt
