@@ -596,13 +596,24 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
   }
 }
 
+// The larger absolute values of two pairs; NaN stays.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
 // (a weight of zero times what lies there need not be zero), and so do NaN and infinities at positions that only some rows
 // of the item attend to: the rows that do add them in finish_rows.
 template <int DP, bool BF16>
 __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, int lane) {
   using S = Smem<DP>;
-  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u, kExp2 = kExp << 16 | kExp, kUnit2 = BF16 ? 0x00800080u : 0x04000400u;
+  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
   Walk w;
   w.start(p, sh.plan);
   Segment s;
@@ -648,21 +659,21 @@ __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, i
       uint8_t* at = v_smem + stage * S::kBlock;
       const int upto = (valid + 15) / 16 * 16;
       const int some = t < s.ct ? valid : max(0, s.i0 + 1 - (t - s.ct) * kTile);  // the first that not all rows attend to
-      // whether there is a NaN or an infinity, whose exponent's carry reaches the sign's place, and only then where
-      uint32_t carry = 0;
+      // whether there is a NaN or an infinity, and only then where (an instruction a word: the products wait for this)
+      uint32_t most = 0;
       for (int hf = 0; hf < DP / 64; ++hf) {
         uint8_t* rows = at + hf * S::kHalf;
         for (int c = valid * 8 + lane; c < upto * 8; c += 32) *(uint4*)(rows + c * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll 8
         for (int c = some * 8 + lane; c < valid * 8; c += 32) {
           const uint4 q = *(const uint4*)(rows + c * 16);
-          carry |= (q.x & kExp2) + kUnit2;
-          carry |= (q.y & kExp2) + kUnit2;
-          carry |= (q.z & kExp2) + kUnit2;
-          carry |= (q.w & kExp2) + kUnit2;
+          most = max_abs<BF16>(most, q.x);
+          most = max_abs<BF16>(most, q.y);
+          most = max_abs<BF16>(most, q.z);
+          most = max_abs<BF16>(most, q.w);
         }
       }
-      const bool odd = __any_sync(0xFFFFFFFFu, carry & 0x80008000u);
+      const bool odd = __any_sync(0xFFFFFFFFu, (most & kExp) == kExp || (most >> 16 & kExp) == kExp);
       if (odd) {
         for (int hf = 0; hf < DP / 64; ++hf) {
           uint32_t* words = (uint32_t*)(at + hf * S::kHalf);
