@@ -42,8 +42,8 @@ constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves
                                 // small ones stay normal in fp16 for longer; it cancels in the quotient
 // Units of the line: a tile, for one group of rows (whose chain of softmax and products takes as long) as for two; an item has
 // kItemUnits more in front for its ends. Tile t of an item at unit u is at u + kItemUnits + t, and belongs to the CTA that this
-// falls to. 16 prompts of up to 2000 tokens, whose CTAs have 8 to 33 items each, take 188 us with one unit for an item, 193 with two
-// and 205 with three; with one and a half tiles 186 beside 185 for one in the same run.
+// falls to. 16 prompts of up to 2000 tokens, whose CTAs have 8 to 33 items each, take 186 us with one unit for an item, 192 with two
+// and 203 with three (one and a half: no difference).
 constexpr int kItemUnits = 1;
 
 // An item that is cut: left by its first CTA for the join.
@@ -558,7 +558,7 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
       tc::bar_arrive(&sh.vempty[v_stage]);
     }
     // The turn is kept for another segment's Q and K too, which are mostly there. (Given to the other group in between, S came
-    // behind that group's products: 16 prompts of up to 2000 tokens 193 us instead of 191.)
+    // behind that group's products: 16 prompts of up to 2000 tokens 190 us instead of 186.)
     if (fresh) {
       if (!more) {
         pass_turn();
