@@ -1095,7 +1095,7 @@ Layout layout_of(const dt_handle* h, int D) {
 }
 
 // Items of few tiles are not cut: a launch to join them costs more than an uneven share. One prompt, 8 x 4 heads of 128, cut
-// and whole: 93 tokens 13.0 and 9.7 us, 512 17.2 and 14.4, 1024 24.0 and 20.7, 1500 32.0 and 32.1, 2000 42.1 and 50.8.
+// and whole: 93 tokens 12.6 and 9.3 us, 512 17.1 and 14.3, 1024 24.3 and 20.2, 1500 31.1 and 33.3, 2000 41.1 and 50.4.
 constexpr int kWholeTiles = 8;
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const PromptParams& p, const CUtensorMap* m, cudaStream_t s) {
