@@ -72,7 +72,8 @@ __device__ __forceinline__ int2 entry_of(const LpArgs& p, int64_t e) {
   }
   const int64_t n = (int64_t)a.n_new[b] + a.n_extra;
   const int64_t first = a.row_off ? (int64_t)a.row_off[b] : (int64_t)b * a.P;
-  const int64_t room = packed ? (int64_t)a.row_off[b + 1] - first : p.per;
+  const int64_t rows = a.row_off ? (int64_t)a.row_off[b + 1] - first : a.P;  // the request's: a path leads to no other's
+  const int64_t room = packed ? rows : min((int64_t)p.per, min(rows, (int64_t)a.P));
   if (n < 0 || n > room) {
     if (j == 0) set_status(p.status, DT_DEV_BAD_TREE);
     return none;
@@ -83,7 +84,7 @@ __device__ __forceinline__ int2 entry_of(const LpArgs& p, int64_t e) {
   if (a.path) {
     pos = a.path[(int64_t)b * a.D_path + j];
     if (k < n) next = a.path[(int64_t)b * a.D_path + k];
-    if (pos < 0 || pos >= a.P) {
+    if (pos < 0 || pos >= a.P || pos >= rows) {
       set_status(p.status, DT_DEV_BAD_TREE);
       return none;
     }
@@ -97,7 +98,7 @@ __device__ __forceinline__ int2 entry_of(const LpArgs& p, int64_t e) {
   if (k >= n) {
     if (a.last) token = a.last[b];
   } else if (a.tokens) {
-    const int64_t at = !a.path ? first + k : next >= 0 && next < a.P ? (int64_t)b * a.P + next : -1;
+    const int64_t at = !a.path ? first + k : next >= 0 && next < a.P && next < rows ? (int64_t)b * a.P + next : -1;
     if (at >= 0 && at < a.n_tokens) token = a.tokens[at];
     else set_status(p.status, DT_DEV_BAD_TREE);
   }

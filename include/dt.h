@@ -644,8 +644,8 @@ int dt_logits_process(dt_handle* h, int32_t B, const void* logits, int64_t ld, v
  * -inf are none: id -1, -inf). Any of logp, entropy, rank, last and (K = 0) top_ids and top_logp may be NULL, tokens too. Where no
  * token is given (-1, or last NULL behind the last one) logp is NaN and rank -1; other ids outside [0, V) set
  * DT_DEV_BAD_TOKEN and count as none. A row with NaN or +inf, or without a finite logit, sets DT_DEV_BAD_LOGITS: NaN, -1 and no
- * alternatives. n past D_path, P or the request's rows, or a position outside [0, P) or the rows, sets DT_DEV_BAD_TREE and
- * is left out. Outputs of no entry are left as they were. V <= 2^31 - 2^16. */
+ * alternatives. n past D_path, P or the request's rows (row_off[b + 1] - row_off[b] of them, with a path too), or a position
+ * outside [0, P) or those rows, sets DT_DEV_BAD_TREE and is left out. Outputs of no entry are left as they were. V <= 2^31 - 2^16. */
 typedef struct {
   int32_t B, P;
   int64_t rows;              /* rows of logits                                          */
