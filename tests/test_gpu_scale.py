@@ -1,0 +1,83 @@
+"""Attention whose scores are far apart: scales up to 1e30, in prompts.
+
+q and k are small whole numbers, so that a score without its scale is a whole number below 2^24 and exact in fp32 in any order of
+summation, as is its distance z from the row's largest. What the kernels may add then does not grow with the scores: the
+factor scale log2 e is rounded twice, the product once, so that an exponent z scale log2 e is off by 3 2^-24 of itself; weights
+with exponents beyond 64 add less than 2^-40 of a sum of up to 2^13 of them, and the others are off by a factor within
+1 +- 2^-15 (0.7 * 64 * 3 * 2^-24 = 2^-17, exp2 2^-22, sums of 2^13 terms in fp32 2^-18 at most as in the ordinary case). Parts with references
+below 2^8 in log2 units may differ by two roundings of those, 2^-15, in their exponents. Together 2^-13 of
+A = sum p |v|; beside it the weights' rounding to the type u A, the result's u |o|, and what is lost of
+fp16 weights below the smallest normal number, 2^-31 sum |v|.
+"""
+import math
+
+import pytest
+
+import test_gpu_prompt as prompt
+from test_gpu_prompt import torch  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+SCALES = [1e-30, 1e-3, 1.0, 30.0, 1e3, 1e6, 1e7, 1e8, 1e10, 1e20, 1e30]
+
+
+def _whole(t, x, g, most):
+    fine = t.isfinite(x)
+    w = t.randint(-most, most + 1, x.shape, generator=g, device="cuda").to(x.dtype)
+    x.copy_(t.where(fine, w, x))
+
+
+def _rows(t, q, k, v, ok, scale):
+    """(out, tolerance) of rows q [n][D] against k, v [L][D] where ok [n][L], in 64 bits."""
+    u = t.finfo(q.dtype).eps / 2
+    z = (q.double() @ k.double().T).masked_fill(~ok, -math.inf)
+    d = (z - z.amax(1, keepdim=True)) * scale  # whole numbers are subtracted first: exact whatever the scale
+    p = t.softmax(d, 1)
+    o, a = p @ v.double(), p @ v.double().abs()
+    return o, (u + 2.0 ** -13) * a + u * o.abs() + 2.0 ** -31 * (ok.double() @ v.double().abs())
+
+
+def _fits(t, got, want, tol, what):
+    got = got.double()
+    assert bool(t.isfinite(got).all()), f"{what}: not a number, or infinite"
+    assert float(((got - want).abs() - tol).max()) <= 0.0, (what, float(((got - want).abs() - tol).max()))
+
+
+PROMPTS = {
+    "short": dict(n=[93, 1, 40], H_kv=2, G=4, D=128),
+    "cut and joined": dict(n=[1500], H_kv=1, G=4, D=64),
+    "behind cached tokens": dict(n=[130, 1], H_kv=1, G=8, D=128, lens=[1700, 2300], page=64),
+    "odd heads": dict(n=[100, 1, 233], H_kv=2, G=5, D=80, lens=[77, 5, 0], page=32),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", list(PROMPTS))
+def test_prompts_of_any_scale(torch, name, dtype):  # noqa: F811
+    import dynamic_draft_tree_gb300 as dt
+
+    t = torch
+    pr = prompt.Problem(t, dtype=dtype, **PROMPTS[name])
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    _whole(t, pr.q, g, 3)
+    for b in range(pr.B):  # keys again, dense, in the pages and in the rows
+        _whole(t, pr.k[b], g, 3)
+        pr.kn[pr.off[b]:pr.off[b + 1]] = pr.k[b][pr.lens[b]:]
+        for e in range(-(-pr.lens[b] // pr.page)):
+            m = min(pr.page, pr.lens[b] - e * pr.page)
+            pr.kp[pr.table[b, e], :m] = pr.k[b][e * pr.page:e * pr.page + m]
+    h, ws = pr.handle(dt)
+    for scale in SCALES:
+        pr.scale = scale
+        pr.out.fill_(7.0)
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == 0
+        for b in range(pr.B):
+            L, n, r0 = pr.lens[b], pr.n[b], pr.off[b]
+            ok = t.arange(L + n, device="cuda")[None, :] <= L + t.arange(n, device="cuda")[:, None]
+            for x in range(pr.q.shape[1]):
+                want, tol = _rows(t, pr.q[r0:r0 + n, x], pr.k[b][:, x // pr.G], pr.v[b][:, x // pr.G], ok, scale)
+                _fits(t, pr.out[r0:r0 + n, x], want, tol, (scale, b, x))
+    h.close()
+
