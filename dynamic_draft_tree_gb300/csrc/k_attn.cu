@@ -49,6 +49,7 @@ constexpr int kAttnThreads = 384;
 constexpr float kLazy = 8.0f;   // the reference maximum moves when a row passes it by 2^kLazy
 constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves: up to 2^14, inside fp16, and
                                 // small ones stay normal in fp16 for longer; it cancels in the quotient
+constexpr float kFar = 256.0f;  // scores of rows whose maximum is beyond this (log2 units) become distances first (softmax_group)
 
 struct AttnHead {  // start of the workspace, written by CTA 0 for the merge
   int32_t per;     // units of a CTA
@@ -64,7 +65,7 @@ struct AttnParams {
   int32_t test_stop;  // test only: every wait that is not over at once gives up
   int32_t pos, rows2; // whole positions of a group's 128 rows (128 / G), rows of an item (2 pos G)
   uint32_t g_magic;   // ceil(2^32 / G), for position_of
-  float c;            // scale * log2 e
+  float c, lazy, far; // scale * log2 e, kLazy / c, kFar / c
   int32_t ns;         // tiles of the shared prefix as items of its own; 0: requests read it with their own tokens
   int32_t skip;       // tokens that a request's own items leave to it
   int64_t own_rows;   // rows of an own item's partials
@@ -690,7 +691,7 @@ __device__ void fix_values(const AttnParams& p, Shared& sh, uint8_t* v_smem, int
 
 // What a softmax thread keeps of its row.
 struct Row {
-  float m, l;  // reference maximum (log2 units), sum of weights
+  float m, l;  // reference maximum (a score, without c), sum of weights
 };
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -741,6 +742,19 @@ __device__ __noinline__ void mask_scores(uint32_t s_at, uint32_t b0, uint32_t b1
   tc::wait_st();
 }
 
+// Scores become distances from `ref`, of rows that are far; others' stay as they are (ref 0).
+__device__ __noinline__ void far_scores(uint32_t s_at, float ref) {
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 32) {
+    uint32_t raw[32];
+    tc::tmem_ld32(s_at + c, raw);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) raw[x] = __float_as_uint(__uint_as_float(raw[x]) - ref);
+    tc::tmem_st32(s_at + c, raw);
+  }
+  tc::wait_st();
+}
+
 // Values that are no numbers at tree positions this row attends to: weight times value, from global memory.
 template <bool BF16>
 __device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int64_t base, int j0, int j1, int i, int g,
@@ -755,7 +769,7 @@ __device__ __noinline__ void add_odd_row(const AttnParams& p, int b, int h, int6
     if (!odd) continue;
     float dot = 0.0f;
     for (int d = 0; d < p.a.D; ++d) dot += unpack16<BF16>(q[d]) * unpack16<BF16>(k[d]);
-    const float wgt = exp2f(dot * p.c - m + kShift);
+    const float wgt = exp2f((dot - m) * p.c + kShift);
     for (int d = 0; d < min(32, p.a.D - d0); ++d) {
       const float x = unpack16<BF16>(v[d0 + d]);
       if (!isfinite(x)) o[d] += wgt * x * scale;
@@ -789,8 +803,8 @@ __device__ void finish_rows(const AttnParams& p, Shared& sh, const Segment& s, i
   if (both) {
     const float2 o = sh.ml[group ^ 1][wl];
     m = fmaxf(row.m, o.x);
-    f0 = row.m == -INFINITY ? 0.0f : exp2f(row.m - m);
-    f1 = o.x == -INFINITY ? 0.0f : exp2f(o.x - m);
+    f0 = row.m == -INFINITY ? 0.0f : exp2f((row.m - m) * p.c);
+    f1 = o.x == -INFINITY ? 0.0f : exp2f((o.x - m) * p.c);
     l = row.l * f0 + o.y * f1;
   }
   const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.tree;
@@ -906,7 +920,7 @@ __device__ bool join_parts(const AttnParams& p, Shared& sh, const Segment& s, ui
 #pragma unroll 2
     for (int k = k0; k < s.parts; k += step) {
       const float2 x = __ldcg(p.ml_own + at + k * p.own_rows);
-      const float w = exp2f(x.x - ref);  // a part that attends to nothing: 0
+      const float w = exp2f((x.x - ref) * p.c);  // a part that attends to nothing: 0
       l += x.x == -INFINITY && x.y == 0.0f ? 0.0f : x.y * w;
       const float* src = p.o_own + (at + k * p.own_rows) * p.a.D + c * 4;
 #pragma unroll
@@ -945,7 +959,7 @@ __device__ bool join_parts(const AttnParams& p, Shared& sh, const Segment& s, ui
     for (int y = 1; y < step; ++y) {
       const float* other = mine + y * blocks * 4 * kRowFloats;
       const float mo = other[DP], lo = other[DP + 1], top = fmaxf(m, mo), ref = top == -INFINITY ? 0.0f : top;
-      const float a = exp2f(m - ref), w = exp2f(mo - ref);
+      const float a = exp2f((m - ref) * p.c), w = exp2f((mo - ref) * p.c);
       l = l * a + lo * w;
       m = top;
 #pragma unroll
@@ -1016,16 +1030,17 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
             for (int y = 0; y < 4; ++y) tops[y] = fmaxf(fmaxf(tops[y], __uint_as_float(raw[x + 2 * y])), __uint_as_float(raw[x + 2 * y + 1]));
           }
         }
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
-        if (k == 0) {
-          row.m = top;
-        } else {
-          const bool up = top > row.m + kLazy;
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        const bool is_far = live && fabsf(top) > p.far && fabsf(top) < INFINITY;
+        const bool up = k > 0 && top > __fadd_rd(row.m, p.lazy);
+        if (k == 0) row.m = top;
+        float ref = row.m;
+        if (__any_sync(0xFFFFFFFFu, up || is_far)) {
           if (__any_sync(0xFFFFFFFFu, up)) {
             // the accumulator of the rows so far moves to the new reference
-            const float fac = up ? (row.m == -INFINITY ? 0.0f : exp2f(row.m - top)) : 1.0f;
+            const float fac = up ? (row.m == -INFINITY ? 0.0f : exp2f((row.m - top) * p.c)) : 1.0f;
             if (up) {
-              row.m = top;
+              row.m = ref = top;
               row.l *= fac;
             }
 #pragma unroll 1
@@ -1037,8 +1052,16 @@ __device__ void softmax_group(const AttnParams& p, Shared& sh, uint8_t* q_smem, 
             }
             tc::wait_st();
           }
+          // A weight is 2^(c s + off), one multiply-add. off is rounded by up to 2^-24 of itself, a factor that all weights of a row
+          // have in common; it cancels, but against other tiles' and parts' (2^-16 up to kFar) and but for what 16 bits hold:
+          // with c m of 2^27 it may overflow fp16, later any type, or leave a sum of zero. Far scores are taken as distances
+          // from the reference first. (A tile whose scores are near has weights of zero beside a reference beyond 2 kFar.)
+          if (__any_sync(0xFFFFFFFFu, is_far)) {
+            far_scores(s_at, is_far ? row.m : 0.0f);
+            if (is_far) ref = 0.0f;
+          }
         }
-        const float off = kShift - (row.m == -INFINITY ? 0.0f : row.m);
+        const float off = fmaf(ref == -INFINITY ? 0.0f : -ref, p.c, kShift);
         const float2 c2 = make_float2(p.c, p.c), off2 = make_float2(off, off);
         float2 l2 = make_float2(0.0f, 0.0f);
         // P's 64 columns lie over S's first half: the second half of S is read before P reaches it
@@ -1220,11 +1243,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_kernel(const __gr
 #pragma unroll
     for (int s = kLanes / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
     // a part that attends to nothing has weight 0 (and l = 0); one with NaN keeps it
-    const float wgt = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+    const float wgt = ml.x == -INFINITY ? 0.0f : exp2f((ml.x - top) * p.c);
     float lw = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : ml.y * wgt;
 #pragma unroll
     for (int s = kLanes / 2; s > 0; s >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, s);
-    const float old = m == -INFINITY ? 0.0f : exp2f(m - top);
+    const float old = m == -INFINITY ? 0.0f : exp2f((m - top) * p.c);
     l = l * old + lw;
     m = top;
     const int here = min(kLanes, parts - k0);  // parts of this lane's head in this turn
@@ -1350,6 +1373,8 @@ cudaError_t launch_attention(dt_handle* h, const dt_attn_args* a, cudaStream_t s
   p.tree_box = 8;  // positions of a tree box: a power of two that covers P, up to a tile
   while (p.tree_box < a->P && p.tree_box < kTile) p.tree_box *= 2;
   p.c = a->scale * kLog2e;
+  p.lazy = kLazy / p.c;
+  p.far = kFar / p.c;
   p.ns = (a->shared_len + kTile - 1) / kTile;
   // units that the requests' own items would have more if they read the prefix with their own tokens
   const int64_t blocks = (a->P + 2 * p.pos - 1) / (2 * p.pos), blocks_s = ((int64_t)a->B * a->P + 2 * p.pos - 1) / (2 * p.pos);

@@ -1,4 +1,4 @@
-"""Attention whose scores are far apart: scales up to 1e30, in prompts.
+"""Attention whose scores are far apart: scales up to 1e30, in prompts and in trees.
 
 q and k are small whole numbers, so that a score without its scale is a whole number below 2^24 and exact in fp32 in any order of
 summation, as is its distance z from the row's largest. What the kernels may add then does not grow with the scores: the
@@ -13,6 +13,7 @@ import math
 
 import pytest
 
+import test_gpu_attention as tree
 import test_gpu_prompt as prompt
 from test_gpu_prompt import torch  # noqa: F401 (the fixture)
 
@@ -81,3 +82,45 @@ def test_prompts_of_any_scale(torch, name, dtype):  # noqa: F811
                 _fits(t, pr.out[r0:r0 + n, x], want, tol, (scale, b, x))
     h.close()
 
+
+TREES = {
+    "one token": dict(B=2, P=1, H_kv=1, G=4, D=128, page=16, lens=[37, 2000], tree=False),
+    "trees": dict(B=3, P=33, H_kv=2, G=4, D=64, page=32, lens=[100, 0, 777], n_pos=[33, 5, 20], packed=True),
+    "many rows": dict(B=1, P=140, H_kv=1, G=2, D=128, page=16, lens=[1300]),
+    "shared": dict(B=5, P=21, H_kv=2, G=4, D=128, page=32, lens=[2048 + 9 * i for i in range(5)], shared=2048),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", list(TREES))
+def test_trees_of_any_scale(torch, name, dtype):  # noqa: F811
+    import dynamic_draft_tree_gb300 as dt
+
+    t = torch
+    pr = tree.Problem(t, dtype=dtype, **TREES[name])
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    _whole(t, pr.q, g, 3)
+    shared = pr.shared // pr.page
+    for b in range(pr.B):
+        _whole(t, pr.k[b], g, 3)
+        if b:
+            pr.k[b][:pr.shared] = pr.k[0][:pr.shared]
+        pr.kn[pr.base[b]:pr.base[b] + pr.n[b]] = pr.k[b][pr.lens[b]:]
+        for e in range(shared if b else 0, -(-pr.lens[b] // pr.page)):
+            m = min(pr.page, pr.lens[b] - e * pr.page)
+            pr.kp[pr.table[b, e], :m] = pr.k[b][e * pr.page:e * pr.page + m]
+    h, ws = pr.handle(dt)
+    for scale in SCALES:
+        pr.scale = scale
+        pr.out.fill_(7.0)
+        pr.call(dt, h, ws)
+        assert dt.dt_get_status(h) == 0
+        for b in range(pr.B):
+            L, n, r0 = pr.lens[b], pr.n[b], pr.base[b]
+            ok = t.ones(n, L + n, dtype=t.bool, device="cuda")
+            ok[:, L:] = pr.mask[b, :n, :n].bool() if pr.mask is not None else ok[:, L:].tril()
+            for x in range(pr.q.shape[1]):
+                want, tol = _rows(t, pr.q[r0:r0 + n, x], pr.k[b][:, x // pr.G], pr.v[b][:, x // pr.G], ok, scale)
+                _fits(t, pr.out[r0:r0 + n, x], want, tol, (scale, b, x))
+    h.close()
