@@ -265,7 +265,8 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Shared& sh)
   do {
     if (__all_sync(0xFFFFFFFFu, tc::bar_try(bar, parity))) return true;
     if ((uint32_t)clock() - t0 > kWaitTicks) *(volatile int*)&sh.stop = 1;
-  } while (!*(volatile int*)&sh.stop);
+    // another warp may set it between two lanes' reads: they leave by a vote
+  } while (__all_sync(0xFFFFFFFFu, !*(volatile int*)&sh.stop));
   return false;
 }
 
