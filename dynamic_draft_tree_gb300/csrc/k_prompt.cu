@@ -928,7 +928,7 @@ __device__ void softmax_group(const PromptParams& p, Shared& sh, const CUtensorM
     // O is read before this group's next weights are handed over, and with them the next segment's first product
     const Segment s = segs.here(sh);
     segs.end(sh);
-    const bool odd = *(volatile int*)&sh.odd_values && s.t1 > s.ct;
+    const bool odd = __any_sync(0xFFFFFFFFu, *(volatile int*)&sh.odd_values) && s.t1 > s.ct;  // another warp may set it just now
     const int end = max(0, min(32, min(half, s.rows - group * half) - (wl & 96)));  // the warp's rows in use
     if (s.t1 - s.t0 == s.tt) {
       if (some && end > 0) write_rows<BF16>(p, s, group, wl, odd, row.l, end, o_at, place, out_map);

@@ -6,6 +6,7 @@ gone while others meet in a vote. Here 32 lanes run one after the other, each up
 place between two of them.
 """
 import os
+import re
 import subprocess
 
 import pytest
@@ -127,3 +128,13 @@ def program(tmp_path_factory):
 def test_a_warp_leaves_its_waits_together(program):
     r = subprocess.run([str(program)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
+
+
+def test_flags_that_steer_a_warp_are_read_by_a_vote():
+    """What the prompts' kernel reads while another warp may write it decides what whole warps do: one answer for all lanes."""
+    text = open(os.path.join(CSRC, "k_prompt.cu")).read()
+    reads = [x.strip() for x in text.split("\n") if "*(volatile int*)&sh." in x]
+    reads = [x for x in reads if not re.search(r"\*\(volatile int\*\)&sh\.\w+ = ", x)]
+    assert len(reads) == 2, reads  # the flag of a wait that gave up, and that of values that are no numbers
+    for x in reads:
+        assert re.search(r"__(any|all)_sync\(0xFFFFFFFFu, !?\*\(volatile int\*\)&sh\.\w+\)", x), x
