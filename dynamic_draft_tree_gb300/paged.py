@@ -86,7 +86,8 @@ class PagedCache:
 
     def fork(self, src, dst, length=None, stream=None):
         """Places dst, which own nothing (but the shared prefix), continue requests src behind their first ``length`` tokens
-        (default: all of them): int32 tensors, one entry a fork."""
+        (default: all of them): int32 tensors, one entry a fork. Token histories go along by ``TokenState.fork``. One that finds
+        no page (DT_DEV_KV_FULL) owns nothing still, and its length stays what the place's last request left."""
         if self.refs is None:
             raise ValueError("the cache was made without forks")
         dt_kv_fork(self.h, self.pool, self.refs, self.pages, src, dst, self.seq_len, length=length, shared_len=self.shared_len,
@@ -133,6 +134,19 @@ class TokenState:
     def prompt(self, tokens, n_new, row_off=None, stream=None):
         """Marks prompt tokens ([B][P], or packed by row_off)."""
         dt_count_tokens(self.h, self.counts, tokens, n_new, row_off=row_off, prompt=True, stream=stream)
+
+    def fork(self, src, dst, stream=None):
+        """Places dst get the histories of requests src (int32 tensors, as for ``PagedCache.fork``, which takes pages and lengths along):
+        a fork behind all of its source's tokens. (One behind fewer has a history of its own: a cleared row and ``prompt``.)
+        Pairs that ``PagedCache.fork`` refuses for their places (outside the batch, a destination named before, a source
+        that is a destination) leave the histories as they are."""
+        with torch.cuda.stream(stream):
+            B = self.counts.shape[0]
+            ok = (src >= 0) & (src < B) & (dst >= 0) & (dst < B) & ~(src[:, None] == dst).any(1)
+            ok &= ~(dst[:, None] == dst).tril(-1).any(1)
+            s, d = (torch.where(ok, x, 0) for x in (src, dst))
+            # differences are added, zero for pairs that are left out: no place is written twice, nor one outside
+            self.counts.index_add_(0, d, (self.counts[s] - self.counts[d]) * ok[:, None])
 
     def process(self, logits, meta, packed=False, out=None, stream=None):
         """Target rows prepared for the verify, in place or into ``out``."""
