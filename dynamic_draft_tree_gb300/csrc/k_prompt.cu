@@ -18,10 +18,11 @@
 // segments too: Q has a buffer a group that is loaded again when the group's last S of a segment is done. S (fp32), P (16-bit,
 // over S) and O live in tensor memory, which they fill (2 x 128 + 2 x 128 columns at D = 128).
 //
-// Bound by the chain S, softmax, P V of the two groups in turn: a tile of both takes 2810 clocks at D = 128, of which the tensor
-// cores need 2048, and by power where all SMs are at it: one prompt of 16384 tokens, 8 x 4 heads of 128, bf16: 1305 us,
-// 1.69 PFLOP/s, at first and 1400 us, 1.57 PFLOP/s, at 1.84 GHz when it goes on. An item's ends cost about 1.4 tiles more: its
-// masked tile, and the softmax of the next item, which begins when the rows have left.
+// Bound by the chain S, softmax, P V of the two groups in turn: a tile of both takes 2815 clocks at D = 128, of which the tensor
+// cores need 2048 (pages of 64 to 256 tokens as whole boxes, pages of 16 tokens 3280), and by power where all SMs are at it: one
+// prompt of 16384 tokens, 8 x 4 heads of 128, bf16: 1310 to 1340 us, 1.65 PFLOP/s, in a few runs and 1480 us, 1.49 PFLOP/s, when
+// it goes on. An item's ends cost 1.2 to 1.5 tiles more: its masked tile, and the softmax of the next item, which begins when the
+// rows have left.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -43,8 +44,8 @@ constexpr float kShift = 6.0f;  // weights are held as 2^kShift times themselves
 constexpr float kFar = 256.0f;  // scores of rows whose maximum is beyond this (log2 units) become distances first (softmax_group)
 // Units of the line: a tile, for one group of rows (whose chain of softmax and products takes as long) as for two; an item has
 // kItemUnits more in front for its ends. Tile t of an item at unit u is at u + kItemUnits + t, and belongs to the CTA that this
-// falls to. 16 prompts of up to 2000 tokens, whose CTAs have 8 to 33 items each, take 186 us with one unit for an item, 192 with two
-// and 203 with three (one and a half: no difference).
+// falls to. 16 prompts of up to 2000 tokens, whose CTAs have 8 to 33 items each, take 189 us with one unit for an item, 195 with two
+// and 207 with three (one and a half: no difference).
 constexpr int kItemUnits = 1;
 
 // An item that is cut: left by its first CTA for the join.
@@ -511,8 +512,8 @@ __device__ void issue_mma(const PromptParams& p, Shared& sh, uint32_t q_smem, ui
     uint32_t parity;
     ring<S::kK>(n, stage, parity);
     const bool fresh = t == t1;  // the next tile is another segment's
-    // What a step waits for has been waited for before its weights are there: K and the turn behind the weights made a tile of
-    // two groups 2760 clocks long instead of 2580.
+    // What a step waits for has been waited for before its weights are there: with K and the turn behind the weights one prompt of
+    // 16384 tokens took 1494 us when it took 1335.
     if (n > 0) {
       uint32_t v_parity;
       ring<S::kV>(n - 1, v_stage, v_parity);
@@ -611,7 +612,7 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
 
 // One warp puts down the segments for the other roles, and clears values. Value rows past the end of a tile become zero
 // (a weight of zero times what lies there need not be zero), and so do NaN and infinities at positions that only some rows
-// of the item attend to: the rows that do add them in finish_rows.
+// of the item attend to: the rows that do add them in add_odd_values.
 template <int DP, bool BF16>
 __device__ void fix_values(const PromptParams& p, Shared& sh, uint8_t* v_smem, int lane) {
   using S = Smem<DP>;
@@ -1119,8 +1120,12 @@ Layout layout_of(const dt_handle* h, int D) {
   return L;
 }
 
-// Items of few tiles are not cut: a launch to join them costs more than an uneven share. One prompt, 8 x 4 heads of 128, cut
-// and whole: 93 tokens 12.6 and 9.3 us, 512 17.1 and 14.3, 1024 24.3 and 20.2, 1500 31.1 and 33.3, 2000 41.1 and 50.4.
+// Items of few tiles are not cut: a launch to join them costs more than an uneven share. One prompt, four heads a key head, heads
+// of 128, cut and whole, us: eight key heads 93 tokens 12.1 and 8.8, 512 17.1 and 13.8, 1024 23.9 and 19.8, 1500 30.5 and 32.7,
+// 2000 40.5 and 49.8; one key head 93 11.8 and 8.5, 512 16.3 and 13.3, 1024 18.7 and 19.0, 1500 21.2 and 24.6; 16 prompts of 93
+// 15.4 and 12.3, with one key head 12.7 and 9.3. The host decides, which knows the buffers and not the lengths: by what the tables
+// and rows could hold. So a short prompt of a cache that may grow past these tiles is cut, and joined (93 tokens, room for 8192:
+// 12.1 us), and so are several whose rows together are more.
 constexpr int kWholeTiles = 8;
 template <int DP, bool BF16>
 cudaError_t launch_t(dt_handle* h, const PromptParams& p, const CUtensorMap* m, cudaStream_t s) {

@@ -106,7 +106,7 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16, 32, 64 or 128 columns of the warp's 32 lanes, complete on return: thread l gets row l. Load and wait are one
+// 16, 32 or 64 columns of the warp's 32 lanes, complete on return: thread l gets row l. Load and wait are one
 // statement, so that no use of the values can be moved between the two.
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* r) {
   asm volatile(
