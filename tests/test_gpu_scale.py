@@ -124,3 +124,47 @@ def test_trees_of_any_scale(torch, name, dtype):  # noqa: F811
                 want, tol = _rows(t, pr.q[r0:r0 + n, x], pr.k[b][:, x // pr.G], pr.v[b][:, x // pr.G], ok, scale)
                 _fits(t, pr.out[r0:r0 + n, x], want, tol, (scale, b, x))
     h.close()
+
+
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e3), ("bf16", 1e18), ("fp16", 3e2), ("fp16", 2e4)])
+@pytest.mark.parametrize("kind", ["prompt", "cut prompt", "tree"])
+def test_large_queries_and_keys(torch, kind, dtype, size):  # noqa: F811
+    """The scores themselves are large, up to 2^127. Rows are convex combinations of values; where the largest score is ahead of the
+    others by more than fp32 sums are off by, on both sides, and a weight below 2^-64, a row is that token's value. (In fp16 some
+    queries and keys of the largest size are infinite: rows whose definition is no number are left out.)"""
+    import dynamic_draft_tree_gb300 as dt
+
+    t = torch
+    pr = tree.Problem(t, B=2, P=9, H_kv=2, G=2, D=128, page=16, lens=[900, 30], dtype=dtype) if kind == "tree" else \
+        prompt.Problem(t, n=[200, 40] if kind == "prompt" else [1400], H_kv=1, G=4, D=64, dtype=dtype)
+    pr.q *= size / 2
+    for x in (pr.kn, pr.kp):
+        x *= size
+    pr.k = [x * size for x in pr.k]
+    h, ws = pr.handle(dt)
+    pr.call(dt, h, ws)
+    assert dt.dt_get_status(h) == 0
+    u, sure = t.finfo(pr.q.dtype).eps / 2, 0
+    for b in range(pr.B):
+        L, n = pr.lens[b], pr.n[b]
+        r0 = pr.base[b] if kind == "tree" else pr.off[b]
+        ok = t.ones(n, L + n, dtype=t.bool, device="cuda")
+        ok[:, L:] = pr.mask[b, :n, :n].bool() if kind == "tree" else ok[:, L:].tril()
+        for x in range(pr.q.shape[1]):
+            q, k, v = (y.double() for y in (pr.q[r0:r0 + n, x], pr.k[b][:, x // pr.G], pr.v[b][:, x // pr.G]))
+            got = pr.out[r0:r0 + n, x].double()
+            z = (q @ k.T).masked_fill(~ok, -math.inf)
+            some = ~(t.isnan(z) | (z == math.inf)).any(1)
+            assert bool(t.isfinite(got[some]).all())
+            most = t.where(ok[:, :, None], v.abs()[None], 0.0).amax((1, 2))
+            assert bool((got.abs().amax(1) <= most * (1 + 3 * u))[some].all())
+            two = z.topk(min(2, z.shape[1]), 1)
+            off = (pr.D + 8) * 2.0 ** -24 * t.where(ok, q.abs() @ k.abs().T, 0.0).amax(1)
+            clear = two.values[:, 0] - two.values[:, -1] > 2 * off + 64 / pr.scale if z.shape[1] > 1 else ok[:, 0]
+            clear &= some
+            sure += int(clear.sum())
+            want = v[two.indices[:, 0]]
+            assert bool(((got - want).abs()[clear] <= 2.0 ** -12 * most[clear, None] + u * want.abs()[clear]).all())
+    # (an infinite element in 900 keys of 128, one in a thousand beyond 3.3 deviations, leaves no row sure)
+    assert sure > 20 or (kind == "tree" and size == 2e4)
+    h.close()
